@@ -366,6 +366,65 @@ int moe_grouped_gemm_bwd_dw_recompute(const void* x, const int32_t* src_token, i
                                       const moe_shared_expert* shared, void* ws, size_t ws_bytes,
                                       moe_stream_t stream);
 
+/* ---------------------------------------------------------------- few tokens
+ * The whole layer for a few tokens (serving), in one call:
+ *   logits = x Wg + bias, idx / gate as moe_route gives them,
+ *   y[t] = residual[t] + shared(x[t]) + sum_j gate[t,j] expert_idx[t,j](x[t])
+ * over the experts of the window [g0, g0+G) (w13 [G,2I,H], w2 [G,H,I]; pairs
+ * of other experts add nothing: they are another device's part of the sum).
+ * Router ([H,E] fp32): the logits are exact sums rounded once to fp32, and
+ * idx / gate follow from them ([T,E], [T,k], [T,k] outputs).  With wg NULL
+ * logits is an input (bias must be NULL).  A logit of -inf masks an expert; a
+ * token whose logits are all -inf gets gates of zero.  Shared expert: ws13
+ * [2I,H] and ws2 [H,I], both or neither.  residual [T,H] is nullable, and y
+ * may be its buffer.  Gate/up values, expert outputs and the sum stay in fp32;
+ * y is rounded once.
+ * T <= 128 and T k <= 4096 (MOE_ERR_UNSUPPORTED beyond: the grouped path is
+ * the faster one there), one expert's w13 and the call's rows below 2 GiB.
+ * ws: moe_decode_workspace_bytes bytes (256-byte aligned, contents scratch),
+ * not shared by calls that may overlap.
+ */
+size_t moe_decode_workspace_bytes(int T, int H, int I, int E, int k, int dt);
+int moe_decode(const void* x, int dt, const float* wg, const float* bias, int T, int H, int I,
+               int E, int k, int g0, int G, const void* w13, const void* w2, const void* ws13,
+               const void* ws2, const void* residual, float* logits, int32_t* idx, float* gate,
+               void* y, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------- fused linear product
+ * The dense products beside the expert layer (projections onto the residual
+ * stream, dense feed-forward layers):
+ *   z = x W^T + bias,  y = act(z) + residual
+ * x [M,K], w [N,K], bias [N] fp32 (nullable), residual [M,N] (nullable; y may
+ * be its buffer), z [M,N] (nullable: kept for the backward).  Products and the
+ * epilogue are fp32; z and y are each rounded once (act sees the unrounded z).
+ * act: MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU (z sigma(z)), MOE_ACT_GELU
+ * (z Phi(z)) or MOE_ACT_GELU_TANH (its tanh form).  N and K are multiples of
+ * 64; M is any number; x, w, y are below 2 GiB each.
+ */
+enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_SILU = 2,
+  MOE_ACT_GELU = 3,
+  MOE_ACT_GELU_TANH = 4
+};
+int moe_linear(const void* x, int dt, int M, int N, int K, const void* w, const float* bias,
+               int act, const void* residual, void* z, void* y, moe_stream_t stream);
+
+/* Its gradients, given dy [M,N] and the z the forward kept (NULL for
+ * MOE_ACT_NONE):
+ *   dz = dy * act'(z),  dx = dz W,  dw = dz^T x,  db = sum_m dz
+ * dx [M,K], dw [N,K] and db [N] (fp32) are each written if not NULL; the
+ * gradient of the residual is dy itself.  dz is rounded to the storage type
+ * for the two products (they read it on the matrix cores); db sums it
+ * unrounded.  M == 0 writes zeros to dw and db.  ws: scratch of
+ * moe_linear_bwd_workspace_bytes bytes, 256-byte aligned.
+ */
+size_t moe_linear_bwd_workspace_bytes(int M, int N, int K, int dt, int act);
+int moe_linear_bwd(const void* dy, const void* z, const void* x, const void* w, int dt, int M,
+                   int N, int K, int act, void* dx, void* dw, float* db, void* ws,
+                   size_t ws_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

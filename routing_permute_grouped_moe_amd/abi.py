@@ -23,6 +23,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 MOE_F32, MOE_BF16 = 0, 1
 MOE_ROUTER_WG_SPLIT = 1          # moe_router_logits_bwd: reuse the forward's split of wg
+MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH = range(5)
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_LAUNCH = range(5)
 
 _P = ctypes.c_void_p
@@ -77,6 +78,12 @@ _SIGS = {
     "moe_grouped_gemm_bwd_dw_recompute": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I,
                                                _I, _I, _P, _P, ctypes.POINTER(SharedExpert), _P,
                                                _SZ, _P]),
+    "moe_decode_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "moe_decode": (_I, [_P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P,
+                        _P, _P, _P, _SZ, _P]),
+    "moe_linear": (_I, [_P, _I, _I, _I, _I, _P, _P, _I, _P, _P, _P, _P]),
+    "moe_linear_bwd_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "moe_linear_bwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -262,3 +269,28 @@ def moe_grouped_gemm_bwd_dw_recompute(x, src_token, T, h13, act, dyp, dh13, offs
     _call("moe_grouped_gemm_bwd_dw_recompute", addr(x), addr(src_token), T, addr(h13),
           addr(act), addr(dyp), addr(dh13), addr(offsets), g0, G, R, dt, H, I, addr(dw13),
           addr(dw2), _sh(shared), addr(ws), ws_bytes, _stream(stream))
+
+
+def moe_decode_workspace_bytes(T, H, I, E, k, dt) -> int:
+    return _lib.moe_decode_workspace_bytes(T, H, I, E, k, dt)
+
+
+def moe_decode(x, dt, wg, bias, T, H, I, E, k, g0, G, w13, w2, ws13, ws2, residual, logits, idx,
+               gate, y, ws, ws_bytes, stream=None):
+    _call("moe_decode", addr(x), dt, addr(wg), addr(bias), T, H, I, E, k, g0, G, addr(w13),
+          addr(w2), addr(ws13), addr(ws2), addr(residual), addr(logits), addr(idx), addr(gate),
+          addr(y), addr(ws), ws_bytes, _stream(stream))
+
+
+def moe_linear(x, dt, M, N, K, w, bias, act, residual, z, y, stream=None):
+    _call("moe_linear", addr(x), dt, M, N, K, addr(w), addr(bias), act, addr(residual), addr(z),
+          addr(y), _stream(stream))
+
+
+def moe_linear_bwd_workspace_bytes(M, N, K, dt, act) -> int:
+    return _lib.moe_linear_bwd_workspace_bytes(M, N, K, dt, act)
+
+
+def moe_linear_bwd(dy, z, x, w, dt, M, N, K, act, dx, dw, db, ws, ws_bytes, stream=None):
+    _call("moe_linear_bwd", addr(dy), addr(z), addr(x), addr(w), dt, M, N, K, act, addr(dx),
+          addr(dw), addr(db), addr(ws), ws_bytes, _stream(stream))

@@ -14,7 +14,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
-SOURCES = ["api.cpp", "route.hip", "permute.hip", "router.hip", "gmm.hip"]
+SOURCES = ["api.cpp", "route.hip", "permute.hip", "router.hip", "gmm.hip", "decode.hip",
+           "linear.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 FLAGS = [

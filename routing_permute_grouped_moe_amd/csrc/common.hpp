@@ -172,3 +172,9 @@ int moe_gmm_router_dx(const void* dlb, const void* wgb, void* dx, int T, int H, 
                       hipStream_t s);
 int moe_gmm_router_dwg(const void* x, const void* dl3s, float* partials, int T, int H, int E, int S,
                        hipStream_t s);
+// dense products of the fused linear calls on the grouped GEMM's tiles (gmm.hip)
+int moe_gmm_linear_fwd(const void* x, int dt, int M, int N, int K, const void* w,
+                       const float* bias, int act, const void* residual, void* z, void* y,
+                       hipStream_t s);
+int moe_gmm_linear_bwd(const void* dz, const void* x, const void* w, int dt, int M, int N, int K,
+                       void* dx, void* dw, hipStream_t s);

@@ -8,6 +8,8 @@
 //   DX1   dact = dyp . W2[e], epilogue SwiGLU backward -> dh13
 //   DX2   dxp = dh13 . W13[e]
 //   DW    dW[e] = P_e^T . Q_e, contraction over the rows of group e
+// and, for the fused linear product of dense layers, a sixth:
+//   LIN   y = act(x . W^T + bias) + residual, z = x . W^T + bias kept on request
 // A group's rows come from the device offsets table, so the host never
 // learns the counts ([MoE-ops] Host-Device section, Fig. 4).
 //
@@ -37,6 +39,7 @@
 //    workgroups sharing a weight panel share an L2.
 #include <type_traits>
 
+#include "act.hpp"
 #include "validate.hpp"
 
 namespace {
@@ -74,7 +77,7 @@ __host__ __device__ __forceinline__ uint32_t out_bytes(long long b) {
   return b <= 0 ? 0u : (b >= 0xFFFFFFE0LL ? 0xFFFFFFE0u : (uint32_t)b);
 }
 
-enum Mode { FWD1 = 0, FWD2 = 1, DX1 = 2, DX2 = 3, DW = 4 };
+enum Mode { FWD1 = 0, FWD2 = 1, DX1 = 2, DX2 = 3, DW = 4, LIN = 5 };
 
 struct GmmArgs {
   const int32_t* offsets;
@@ -102,6 +105,8 @@ struct GmmArgs {
   // operand is row gather[r] of X (gather_rows rows) instead of row r --
   // FWD1's A rows, DW's Q rows (the K rows of the second factor)
   const int32_t* gather; int gather_rows;
+  // LIN: epilogue operands (nullable), rows of N elements like C; C2 is z
+  const float* bias; const void* res; int act;
 };
 
 // Per element type: K step BK (KS MFMA k-steps), ring of STAGES stages of two
@@ -1305,7 +1310,39 @@ __device__ __forceinline__ void run_tile(const GmmArgs& a, const GroupLds& gl, c
           ok = m < lim_m && n < a.N;
           return (uint32_t)(m * a.ldc + n);
         };
-        if (a.out_f32) {
+        if constexpr (MODE == LIN) {
+          const __amdgpu_buffer_rsrc_t br = make_rsrc(a.bias, (uint32_t)a.N * 4u);
+          const __amdgpu_buffer_rsrc_t rr =
+              make_rsrc((const char*)a.res + (long long)rows0 * a.ldc * ES, clamp_bytes(cbytes));
+          const __amdgpu_buffer_rsrc_t zr =
+              make_rsrc((char*)a.C2 + (long long)rows0 * a.ldc * ES, out_bytes(cbytes));
+          emit(hc, [&](int row, int c, const float* v) {
+            bool ok;
+            const uint32_t e = place(row, c, ok);
+            const uint32_t n = (uint32_t)(n0 + (c / HW) * (2 * HW) + HW * h + (c % HW));
+            float o[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) o[q] = v[q];
+            if (a.bias != nullptr) {
+              float b[8];
+              unpack16(buf_load16(br, n * 4u), b, 0.f);
+              unpack16(buf_load16(br, n * 4u + 16u), b + 4, 0.f);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) o[q] += b[q];
+            }
+            if (a.C2 != nullptr) store8(zr, ok, e, o);
+            if (a.act != MOE_ACT_NONE)
+#pragma unroll
+              for (int q = 0; q < 8; ++q) o[q] = act_value(o[q], a.act);
+            if (a.res != nullptr) {
+              float r[8];
+              load8(rr, ok, e, r);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) o[q] += r[q];
+            }
+            store8(cr, ok, e, o);
+          });
+        } else if (a.out_f32) {
           emit(hc, [&](int row, int c, const float* v) {
             bool ok;
             const uint32_t e = place(row, c, ok);
@@ -1516,13 +1553,14 @@ __global__ __launch_bounds__(Waves<W>::NT, 1) void gmm_pair_kernel(GmmArgs a1, G
   const Space s2 = tile_space<M2, false>(a2, gl, &s_next);
   const int P = gridDim.x;
   const bool second = a0.M > 0;
+  const bool alone = a0.M < 0;   // a launch without a partner: every tile runs here
   Space s0 = s2;
   // positions: [mv tiles of a0 from tile t0][splitA gradient tiles][row-tiled
   // product][gradient tiles from splitA + skip on]
   int mv = 0, t0 = 0, splitA, skip = 0;
   if (!second) {
     const int L = lead_tiles(gl, ng, a1.K, s2);
-    splitA = lead_kept(s1.total, L, P);
+    splitA = alone ? L : lead_kept(s1.total, L, P);
     skip = L - splitA;
   } else {
     s0 = tile_space<M2, false>(a0, gl, &s_next);
@@ -1802,7 +1840,7 @@ int launch(const GmmArgs& a, hipStream_t s, const char* what) {
 
 // a0: for the second launch of a backward call, the first launch's gradient
 // product (its leading tiles beyond the first launch's share run here);
-// M = 0 otherwise
+// M = 0 for that first launch, M < 0 for a launch on its own
 template <int M1, int M2>
 int launch_pair(int dt, const GmmArgs& a1, const GmmArgs& a2, const GmmArgs& a0, hipStream_t s,
                 const char* what) {
@@ -1832,7 +1870,7 @@ int launch_chain(int dt, const GmmArgs& a1, const GmmArgs& a2, hipStream_t s, co
 // modes), for calls whose groups average at most half a tile of rows
 template <int MODE>
 int launch_dt(int dt, const GmmArgs& a, hipStream_t s, const char* what, bool light = false) {
-  if constexpr (MODE != DW) {
+  if constexpr (MODE != DW && MODE != LIN) {
     if (light && dt == MOE_BF16) {
       if constexpr (MODE == FWD1)
         if (a.gather != nullptr) return launch<bf16_t, MODE, true, true>(a, s, what);
@@ -2266,4 +2304,45 @@ int moe_gmm_router_dwg(const void* x, const void* dl3s, float* partials, int T, 
   a.W = dl3s; a.ldw = E; a.w_gs = 3LL * (T / S) * E;
   a.C = partials; a.ldc = E; a.c_gs = (long long)H * E; a.out_f32 = 1;
   return launch<bf16_t, DW>(a, s, "moe_router_logits_bwd(dwg)");
+}
+
+// ---------------------------------------------------------------- fused linear product
+// Dense products of the linear calls: one group of M rows.
+
+int moe_gmm_linear_fwd(const void* x, int dt, int M, int N, int K, const void* w,
+                       const float* bias, int act, const void* residual, void* z, void* y,
+                       hipStream_t s) {
+  GmmArgs a = {};
+  a.dense = 1; a.G = 1; a.shT = M; a.R = M;
+  a.N = N; a.K = K;
+  a.X = x; a.ldx = K;
+  a.W = w; a.ldw = K;
+  a.C = y; a.ldc = N;
+  a.C2 = z;
+  a.bias = bias; a.res = residual; a.act = act;
+  return launch_dt<LIN>(dt, a, s, "moe_linear");
+}
+
+// dx = dz . W (W stored [K = N][N = K]) and dW = dz^T . x in one launch
+int moe_gmm_linear_bwd(const void* dz, const void* x, const void* w, int dt, int M, int N, int K,
+                       void* dx, void* dw, hipStream_t s) {
+  const char* fn = "moe_linear_bwd";
+  GmmArgs a1 = {};
+  a1.dense = 1; a1.G = 1; a1.shT = M; a1.R = M;
+  GmmArgs a2 = a1;
+  a1.N = K; a1.K = N;
+  a1.X = dz; a1.ldx = N;
+  a1.W = w; a1.ldw = K;
+  a1.C = dx; a1.ldc = K;
+  a2.M = N; a2.N = K;
+  a2.X = dz; a2.ldx = N;
+  a2.W = x; a2.ldw = K;
+  a2.C = dw; a2.ldc = K;
+  if (dx != nullptr && dw != nullptr && M > 0) {
+    GmmArgs none = {};
+    none.M = -1;
+    return launch_pair<DX2, DW>(dt, a1, a2, none, s, fn);
+  }
+  if (dx != nullptr && M > 0) MOE_TRY(launch_dt<DX2>(dt, a1, s, fn));
+  return dw != nullptr ? launch_dt<DW>(dt, a2, s, fn) : MOE_OK;
 }

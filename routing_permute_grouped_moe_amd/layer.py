@@ -32,7 +32,7 @@ no weight gradients.
 from __future__ import annotations
 
 from dataclasses import dataclass, field
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -314,3 +314,189 @@ class MoeLayer:
     def step(self, stream=None):
         self.forward(stream)
         self.backward(stream)
+
+
+# ---------------------------------------------------------------------- checked calls
+def _check(name, t, dtype, device, *shape):
+    """A tensor the kernels can read as it lies: dense, of this shape, type and device."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, not {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the weights are on {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+
+
+class _On:
+    """The device of a call's tensors, and its stream as torch's current one, so
+    that outputs and workspaces allocated inside belong to that stream."""
+    __slots__ = ("guards",)
+
+    def __init__(self, device, stream):
+        self.guards = []
+        if torch.cuda.current_device() != device.index:
+            self.guards.append(torch.cuda.device(device))
+        if stream is not None:
+            self.guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def _device(t):
+    if not t.is_cuda:
+        raise ValueError(f"weights are on {t.device}, not on a GPU")
+    return t.device
+
+
+class Decoded(NamedTuple):
+    """One pass of :class:`MoeDecode`."""
+    y: torch.Tensor        # [T, H]
+    idx: torch.Tensor      # [T, k] int32, chosen experts
+    gate: torch.Tensor     # [T, k] fp32
+    logits: torch.Tensor   # [T, E] fp32
+
+
+class MoeDecode:
+    """The expert layer for a few tokens (serving), on parameters that stay
+    where they are: those of a ``MoeLayer``, or of a loaded model.
+
+    ``shape.T`` is the most tokens of a call (at most 128); ``shape.router``
+    says whether the logits come from ``wg`` (and ``bias``) or with each call;
+    ``shape.g0`` / ``shape.G`` is the window of experts that w13 and w2 hold."""
+
+    def __init__(self, shape: LayerShape, w13, w2, wg=None, bias=None, ws13=None, ws2=None):
+        s = self.s = shape
+        if s.capacity is not None:
+            raise ValueError("the few-token layer drops no pairs: capacity must be None")
+        if s.router != (wg is not None):
+            raise ValueError("wg comes with shape.router, and only with it")
+        if s.shared != (ws13 is not None) or s.shared != (ws2 is not None):
+            raise ValueError("ws13 and ws2 come with shape.shared, and only with it")
+        dev = self.device = _device(w13)
+        f32 = torch.float32
+        self.dt = abi.dtype_code(w13)
+        _check("w13", w13, s.dtype, dev, s.groups, 2 * s.I, s.H)
+        _check("w2", w2, s.dtype, dev, s.groups, s.H, s.I)
+        if wg is not None:
+            _check("wg", wg, f32, dev, s.H, s.E)
+        if bias is not None:
+            _check("bias", bias, f32, dev, s.E)
+        if ws13 is not None:
+            _check("ws13", ws13, s.dtype, dev, 2 * s.I, s.H)
+            _check("ws2", ws2, s.dtype, dev, s.H, s.I)
+        self.w13, self.w2, self.wg, self.bias, self.ws13, self.ws2 = w13, w2, wg, bias, ws13, ws2
+        self._ws_bytes = {}
+
+    @classmethod
+    def of_layer(cls, layer: "MoeLayer", max_tokens: int = 128) -> "MoeDecode":
+        """On the parameters of a training layer."""
+        from dataclasses import replace
+        return cls(replace(layer.s, T=max_tokens, capacity=None), layer.w13, layer.w2,
+                   wg=layer.wg, bias=layer.bias, ws13=layer.ws13, ws2=layer.ws2)
+
+    def forward(self, x, residual=None, logits=None, out=None, stream=None) -> Decoded:
+        """``x`` [T, H] -> :class:`Decoded`.  ``out``: y's buffer (the
+        residual's will do; allocated if None).  Everything is enqueued on
+        ``stream`` (None: the current one)."""
+        s, dev = self.s, self.device
+        T = x.shape[0]
+        if T > s.T:
+            raise ValueError(f"{T} tokens in a layer built for at most {s.T}")
+        _check("x", x, s.dtype, dev, T, s.H)
+        if residual is not None:
+            _check("residual", residual, s.dtype, dev, T, s.H)
+        if (logits is None) != s.router:
+            raise ValueError("logits come with the call if, and only if, there is no router")
+        if logits is not None:
+            _check("logits", logits, torch.float32, dev, T, s.E)
+        with _On(dev, stream) as st:
+            f32 = torch.float32
+            if out is None:
+                out = torch.empty_like(x)
+            else:
+                _check("out", out, s.dtype, dev, T, s.H)
+            if logits is None:
+                logits = torch.empty((T, s.E), dtype=f32, device=dev)
+            idx = torch.empty((T, s.k), dtype=torch.int32, device=dev)
+            gate = torch.empty((T, s.k), dtype=f32, device=dev)
+            if T not in self._ws_bytes:
+                self._ws_bytes[T] = abi.moe_decode_workspace_bytes(T, s.H, s.I, s.E, s.k, self.dt)
+            n = self._ws_bytes[T]
+            # a workspace per call, from the stream's own pool: calls on several
+            # streams, or captured into several graphs, never share one
+            ws = torch.empty(n, dtype=torch.uint8, device=dev)
+            abi.moe_decode(x, self.dt, self.wg, self.bias, T, s.H, s.I, s.E, s.k, s.g0, s.groups,
+                           self.w13, self.w2, self.ws13, self.ws2, residual, logits, idx, gate,
+                           out, ws, n, st)
+        return Decoded(out, idx, gate, logits)
+
+
+ACTS = {"none": abi.MOE_ACT_NONE, "relu": abi.MOE_ACT_RELU, "silu": abi.MOE_ACT_SILU,
+        "gelu": abi.MOE_ACT_GELU, "gelu_tanh": abi.MOE_ACT_GELU_TANH}
+
+
+class Linear:
+    """``y = act(x W^T + bias) + residual`` on a weight W [N, K], and its
+    gradients; ``bias`` is [N] fp32."""
+
+    def __init__(self, w, bias=None, act: str = "none"):
+        self.device = _device(w)
+        if w.dim() != 2:
+            raise ValueError(f"w has {w.dim()} dimensions, not 2")
+        self.N, self.K = w.shape
+        self.dt, self.dtype = abi.dtype_code(w), w.dtype
+        _check("w", w, w.dtype, self.device, self.N, self.K)
+        if bias is not None:
+            _check("bias", bias, torch.float32, self.device, self.N)
+        if act not in ACTS:
+            raise ValueError(f"act {act!r} is none of {', '.join(ACTS)}")
+        self.w, self.bias, self.act = w, bias, ACTS[act]
+
+    def forward(self, x, residual=None, save_z=False, out=None, stream=None):
+        """``x`` [M, K] -> y [M, N], or (y, z) with ``save_z``.  ``out``: y's
+        buffer (the residual's will do)."""
+        M, dev = x.shape[0], self.device
+        _check("x", x, self.dtype, dev, M, self.K)
+        if residual is not None:
+            _check("residual", residual, self.dtype, dev, M, self.N)
+        with _On(dev, stream) as st:
+            if out is None:
+                out = torch.empty((M, self.N), dtype=self.dtype, device=dev)
+            else:
+                _check("out", out, self.dtype, dev, M, self.N)
+            z = torch.empty((M, self.N), dtype=self.dtype, device=dev) if save_z else None
+            abi.moe_linear(x, self.dt, M, self.N, self.K, self.w, self.bias, self.act, residual,
+                           z, out, st)
+        return (out, z) if save_z else out
+
+    def backward(self, dy, x, z=None, bias_grad=None, stream=None):
+        """(dx, dw, db) of ``dy`` [M, N], the forward's ``x`` and the ``z`` it
+        kept (None without an activation).  db is None unless ``bias_grad``
+        (by default: unless there is a bias).  The residual's gradient is dy."""
+        M, dev = dy.shape[0], self.device
+        _check("dy", dy, self.dtype, dev, M, self.N)
+        _check("x", x, self.dtype, dev, M, self.K)
+        if (z is None) != (self.act == abi.MOE_ACT_NONE):
+            raise ValueError("z comes with an activation, and only with it")
+        if z is not None:
+            _check("z", z, self.dtype, dev, M, self.N)
+        if bias_grad is None:
+            bias_grad = self.bias is not None
+        with _On(dev, stream) as st:
+            dx = torch.empty_like(x)
+            dw = torch.empty_like(self.w)
+            db = torch.empty(self.N, dtype=torch.float32, device=dev) if bias_grad else None
+            n = abi.moe_linear_bwd_workspace_bytes(M, self.N, self.K, self.dt, self.act)
+            ws = torch.empty(n, dtype=torch.uint8, device=dev)
+            abi.moe_linear_bwd(dy, z, x, self.w, self.dt, M, self.N, self.K, self.act, dx, dw, db,
+                               ws, n, st)
+        return dx, dw, db

@@ -1,0 +1,246 @@
+"""The few-token layer against its definition in 64 bits (GPU only)."""
+import pytest
+import torch
+
+from decode_util import (U, assert_within, ref_decode, ref_linear, ref_logits, ref_route)
+from gpu_util import have_gpu
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not have_gpu(), reason="needs a GPU")]
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def make(T, H, I, E, k, g0=0, G=None, dt=BF, shared=False, router=True, bias=True, seed=0):
+    from routing_permute_grouped_moe_amd.layer import LayerShape, MoeDecode
+    gen = torch.Generator(device="cuda").manual_seed(1000 + seed)
+    shape = LayerShape(T=T, H=H, I=I, E=E, k=k, dtype=dt, g0=g0, G=G, shared=shared,
+                       router=router)
+    n = lambda *s, std=1.0, d=dt: torch.empty(s, dtype=d, device="cuda").normal_(0, std,
+                                                                                generator=gen)
+    G = shape.groups
+    p = {"w13": n(G, 2 * I, H, std=H ** -0.5), "w2": n(G, H, I, std=I ** -0.5)}
+    if router:
+        p["wg"] = n(H, E, std=1.5 * H ** -0.5, d=F32)
+        if bias:
+            p["bias"] = n(E, std=0.5, d=F32)
+    if shared:
+        p["ws13"], p["ws2"] = n(2 * I, H, std=H ** -0.5), n(H, I, std=I ** -0.5)
+    return MoeDecode(shape, **p), n
+
+
+def check(op, x, r, residual=None, logits=None):
+    """Every output of one pass: logits, choices, gates and y."""
+    s = op.s
+    if s.router:
+        full = ref_logits(x, op.wg, op.bias)
+        # one rounding to fp32 of a sum that is exact to far below it
+        assert_within("logits", r.logits, (full, 1.001 * U * full.abs() + 1e-12))
+        lg = full.float()
+        same = lg == r.logits.cpu()
+        assert same.float().mean() > 0.999      # (a sum within 1e-12 of a rounding border)
+        lg = r.logits.cpu()
+    else:
+        assert torch.equal(r.logits, logits)
+        lg = logits.cpu()
+    idx, gate, dgate = ref_route(lg, s.k)
+    assert torch.equal(r.idx.cpu().long(), idx)
+    assert_within("gate", r.gate, (gate, dgate))
+    assert_within("y", r.y, ref_decode(x, idx, gate, dgate, s.g0, s.groups, op.w13, op.w2, op.ws13,
+                                       op.ws2, residual, s.dtype))
+
+
+CASES = [
+    # T, H, I, E, k, extra
+    (1, 64, 64, 1, 1, {}),
+    (1, 128, 64, 8, 2, {"dt": F32}),
+    (1, 2048, 1408, 64, 6, {"residual": True}),
+    (2, 192, 320, 5, 5, {"shared": True}),
+    (5, 128, 64, 8, 2, {"dt": F32, "shared": True, "residual": True}),
+    (7, 64, 192, 100, 3, {"bias": False}),
+    (15, 320, 64, 300, 8, {"g0": 17, "G": 101}),
+    (16, 1024, 512, 16, 4, {"residual": True, "shared": True}),
+    (17, 448, 128, 3, 2, {}),
+    (17, 448, 128, 3, 2, {"dt": F32}),
+    (33, 256, 256, 6, 1, {"shared": True}),
+    (64, 512, 64, 9, 3, {"g0": 2, "G": 4, "residual": True}),
+    (65, 128, 128, 4, 4, {}),
+    (128, 256, 192, 12, 6, {"shared": True, "residual": True}),
+    (128, 192, 64, 33, 32, {}),                       # the most pairs
+    (100, 64, 64, 40, 2, {"dt": F32, "g0": 39, "G": 1}),
+    (4, 64, 64, 1024, 1024, {}),                      # every expert chosen
+    (9, 128, 64, 1000, 7, {"g0": 0, "G": 1}),
+    (3, 128, 64, 8, 2, {"G": 0, "shared": True}),     # no routed expert on this device
+    (3, 128, 64, 8, 2, {"G": 0, "residual": True}),
+]
+
+
+@pytest.mark.parametrize("T,H,I,E,k,extra", CASES)
+def test_layer(T, H, I, E, k, extra):
+    extra = dict(extra)
+    print(f"\n[decode] T={T} H={H} I={I} E={E} k={k} {extra}", flush=True)
+    with_res = extra.pop("residual", False)
+    op, n = make(T, H, I, E, k, **extra, seed=T + H)
+    x = n(T, H)
+    res = n(T, H) if with_res else None
+    r = op.forward(x, residual=res)
+    torch.cuda.synchronize()
+    check(op, x, r, residual=res)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("T", [1, 18, 70, 128])
+def test_masked_and_hot_experts(T, dt):
+    """Logits from elsewhere: experts masked by -inf, a token with every expert
+    masked, one expert that every token takes, ties."""
+    E, k, H, I = 11, 3, 128, 64
+    op, n = make(T, H, I, E, k, dt=dt, router=False, g0=1, G=9, seed=T)
+    lg = torch.round(n(T, E, d=F32) * 2) / 2               # many ties
+    lg[:, 4] = 9.0                                         # the hot expert
+    lg[:, 6:9] = -float("inf")
+    lg[0, 1] = -0.0
+    lg[0, 2] = 0.0
+    lg[T // 2] = -float("inf")                             # nothing left (T = 1: of the only token)
+    x = n(T, H)
+    r = op.forward(x, logits=lg)
+    torch.cuda.synchronize()
+    assert (r.gate[T // 2] == 0).all() and (r.y[T // 2] == 0).all()
+    check(op, x, r, logits=lg)
+
+
+def test_token_with_no_expert_here():
+    """Every choice outside the window: y is the residual, bit for bit."""
+    op, n = make(6, 192, 64, 8, 2, g0=6, G=2, router=False)
+    lg = torch.zeros(6, 8, device="cuda")
+    lg[:, 1], lg[:, 3] = 3.0, 2.0
+    x, res = n(6, 192), n(6, 192)
+    r = op.forward(x, residual=res, logits=lg)
+    assert torch.equal(r.y, res)
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_in_place_on_the_residual_and_nothing_behind(T):
+    op, n = make(T, 256, 128, 16, 4, shared=True)
+    x = n(T, 256)
+    buf = n(T + 3, 256)
+    keep = buf.clone()
+    r0 = op.forward(x, residual=keep[:T])
+    r1 = op.forward(x, residual=buf[:T], out=buf[:T])
+    assert r1.y.data_ptr() == buf.data_ptr()
+    assert torch.equal(r0.y, buf[:T]) and torch.equal(buf[T:], keep[T:])
+
+
+def test_same_bits_on_every_run():
+    op, n = make(23, 640, 448, 24, 5, shared=True)
+    x = n(23, 640)
+    first = op.forward(x)
+    for _ in range(5):
+        r = op.forward(x)
+        assert all(torch.equal(a, b) for a, b in zip(first, r))
+
+
+def test_two_streams_at_once():
+    """Calls of one layer on two streams, nothing between them: each has its own workspace."""
+    op, n = make(64, 1024, 512, 32, 4, shared=True)
+    xs = [n(64, 1024) for _ in range(2)]
+    want = [op.forward(x) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(8):
+        for i, st in enumerate(streams):
+            got[i].append(op.forward(xs[i], stream=st))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(want[i], r))
+
+
+def test_two_captured_graphs():
+    """Two graphs of one layer, replayed in turn and side by side, with eager
+    work between."""
+    op, n = make(5, 512, 256, 16, 4, shared=True)
+    xs = [n(5, 512) for _ in range(2)]
+    want = [op.forward(x) for x in xs]
+    side = torch.cuda.Stream()
+    graphs, outs = [], []
+    for x in xs:
+        g = torch.cuda.CUDAGraph()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            op.forward(x)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            outs.append(op.forward(x))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    junk = torch.randn(1 << 18, device="cuda")
+    for rep in range(6):
+        for o in outs:
+            o.y.zero_()
+            o.idx.fill_(-1)
+        junk.mul_(1.01).sum().item()
+        torch.cuda.synchronize()
+        for st, g in zip(streams, graphs):
+            if rep % 2:
+                with torch.cuda.stream(st):
+                    g.replay()
+            else:
+                g.replay()
+        torch.cuda.synchronize()
+        eager = op.forward(xs[0])
+        for o, w in zip(outs, want):
+            assert all(torch.equal(a, b) for a, b in zip(o, w)), rep
+        assert torch.equal(eager.y, want[0].y)
+
+
+def test_fewer_tokens_than_built_for_and_none():
+    op, n = make(16, 128, 64, 8, 2)
+    for T in (16, 3, 0, 1):
+        x = n(T, 128)
+        r = op.forward(x)
+        torch.cuda.synchronize()
+        assert r.y.shape == (T, 128) and r.idx.shape == (T, 2)
+        if T:
+            check(op, x, r)
+
+
+def test_of_a_training_layer():
+    """On a MoeLayer's parameters: the choices and gates are its own, y agrees
+    to the roundings the training path makes on the way (h13, act, yp)."""
+    import synth
+    from gpu_util import make_layer
+    from routing_permute_grouped_moe_amd.layer import MoeDecode
+    cfg = synth.get_config("small", T=48, H=512, I=256, E=16, k=4)
+    L = make_layer(cfg, synth.make_inputs(cfg))
+    L.forward()
+    r = MoeDecode.of_layer(L).forward(L.x)
+    torch.cuda.synchronize()
+    assert torch.equal(r.idx, L.idx)
+    # the training path rounds h13, act, yp and y to bf16: four half steps, each
+    # spread over the sum by at most its magnitude
+    mag = r.y.float().abs().amax()
+    assert (r.y.float() - L.y.float()).abs().amax() <= 2e-2 * mag
+
+
+def test_block_of_a_decoder():
+    """A block's tail as it runs: attention output through the projection onto
+    the residual stream, the expert layer onto it, then a dense feed-forward --
+    every step from the values the step before left."""
+    from routing_permute_grouped_moe_amd.layer import Linear
+    T, H = 6, 512
+    op, n = make(T, H, 256, 16, 4, shared=True)
+    proj = Linear(n(H, H, std=H ** -0.5), bias=n(H, std=0.5, d=F32))
+    up = Linear(n(4 * H, H, std=H ** -0.5), bias=n(4 * H, std=0.5, d=F32), act="gelu_tanh")
+    down = Linear(n(H, 4 * H, std=(4 * H) ** -0.5))
+    attn, stream = n(T, H), n(T, H)
+    h0 = proj.forward(attn, residual=stream)
+    assert_within("proj", h0, ref_linear(attn, proj.w, proj.bias, "none", stream, BF)[0])
+    r = op.forward(h0, residual=h0)
+    check(op, h0, r, residual=h0)
+    f = up.forward(r.y)
+    assert_within("up", f, ref_linear(r.y, up.w, up.bias, "gelu_tanh", None, BF)[0])
+    keep = r.y.clone()
+    y = down.forward(f, residual=r.y, out=r.y)
+    assert_within("down", y, ref_linear(f, down.w, None, "none", keep, BF)[0])

@@ -1,0 +1,211 @@
+"""The fused linear product and its gradients against 64 bits (GPU only)."""
+import pytest
+import torch
+
+from decode_util import assert_within, f64, ref_act, ref_linear, ref_linear_bwd
+from gpu_util import have_gpu
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not have_gpu(), reason="needs a GPU")]
+
+BF, F32 = torch.bfloat16, torch.float32
+ACTS = ["none", "relu", "silu", "gelu", "gelu_tanh"]
+
+
+def normal(seed):
+    gen = torch.Generator(device="cuda").manual_seed(2000 + seed)
+    return lambda *s, std=1.0, d=BF: torch.empty(s, dtype=d, device="cuda").normal_(
+        0, std, generator=gen)
+
+
+FWD = [
+    # M, N, K, act, dt, bias, residual, z
+    (1, 64, 64, "none", BF, False, False, False),
+    (1, 7680, 512, "none", BF, True, True, False),
+    (1, 192, 2112, "silu", F32, True, True, True),
+    (3, 64, 192, "gelu", BF, True, False, True),
+    (16, 320, 1408, "gelu_tanh", BF, True, True, True),
+    (17, 128, 64, "relu", BF, False, True, True),
+    (31, 64, 128, "gelu", F32, True, False, True),
+    (33, 448, 320, "silu", BF, True, True, False),
+    (64, 256, 256, "gelu_tanh", F32, False, True, True),
+    (65, 256, 256, "gelu_tanh", BF, True, True, True),
+    (65, 64, 64, "none", F32, True, True, False),
+    (127, 192, 448, "relu", BF, True, False, False),
+    (129, 320, 128, "silu", F32, True, True, True),
+    (255, 576, 192, "gelu", BF, True, True, True),
+    (256, 64, 2048, "none", BF, False, False, False),
+    (300, 1088, 320, "gelu", F32, True, True, True),
+    (419, 512, 1024, "none", BF, True, True, False),
+    (513, 128, 64, "silu", BF, False, True, True),
+    (1025, 1280, 128, "gelu_tanh", BF, True, True, True),
+    (4100, 192, 64, "silu", BF, True, True, True),
+]
+
+
+@pytest.mark.parametrize("M,N,K,act,dt,bias,residual,z", FWD)
+def test_forward(M, N, K, act, dt, bias, residual, z):
+    from routing_permute_grouped_moe_amd.layer import Linear
+    print(f"\n[linear] M={M} N={N} K={K} {act} {dt}", flush=True)
+    n = normal(M + N)
+    x, w = n(M, K, d=dt), n(N, K, std=1.5 * K ** -0.5, d=dt)
+    b = n(N, std=0.5, d=F32) if bias else None
+    res = n(M, N, d=dt) if residual else None
+    op = Linear(w, bias=b, act=act)
+    got = op.forward(x, residual=res, save_z=z)
+    y, zz = got if z else (got, None)
+    ry, rz = ref_linear(x, w, b, act, res, dt)
+    assert_within("y", y, ry)
+    if z:
+        assert_within("z", zz, rz)
+
+
+BWD = [
+    (1, 64, 64, "silu", BF), (5, 192, 128, "gelu", F32), (31, 64, 320, "none", BF),
+    (64, 128, 64, "relu", BF), (65, 320, 192, "gelu_tanh", F32), (127, 64, 448, "silu", F32),
+    (257, 256, 576, "gelu_tanh", BF), (333, 512, 256, "gelu", F32), (300, 1024, 64, "none", F32),
+    (1031, 192, 320, "gelu", BF), (700, 768, 1024, "silu", BF), (2050, 64, 64, "relu", BF),
+    (9000, 64, 128, "silu", BF),
+]
+
+
+@pytest.mark.parametrize("M,N,K,act,dt", BWD)
+def test_backward(M, N, K, act, dt):
+    from routing_permute_grouped_moe_amd.layer import Linear
+    print(f"\n[linear bwd] M={M} N={N} K={K} {act} {dt}", flush=True)
+    n = normal(M + N + 1)
+    x, w, dy = n(M, K, d=dt), n(N, K, std=K ** -0.5, d=dt), n(M, N, d=dt)
+    z = n(M, N, std=1.5, d=dt) if act != "none" else None
+    op = Linear(w, act=act)
+    dx, dw, db = op.backward(dy, x, z=z, bias_grad=True)
+    rx, rw, rb = ref_linear_bwd(dy, z, x, w, act, dt)
+    assert_within("db", db, rb)
+    assert_within("dx", dx, rx)
+    assert_within("dw", dw, rw)
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_gradients_against_differences(act):
+    """fp32: the derivative of <y, dy> along random directions of x, W and b, by
+    central differences of the 64-bit forward."""
+    from routing_permute_grouped_moe_amd.layer import Linear
+    M, N, K = 70, 128, 64
+    n = normal(7)
+    x, w, dy = n(M, K, d=F32), n(N, K, std=K ** -0.5, d=F32), n(M, N, d=F32)
+    b = n(N, std=0.5, d=F32)
+    op = Linear(w, bias=b, act=act)
+    y, z = op.forward(x, save_z=True)
+    dx, dw, db = op.backward(dy, x, z=z if act != "none" else None)
+    X, W, B, D = f64(x), f64(w), f64(b), f64(dy)
+    phi = lambda X, W, B: (ref_act(X @ W.T + B, act)[0] * D).sum()
+    eps = 1e-5
+    for grad, at in ((dx, 0), (dw, 1), (db, 2)):
+        v = torch.randn((X, W, B)[at].shape, dtype=torch.float64,
+                        generator=torch.Generator().manual_seed(at))
+        args = lambda s: [p + s * v if i == at else p for i, p in enumerate((X, W, B))]
+        num = (phi(*args(eps)) - phi(*args(-eps))) / (2 * eps)
+        got = (f64(grad) * v).sum()
+        # differences: eps^2 of the third derivative (relu: none, or one kink
+        # within eps); the kernel: its bound, summed along the direction
+        ref = ref_linear_bwd(dy, z if act != "none" else None, x, w, act, F32)[at][1]
+        slack = (ref * v.abs()).sum() + 1e-4 * abs(num) + 1e-4
+        assert abs(num - got) <= slack, (act, at, num.item(), got.item(), slack.item())
+
+
+@pytest.mark.parametrize("M", [1, 100, 600])
+def test_in_place_on_the_residual_and_nothing_behind(M):
+    from routing_permute_grouped_moe_amd.layer import Linear
+    n = normal(3)
+    x, w = n(M, 256), n(192, 256, std=1 / 16)
+    buf = n(M + 5, 192)
+    keep = buf.clone()
+    op = Linear(w, act="silu")
+    y = op.forward(x, residual=keep[:M])
+    op.forward(x, residual=buf[:M], out=buf[:M])
+    assert torch.equal(buf[:M], y) and torch.equal(buf[M:], keep[M:])
+
+
+def test_parts_of_the_gradient_and_no_rows():
+    """Each gradient alone gives the bits it has with the others; without rows
+    the sums are zero."""
+    from routing_permute_grouped_moe_amd import abi
+    from routing_permute_grouped_moe_amd.layer import Linear
+    n = normal(4)
+    M, N, K = 300, 256, 192
+    x, w, dy, z = n(M, K), n(N, K), n(M, N), n(M, N)
+    op = Linear(w, act="gelu")
+    dx, dw, db = op.backward(dy, x, z=z, bias_grad=True)
+    ws = torch.empty(abi.moe_linear_bwd_workspace_bytes(M, N, K, op.dt, op.act),
+                     dtype=torch.uint8, device="cuda")
+    for part in range(3):
+        outs = [torch.full_like(t, 7.0) if i == part else None
+                for i, t in enumerate((dx, dw, db))]
+        abi.moe_linear_bwd(dy, z, x, w, op.dt, M, N, K, op.act, *outs, ws, ws.numel())
+        assert torch.equal(outs[part], (dx, dw, db)[part])
+    dx0, dw0, db0 = op.backward(dy[:0], x[:0], z=z[:0], bias_grad=True)
+    assert dx0.shape == (0, K) and (dw0 == 0).all() and (db0 == 0).all()
+    y, zz = op.forward(x[:0], save_z=True)
+    assert y.shape == (0, N) and zz.shape == (0, N)
+
+
+def test_extreme_pre_activations():
+    """Large |z|, infinities and NaN: slopes and values at their limits, a NaN
+    stays in its own row and column."""
+    from routing_permute_grouped_moe_amd.layer import Linear
+    K, N = 64, 64
+    big = torch.tensor([-3e38, -1e20, -200.0, -30.0, 0.0, 30.0, 200.0, 1e20, 3e38])
+    z = big.to(BF).cuda()[:, None].repeat(1, N).contiguous()
+    M = z.shape[0]
+    dy = torch.ones(M, N, dtype=BF, device="cuda")
+    n = normal(5)
+    x = n(M, K)
+    for act in ACTS[1:]:
+        op = Linear(torch.eye(N, K, device="cuda").to(BF), act=act)
+        dx, _, _ = op.backward(dy, x, z=z, bias_grad=True)
+        want = ref_act(f64(z), act)[1]
+        assert torch.isfinite(dx).all(), act
+        assert (f64(dx) - want).abs().max() <= 2.0 ** -7 * 1.13, act
+        # forward: x = z through the identity
+        y = op.forward(z)
+        assert torch.isfinite(y).all(), act
+        v = ref_act(f64(z), act)[0]
+        assert ((f64(y) - v).abs() <= 2.0 ** -7 * v.abs() + 1e-6).all(), act
+        bad = z.clone()
+        bad[2, 5] = float("nan")
+        y = op.forward(bad)
+        assert torch.isnan(y[2]).all() and torch.isfinite(y[[0, 1, 3, 4]]).all(), act
+
+
+def test_backward_replays_from_a_graph():
+    from routing_permute_grouped_moe_amd.layer import Linear
+    n = normal(6)
+    M, N, K = 520, 320, 256
+    x, w, dy = n(M, K), n(N, K, std=1 / 16), n(M, N)
+    op = Linear(w, bias=n(N, std=0.5, d=F32), act="silu")
+
+    def step():
+        y, z = op.forward(x, save_z=True)
+        return (y, z) + op.backward(dy, x, z=z)
+
+    want = [t.clone() for t in step()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = step()
+    junk = torch.randn(1 << 18, device="cuda")
+    for _ in range(4):
+        for t in outs:
+            t.fill_(float("nan"))
+        junk.mul_(1.01).sum().item()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, want):
+            assert torch.equal(a, b)
+        for a, b in zip(step(), want):
+            assert torch.equal(a, b)
