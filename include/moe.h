@@ -399,7 +399,8 @@ int moe_decode(const void* x, int dt, const float* wg, const float* bias, int T,
  * epilogue are fp32; z and y are each rounded once (act sees the unrounded z).
  * act: MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU (z sigma(z)), MOE_ACT_GELU
  * (z Phi(z)) or MOE_ACT_GELU_TANH (its tanh form).  N and K are multiples of
- * 64; M is any number; x, w, y are below 2 GiB each.
+ * 64; M is any number; x, w, y are below 2 GiB each.  ws: scratch of
+ * moe_linear_workspace_bytes bytes, 256-byte aligned (NULL where that is 0).
  */
 enum {
   MOE_ACT_NONE = 0,
@@ -408,8 +409,10 @@ enum {
   MOE_ACT_GELU = 3,
   MOE_ACT_GELU_TANH = 4
 };
+size_t moe_linear_workspace_bytes(int M, int N, int K, int dt);
 int moe_linear(const void* x, int dt, int M, int N, int K, const void* w, const float* bias,
-               int act, const void* residual, void* z, void* y, moe_stream_t stream);
+               int act, const void* residual, void* z, void* y, void* ws, size_t ws_bytes,
+               moe_stream_t stream);
 
 /* Its gradients, given dy [M,N] and the z the forward kept (NULL for
  * MOE_ACT_NONE):

@@ -81,7 +81,8 @@ _SIGS = {
     "moe_decode_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "moe_decode": (_I, [_P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P,
                         _P, _P, _P, _SZ, _P]),
-    "moe_linear": (_I, [_P, _I, _I, _I, _I, _P, _P, _I, _P, _P, _P, _P]),
+    "moe_linear_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "moe_linear": (_I, [_P, _I, _I, _I, _I, _P, _P, _I, _P, _P, _P, _P, _SZ, _P]),
     "moe_linear_bwd_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
     "moe_linear_bwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
 }
@@ -282,9 +283,13 @@ def moe_decode(x, dt, wg, bias, T, H, I, E, k, g0, G, w13, w2, ws13, ws2, residu
           addr(y), addr(ws), ws_bytes, _stream(stream))
 
 
-def moe_linear(x, dt, M, N, K, w, bias, act, residual, z, y, stream=None):
+def moe_linear_workspace_bytes(M, N, K, dt) -> int:
+    return _lib.moe_linear_workspace_bytes(M, N, K, dt)
+
+
+def moe_linear(x, dt, M, N, K, w, bias, act, residual, z, y, ws=None, ws_bytes=0, stream=None):
     _call("moe_linear", addr(x), dt, M, N, K, addr(w), addr(bias), act, addr(residual), addr(z),
-          addr(y), _stream(stream))
+          addr(y), addr(ws), ws_bytes, _stream(stream))
 
 
 def moe_linear_bwd_workspace_bytes(M, N, K, dt, act) -> int:

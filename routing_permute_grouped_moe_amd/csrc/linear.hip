@@ -2,10 +2,10 @@
 // its gradients:
 //   z = x W^T + b,  y = act(z) + residual           (x [M,K], W [N,K])
 //   dz = dy * act'(z),  dx = dz W,  dW = dz^T x,  db = sum_m dz
-// Few rows (decode batches) run as a stream of W (stream.hpp); more rows run
-// on the grouped GEMM's tiles (gmm.hip), whose epilogue takes the bias,
-// activation and residual, and the two products of the backward share one
-// launch.  What is here: the few-row kernel, the elementwise half of the
+// Few rows (decode batches) run as a stream of W (stream.hpp); large products
+// run on the grouped GEMM's 256 x 256 tiles (gmm.hip), those between on
+// smaller tiles (dense.hip).  The epilogues take the bias, activation and
+// residual, and the two products of the backward share one launch.  What is here: the few-row kernel, the elementwise half of the
 // backward, the checks and the choice between the kernels.
 #include <type_traits>
 
@@ -16,6 +16,10 @@
 namespace {
 
 constexpr int LIN_FEW_ROWS = 64;    // most rows of the streaming kernel
+#ifndef LIN_TILES
+#define LIN_TILES 192
+#endif
+constexpr int LIN_BIG_TILES = LIN_TILES;   // 256 x 256 tiles from which the large-tile kernels run
 constexpr int LIN_NW = 8;
 constexpr int LIN_NT = 64 * LIN_NW;
 
@@ -146,17 +150,27 @@ __global__ __launch_bounds__(256) void linear_db_kernel(const float* __restrict_
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
+// 256 x 256 tiles of an M x N product
+long long big_tiles(long long M, long long N) { return ((M + 255) / 256) * ((N + 255) / 256); }
+bool fwd_big(int M, int N) { return big_tiles(M, N) >= LIN_BIG_TILES; }
+bool bwd_big(int M, int N, int K) { return big_tiles(M, K) + big_tiles(N, K) >= LIN_BIG_TILES; }
+
+size_t fwd_ws(int M, int N, int K, int dt) {
+  return M <= LIN_FEW_ROWS || fwd_big(M, N) ? 0 : round256(moe_dense_fwd_bytes(M, N, K, dt));
+}
+
 struct BwdWs {
-  size_t part, dz, total;
+  size_t part, dz, dense, total;
   int rows, parts;
 };
-BwdWs bwd_ws(int M, int N, int dt, int act) {
+BwdWs bwd_ws(int M, int N, int K, int dt, int act) {
   BwdWs w;
   w.rows = dz_rows(M);
   w.parts = (M + w.rows - 1) / w.rows;
   w.part = 0;
   w.dz = round256((size_t)w.parts * N * 4);
-  w.total = w.dz + (act == MOE_ACT_NONE ? 0 : round256((size_t)M * N * moe_dt_bytes(dt)));
+  w.dense = w.dz + (act == MOE_ACT_NONE ? 0 : round256((size_t)M * N * moe_dt_bytes(dt)));
+  w.total = w.dense + (bwd_big(M, N, K) ? 0 : round256(moe_dense_bwd_bytes(M, N, K, dt)));
   if (w.total == 0) w.total = 256;
   return w;
 }
@@ -187,9 +201,14 @@ int lin_tile_checks(const char* fn, int dt, int M, int N, int K) {
 
 }  // namespace
 
+extern "C" size_t moe_linear_workspace_bytes(int M, int N, int K, int dt) {
+  if (lin_checks("moe_linear_workspace_bytes", dt, M, N, K, MOE_ACT_NONE) != MOE_OK) return 0;
+  return fwd_ws(M, N, K, dt);
+}
+
 extern "C" int moe_linear(const void* x, int dt, int M, int N, int K, const void* w,
                           const float* bias, int act, const void* residual, void* z, void* y,
-                          moe_stream_t stream) {
+                          void* ws, size_t ws_bytes, moe_stream_t stream) {
   const char* fn = "moe_linear";
   MOE_TRY(lin_checks(fn, dt, M, N, K, act));
   if (M == 0) return MOE_OK;
@@ -208,12 +227,18 @@ extern "C" int moe_linear(const void* x, int dt, int M, int N, int K, const void
     return dt == MOE_BF16 ? launch_rows<bf16_t>(a, s, fn) : launch_rows<float>(a, s, fn);
   }
   MOE_TRY(lin_tile_checks(fn, dt, M, N, K));
+  const size_t need = fwd_ws(M, N, K, dt);
+  if (need > 0) MOE_TRY(moe_need_ptr(ws, fn, "ws", 256));
+  if (ws_bytes < need)
+    return moe_fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", fn, ws_bytes, need);
+  if (!fwd_big(M, N))
+    return moe_dense_fwd(x, dt, M, N, K, w, bias, act, residual, z, y, ws, s);
   return moe_gmm_linear_fwd(x, dt, M, N, K, w, bias, act, residual, z, y, s);
 }
 
 extern "C" size_t moe_linear_bwd_workspace_bytes(int M, int N, int K, int dt, int act) {
   if (lin_checks("moe_linear_bwd_workspace_bytes", dt, M, N, K, act) != MOE_OK) return 0;
-  return bwd_ws(M, N, dt, act).total;
+  return bwd_ws(M, N, K, dt, act).total;
 }
 
 extern "C" int moe_linear_bwd(const void* dy, const void* z, const void* x, const void* w, int dt,
@@ -225,7 +250,7 @@ extern "C" int moe_linear_bwd(const void* dy, const void* z, const void* x, cons
   MOE_TRY(moe_opt_ptr(dx, fn, "dx"));
   MOE_TRY(moe_opt_ptr(dw, fn, "dw"));
   MOE_TRY(moe_opt_ptr(db, fn, "db"));
-  const BwdWs lay = bwd_ws(M, N, dt, act);
+  const BwdWs lay = bwd_ws(M, N, K, dt, act);
   if (M > 0) {
     MOE_TRY(moe_need_ptr(dy, fn, "dy"));
     if (act != MOE_ACT_NONE) MOE_TRY(moe_need_ptr(z, fn, "z"));
@@ -260,5 +285,7 @@ extern "C" int moe_linear_bwd(const void* dy, const void* z, const void* x, cons
                        (const float*)((char*)ws + lay.part), M > 0 ? lay.parts : 0, N, db);
     MOE_TRY(moe_check_launch(fn));
   }
+  if (M > 0 && !bwd_big(M, N, K))
+    return moe_dense_bwd(dz, x, w, dt, M, N, K, dx, dw, (char*)ws + lay.dense, s);
   return moe_gmm_linear_bwd(dz, x, w, dt, M, N, K, dx, dw, s);
 }

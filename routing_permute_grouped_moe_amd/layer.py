@@ -474,8 +474,10 @@ class Linear:
             else:
                 _check("out", out, self.dtype, dev, M, self.N)
             z = torch.empty((M, self.N), dtype=self.dtype, device=dev) if save_z else None
+            n = abi.moe_linear_workspace_bytes(M, self.N, self.K, self.dt)
+            ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
             abi.moe_linear(x, self.dt, M, self.N, self.K, self.w, self.bias, self.act, residual,
-                           z, out, st)
+                           z, out, ws, n, st)
         return (out, z) if save_z else out
 
     def backward(self, dy, x, z=None, bias_grad=None, stream=None):

@@ -80,7 +80,7 @@ def test_decode_workspace(abi):
 
 
 LINEAR = dict(x=P, dt=1, M=4, N=128, K=64, w=P, bias=None, act=0, residual=None, z=None, y=2 * P,
-              stream=None)
+              ws=None, ws_bytes=0, stream=None)
 
 
 @pytest.mark.parametrize("change,status,text", [
@@ -102,6 +102,8 @@ LINEAR = dict(x=P, dt=1, M=4, N=128, K=64, w=P, bias=None, act=0, residual=None,
     ({"y": P}, "INVALID_ARG", "buffers of their own"),
     ({"z": 2 * P}, "INVALID_ARG", "buffers of their own"),
     ({"z": 3 * P, "residual": 3 * P}, "INVALID_ARG", "buffers of their own"),
+    ({"M": 100, "K": 4096}, "INVALID_ARG", "ws is NULL"),
+    ({"M": 100, "K": 4096, "ws": P, "ws_bytes": 256}, "WORKSPACE", "workspace 256"),
 ])
 def test_linear_refuses(abi, change, status, text):
     args = {**LINEAR, **change}
@@ -143,6 +145,22 @@ def test_nothing_asked_for_is_a_noop(abi):
     assert abi._lib.moe_linear(*args.values()) == abi.MOE_OK
     args = {**BWD, "dx": None, "dw": None, "db": None}
     assert abi._lib.moe_linear_bwd(*args.values()) == abi.MOE_OK
+
+
+@pytest.mark.parametrize("dt", [0, 1])
+def test_workspace_sizes_of_every_shape(abi, dt):
+    """No shape, empty ones included, trips the host's planning; sizes grow
+    from what the pieces need."""
+    es = 2 if dt else 4
+    for M in (0, 1, 63, 64, 65, 100, 1000, 5000, 100000):
+        for N in (64, 192, 2048):
+            for K in (64, 1088):
+                assert abi.moe_linear_workspace_bytes(M, N, K, dt) % 256 == 0
+                for act in (0, 2):
+                    n = abi.moe_linear_bwd_workspace_bytes(M, N, K, dt, act)
+                    assert n > 0 and n % 256 == 0
+                    assert n >= (M * N * es if act else 0)
+    assert abi.moe_linear_workspace_bytes(4, 100, 64, dt) == 0
 
 
 def test_layers_want_weights_on_a_gpu(abi):
