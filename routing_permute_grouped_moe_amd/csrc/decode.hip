@@ -1,12 +1,23 @@
 // The whole expert layer for a few tokens (serving): router projection,
 // softmax top-k, the chosen SwiGLU experts, the shared expert, the
-// gate-weighted sum and the residual.  For at most 128 tokens the layer is a
-// stream of the chosen experts' weights; sorting rows into groups, as the
-// training path does, would be latency only, so the rows of an expert are
-// found from the token's choices directly and the products read tokens in
-// place (stream.hpp).
+// gate-weighted sum and the residual.
+//
+// For at most 128 tokens the layer is a stream of the chosen experts' weights,
+// every byte read once, with the multiplications in its shade (2 m flops per
+// weight for m rows, far below the 300 flops per byte at which the matrix
+// cores and HBM balance).  Sorting rows into groups, as the training path
+// does, would be latency only: the rows of an expert are found from the
+// tokens' choices directly and the products read tokens in place.  Two
+// launches:
+//  1. the router product in K slices (and the second launch's counters set
+//     to zero);
+//  2. everything else in one persistent launch of one workgroup per CU, whose
+//     units of work -- route a few tokens, 16 gate/up columns of an expert, 32
+//     output columns of an expert -- are drawn from one counter in an order in
+//     which a unit depends on earlier ones only.
 #include <type_traits>
 
+#include "lds_copy.hpp"
 #include "route_select.hpp"
 #include "stream.hpp"
 #include "validate.hpp"
@@ -15,10 +26,11 @@ namespace {
 
 constexpr int DEC_MAX_T = 128;       // tokens of a call
 constexpr int DEC_MAX_PAIRS = 4096;  // (token, slot) pairs of a call
-constexpr int DEC_NW = 8;            // waves of a workgroup of the expert products
-constexpr int DEC_NT = 64 * DEC_NW;
+constexpr int DEC_SW = 4;            // streaming waves of a workgroup of the second launch
+constexpr int DEC_NT = 64 * (DEC_SW + 2);   // and one that schedules, one that finishes tiles
 constexpr int DEC_GU = 16;           // gate/up columns of a unit (16 gate and 16 up rows of W13)
 constexpr int DEC_DN = 32;           // output columns of a unit of the second product
+constexpr int DEC_FUSED_T = 8;       // tokens up to which the last unit of a column block sums it
 constexpr int RT_NW = 4;             // waves of a router workgroup
 constexpr int RT_COLS = 16;          // experts of a router workgroup
 constexpr int RT_MAX_S = 32;         // K slices of the router product
@@ -34,6 +46,11 @@ struct DecArgs {
   double* part;       // [S][T][E] partial logits
   void* act;          // [planes][T k + T][I] activations, shared rows last
   float* yp;          // [T k + T][H] expert outputs
+  // counters, zero when the second launch starts: the next unit, tokens
+  // routed, finished gate/up units of each expert (window index; the shared
+  // expert last), finished units of each block of DEC_DN output columns
+  int* next; int* routed; int* act_done; int* col_done;
+  int n_count;        // all of them, from next on
 };
 
 // 8 elements of T as fp32, from byte offset off
@@ -43,6 +60,14 @@ __device__ __forceinline__ void load8(__amdgpu_buffer_rsrc_t r, uint32_t off, fl
 __device__ __forceinline__ void load8(__amdgpu_buffer_rsrc_t r, uint32_t off, float* v, float) {
   unpack16(buf_load16(r, off), v, 0.f);
   unpack16(buf_load16(r, off + 16), v + 4, 0.f);
+}
+
+// The second launch's counters (workgroup b of n, 256 threads).
+__device__ __forceinline__ void decode_clear(const DecArgs& a, int b, int n) {
+  for (int i = b * 256 + threadIdx.x; i < a.n_count; i += n * 256) a.next[i] = 0;
+}
+__global__ __launch_bounds__(256) void decode_clear_kernel(DecArgs a) {
+  decode_clear(a, blockIdx.x, gridDim.x);
 }
 
 // ---------------------------------------------------------------- router
@@ -56,6 +81,7 @@ template <typename T, int MT>
 __global__ __launch_bounds__(64 * RT_NW) void decode_router_kernel(DecArgs a) {
   constexpr int ES = sizeof(T);
   __shared__ double red[RT_NW][4][64];
+  decode_clear(a, blockIdx.y * gridDim.x + blockIdx.x, gridDim.x * gridDim.y);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = lane & 15, kg = lane >> 4;
   const int e0 = blockIdx.x * RT_COLS, slice = blockIdx.y;
@@ -99,6 +125,26 @@ __global__ __launch_bounds__(64 * RT_NW) void decode_router_kernel(DecArgs a) {
   }
 }
 
+// Device-scope stores and loads: data that another workgroup of the same
+// launch reads.  A store goes through this XCD's L2; it is visible to whoever
+// learns, through a counter raised after the store completed, that it is there
+// and then drops what its own caches may hold (acquire).
+__device__ __forceinline__ void dev_store(float* p, float v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void dev_store(int32_t* p, int32_t v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void dev_store(bf16_t* p, uint32_t v) {
+  __hip_atomic_store(p, (bf16_t)v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ int dev_load(const int* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void dev_add(int* p, int v) {
+  __hip_atomic_fetch_add(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // One wave per token: the logits (sum of the partials and the bias, rounded
 // once to fp32), the k largest and their softmax weights.
 template <int V>
@@ -107,22 +153,44 @@ __device__ __forceinline__ void decode_route_token(const DecArgs& a, int t) {
   float v[V];
   uint32_t key[V];
   float m = -INFINITY;
+  if (a.S > 0) {
+    // slices 8 at a time, all loads of a batch in flight
+    double s[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = lane + i * MOE_WAVE;
+      s[i] = a.bias != nullptr && e < a.E ? (double)a.bias[e] : 0.0;
+    }
+    constexpr int B = V <= 4 ? 8 : 2;
+    for (int p = 0; p < a.S; p += B) {
+      double d[V][B];
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int q = 0; q < B; ++q)
+          d[i][q] = a.part[((long long)min(p + q, a.S - 1) * a.T + t) * a.E +
+                           min(lane + i * MOE_WAVE, a.E - 1)];
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int q = 0; q < B; ++q) s[i] += p + q < a.S ? d[i][q] : 0.0;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = lane + i * MOE_WAVE;
+      v[i] = e < a.E ? (float)s[i] : -INFINITY;
+      if (e < a.E) a.logits[(long long)t * a.E + e] = v[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = lane + i * MOE_WAVE;
+      v[i] = e < a.E ? a.logits[(long long)t * a.E + e] : -INFINITY;
+    }
+  }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int e = lane + i * MOE_WAVE;
-    v[i] = -INFINITY;
-    if (e < a.E) {
-      if (a.S > 0) {
-        double s = 0;
-        for (int p = 0; p < a.S; ++p) s += a.part[((long long)p * a.T + t) * a.E + e];
-        if (a.bias != nullptr) s += (double)a.bias[e];
-        v[i] = (float)s;
-        a.logits[(long long)t * a.E + e] = v[i];
-      } else {
-        v[i] = a.logits[(long long)t * a.E + e];
-      }
-    }
-    key[i] = e < a.E ? route_key(v[i]) : 0u;
+    key[i] = lane + i * MOE_WAVE < a.E ? route_key(v[i]) : 0u;
     m = fmaxf(m, v[i]);
   }
   m = wave_max(m);
@@ -133,76 +201,525 @@ __device__ __forceinline__ void decode_route_token(const DecArgs& a, int t) {
   s = wave_sum(s);
   const float inv = 1.0f / s;
   route_select<V>(key, a.k, [&](int slot, int i) {
-    a.idx[(long long)t * a.k + slot] = lane + i * MOE_WAVE;
-    a.gate[(long long)t * a.k + slot] = none ? 0.f : expf(v[i] - m) * inv;
+    dev_store(a.idx + (long long)t * a.k + slot, lane + i * MOE_WAVE);
+    dev_store(a.gate + (long long)t * a.k + slot, none ? 0.f : expf(v[i] - m) * inv);
   });
 }
 
-template <int V>
-__global__ __launch_bounds__(256) void decode_route_kernel(DecArgs a) {
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t < a.T) decode_route_token<V>(a, t);
-}
-
 // ---------------------------------------------------------------- experts
-struct DecLds {
-  int16_t loc[DEC_MAX_PAIRS];   // window index of each pair's expert, -1 outside it
-  int16_t list[MOE_MAX_E];      // window indices of the experts some token chose, ascending
-  int n_list;
-  int rows[DEC_MAX_T];          // rows of the current unit: pair indices, or T k + token
-  int n_rows;
-  float red[DEC_NW * 2 * 256];
+// The second launch.  A workgroup has four streaming waves, one that schedules
+// and one that finishes tiles; they meet in LDS words only, never at a
+// barrier, so the stream of weights does not stop between units.
+//
+// Streaming.  A unit is 32 weight rows (two 16-row tiles) times at most 32
+// rows of the other operand.  K runs in steps of 128 bytes of a row (64 bf16,
+// 32 fp32) dealt to the four waves in turn; a step's weights and operand rows
+// go HBM -> LDS in 1 KB copies (lds_copy.hpp) into a ring that belongs to the
+// wave alone, several steps ahead.  A copy covers 8 whole 128-byte lines: read
+// that way with the streaming policy HBM gives 7.0 TB/s here, against 5.1 TB/s
+// for loads straight into the MFMA's operand layout (16 rows x 64 bytes).
+// 16-byte chunk c of row r sits in slot c ^ ((r >> 1) & 7) of its row, so the
+// 16 rows of a fragment read hit all banks.  At the end of a unit the waves
+// leave their partial tiles in LDS and go on to the next, whose first steps
+// are copied while the last of this one are multiplied.
+//
+// Finishing.  The finishing wave adds the four partial tiles in wave order
+// (the same bits on every run), applies silu(g) u or stores the rows of the
+// second product, and raises the unit's counter.
+//
+// Scheduling.  Units are numbered [route][shared gate/up][gate/up of each
+// chosen expert][second product, same order].  A unit waits only for units of
+// lower numbers, and numbers are drawn in order by running workgroups, so the
+// lowest unfinished unit never waits: no residency of the grid is assumed.
+constexpr int DEC_ROWS = 32;         // operand rows of a unit
+constexpr int DEC_DESCS = 4;
+constexpr int DEC_RING = 30 * 1024;  // of a streaming wave
+constexpr unsigned long long DEC_WAIT_TICKS = 100000000ull;   // 1 s of the 100 MHz clock
+
+enum { U_GATEUP = 0, U_DOWN = 1, U_ROUTE = 2, U_SUM = 3, U_EXIT = 4 };
+
+struct DecDesc {
+  int kind, at, mt;            // A tiles (operand copies of 16 rows), row tiles of the result
+  int packed;                  // rows 8-15 are the low halves of rows 0-7
+  int steps;                   // K steps of 128 bytes
+  int n;                       // rows
+  int slot;                    // counter the unit raises (expert, or column block)
+  int col;                     // first gate/up or output column
+  unsigned long long w, a;     // operand addresses
+  uint32_t wbytes, abytes;     // and extents
+  int ldw, tile1;              // bytes of a weight row, and from the first tile to the second
+  uint32_t arow[4 * 16];       // byte offset of each A row
+  int rows[DEC_ROWS];          // pair indices, or T k + token
 };
 
-// loc and list of the call, by every workgroup for itself.
-__device__ __forceinline__ void decode_plan(const DecArgs& a, DecLds& l) {
-  const int P = a.T * a.k;
-  int* const flag = (int*)l.red;
-  for (int g = threadIdx.x; g < a.G; g += DEC_NT) flag[g] = 0;
-  __syncthreads();
-  for (int p = threadIdx.x; p < P; p += DEC_NT) {
-    const int g = a.idx[p] - a.g0;
-    const bool in = g >= 0 && g < a.G;
-    l.loc[p] = in ? (int16_t)g : (int16_t)-1;
-    if (in) flag[g] = 1;
-  }
-  __syncthreads();
-  if (threadIdx.x < 64) {
-    int n = 0;
-    for (int g0 = 0; g0 < a.G; g0 += 64) {
-      const int g = g0 + threadIdx.x;
-      const bool on = g < a.G && flag[g];
-      const unsigned long long b = __ballot(on);
-      if (on) l.list[n + __popcll(b & ((1ull << threadIdx.x) - 1))] = (int16_t)g;
-      n += __popcll(b);
-    }
-    if (threadIdx.x == 0) l.n_list = n;
-  }
-  __syncthreads();
+struct DecLds {
+  char ring[DEC_SW][DEC_RING];
+  float red[2][DEC_SW][2 * 256];   // partial tiles (units of two row tiles take both halves)
+  int16_t loc[DEC_MAX_PAIRS];      // window index of each pair's expert, -1 outside it
+  int16_t list[MOE_MAX_E + 1];     // experts some token chose, ascending; the shared one first (-1)
+  int16_t pre_g[MOE_MAX_E + 2];    // row blocks before each listed expert
+  int16_t cnt[MOE_MAX_E];          // rows of each expert of the window
+  DecDesc desc[DEC_DESCS];
+  // words the waves meet in
+  int ready;                       // descriptors written
+  int parts[DEC_SW];               // units whose partial tiles each streaming wave has left
+  int taken;                       // units whose partial tiles were read
+  int done;                        // units finished
+  int per_col;                     // units of a column block
+};
+
+__device__ __forceinline__ int lds_peek(const int* p) {
+  return *(const volatile int*)p;
+}
+// wait until *p >= v: another wave of the workgroup raises it
+__device__ __forceinline__ void lds_wait(const int* p, int v) {
+  while (uniform(lds_peek(p)) < v) __builtin_amdgcn_s_sleep(1);
+  asm volatile("" ::: "memory");
+}
+__device__ __forceinline__ void lds_drain() {   // this wave's LDS accesses have happened
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+}
+template <int n>
+__device__ __forceinline__ void vm_drain() {    // all but n of its memory operations have
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(n) : "memory");
 }
 
-// Rows of the unit's expert: window index g, or the shared expert (g < 0).
-// Begins and ends with a barrier.
-__device__ __forceinline__ void decode_rows(const DecArgs& a, DecLds& l, int g) {
-  __syncthreads();
-  const int P = a.T * a.k;
-  if (g < 0) {
-    for (int t = threadIdx.x; t < a.T; t += DEC_NT) l.rows[t] = P + t;
-    if (threadIdx.x == 0) l.n_rows = a.T;
-  } else if (threadIdx.x < 64) {
-    int n = 0;
-    for (int p0 = 0; p0 < P; p0 += 64) {
-      const int p = p0 + threadIdx.x;
-      const bool on = p < P && l.loc[p] == g;
-      const unsigned long long b = __ballot(on);
-      // (a token chooses an expert once, so at most T <= DEC_MAX_T rows)
-      if (on) l.rows[n + __popcll(b & ((1ull << threadIdx.x) - 1))] = p;
-      n += __popcll(b);
+// row blocks of an expert with m rows
+__device__ __forceinline__ int row_blocks(int m) { return (m + DEC_ROWS - 1) / DEC_ROWS; }
+
+template <typename T> constexpr int DEC_PLANES = sizeof(T) == 2 ? 2 : 1;
+
+// ---- the scheduling wave
+
+// The launch's arguments where they lie, read again where they are used: held
+// in scalar registers across the scheduler's loop they would spill.
+typedef const __attribute__((address_space(4))) DecArgs DecConst;
+
+// Wait for a device-scope counter, at most a second (only calls that share a
+// workspace ever wait that long; their results are wrong, but they end).
+__device__ __forceinline__ void dev_wait(const int* p, int v, bool& lost) {
+  if (!lost) {
+    const unsigned long long t0 = wall_clock64();
+    while (uniform(dev_load(p)) < v) {
+      if (wall_clock64() - t0 > DEC_WAIT_TICKS) {
+        lost = true;
+        break;
+      }
+      __builtin_amdgcn_s_sleep(2);
     }
-    if (threadIdx.x == 0) l.n_rows = n;
   }
-  __syncthreads();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
 }
+
+// Tables of the call, from the tokens' choices: loc, cnt, the list of chosen
+// experts (shared first) and the row blocks before each.  Returns the length
+// of the list.
+__device__ __forceinline__ int decode_tables(DecConst& a, DecLds& l) {
+  const int lane = threadIdx.x & 63, P = a.T * a.k;
+  for (int g = lane; g < a.G; g += 64) l.cnt[g] = 0;
+  lds_drain();
+  for (int p0 = 0; p0 < P; p0 += 64 * 8) {
+    int e[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) e[q] = a.idx[min(p0 + q * 64 + lane, P - 1)];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int p = p0 + q * 64 + lane, g = e[q] - a.g0;
+      if (p < P) l.loc[p] = g >= 0 && g < a.G ? (int16_t)g : (int16_t)-1;
+    }
+  }
+  lds_drain();
+  // rows of each expert: lane by lane over the pairs of a 64-pair group that
+  // share its expert, one leader each
+  for (int p0 = 0; p0 < P; p0 += 64) {
+    const int p = p0 + lane;
+    const int g = p < P ? l.loc[p] : -1;
+    unsigned long long todo = __ballot(g >= 0);
+    while (todo) {
+      const int first = __builtin_ctzll(todo);
+      const int g1 = __builtin_amdgcn_readlane(g, first);
+      const unsigned long long same = __ballot(g == g1);
+      if (lane == first) l.cnt[g1] = (int16_t)(l.cnt[g1] + __popcll(same));
+      todo &= ~same;
+    }
+    lds_drain();
+  }
+  int n = 0, blocks = 0;
+  if (a.shared) {
+    if (lane == 0) {
+      l.list[0] = -1;
+      l.pre_g[0] = 0;
+    }
+    n = 1;
+    blocks = row_blocks(a.T);
+  }
+  for (int g0 = 0; g0 < a.G; g0 += 64) {
+    const int g = g0 + lane;
+    const int m = g < a.G ? l.cnt[g] : 0;
+    const unsigned long long b = __ballot(m > 0);
+    int incl = row_blocks(m);
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(incl, o, 64);
+      if (lane >= o) incl += v;
+    }
+    if (m > 0) {
+      const int at = n + __popcll(b & ((1ull << lane) - 1));
+      l.list[at] = (int16_t)g;
+      l.pre_g[at] = (int16_t)(blocks + incl - row_blocks(m));
+    }
+    n += __popcll(b);
+    blocks += __shfl(incl, 63, 64);
+  }
+  if (lane == 0) {
+    l.pre_g[n] = (int16_t)blocks;
+    l.per_col = blocks;
+  }
+  lds_drain();
+  return n;
+}
+
+// Rows of the expert in list place s, row block rb, into d.rows.
+__device__ __forceinline__ int decode_rows(DecConst& a, const DecLds& l, DecDesc& d, int g,
+                                           int rb) {
+  const int lane = threadIdx.x & 63, P = a.T * a.k, r0 = rb * DEC_ROWS;
+  if (g < 0) {
+    const int n = min(DEC_ROWS, a.T - r0);
+    if (lane < n) d.rows[lane] = P + r0 + lane;
+    return n;
+  }
+  int n = 0;
+  for (int p0 = 0; p0 < P; p0 += 64) {
+    const int p = p0 + lane;
+    const bool on = p < P && l.loc[p] == g;
+    const unsigned long long b = __ballot(on);
+    const int at = n + __popcll(b & ((1ull << lane) - 1)) - r0;
+    if (on && at >= 0 && at < DEC_ROWS) d.rows[at] = p;
+    n += __popcll(b);
+  }
+  return min(DEC_ROWS, n - r0);
+}
+
+template <typename T>
+__device__ __forceinline__ void decode_schedule(DecLds& l) {
+  constexpr int ES = sizeof(T), PL = DEC_PLANES<T>;
+  const int lane = threadIdx.x & 63;
+  DecConst* args = (DecConst*)__builtin_amdgcn_kernarg_segment_ptr();
+  int n_list = -1, blocks = 0;
+  bool lost = false;
+  int held = 0;          // the number drawn for the next unit
+  auto draw = [&]() {
+    int v = 0;
+    if (lane == 0)
+      v = __hip_atomic_fetch_add(args->next, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return v;
+  };
+  held = draw();
+  int last_g = -2, last_rb = -1, last_n = 0, last_at = 0;   // rows of the last descriptor
+  for (int seq = 0;; ++seq) {
+    int u = uniform(held);
+    // (kept in a vector register, and all that follows from it: the scheduling
+    // arithmetic would not fit the scalar ones)
+    asm volatile("" : "+v"(u));
+    asm volatile("" : "+s"(args));
+    DecConst& a = *args;
+    const int P = a.T * a.k;
+    const int n_route = (a.T + DEC_SW - 1) / DEC_SW;
+    const int per_g = a.I / DEC_GU, per_d = a.H / DEC_DN;
+    const int n_shared = a.shared ? row_blocks(a.T) * per_g : 0;
+    held = draw();       // (returns while this one is prepared)
+    lds_wait(&l.done, seq - DEC_DESCS + 1);   // the descriptor's last user is through
+    DecDesc& d = l.desc[seq % DEC_DESCS];
+    int kind, g = -2, s = 0, rb = 0, col = 0;
+    if (u < n_route) {
+      kind = U_ROUTE;
+      col = u * DEC_SW;
+    } else if (u < n_route + n_shared) {
+      // (the shared expert needs no routing)
+      const int v = u - n_route;
+      kind = U_GATEUP;
+      g = -1;
+      rb = v % row_blocks(a.T);
+      col = v / row_blocks(a.T) * DEC_GU;
+    } else {
+      if (n_list < 0) {
+        dev_wait(a.routed, a.T, lost);
+        n_list = decode_tables(a, l);
+        blocks = lds_peek(&l.per_col);
+      }
+      int v = u - n_route;
+      const int n_gu = blocks * per_g, n_dn = blocks * per_d;
+      if (v < n_gu + n_dn) {
+        kind = v < n_gu ? U_GATEUP : U_DOWN;
+        const int per = v < n_gu ? per_g : per_d;
+        if (v >= n_gu) v -= n_gu;
+        // place in the list: the last with pre_g * per <= v
+        int lo = 0, hi = n_list - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (l.pre_g[mid] * per <= v) lo = mid;
+          else hi = mid - 1;
+        }
+        s = lo;
+        g = l.list[s];
+        const int nb = l.pre_g[s + 1] - l.pre_g[s];
+        v -= l.pre_g[s] * per;
+        rb = v % nb;
+        col = v / nb * (kind == U_GATEUP ? DEC_GU : DEC_DN);
+        if (kind == U_DOWN) dev_wait(a.act_done + (g < 0 ? a.G : g), nb * per_g, lost);
+      } else if (blocks == 0 && v < per_d && a.T <= DEC_FUSED_T) {
+        kind = U_SUM;    // nothing but the residual
+        col = v * DEC_DN;
+      } else {
+        kind = U_EXIT;
+      }
+    }
+    if (kind <= U_DOWN) {
+      int n = last_n;
+      if (g == last_g && rb == last_rb) {
+        if (lane < n) d.rows[lane] = l.desc[last_at].rows[lane];
+      } else {
+        n = decode_rows(a, l, d, g, rb);
+      }
+      last_g = g; last_rb = rb; last_n = n; last_at = seq % DEC_DESCS;
+      lds_drain();
+      const bool down = kind == U_DOWN;
+      const bool two = down && PL == 2;
+      const bool packed = two && n <= 8;
+      const int mt = n <= 16 ? 1 : 2;
+      const int at = packed ? 1 : mt * (two ? 2 : 1);
+      const uint32_t plane = (uint32_t)(P + a.T) * (uint32_t)(a.I * ES);
+      // A row `lane`: packed tiles hold the high halves in rows 0-7 and the low
+      // ones in rows 8-15; else the tiles of the low halves follow
+      const int per_plane = packed ? 8 : 16 * mt;
+      const int r = min(lane % per_plane, n - 1), pl = lane / per_plane;
+      if (lane < 16 * at) {
+        const int row = d.rows[r];
+        const int tok = row >= P ? row - P : row / a.k;
+        d.arow[lane] = down ? (uint32_t)row * (uint32_t)(a.I * ES) + pl * plane
+                            : (uint32_t)tok * (uint32_t)(a.H * ES);
+      }
+      if (lane == 0) {
+        d.at = at;
+        d.mt = mt;
+        d.packed = packed;
+        d.n = n;
+        const long long ld = (long long)(down ? a.I : a.H) * ES;
+        d.steps = (int)(ld / 128);
+        d.slot = down ? col / DEC_DN : (g < 0 ? a.G : g);
+        const char* base =
+            down ? (g < 0 ? (const char*)a.ws2 : (const char*)a.w2 + (long long)g * a.H * ld)
+                 : (g < 0 ? (const char*)a.ws13 : (const char*)a.w13 + (long long)g * 2 * a.I * ld);
+        d.w = (unsigned long long)(base + col * ld);
+        d.tile1 = (int)((down ? 16 : a.I) * ld);
+        d.wbytes = (uint32_t)((down ? DEC_DN : a.I + DEC_GU) * ld);
+        d.ldw = (int)ld;
+        d.a = (unsigned long long)(down ? a.act : a.x);
+        d.abytes = down ? plane * PL : (uint32_t)(a.T * a.H * ES);
+      }
+    }
+    if (lane == 0) {
+      d.kind = kind;
+      d.col = col;
+    }
+    lds_drain();
+    if (lane == 0) *(volatile int*)&l.ready = seq + 1;
+    if (uniform(kind) == U_EXIT) break;
+  }
+}
+
+// ---- the streaming waves
+
+// descriptor words of an operand (the last one is the same for all)
+struct StreamBase {
+  int lo, hi, bytes;
+  __device__ __forceinline__ void set(unsigned long long p, uint32_t n) {
+    lo = uniform((int)(uint32_t)p);
+    hi = uniform((int)((p >> 32) & 0xffffu));
+    bytes = uniform((int)n);
+  }
+  __device__ __forceinline__ i32x4 rsrc() const {
+    return i32x4{uniform(lo), uniform(hi), uniform(bytes), MOE_RSRC_DW3};
+  }
+};
+
+// 1 KB of a step, W with the streaming policy: it is read once
+__device__ __forceinline__ void dma16_nt(const i32x4& rs, uint32_t lds, uint32_t voff, int soff) {
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
+               :
+               : "v"(voff), "s"(rs), "s"(uniform(soff)), "s"(uniform((int)lds))
+               : "memory", "m0");
+}
+
+// AT tiles of A (16 rows each) feeding MT row tiles of the result: A tile i
+// adds to row tile i % MT.
+template <typename T, int AT, int MT>
+struct Streamer {
+  static constexpr int SLOT = 4096 + 2048 * AT;       // W: 2 tiles of 2 KB, then A
+  static constexpr int D = DEC_RING / SLOT;           // steps in flight: 5, 3 or 2
+  static constexpr int OPS = 4 + 2 * AT;              // copies of a step
+  static_assert(D >= 2 && (D - 1) * OPS < 64, "ring");
+
+  // the unit whose steps are being copied: this one, then the next
+  StreamBase bw, ba;
+  uint32_t wo[2], ao[2 * AT];
+  int tile1;
+
+  // bind the copies to a unit; returns its steps of this wave
+  __device__ __forceinline__ int bind(const DecDesc& d) {
+    const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
+    bw.set(d.w, d.wbytes);
+    ba.set(d.a, d.abytes);
+    tile1 = uniform(d.tile1);
+    const int ldw = uniform(d.ldw);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int r = 8 * j + (lane >> 3);
+      wo[j] = (uint32_t)(r * ldw + (((lane & 7) ^ ((r >> 1) & 7)) << 4));
+    }
+#pragma unroll
+    for (int j = 0; j < 2 * AT; ++j) {
+      const int r = 8 * j + (lane >> 3);
+      ao[j] = d.arow[r] + (uint32_t)(((lane & 7) ^ ((r >> 1) & 7)) << 4);
+    }
+    return (uniform(d.steps) - wave + DEC_SW - 1) / DEC_SW;
+  }
+  // step i of the wave's into ring slot p
+  __device__ __forceinline__ void copy(uint32_t ring, int p, int i) {
+    const int wave = uniform((int)(threadIdx.x >> 6));
+    const uint32_t at = ring + (uint32_t)(p * SLOT);
+    const int k = (i * DEC_SW + wave) * 128;
+    const i32x4 rw = bw.rsrc(), ra = ba.rsrc();
+    dma16_nt(rw, at, wo[0], k);
+    dma16_nt(rw, at + 1024, wo[1], k);
+    dma16_nt(rw, at + 2048, wo[0], k + tile1);
+    dma16_nt(rw, at + 3072, wo[1], k + tile1);
+#pragma unroll
+    for (int j = 0; j < 2 * AT; ++j) dma16(ra, at + 4096 + j * 1024, ao[j], k);
+  }
+  // until at most x steps of copies are outstanding
+  __device__ __forceinline__ void landed(int x) {
+    if constexpr (D > 4) if (x == 4) { vm_drain<4 * OPS>(); return; }
+    if constexpr (D > 3) if (x == 3) { vm_drain<3 * OPS>(); return; }
+    if constexpr (D > 2) if (x == 2) { vm_drain<2 * OPS>(); return; }
+    if (x == 1) vm_drain<OPS>();
+    else vm_drain<0>();
+  }
+  // One unit, number seq.  ahead: steps of it that are in the ring already,
+  // from slot pos on; both are the next unit's on return.
+  __device__ __forceinline__ void run(DecLds& l, int seq, int& pos, int& ahead, int& prev_mt) {
+    const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
+    const uint32_t ring = lds_addr(l.ring[wave]);
+    const int n = bind(l.desc[seq % DEC_DESCS]);
+    int put = ahead;                 // steps of this unit copied or on their way
+    int np = 0, nn = -1;             // and of the next, and its steps (-1: not known)
+    int wp = (pos + put) % D;        // slot of the next copy
+    while (put < n && put < D) {
+      copy(ring, wp, put++);
+      wp = wp + 1 == D ? 0 : wp + 1;
+    }
+    f32x4 acc[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = f32x4{0, 0, 0, 0};
+    // byte of this lane's 16 in a 16-row tile, for the two halves of a step
+    const int r = lane & 15, kg = lane >> 4;
+    const int f0 = r * 128 + (((kg) ^ ((r >> 1) & 7)) << 4);
+    const int f1 = r * 128 + (((4 + kg) ^ ((r >> 1) & 7)) << 4);
+    for (int i = 0; i < n; ++i) {
+      landed(put - i - 1 + np);
+      const char* st = l.ring[wave] + pos * SLOT;
+      u32x4 w[2][2], x[2][AT];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        w[0][t] = *(const u32x4*)(st + t * 2048 + f0);
+        w[1][t] = *(const u32x4*)(st + t * 2048 + f1);
+      }
+#pragma unroll
+      for (int t = 0; t < AT; ++t) {
+        x[0][t] = *(const u32x4*)(st + 4096 + t * 2048 + f0);
+        x[1][t] = *(const u32x4*)(st + 4096 + t * 2048 + f1);
+      }
+      lds_drain();                   // the slot is read: it can be filled again
+      pos = pos + 1 == D ? 0 : pos + 1;
+      if (put < n) {
+        copy(ring, wp, put++);
+        wp = wp + 1 == D ? 0 : wp + 1;
+      } else {
+        if (nn < 0 && uniform(lds_peek(&l.ready)) > seq + 1) {
+          asm volatile("" ::: "memory");
+          const DecDesc& d = l.desc[(seq + 1) % DEC_DESCS];
+          if (uniform(d.kind) <= U_DOWN && uniform(d.at) == AT) nn = bind(d);
+        }
+        while (np < nn && put - i - 1 + np < D) {
+          copy(ring, wp, np++);
+          wp = wp + 1 == D ? 0 : wp + 1;
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int t = 0; t < AT; ++t) {
+          acc[t % MT][0] = stream_mma(x[h][t], w[h][0], acc[t % MT][0], T());
+          acc[t % MT][1] = stream_mma(x[h][t], w[h][1], acc[t % MT][1], T());
+        }
+    }
+    ahead = np;
+    // partial tiles; units of two row tiles take the room of two units
+    lds_wait(&l.taken, MT == 2 || prev_mt == 2 ? seq : seq - 1);
+    prev_mt = MT;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      float* red = l.red[MT == 2 ? m : seq & 1][wave];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) red[t * 256 + q * 64 + lane] = acc[m][t][q];
+    }
+    lds_drain();
+    if (lane == 0) *(volatile int*)&l.parts[wave] = seq + 1;
+  }
+};
+
+template <typename T, int V>
+__device__ __forceinline__ void decode_stream(const DecArgs& a, DecLds& l) {
+  const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
+  int pos = 0, ahead = 0, prev_mt = 1;
+  for (int seq = 0;; ++seq) {
+    lds_wait(&l.ready, seq + 1);
+    const DecDesc& d = l.desc[seq % DEC_DESCS];
+    const int kind = uniform(d.kind);
+    if (kind == U_EXIT) break;
+    if (kind <= U_DOWN) {
+      const int at = uniform(d.at), mt = uniform(d.mt);
+      if (at == 1) {
+        Streamer<T, 1, 1> s;
+        s.run(l, seq, pos, ahead, prev_mt);
+      } else if (at == 2 && mt == 2) {
+        Streamer<T, 2, 2> s;
+        s.run(l, seq, pos, ahead, prev_mt);
+      } else if constexpr (DEC_PLANES<T> == 2) {
+        if (at == 2) {
+          Streamer<T, 2, 1> s;
+          s.run(l, seq, pos, ahead, prev_mt);
+        } else {
+          Streamer<T, 4, 2> s;
+          s.run(l, seq, pos, ahead, prev_mt);
+        }
+      }
+      // (a ring of another slot size starts over; nothing is ahead in it)
+      if (ahead == 0) pos = 0;
+    } else {
+      if (kind == U_ROUTE) {
+        const int t = uniform(d.col) + wave;
+        if (t < a.T) decode_route_token<V>(a, t);
+        vm_drain<0>();
+      }
+      if (lane == 0) *(volatile int*)&l.parts[wave] = seq + 1;
+    }
+  }
+}
+
+// ---- the finishing wave
 
 // silu(g) u; the sum of two bf16 that the second product reads carries 16
 // bits of it, so its rounding does not show beside that of the result
@@ -210,127 +727,146 @@ __device__ __forceinline__ float decode_swiglu(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
 
-template <typename T> constexpr int DEC_PLANES = sizeof(T) == 2 ? 2 : 1;
-
-// act[row, i0 .. i0 + 15] of the unit's rows.
-template <typename T, int MT>
-__device__ __forceinline__ void decode_gateup(const DecArgs& a, DecLds& l, int g, int i0) {
-  constexpr int ES = sizeof(T);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int P = a.T * a.k, n = l.n_rows;
-  const char* w = (g < 0 ? (const char*)a.ws13 : (const char*)a.w13 + (long long)g * 2 * a.I * a.H * ES) +
-                  (long long)i0 * a.H * ES;
-  const __amdgpu_buffer_rsrc_t wr =
-      make_rsrc(w, (uint32_t)((long long)(2 * a.I - i0) * a.H * ES));
-  const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x, (uint32_t)((long long)a.T * a.H * ES));
-  const uint32_t k16 = (uint32_t)(lane >> 4) * 16u;
-  const uint32_t row0 = (uint32_t)(lane & 15) * (uint32_t)(a.H * ES) + k16;
-  const uint32_t woff[2] = {row0, row0 + (uint32_t)a.I * (uint32_t)(a.H * ES)};
-  uint32_t aoff[1][MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int r = l.rows[min(m * 16 + (lane & 15), n - 1)];
-    const int t = r >= P ? r - P : r / a.k;
-    aoff[0][m] = (uint32_t)t * (uint32_t)(a.H * ES) + k16;
-  }
-  f32x4 acc[MT][2];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = f32x4{0, 0, 0, 0};
-  stream_product<T, MT, 2, 1, STREAM_CS<MT>, DEC_NW, 2>(acc, wr, woff, xr, aoff, a.H * ES, wave);
-  T* const act = (T*)a.act;
-  stream_reduce<MT, 2, DEC_NW>(acc, l.red, [&](int mt, int m, int c, const float* v) {
-    const int r = mt * 16 + m;
-    if (r >= n) return;
-    const float s = decode_swiglu(v[0], v[1]);
-    const long long at = (long long)l.rows[r] * a.I + i0 + c;
-    if constexpr (sizeof(T) == 2) {
-      const uint32_t hi = f32_to_bf16(s);
-      act[at] = (T)hi;
-      act[(long long)(P + a.T) * a.I + at] = (T)f32_to_bf16(s - bf16_to_f32(hi));
-    } else {
-      act[at] = s;
-    }
-  });
+template <typename T>
+__device__ __forceinline__ float elem_load(const void* p, long long i) {
+  if constexpr (sizeof(T) == 2) return bf16_to_f32(((const T*)p)[i]);
+  else return ((const T*)p)[i];
 }
-
-// yp[row, h0 .. h0 + 31] of the unit's rows.
-template <typename T, int MT>
-__device__ __forceinline__ void decode_down(const DecArgs& a, DecLds& l, int g, int h0) {
-  constexpr int ES = sizeof(T), AP = DEC_PLANES<T>;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int P = a.T * a.k, n = l.n_rows;
-  const char* w = (g < 0 ? (const char*)a.ws2 : (const char*)a.w2 + (long long)g * a.H * a.I * ES) +
-                  (long long)h0 * a.I * ES;
-  const __amdgpu_buffer_rsrc_t wr = make_rsrc(w, (uint32_t)((long long)(a.H - h0) * a.I * ES));
-  const long long plane = (long long)(P + a.T) * a.I * ES;
-  const __amdgpu_buffer_rsrc_t ar = make_rsrc(a.act, (uint32_t)(AP * plane));
-  const uint32_t k16 = (uint32_t)(lane >> 4) * 16u, rowb = (uint32_t)(a.I * ES);
-  const uint32_t woff[2] = {(uint32_t)(lane & 15) * rowb + k16, (uint32_t)(16 + (lane & 15)) * rowb + k16};
-  uint32_t aoff[AP][MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int p = 0; p < AP; ++p)
-      aoff[p][m] = (uint32_t)l.rows[min(m * 16 + (lane & 15), n - 1)] * rowb + k16 +
-                   (uint32_t)(p * plane);
-  f32x4 acc[MT][2];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = f32x4{0, 0, 0, 0};
-  stream_product<T, MT, 2, AP, STREAM_CS<MT>, DEC_NW, 2>(acc, wr, woff, ar, aoff, a.I * ES, wave);
-  stream_reduce<MT, 2, DEC_NW>(acc, l.red, [&](int mt, int m, int c, const float* v) {
-    const int r = mt * 16 + m;
-    if (r >= n) return;
-    float* const out = a.yp + (long long)l.rows[r] * a.H + h0 + c;
-    out[0] = v[0];
-    out[16] = v[1];
-  });
-}
-
-// run f<MT> with the fewest 16-row tiles that hold the unit's rows
-template <typename F>
-__device__ __forceinline__ void decode_by_tiles(int n, F&& f) {
-  if (n <= 16) f(std::integral_constant<int, 1>{});
-  else if (n <= 32) f(std::integral_constant<int, 2>{});
-  else if (n <= 64) f(std::integral_constant<int, 4>{});
-  else f(std::integral_constant<int, 8>{});
-}
-
-template <typename T, bool DOWN>
-__global__ __launch_bounds__(DEC_NT) void decode_expert_kernel(DecArgs a) {
-  __shared__ DecLds l;
-  decode_plan(a, l);
-  const int per = DOWN ? a.H / DEC_DN : a.I / DEC_GU;
-  const int total = (l.n_list + a.shared) * per;
-  for (int u = blockIdx.x; u < total; u += gridDim.x) {
-    const int s = u / per, b = u % per;
-    const int g = s < l.n_list ? l.list[s] : -1;
-    decode_rows(a, l, g);
-    decode_by_tiles(l.n_rows, [&](auto mt) {
-      constexpr int MT = decltype(mt)::value;
-      if constexpr (DOWN) decode_down<T, MT>(a, l, g, b * DEC_DN);
-      else decode_gateup<T, MT>(a, l, g, b * DEC_GU);
-    });
-  }
+template <typename T>
+__device__ __forceinline__ void elem_store(void* p, long long i, float v) {
+  if constexpr (sizeof(T) == 2) ((T*)p)[i] = (T)f32_to_bf16(v);
+  else ((T*)p)[i] = v;
 }
 
 // y[t, h] = residual + shared + sum_j gate yp[t, j], in that order
 template <typename T>
-__global__ __launch_bounds__(256) void decode_combine_kernel(DecArgs a) {
-  const int h = blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
-  if (h >= a.H) return;
+__device__ __forceinline__ void decode_sum(const DecArgs& a, int t, int h) {
   const long long at = (long long)t * a.H + h;
-  float s = 0.f;
-  if (a.residual != nullptr) {
-    if constexpr (sizeof(T) == 2) s = bf16_to_f32(((const T*)a.residual)[at]);
-    else s = ((const T*)a.residual)[at];
-  }
+  float s = a.residual != nullptr ? elem_load<T>(a.residual, at) : 0.f;
   if (a.shared) s += a.yp[((long long)a.T * a.k + t) * a.H + h];
-  for (int j = 0; j < a.k; ++j) {
-    const int p = t * a.k + j, g = a.idx[p] - a.g0;
-    if (g >= 0 && g < a.G) s += a.gate[p] * a.yp[(long long)p * a.H + h];
+  for (int j0 = 0; j0 < a.k; j0 += 8) {
+    float gate[8], v[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int p = t * a.k + min(j0 + q, a.k - 1), g = a.idx[p] - a.g0;
+      const bool in = j0 + q < a.k && g >= 0 && g < a.G;
+      gate[q] = in ? a.gate[p] : 0.f;
+      v[q] = in ? a.yp[(long long)p * a.H + h] : 0.f;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) s += gate[q] * v[q];
   }
-  if constexpr (sizeof(T) == 2) ((T*)a.y)[at] = (T)f32_to_bf16(s);
-  else ((T*)a.y)[at] = s;
+  elem_store<T>(a.y, at, s);
+}
+
+template <typename T>
+__device__ __forceinline__ void decode_finish(const DecArgs& a, DecLds& l) {
+  const int lane = threadIdx.x & 63, P = a.T * a.k;
+  const bool fused = a.T <= DEC_FUSED_T;
+  const long long plane = (long long)(P + a.T) * a.I;
+  auto sum_block = [&](int col) {
+    for (int t = lane >> 5; t < a.T; t += 2) decode_sum<T>(a, t, col + (lane & 31));
+  };
+  for (int seq = 0;; ++seq) {
+    lds_wait(&l.ready, seq + 1);
+    const DecDesc& d = l.desc[seq % DEC_DESCS];
+    const int kind = uniform(d.kind), col = uniform(d.col);
+    if (kind == U_EXIT) break;
+#pragma unroll
+    for (int w = 0; w < DEC_SW; ++w) lds_wait(&l.parts[w], seq + 1);
+    if (kind <= U_DOWN) {
+      const int n = uniform(d.n), mt = uniform(d.mt);
+      const bool packed = uniform(d.packed);
+      float v[2][2][4];   // [row tile][weight tile][register]
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        if (m < mt) {
+          const int b = mt == 2 ? m : seq & 1;
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float s = l.red[b][0][t * 256 + q * 64 + lane];
+#pragma unroll
+              for (int w = 1; w < DEC_SW; ++w) s += l.red[b][w][t * 256 + q * 64 + lane];
+              v[m][t][q] = s;
+            }
+        }
+      lds_drain();
+      if (lane == 0) *(volatile int*)&l.taken = seq + 1;
+      // register q: row 4 (lane / 16) + q, column lane % 16
+      const int c = lane & 15;
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        if (m < mt)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float s0 = v[m][0][q], s1 = v[m][1][q];
+            if (packed) {   // rows 8-15: the low halves' part of rows 0-7
+              s0 += __shfl_xor(s0, 32, 64);
+              s1 += __shfl_xor(s1, 32, 64);
+            }
+            const int r = 16 * m + 4 * (lane >> 4) + q;
+            if (r >= n || (packed && lane >= 32)) continue;
+            const int row = d.rows[r];
+            if (kind == U_GATEUP) {
+              const float s = decode_swiglu(s0, s1);
+              const long long at = (long long)row * a.I + col + c;
+              if constexpr (sizeof(T) == 2) {
+                const uint32_t hi = f32_to_bf16(s);
+                dev_store((bf16_t*)a.act + at, hi);
+                dev_store((bf16_t*)a.act + plane + at, f32_to_bf16(s - bf16_to_f32(hi)));
+              } else {
+                dev_store((float*)a.act + at, s);
+              }
+            } else {
+              float* out = a.yp + (long long)row * a.H + col + c;
+              dev_store(out, s0);
+              dev_store(out + 16, s1);
+            }
+          }
+      vm_drain<0>();   // the stores are out: the unit counts
+      if (kind == U_GATEUP) {
+        if (lane == 0) dev_add(a.act_done + uniform(d.slot), 1);
+      } else if (fused) {
+        int before = 0;
+        if (lane == 0)
+          before = __hip_atomic_fetch_add(a.col_done + uniform(d.slot), 1, __ATOMIC_RELAXED,
+                                          __HIP_MEMORY_SCOPE_AGENT);
+        if (uniform(before) == uniform(lds_peek(&l.per_col)) - 1) {
+          __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+          sum_block(col);
+        }
+      }
+    } else {
+      if (lane == 0) *(volatile int*)&l.taken = seq + 1;
+      if (kind == U_ROUTE) {
+        if (lane == 0) dev_add(a.routed, min(DEC_SW, a.T - col));
+      } else {
+        sum_block(col);
+      }
+    }
+    if (lane == 0) *(volatile int*)&l.done = seq + 1;
+  }
+}
+
+template <typename T, int V>
+__global__ __launch_bounds__(DEC_NT) void decode_kernel(DecArgs a) {
+  __shared__ __attribute__((aligned(1024))) DecLds l;
+  if (threadIdx.x < DEC_SW) l.parts[threadIdx.x] = 0;
+  if (threadIdx.x == 0) l.ready = l.taken = l.done = 0;
+  __syncthreads();
+  const int wave = uniform((int)(threadIdx.x >> 6));
+  if (wave < DEC_SW) decode_stream<T, V>(a, l);
+  else if (wave == DEC_SW) decode_schedule<T>(l);
+  else decode_finish<T>(a, l);
+}
+
+// the sum as a launch of its own, for more tokens than one wave should add
+template <typename T>
+__global__ __launch_bounds__(256) void decode_sum_kernel(DecArgs a) {
+  const int h = blockIdx.x * 256 + threadIdx.x;
+  if (h < a.H) decode_sum<T>(a, blockIdx.y, h);
 }
 
 // ---------------------------------------------------------------- host side
@@ -348,16 +884,20 @@ int router_slices(int H, int E) {
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct DecWs {
-  size_t part, act, yp, total;   // byte offsets
+  size_t count, part, act, yp, total;   // byte offsets
+  int n_count;
 };
-DecWs decode_ws(int T, int H, int I, int E, int k, int dt) {
+DecWs decode_ws(int T, int H, int I, int E, int k) {
   DecWs w;
   const size_t rows = (size_t)T * k + T;
-  w.part = 0;
+  // 16 ints for the two scalars, one per expert of the window and the shared
+  // one, one per column block
+  w.n_count = 16 + E + 1 + H / DEC_DN;
+  w.count = 0;
+  w.part = w.count + round256((size_t)w.n_count * 4);
   w.act = w.part + round256((size_t)router_slices(H, E) * T * E * 8);
   w.yp = w.act + round256(rows * I * 4);   // two bf16 planes, or one fp32
   w.total = w.yp + round256(rows * H * 4);
-  (void)dt;
   return w;
 }
 
@@ -390,30 +930,25 @@ int decode_launch(const DecArgs& a, hipStream_t s, const char* fn) {
     if (a.T <= 16) hipLaunchKernelGGL((decode_router_kernel<T, 1>), grid, block, 0, s, a);
     else if (a.T <= 64) hipLaunchKernelGGL((decode_router_kernel<T, 4>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((decode_router_kernel<T, 8>), grid, block, 0, s, a);
-    MOE_TRY(moe_check_launch(fn));
-  }
-  const dim3 rg((a.T + 3) / 4), rb(256);
-  switch (route_width(a.E)) {
-    case 1: hipLaunchKernelGGL(decode_route_kernel<1>, rg, rb, 0, s, a); break;
-    case 2: hipLaunchKernelGGL(decode_route_kernel<2>, rg, rb, 0, s, a); break;
-    case 4: hipLaunchKernelGGL(decode_route_kernel<4>, rg, rb, 0, s, a); break;
-    case 8: hipLaunchKernelGGL(decode_route_kernel<8>, rg, rb, 0, s, a); break;
-    default: hipLaunchKernelGGL(decode_route_kernel<16>, rg, rb, 0, s, a); break;
+  } else {
+    hipLaunchKernelGGL(decode_clear_kernel, dim3((a.n_count + 255) / 256), dim3(256), 0, s, a);
   }
   MOE_TRY(moe_check_launch(fn));
-  const int P = a.T * a.k;
-  const long long experts = (P < a.G ? P : a.G) + a.shared;   // most that can be active
+  // one workgroup per CU (its LDS fills one), no more than there can be units
+  const long long P = (long long)a.T * a.k;
+  const long long experts = (P < a.G ? P : a.G) + a.shared;
+  const long long units = experts * (a.I / DEC_GU + a.H / DEC_DN) + a.H / DEC_DN;
   const int cus = moe_cu_count();
-  auto grid = [&](long long units) {
-    return dim3((unsigned)(units < 1 ? 1 : units < 2LL * cus ? units : 2LL * cus));
-  };
-  hipLaunchKernelGGL((decode_expert_kernel<T, false>), grid(experts * (a.I / DEC_GU)),
-                     dim3(DEC_NT), 0, s, a);
+  const dim3 grid((unsigned)(units < cus ? units : cus)), block(DEC_NT);
+  switch (route_width(a.E)) {
+    case 1: hipLaunchKernelGGL((decode_kernel<T, 1>), grid, block, 0, s, a); break;
+    case 2: hipLaunchKernelGGL((decode_kernel<T, 2>), grid, block, 0, s, a); break;
+    case 4: hipLaunchKernelGGL((decode_kernel<T, 4>), grid, block, 0, s, a); break;
+    default: hipLaunchKernelGGL((decode_kernel<T, 16>), grid, block, 0, s, a); break;
+  }
   MOE_TRY(moe_check_launch(fn));
-  hipLaunchKernelGGL((decode_expert_kernel<T, true>), grid(experts * (a.H / DEC_DN)),
-                     dim3(DEC_NT), 0, s, a);
-  MOE_TRY(moe_check_launch(fn));
-  hipLaunchKernelGGL(decode_combine_kernel<T>, dim3((a.H + 255) / 256, a.T), dim3(256), 0, s, a);
+  if (a.T <= DEC_FUSED_T) return MOE_OK;
+  hipLaunchKernelGGL(decode_sum_kernel<T>, dim3((a.H + 255) / 256, a.T), dim3(256), 0, s, a);
   return moe_check_launch(fn);
 }
 
@@ -421,7 +956,7 @@ int decode_launch(const DecArgs& a, hipStream_t s, const char* fn) {
 
 extern "C" size_t moe_decode_workspace_bytes(int T, int H, int I, int E, int k, int dt) {
   if (decode_shape("moe_decode_workspace_bytes", T, H, I, E, k, dt) != MOE_OK) return 0;
-  return decode_ws(T, H, I, E, k, dt).total;
+  return decode_ws(T, H, I, E, k).total;
 }
 
 extern "C" int moe_decode(const void* x, int dt, const float* wg, const float* bias, int T, int H,
@@ -458,7 +993,7 @@ extern "C" int moe_decode(const void* x, int dt, const float* wg, const float* b
   if (y == x)
     return moe_fail(MOE_ERR_INVALID_ARG, "%s: y is x's buffer (it may be residual's)", fn);
   MOE_TRY(moe_need_ptr(ws, fn, "ws", 256));
-  const DecWs w = decode_ws(T, H, I, E, k, dt);
+  const DecWs w = decode_ws(T, H, I, E, k);
   if (ws_bytes < w.total)
     return moe_fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", fn, ws_bytes,
                     w.total);
@@ -469,6 +1004,11 @@ extern "C" int moe_decode(const void* x, int dt, const float* wg, const float* b
   a.w13 = w13; a.w2 = w2; a.ws13 = ws13; a.ws2 = ws2; a.residual = residual;
   a.logits = logits; a.idx = idx; a.gate = gate; a.y = y;
   a.S = wg != nullptr ? router_slices(H, E) : 0;
+  a.n_count = w.n_count;
+  a.next = (int*)((char*)ws + w.count);
+  a.routed = a.next + 8;
+  a.act_done = a.next + 16;
+  a.col_done = a.act_done + E + 1;
   a.part = (double*)((char*)ws + w.part);
   a.act = (char*)ws + w.act;
   a.yp = (float*)((char*)ws + w.yp);
