@@ -379,7 +379,7 @@ int moe_grouped_gemm_bwd_dw_recompute(const void* x, const int32_t* src_token, i
  * [2I,H] and ws2 [H,I], both or neither.  residual [T,H] is nullable, and y
  * may be its buffer.  Gate/up values, expert outputs and the sum stay in fp32;
  * y is rounded once.
- * T <= 128 and T k <= 4096 (MOE_ERR_UNSUPPORTED beyond: the grouped path is
+ * T <= 128 and T k <= 2048 (MOE_ERR_UNSUPPORTED beyond: the grouped path is
  * the faster one there), one expert's w13 and the call's rows below 2 GiB.
  * ws: moe_decode_workspace_bytes bytes (256-byte aligned, contents scratch),
  * not shared by calls that may overlap.

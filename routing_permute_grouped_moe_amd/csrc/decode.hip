@@ -25,7 +25,7 @@
 namespace {
 
 constexpr int DEC_MAX_T = 128;       // tokens of a call
-constexpr int DEC_MAX_PAIRS = 4096;  // (token, slot) pairs of a call
+constexpr int DEC_MAX_PAIRS = 2048;  // (token, slot) pairs of a call
 constexpr int DEC_SW = 4;            // streaming waves of a workgroup of the second launch
 constexpr int DEC_NT = 64 * (DEC_SW + 2);   // and one that schedules, one that finishes tiles
 constexpr int DEC_GU = 16;           // gate/up columns of a unit (16 gate and 16 up rows of W13)
@@ -50,6 +50,7 @@ struct DecArgs {
   // routed, finished gate/up units of each expert (window index; the shared
   // expert last), finished units of each block of DEC_DN output columns
   int* next; int* routed; int* act_done; int* col_done;
+  int* go;            // one word a cache line for each workgroup: the activations are complete
   int n_count;        // all of them, from next on
 };
 
@@ -147,21 +148,23 @@ __device__ __forceinline__ void dev_add(int* p, int v) {
 
 // One wave per token: the logits (sum of the partials and the bias, rounded
 // once to fp32), the k largest and their softmax weights.
-template <int V>
-__device__ __forceinline__ void decode_route_token(const DecArgs& a, int t) {
+// emit(slot, expert, gate) for each; keep: the logits are written out.
+template <int V, typename Emit>
+__device__ __forceinline__ void decode_route_token(const DecArgs& a, int t, bool keep,
+                                                   Emit&& emit) {
   const int lane = threadIdx.x & 63;
   float v[V];
   uint32_t key[V];
   float m = -INFINITY;
   if (a.S > 0) {
-    // slices 8 at a time, all loads of a batch in flight
+    // all loads of a batch of slices in flight
     double s[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int e = lane + i * MOE_WAVE;
       s[i] = a.bias != nullptr && e < a.E ? (double)a.bias[e] : 0.0;
     }
-    constexpr int B = V <= 4 ? 8 : 2;
+    constexpr int B = V == 1 ? 32 : V == 2 ? 16 : V == 4 ? 16 : 2;
     for (int p = 0; p < a.S; p += B) {
       double d[V][B];
 #pragma unroll
@@ -179,7 +182,7 @@ __device__ __forceinline__ void decode_route_token(const DecArgs& a, int t) {
     for (int i = 0; i < V; ++i) {
       const int e = lane + i * MOE_WAVE;
       v[i] = e < a.E ? (float)s[i] : -INFINITY;
-      if (e < a.E) a.logits[(long long)t * a.E + e] = v[i];
+      if (keep && e < a.E) a.logits[(long long)t * a.E + e] = v[i];
     }
   } else {
 #pragma unroll
@@ -201,8 +204,7 @@ __device__ __forceinline__ void decode_route_token(const DecArgs& a, int t) {
   s = wave_sum(s);
   const float inv = 1.0f / s;
   route_select<V>(key, a.k, [&](int slot, int i) {
-    dev_store(a.idx + (long long)t * a.k + slot, lane + i * MOE_WAVE);
-    dev_store(a.gate + (long long)t * a.k + slot, none ? 0.f : expf(v[i] - m) * inv);
+    emit(slot, lane + i * MOE_WAVE, none ? 0.f : expf(v[i] - m) * inv);
   });
 }
 
@@ -211,7 +213,7 @@ __device__ __forceinline__ void decode_route_token(const DecArgs& a, int t) {
 // and one that finishes tiles; they meet in LDS words only, never at a
 // barrier, so the stream of weights does not stop between units.
 //
-// Streaming.  A unit is 32 weight rows (two 16-row tiles) times at most 32
+// Streaming.  A unit is 32 weight rows (two 16-row tiles) times at most 16
 // rows of the other operand.  K runs in steps of 128 bytes of a row (64 bf16,
 // 32 fp32) dealt to the four waves in turn; a step's weights and operand rows
 // go HBM -> LDS in 1 KB copies (lds_copy.hpp) into a ring that belongs to the
@@ -219,9 +221,13 @@ __device__ __forceinline__ void decode_route_token(const DecArgs& a, int t) {
 // that way with the streaming policy HBM gives 7.0 TB/s here, against 5.1 TB/s
 // for loads straight into the MFMA's operand layout (16 rows x 64 bytes).
 // 16-byte chunk c of row r sits in slot c ^ ((r >> 1) & 7) of its row, so the
-// 16 rows of a fragment read hit all banks.  At the end of a unit the waves
-// leave their partial tiles in LDS and go on to the next, whose first steps
-// are copied while the last of this one are multiplied.
+// 16 rows of a fragment read hit all banks.  The stream is one flat sequence of
+// steps, unit after unit: at the end of a unit the waves leave their partial
+// tiles in LDS while the next one's steps are on their way.  A wave has a SIMD
+// to itself, so a branch costs it as much as a dozen instructions, and a step
+// has 590 ns at HBM's rate (16 KB for the four waves): every step is the same
+// few copies, reads and MFMAs, and while there is nothing to copy the copies
+// go through an empty range, whose zeros add nothing to whatever tile is next.
 //
 // Finishing.  The finishing wave adds the four partial tiles in wave order
 // (the same bits on every run), applies silu(g) u or stores the rows of the
@@ -231,15 +237,20 @@ __device__ __forceinline__ void decode_route_token(const DecArgs& a, int t) {
 // chosen expert][second product, same order].  A unit waits only for units of
 // lower numbers, and numbers are drawn in order by running workgroups, so the
 // lowest unfinished unit never waits: no residency of the grid is assumed.
-constexpr int DEC_ROWS = 32;         // operand rows of a unit
+// For few tokens every workgroup routes them itself (they cost each about a
+// microsecond) instead of waiting for the one that would.
+constexpr int DEC_ROWS = 16;         // operand rows of a unit
 constexpr int DEC_DESCS = 4;
-constexpr int DEC_RING = 30 * 1024;  // of a streaming wave
+constexpr int DEC_PAGE = 2048;       // a 16-row tile of a step
+constexpr int DEC_PAGES = 16;        // of a streaming wave's ring
+constexpr int DEC_OWN_T = 8;         // tokens, and pairs, that every workgroup routes itself
+constexpr int DEC_OWN_PAIRS = 256;
 constexpr unsigned long long DEC_WAIT_TICKS = 100000000ull;   // 1 s of the 100 MHz clock
 
 enum { U_GATEUP = 0, U_DOWN = 1, U_ROUTE = 2, U_SUM = 3, U_EXIT = 4 };
 
 struct DecDesc {
-  int kind, at, mt;            // A tiles (operand copies of 16 rows), row tiles of the result
+  int kind, at;                // A tiles (operand copies of 16 rows)
   int packed;                  // rows 8-15 are the low halves of rows 0-7
   int steps;                   // K steps of 128 bytes
   int n;                       // rows
@@ -248,28 +259,36 @@ struct DecDesc {
   unsigned long long w, a;     // operand addresses
   uint32_t wbytes, abytes;     // and extents
   int ldw, tile1;              // bytes of a weight row, and from the first tile to the second
-  uint32_t arow[4 * 16];       // byte offset of each A row
+  uint32_t arow[2 * 16];       // byte offset of each A row
   int rows[DEC_ROWS];          // pair indices, or T k + token
 };
 
 struct DecLds {
-  char ring[DEC_SW][DEC_RING];
-  float red[2][DEC_SW][2 * 256];   // partial tiles (units of two row tiles take both halves)
-  int16_t loc[DEC_MAX_PAIRS];      // window index of each pair's expert, -1 outside it
+  char ring[DEC_SW][DEC_PAGES * DEC_PAGE];
+  float red[2][DEC_SW][2 * 256];   // partial tiles, of units of even and of odd number
+  int16_t order[DEC_MAX_PAIRS];    // pairs of the window, expert by expert
+  int cur[(MOE_MAX_E + 1) / 2];    // (while that is built: two counters a word)
   int16_t list[MOE_MAX_E + 1];     // experts some token chose, ascending; the shared one first (-1)
-  int16_t pre_g[MOE_MAX_E + 2];    // row blocks before each listed expert
-  int16_t cnt[MOE_MAX_E];          // rows of each expert of the window
+  int16_t first[MOE_MAX_E + 2];    // their places in order
+  int16_t pre[MOE_MAX_E + 2];      // row blocks before each
+  int16_t own_idx[DEC_OWN_PAIRS];  // choices and gates, where every workgroup routes itself
+  float own_gate[DEC_OWN_PAIRS];
   DecDesc desc[DEC_DESCS];
   // words the waves meet in
   int ready;                       // descriptors written
+  int a_ready;                     // units whose A operand is there
   int parts[DEC_SW];               // units whose partial tiles each streaming wave has left
   int taken;                       // units whose partial tiles were read
   int done;                        // units finished
   int per_col;                     // units of a column block
 };
+static_assert(sizeof(DecLds) <= 160 * 1024, "LDS of a CU");
 
 __device__ __forceinline__ int lds_peek(const int* p) {
   return *(const volatile int*)p;
+}
+__device__ __forceinline__ void lds_post(int* p, int v) {   // (by one lane)
+  *(volatile int*)p = v;
 }
 // wait until *p >= v: another wave of the workgroup raises it
 __device__ __forceinline__ void lds_wait(const int* p, int v) {
@@ -289,75 +308,61 @@ __device__ __forceinline__ int row_blocks(int m) { return (m + DEC_ROWS - 1) / D
 
 template <typename T> constexpr int DEC_PLANES = sizeof(T) == 2 ? 2 : 1;
 
+__device__ __host__ __forceinline__ bool dec_own(int T, int k) {
+  return T <= DEC_OWN_T && T * k <= DEC_OWN_PAIRS;
+}
+
 // ---- the scheduling wave
 
 // The launch's arguments where they lie, read again where they are used: held
 // in scalar registers across the scheduler's loop they would spill.
 typedef const __attribute__((address_space(4))) DecArgs DecConst;
 
-// Wait for a device-scope counter, at most a second (only calls that share a
-// workspace ever wait that long; their results are wrong, but they end).
-__device__ __forceinline__ void dev_wait(const int* p, int v, bool& lost) {
-  if (!lost) {
-    const unsigned long long t0 = wall_clock64();
-    while (uniform(dev_load(p)) < v) {
-      if (wall_clock64() - t0 > DEC_WAIT_TICKS) {
-        lost = true;
-        break;
-      }
-      __builtin_amdgcn_s_sleep(2);
-    }
-  }
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-}
-
-// Tables of the call, from the tokens' choices: loc, cnt, the list of chosen
-// experts (shared first) and the row blocks before each.  Returns the length
-// of the list.
+// Tables of the call, from the tokens' choices: the list of chosen experts
+// (shared first), the row blocks before each, and the pairs expert by expert
+// (in any order within one: a row's result does not depend on its place).
+// Returns the length of the list.
 __device__ __forceinline__ int decode_tables(DecConst& a, DecLds& l) {
   const int lane = threadIdx.x & 63, P = a.T * a.k;
-  for (int g = lane; g < a.G; g += 64) l.cnt[g] = 0;
+  const bool own = dec_own(a.T, a.k);
+  for (int g = lane; g < (a.G + 1) / 2; g += 64) l.cur[g] = 0;
   lds_drain();
-  for (int p0 = 0; p0 < P; p0 += 64 * 8) {
-    int e[8];
+  // counter of expert g: a half of a word (at most 2048 pairs in all)
+  auto add = [&](int g, int v) {
+    return (atomicAdd(&l.cur[g >> 1], v << ((g & 1) * 16)) >> ((g & 1) * 16)) & 0xffff;
+  };
+  auto pairs = [&](auto&& f) {   // f(pair, window index) for every pair of the window
+    for (int p0 = 0; p0 < P; p0 += 64 * 8) {
+      int e[8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) e[q] = a.idx[min(p0 + q * 64 + lane, P - 1)];
+      for (int q = 0; q < 8; ++q) {
+        const int p = min(p0 + q * 64 + lane, P - 1);
+        e[q] = own ? (int)l.own_idx[p & (DEC_OWN_PAIRS - 1)] : a.idx[p];
+      }
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int p = p0 + q * 64 + lane, g = e[q] - a.g0;
-      if (p < P) l.loc[p] = g >= 0 && g < a.G ? (int16_t)g : (int16_t)-1;
-    }
-  }
-  lds_drain();
-  // rows of each expert: lane by lane over the pairs of a 64-pair group that
-  // share its expert, one leader each
-  for (int p0 = 0; p0 < P; p0 += 64) {
-    const int p = p0 + lane;
-    const int g = p < P ? l.loc[p] : -1;
-    unsigned long long todo = __ballot(g >= 0);
-    while (todo) {
-      const int first = __builtin_ctzll(todo);
-      const int g1 = __builtin_amdgcn_readlane(g, first);
-      const unsigned long long same = __ballot(g == g1);
-      if (lane == first) l.cnt[g1] = (int16_t)(l.cnt[g1] + __popcll(same));
-      todo &= ~same;
+      for (int q = 0; q < 8; ++q) {
+        const int p = p0 + q * 64 + lane, g = e[q] - a.g0;
+        if (p < P && g >= 0 && g < a.G) f(p, g);
+      }
     }
     lds_drain();
-  }
-  int n = 0, blocks = 0;
+  };
+  pairs([&](int, int g) { add(g, 1); });
+  int n = 0, blocks = 0, rows = 0;
   if (a.shared) {
     if (lane == 0) {
       l.list[0] = -1;
-      l.pre_g[0] = 0;
+      l.first[0] = 0;
+      l.pre[0] = 0;
     }
     n = 1;
     blocks = row_blocks(a.T);
   }
   for (int g0 = 0; g0 < a.G; g0 += 64) {
     const int g = g0 + lane;
-    const int m = g < a.G ? l.cnt[g] : 0;
+    const int m = g < a.G ? (l.cur[g >> 1] >> ((g & 1) * 16)) & 0xffff : 0;
     const unsigned long long b = __ballot(m > 0);
-    int incl = row_blocks(m);
+    int incl = m | row_blocks(m) << 16;   // both sums at once
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
       const int v = __shfl_up(incl, o, 64);
@@ -366,38 +371,23 @@ __device__ __forceinline__ int decode_tables(DecConst& a, DecLds& l) {
     if (m > 0) {
       const int at = n + __popcll(b & ((1ull << lane) - 1));
       l.list[at] = (int16_t)g;
-      l.pre_g[at] = (int16_t)(blocks + incl - row_blocks(m));
+      l.first[at] = (int16_t)(rows + (incl & 0xffff) - m);
+      l.pre[at] = (int16_t)(blocks + (incl >> 16) - row_blocks(m));
+      add(g, rows + (incl & 0xffff) - 2 * m);   // m counted there -> its first place
     }
+    const int all = __shfl(incl, 63, 64);
     n += __popcll(b);
-    blocks += __shfl(incl, 63, 64);
+    rows += all & 0xffff;
+    blocks += all >> 16;
   }
   if (lane == 0) {
-    l.pre_g[n] = (int16_t)blocks;
+    l.first[n] = (int16_t)rows;
+    l.pre[n] = (int16_t)blocks;
     l.per_col = blocks;
   }
   lds_drain();
+  pairs([&](int p, int g) { l.order[add(g, 1)] = (int16_t)p; });
   return n;
-}
-
-// Rows of the expert in list place s, row block rb, into d.rows.
-__device__ __forceinline__ int decode_rows(DecConst& a, const DecLds& l, DecDesc& d, int g,
-                                           int rb) {
-  const int lane = threadIdx.x & 63, P = a.T * a.k, r0 = rb * DEC_ROWS;
-  if (g < 0) {
-    const int n = min(DEC_ROWS, a.T - r0);
-    if (lane < n) d.rows[lane] = P + r0 + lane;
-    return n;
-  }
-  int n = 0;
-  for (int p0 = 0; p0 < P; p0 += 64) {
-    const int p = p0 + lane;
-    const bool on = p < P && l.loc[p] == g;
-    const unsigned long long b = __ballot(on);
-    const int at = n + __popcll(b & ((1ull << lane) - 1)) - r0;
-    if (on && at >= 0 && at < DEC_ROWS) d.rows[at] = p;
-    n += __popcll(b);
-  }
-  return min(DEC_ROWS, n - r0);
 }
 
 template <typename T>
@@ -406,16 +396,18 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
   const int lane = threadIdx.x & 63;
   DecConst* args = (DecConst*)__builtin_amdgcn_kernarg_segment_ptr();
   int n_list = -1, blocks = 0;
-  bool lost = false;
-  int held = 0;          // the number drawn for the next unit
+  bool go = false;       // the activations are complete
+  bool lost = false;     // a wait took a second (calls that share a workspace): wait no more
   auto draw = [&]() {
     int v = 0;
     if (lane == 0)
       v = __hip_atomic_fetch_add(args->next, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     return v;
   };
-  held = draw();
-  int last_g = -2, last_rb = -1, last_n = 0, last_at = 0;   // rows of the last descriptor
+  // two numbers are drawn ahead: they take microseconds under load (the second
+  // one only when the first unit is on its way -- 256 workgroups start at once,
+  // and their draws queue up)
+  int held = draw(), held2 = 0;
   for (int seq = 0;; ++seq) {
     int u = uniform(held);
     // (kept in a vector register, and all that follows from it: the scheduling
@@ -424,10 +416,9 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
     asm volatile("" : "+s"(args));
     DecConst& a = *args;
     const int P = a.T * a.k;
-    const int n_route = (a.T + DEC_SW - 1) / DEC_SW;
+    const int n_route = dec_own(a.T, a.k) ? 0 : (a.T + DEC_SW - 1) / DEC_SW;
     const int per_g = a.I / DEC_GU, per_d = a.H / DEC_DN;
     const int n_shared = a.shared ? row_blocks(a.T) * per_g : 0;
-    held = draw();       // (returns while this one is prepared)
     lds_wait(&l.done, seq - DEC_DESCS + 1);   // the descriptor's last user is through
     DecDesc& d = l.desc[seq % DEC_DESCS];
     int kind, g = -2, s = 0, rb = 0, col = 0;
@@ -436,14 +427,21 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
       col = u * DEC_SW;
     } else if (u < n_route + n_shared) {
       // (the shared expert needs no routing)
-      const int v = u - n_route;
+      const int v = u - n_route, nb = row_blocks(a.T);
       kind = U_GATEUP;
       g = -1;
-      rb = v % row_blocks(a.T);
-      col = v / row_blocks(a.T) * DEC_GU;
+      rb = v % nb;
+      col = v / nb * DEC_GU;
     } else {
       if (n_list < 0) {
-        dev_wait(a.routed, a.T, lost);
+        if (n_route > 0) {
+          const unsigned long long t0 = wall_clock64();
+          while (uniform(dev_load(a.routed)) < a.T && !lost) {
+            lost = wall_clock64() - t0 > DEC_WAIT_TICKS;
+            __builtin_amdgcn_s_sleep(1);
+          }
+          __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+        }
         n_list = decode_tables(a, l);
         blocks = lds_peek(&l.per_col);
       }
@@ -453,20 +451,17 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
         kind = v < n_gu ? U_GATEUP : U_DOWN;
         const int per = v < n_gu ? per_g : per_d;
         if (v >= n_gu) v -= n_gu;
-        // place in the list: the last with pre_g * per <= v
-        int lo = 0, hi = n_list - 1;
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (l.pre_g[mid] * per <= v) lo = mid;
-          else hi = mid - 1;
+        // place in the list: the last with pre * per <= v
+        for (int s0 = 0; s0 < n_list; s0 += 64) {
+          const unsigned long long le =
+              __ballot(s0 + lane < n_list && l.pre[s0 + lane] * per <= v);
+          if (le) s = s0 + 63 - __builtin_clzll(le);
         }
-        s = lo;
         g = l.list[s];
-        const int nb = l.pre_g[s + 1] - l.pre_g[s];
-        v -= l.pre_g[s] * per;
+        const int nb = l.pre[s + 1] - l.pre[s];
+        v -= l.pre[s] * per;
         rb = v % nb;
         col = v / nb * (kind == U_GATEUP ? DEC_GU : DEC_DN);
-        if (kind == U_DOWN) dev_wait(a.act_done + (g < 0 ? a.G : g), nb * per_g, lost);
       } else if (blocks == 0 && v < per_d && a.T <= DEC_FUSED_T) {
         kind = U_SUM;    // nothing but the residual
         col = v * DEC_DN;
@@ -475,33 +470,35 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
       }
     }
     if (kind <= U_DOWN) {
-      int n = last_n;
-      if (g == last_g && rb == last_rb) {
-        if (lane < n) d.rows[lane] = l.desc[last_at].rows[lane];
+      const int r0 = rb * DEC_ROWS;
+      int n, row = 0;
+      if (g < 0) {
+        n = min(DEC_ROWS, a.T - r0);
+        row = P + r0 + min(lane, n - 1);
       } else {
-        n = decode_rows(a, l, d, g, rb);
+        const int f = l.first[s] + r0;
+        n = min(DEC_ROWS, l.first[s + 1] - f);
+        row = l.order[f + min(lane, n - 1)];
       }
-      last_g = g; last_rb = rb; last_n = n; last_at = seq % DEC_DESCS;
-      lds_drain();
+      if (lane < n) d.rows[lane] = row;
       const bool down = kind == U_DOWN;
+      // (packed or not goes by the call: one number of tiles all through a phase)
       const bool two = down && PL == 2;
-      const bool packed = two && n <= 8;
-      const int mt = n <= 16 ? 1 : 2;
-      const int at = packed ? 1 : mt * (two ? 2 : 1);
+      const bool packed = two && a.T <= 8;
+      const int at = two && !packed ? 2 : 1;
       const uint32_t plane = (uint32_t)(P + a.T) * (uint32_t)(a.I * ES);
       // A row `lane`: packed tiles hold the high halves in rows 0-7 and the low
-      // ones in rows 8-15; else the tiles of the low halves follow
-      const int per_plane = packed ? 8 : 16 * mt;
-      const int r = min(lane % per_plane, n - 1), pl = lane / per_plane;
-      if (lane < 16 * at) {
-        const int row = d.rows[r];
-        const int tok = row >= P ? row - P : row / a.k;
-        d.arow[lane] = down ? (uint32_t)row * (uint32_t)(a.I * ES) + pl * plane
-                            : (uint32_t)tok * (uint32_t)(a.H * ES);
-      }
+      // ones in rows 8-15; else the tile of the low halves follows
+      const int per_plane = packed ? 8 : 16;
+      // (padding rows lie out of range: they read as zeros and move nothing)
+      const int mine = __shfl(row, min(lane % per_plane, n - 1), 64);
+      const int tok = mine >= P ? mine - P : mine / a.k;
+      if (lane < 16 * at)
+        d.arow[lane] = lane % per_plane >= n ? STREAM_OOB
+                       : down ? (uint32_t)mine * (uint32_t)(a.I * ES) + lane / per_plane * plane
+                              : (uint32_t)tok * (uint32_t)(a.H * ES);
       if (lane == 0) {
         d.at = at;
-        d.mt = mt;
         d.packed = packed;
         d.n = n;
         const long long ld = (long long)(down ? a.I : a.H) * ES;
@@ -523,8 +520,41 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
       d.col = col;
     }
     lds_drain();
-    if (lane == 0) *(volatile int*)&l.ready = seq + 1;
+    if (lane == 0) lds_post(&l.ready, seq + 1);
     if (uniform(kind) == U_EXIT) break;
+    held = seq == 0 ? draw() : held2;
+    held2 = draw();
+    // The second product begins when all activations are complete.  One
+    // workgroup, whoever drew its first unit, watches the experts' counters (64
+    // at a look) and tells each of the others on a line of its own: 256 of them
+    // watching the same lines took so long for every look that the copies
+    // queued behind it in their CUs' memory pipelines stood still.
+    if (kind == U_DOWN && !go) {
+      const unsigned long long t0 = wall_clock64();
+      if (u == n_route + blocks * per_g) {
+        int known = 0;
+        while (known < n_list && !lost) {
+          const int q = known + lane;
+          bool there = false;
+          if (q < n_list) {
+            const int gq = l.list[q];
+            there = dev_load(a.act_done + (gq < 0 ? a.G : gq)) >= (l.pre[q + 1] - l.pre[q]) * per_g;
+          }
+          const unsigned long long no = ~__ballot(there);
+          known += no ? __builtin_ctzll(no) : 64;
+          lost = wall_clock64() - t0 > DEC_WAIT_TICKS;
+        }
+        for (int w = lane; w < (int)gridDim.x; w += 64) dev_store(a.go + w * 32, 1);
+      } else {
+        while (uniform(dev_load(a.go + blockIdx.x * 32)) == 0 && !lost) {
+          lost = wall_clock64() - t0 > DEC_WAIT_TICKS;
+          __builtin_amdgcn_s_sleep(2);
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+      go = true;
+    }
+    if (lane == 0) lds_post(&l.a_ready, seq + 1);
   }
 }
 
@@ -551,26 +581,48 @@ __device__ __forceinline__ void dma16_nt(const i32x4& rs, uint32_t lds, uint32_t
                : "memory", "m0");
 }
 
-// AT tiles of A (16 rows each) feeding MT row tiles of the result: A tile i
-// adds to row tile i % MT.
-template <typename T, int AT, int MT>
-struct Streamer {
-  static constexpr int SLOT = 4096 + 2048 * AT;       // W: 2 tiles of 2 KB, then A
-  static constexpr int D = DEC_RING / SLOT;           // steps in flight: 5, 3 or 2
-  static constexpr int OPS = 4 + 2 * AT;              // copies of a step
-  static_assert(D >= 2 && (D - 1) * OPS < 64, "ring");
+// The flat stream of one streaming wave over the units from seq on that have AT
+// A tiles each; returns the number of the first unit that has not.  Steps are
+// counted as they are copied (`put`) and read (`got`); a unit's tile is complete
+// when got reaches the put at which its last step was copied.  The copies are
+// at most one unit ahead.
+template <typename T, int AT>
+__device__ __forceinline__ int stream_units(DecLds& l, int seq) {
+  constexpr int SIZE = 2 + AT, OPS = 4 + 2 * AT, D = DEC_PAGES / SIZE;
+  constexpr int NEVER = 0x7fffffff;
+  const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
+  char* const ring = l.ring[wave];
+  const uint32_t lds = lds_addr(ring);
+  // the unit being copied
+  int at_unit = seq - 1, left = 0, end = NEVER;
+  bool stop = false;
+  StreamBase bw = {0, 0, 0}, ba = {0, 0, 0};
+  uint32_t wo[2] = {0, 0}, ao[2 * AT];
+#pragma unroll
+  for (int j = 0; j < 2 * AT; ++j) ao[j] = 0;
+  int tile1 = 0, k = 0;
+  // the unit being read
+  int got_end = NEVER;
+  int put = 0, got = 0;
+  uint32_t wslot = 0, rslot = 0;   // byte of the ring
 
-  // the unit whose steps are being copied: this one, then the next
-  StreamBase bw, ba;
-  uint32_t wo[2], ao[2 * AT];
-  int tile1;
-
-  // bind the copies to a unit; returns its steps of this wave
-  __device__ __forceinline__ int bind(const DecDesc& d) {
-    const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
+  // on to the next unit, if it is known and its operand is there
+  auto bind = [&]() {
+    const int u = at_unit + 1;
+    if (u > seq + 1 || stop || uniform(lds_peek(&l.ready)) <= u) return;
+    asm volatile("" ::: "memory");
+    const DecDesc& d = l.desc[u % DEC_DESCS];
+    if (uniform(d.kind) > U_DOWN || uniform(d.at) != AT) {
+      stop = true;
+      return;
+    }
+    if (uniform(lds_peek(&l.a_ready)) <= u) return;
+    asm volatile("" ::: "memory");
     bw.set(d.w, d.wbytes);
     ba.set(d.a, d.abytes);
     tile1 = uniform(d.tile1);
+    left = (uniform(d.steps) - wave + DEC_SW - 1) / DEC_SW;
+    k = wave * 128;
     const int ldw = uniform(d.ldw);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -582,140 +634,113 @@ struct Streamer {
       const int r = 8 * j + (lane >> 3);
       ao[j] = d.arow[r] + (uint32_t)(((lane & 7) ^ ((r >> 1) & 7)) << 4);
     }
-    return (uniform(d.steps) - wave + DEC_SW - 1) / DEC_SW;
-  }
-  // step i of the wave's into ring slot p
-  __device__ __forceinline__ void copy(uint32_t ring, int p, int i) {
-    const int wave = uniform((int)(threadIdx.x >> 6));
-    const uint32_t at = ring + (uint32_t)(p * SLOT);
-    const int k = (i * DEC_SW + wave) * 128;
-    const i32x4 rw = bw.rsrc(), ra = ba.rsrc();
-    dma16_nt(rw, at, wo[0], k);
-    dma16_nt(rw, at + 1024, wo[1], k);
-    dma16_nt(rw, at + 2048, wo[0], k + tile1);
-    dma16_nt(rw, at + 3072, wo[1], k + tile1);
+    at_unit = u;
+    end = put + left;
+    if (u == seq) got_end = end;
+  };
+  auto copy = [&]() {
+    if (left == 0) bind();
+    const int live = uniform(left > 0 ? -1 : 0);
+    const i32x4 rw = {uniform(bw.lo), uniform(bw.hi), uniform(bw.bytes & live), MOE_RSRC_DW3};
+    const i32x4 ra = {uniform(ba.lo), uniform(ba.hi), uniform(ba.bytes & live), MOE_RSRC_DW3};
+    const uint32_t p = (uint32_t)uniform((int)(lds + wslot));
+    const int k0 = uniform(k & live), k1 = uniform((k + tile1) & live);
+    dma16_nt(rw, p, wo[0], k0);
+    dma16_nt(rw, p + 1024, wo[1], k0);
+    dma16_nt(rw, p + 2048, wo[0], k1);
+    dma16_nt(rw, p + 3072, wo[1], k1);
 #pragma unroll
-    for (int j = 0; j < 2 * AT; ++j) dma16(ra, at + 4096 + j * 1024, ao[j], k);
-  }
-  // until at most x steps of copies are outstanding
-  __device__ __forceinline__ void landed(int x) {
-    if constexpr (D > 4) if (x == 4) { vm_drain<4 * OPS>(); return; }
-    if constexpr (D > 3) if (x == 3) { vm_drain<3 * OPS>(); return; }
-    if constexpr (D > 2) if (x == 2) { vm_drain<2 * OPS>(); return; }
-    if (x == 1) vm_drain<OPS>();
-    else vm_drain<0>();
-  }
-  // One unit, number seq.  ahead: steps of it that are in the ring already,
-  // from slot pos on; both are the next unit's on return.
-  __device__ __forceinline__ void run(DecLds& l, int seq, int& pos, int& ahead, int& prev_mt) {
-    const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
-    const uint32_t ring = lds_addr(l.ring[wave]);
-    const int n = bind(l.desc[seq % DEC_DESCS]);
-    int put = ahead;                 // steps of this unit copied or on their way
-    int np = 0, nn = -1;             // and of the next, and its steps (-1: not known)
-    int wp = (pos + put) % D;        // slot of the next copy
-    while (put < n && put < D) {
-      copy(ring, wp, put++);
-      wp = wp + 1 == D ? 0 : wp + 1;
+    for (int j = 0; j < 2 * AT; ++j) dma16(ra, p + 4096 + j * 1024, ao[j], k0);
+    wslot = (uint32_t)uniform((int)(wslot + SIZE * DEC_PAGE == D * SIZE * DEC_PAGE
+                                        ? 0 : wslot + SIZE * DEC_PAGE));
+    k = uniform(k + DEC_SW * 128);
+    left = uniform(left + live);
+    ++put;
+  };
+  f32x4 acc[2];
+  acc[0] = acc[1] = f32x4{0, 0, 0, 0};
+  // byte of this lane's 16 in a page, for the two halves of a step
+  const int r = lane & 15, kg = lane >> 4;
+  const int f0 = r * 128 + (((kg) ^ ((r >> 1) & 7)) << 4);
+  const int f1 = r * 128 + (((4 + kg) ^ ((r >> 1) & 7)) << 4);
+#pragma unroll 1
+  for (int d = 0; d < D - 1; ++d) copy();
+  for (;;) {
+    copy();                        // into the slot read last
+    vm_drain<(D - 1) * OPS>();     // the oldest step has landed
+    const char* p = ring + rslot;
+    u32x4 w[2][2], x[2][AT];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      w[0][t] = *(const u32x4*)(p + t * DEC_PAGE + f0);
+      w[1][t] = *(const u32x4*)(p + t * DEC_PAGE + f1);
     }
-    f32x4 acc[MT][2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = f32x4{0, 0, 0, 0};
-    // byte of this lane's 16 in a 16-row tile, for the two halves of a step
-    const int r = lane & 15, kg = lane >> 4;
-    const int f0 = r * 128 + (((kg) ^ ((r >> 1) & 7)) << 4);
-    const int f1 = r * 128 + (((4 + kg) ^ ((r >> 1) & 7)) << 4);
-    for (int i = 0; i < n; ++i) {
-      landed(put - i - 1 + np);
-      const char* st = l.ring[wave] + pos * SLOT;
-      u32x4 w[2][2], x[2][AT];
+    for (int t = 0; t < AT; ++t) {
+      x[0][t] = *(const u32x4*)(p + (2 + t) * DEC_PAGE + f0);
+      x[1][t] = *(const u32x4*)(p + (2 + t) * DEC_PAGE + f1);
+    }
+    rslot = (uint32_t)uniform((int)(rslot + SIZE * DEC_PAGE == D * SIZE * DEC_PAGE
+                                        ? 0 : rslot + SIZE * DEC_PAGE));
+    ++got;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        w[0][t] = *(const u32x4*)(st + t * 2048 + f0);
-        w[1][t] = *(const u32x4*)(st + t * 2048 + f1);
-      }
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int t = 0; t < AT; ++t) {
-        x[0][t] = *(const u32x4*)(st + 4096 + t * 2048 + f0);
-        x[1][t] = *(const u32x4*)(st + 4096 + t * 2048 + f1);
+        acc[0] = stream_mma(x[h][t], w[h][0], acc[0], T());
+        acc[1] = stream_mma(x[h][t], w[h][1], acc[1], T());
       }
-      lds_drain();                   // the slot is read: it can be filled again
-      pos = pos + 1 == D ? 0 : pos + 1;
-      if (put < n) {
-        copy(ring, wp, put++);
-        wp = wp + 1 == D ? 0 : wp + 1;
-      } else {
-        if (nn < 0 && uniform(lds_peek(&l.ready)) > seq + 1) {
-          asm volatile("" ::: "memory");
-          const DecDesc& d = l.desc[(seq + 1) % DEC_DESCS];
-          if (uniform(d.kind) <= U_DOWN && uniform(d.at) == AT) nn = bind(d);
-        }
-        while (np < nn && put - i - 1 + np < D) {
-          copy(ring, wp, np++);
-          wp = wp + 1 == D ? 0 : wp + 1;
-        }
+    lds_drain();                   // the slot is read
+    if (got >= got_end) {
+      // (>: a unit without steps of this wave ends where it was bound)
+      lds_wait(&l.taken, seq - 1);
+      float* red = l.red[seq & 1][wave];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) red[t * 256 + q * 64 + lane] = acc[t][q];
+        acc[t] = f32x4{0, 0, 0, 0};
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int t = 0; t < AT; ++t) {
-          acc[t % MT][0] = stream_mma(x[h][t], w[h][0], acc[t % MT][0], T());
-          acc[t % MT][1] = stream_mma(x[h][t], w[h][1], acc[t % MT][1], T());
-        }
+      lds_drain();
+      if (lane == 0) lds_post(&l.parts[wave], seq + 1);
+      ++seq;
+      got_end = at_unit == seq ? end : NEVER;
     }
-    ahead = np;
-    // partial tiles; units of two row tiles take the room of two units
-    lds_wait(&l.taken, MT == 2 || prev_mt == 2 ? seq : seq - 1);
-    prev_mt = MT;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      float* red = l.red[MT == 2 ? m : seq & 1][wave];
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) red[t * 256 + q * 64 + lane] = acc[m][t][q];
-    }
-    lds_drain();
-    if (lane == 0) *(volatile int*)&l.parts[wave] = seq + 1;
+    if (stop && at_unit < seq) break;
   }
-};
+  vm_drain<0>();                   // (empty copies)
+  return seq;
+}
 
-template <typename T, int V>
+template <typename T, int V, bool OWN>
 __device__ __forceinline__ void decode_stream(const DecArgs& a, DecLds& l) {
   const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
-  int pos = 0, ahead = 0, prev_mt = 1;
-  for (int seq = 0;; ++seq) {
+  for (int seq = 0;;) {
     lds_wait(&l.ready, seq + 1);
     const DecDesc& d = l.desc[seq % DEC_DESCS];
     const int kind = uniform(d.kind);
     if (kind == U_EXIT) break;
     if (kind <= U_DOWN) {
-      const int at = uniform(d.at), mt = uniform(d.mt);
-      if (at == 1) {
-        Streamer<T, 1, 1> s;
-        s.run(l, seq, pos, ahead, prev_mt);
-      } else if (at == 2 && mt == 2) {
-        Streamer<T, 2, 2> s;
-        s.run(l, seq, pos, ahead, prev_mt);
-      } else if constexpr (DEC_PLANES<T> == 2) {
-        if (at == 2) {
-          Streamer<T, 2, 1> s;
-          s.run(l, seq, pos, ahead, prev_mt);
-        } else {
-          Streamer<T, 4, 2> s;
-          s.run(l, seq, pos, ahead, prev_mt);
+      if constexpr (DEC_PLANES<T> == 2 && !OWN) {
+        if (uniform(d.at) == 2) {
+          seq = stream_units<T, 2>(l, seq);
+          continue;
         }
       }
-      // (a ring of another slot size starts over; nothing is ahead in it)
-      if (ahead == 0) pos = 0;
-    } else {
-      if (kind == U_ROUTE) {
-        const int t = uniform(d.col) + wave;
-        if (t < a.T) decode_route_token<V>(a, t);
-        vm_drain<0>();
-      }
-      if (lane == 0) *(volatile int*)&l.parts[wave] = seq + 1;
+      seq = stream_units<T, 1>(l, seq);
+      continue;
     }
+    if constexpr (!OWN) {
+      const int t = uniform(d.col) + wave;
+      if (kind == U_ROUTE && t < a.T)
+        decode_route_token<V>(a, t, true, [&](int slot, int e, float gate) {
+          dev_store(a.idx + (long long)t * a.k + slot, e);
+          dev_store(a.gate + (long long)t * a.k + slot, gate);
+        });
+      vm_drain<0>();
+    }
+    if (lane == 0) lds_post(&l.parts[wave], seq + 1);
+    ++seq;
   }
 }
 
@@ -738,9 +763,10 @@ __device__ __forceinline__ void elem_store(void* p, long long i, float v) {
   else ((T*)p)[i] = v;
 }
 
-// y[t, h] = residual + shared + sum_j gate yp[t, j], in that order
-template <typename T>
-__device__ __forceinline__ void decode_sum(const DecArgs& a, int t, int h) {
+// y[t, h] = residual + shared + sum_j gate yp[t, j], in that order; pair(p)
+// gives a pair's expert and gate
+template <typename T, typename Pair>
+__device__ __forceinline__ void decode_sum(const DecArgs& a, int t, int h, Pair&& pair) {
   const long long at = (long long)t * a.H + h;
   float s = a.residual != nullptr ? elem_load<T>(a.residual, at) : 0.f;
   if (a.shared) s += a.yp[((long long)a.T * a.k + t) * a.H + h];
@@ -748,9 +774,12 @@ __device__ __forceinline__ void decode_sum(const DecArgs& a, int t, int h) {
     float gate[8], v[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const int p = t * a.k + min(j0 + q, a.k - 1), g = a.idx[p] - a.g0;
-      const bool in = j0 + q < a.k && g >= 0 && g < a.G;
-      gate[q] = in ? a.gate[p] : 0.f;
+      const int p = t * a.k + min(j0 + q, a.k - 1);
+      int e;
+      float w;
+      pair(p, e, w);
+      const bool in = j0 + q < a.k && e >= a.g0 && e - a.g0 < a.G;
+      gate[q] = in ? w : 0.f;
       v[q] = in ? a.yp[(long long)p * a.H + h] : 0.f;
     }
 #pragma unroll
@@ -764,8 +793,13 @@ __device__ __forceinline__ void decode_finish(const DecArgs& a, DecLds& l) {
   const int lane = threadIdx.x & 63, P = a.T * a.k;
   const bool fused = a.T <= DEC_FUSED_T;
   const long long plane = (long long)(P + a.T) * a.I;
+  const bool own = dec_own(a.T, a.k);
   auto sum_block = [&](int col) {
-    for (int t = lane >> 5; t < a.T; t += 2) decode_sum<T>(a, t, col + (lane & 31));
+    for (int t = lane >> 5; t < a.T; t += 2)
+      decode_sum<T>(a, t, col + (lane & 31), [&](int p, int& e, float& w) {
+        e = own ? (int)l.own_idx[p & (DEC_OWN_PAIRS - 1)] : a.idx[p];
+        w = own ? l.own_gate[p & (DEC_OWN_PAIRS - 1)] : a.gate[p];
+      });
   };
   for (int seq = 0;; ++seq) {
     lds_wait(&l.ready, seq + 1);
@@ -775,56 +809,48 @@ __device__ __forceinline__ void decode_finish(const DecArgs& a, DecLds& l) {
 #pragma unroll
     for (int w = 0; w < DEC_SW; ++w) lds_wait(&l.parts[w], seq + 1);
     if (kind <= U_DOWN) {
-      const int n = uniform(d.n), mt = uniform(d.mt);
+      const int n = uniform(d.n);
       const bool packed = uniform(d.packed);
-      float v[2][2][4];   // [row tile][weight tile][register]
+      float v[2][4];   // [weight tile][register]
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
-        if (m < mt) {
-          const int b = mt == 2 ? m : seq & 1;
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+        for (int q = 0; q < 4; ++q) {
+          float s = l.red[seq & 1][0][t * 256 + q * 64 + lane];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              float s = l.red[b][0][t * 256 + q * 64 + lane];
-#pragma unroll
-              for (int w = 1; w < DEC_SW; ++w) s += l.red[b][w][t * 256 + q * 64 + lane];
-              v[m][t][q] = s;
-            }
+          for (int w = 1; w < DEC_SW; ++w) s += l.red[seq & 1][w][t * 256 + q * 64 + lane];
+          v[t][q] = s;
         }
       lds_drain();
-      if (lane == 0) *(volatile int*)&l.taken = seq + 1;
+      if (lane == 0) lds_post(&l.taken, seq + 1);
       // register q: row 4 (lane / 16) + q, column lane % 16
       const int c = lane & 15;
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
-        if (m < mt)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float s0 = v[m][0][q], s1 = v[m][1][q];
-            if (packed) {   // rows 8-15: the low halves' part of rows 0-7
-              s0 += __shfl_xor(s0, 32, 64);
-              s1 += __shfl_xor(s1, 32, 64);
-            }
-            const int r = 16 * m + 4 * (lane >> 4) + q;
-            if (r >= n || (packed && lane >= 32)) continue;
-            const int row = d.rows[r];
-            if (kind == U_GATEUP) {
-              const float s = decode_swiglu(s0, s1);
-              const long long at = (long long)row * a.I + col + c;
-              if constexpr (sizeof(T) == 2) {
-                const uint32_t hi = f32_to_bf16(s);
-                dev_store((bf16_t*)a.act + at, hi);
-                dev_store((bf16_t*)a.act + plane + at, f32_to_bf16(s - bf16_to_f32(hi)));
-              } else {
-                dev_store((float*)a.act + at, s);
-              }
-            } else {
-              float* out = a.yp + (long long)row * a.H + col + c;
-              dev_store(out, s0);
-              dev_store(out + 16, s1);
-            }
+      for (int q = 0; q < 4; ++q) {
+        float s0 = v[0][q], s1 = v[1][q];
+        if (packed) {   // rows 8-15: the low halves' part of rows 0-7
+          s0 += __shfl_xor(s0, 32, 64);
+          s1 += __shfl_xor(s1, 32, 64);
+        }
+        const int r = 4 * (lane >> 4) + q;
+        if (r >= n || (packed && lane >= 32)) continue;
+        const int row = d.rows[r];
+        if (kind == U_GATEUP) {
+          const float s = decode_swiglu(s0, s1);
+          const long long at = (long long)row * a.I + col + c;
+          if constexpr (sizeof(T) == 2) {
+            const uint32_t hi = f32_to_bf16(s);
+            dev_store((bf16_t*)a.act + at, hi);
+            dev_store((bf16_t*)a.act + plane + at, f32_to_bf16(s - bf16_to_f32(hi)));
+          } else {
+            dev_store((float*)a.act + at, s);
           }
+        } else {
+          float* out = a.yp + (long long)row * a.H + col + c;
+          dev_store(out, s0);
+          dev_store(out + 16, s1);
+        }
+      }
       vm_drain<0>();   // the stores are out: the unit counts
       if (kind == U_GATEUP) {
         if (lane == 0) dev_add(a.act_done + uniform(d.slot), 1);
@@ -839,25 +865,38 @@ __device__ __forceinline__ void decode_finish(const DecArgs& a, DecLds& l) {
         }
       }
     } else {
-      if (lane == 0) *(volatile int*)&l.taken = seq + 1;
+      if (lane == 0) lds_post(&l.taken, seq + 1);
       if (kind == U_ROUTE) {
         if (lane == 0) dev_add(a.routed, min(DEC_SW, a.T - col));
       } else {
         sum_block(col);
       }
     }
-    if (lane == 0) *(volatile int*)&l.done = seq + 1;
+    if (lane == 0) lds_post(&l.done, seq + 1);
   }
 }
 
-template <typename T, int V>
+template <typename T, int V, bool OWN>
 __global__ __launch_bounds__(DEC_NT) void decode_kernel(DecArgs a) {
   __shared__ __attribute__((aligned(1024))) DecLds l;
   if (threadIdx.x < DEC_SW) l.parts[threadIdx.x] = 0;
-  if (threadIdx.x == 0) l.ready = l.taken = l.done = 0;
-  __syncthreads();
+  if (threadIdx.x == 0) l.ready = l.a_ready = l.taken = l.done = 0;
   const int wave = uniform((int)(threadIdx.x >> 6));
-  if (wave < DEC_SW) decode_stream<T, V>(a, l);
+  if (OWN && wave < DEC_SW) {
+    const bool keep = blockIdx.x == 0;   // (one of them writes the choices out)
+    for (int t = wave; t < a.T; t += DEC_SW)
+      decode_route_token<V>(a, t, keep, [&](int slot, int e, float gate) {
+        const int p = t * a.k + slot;
+        l.own_idx[p & (DEC_OWN_PAIRS - 1)] = (int16_t)e;
+        l.own_gate[p & (DEC_OWN_PAIRS - 1)] = gate;
+        if (keep) {
+          a.idx[p] = e;
+          a.gate[p] = gate;
+        }
+      });
+  }
+  __syncthreads();
+  if (wave < DEC_SW) decode_stream<T, V, OWN>(a, l);
   else if (wave == DEC_SW) decode_schedule<T>(l);
   else decode_finish<T>(a, l);
 }
@@ -866,7 +905,11 @@ __global__ __launch_bounds__(DEC_NT) void decode_kernel(DecArgs a) {
 template <typename T>
 __global__ __launch_bounds__(256) void decode_sum_kernel(DecArgs a) {
   const int h = blockIdx.x * 256 + threadIdx.x;
-  if (h < a.H) decode_sum<T>(a, blockIdx.y, h);
+  if (h < a.H)
+    decode_sum<T>(a, blockIdx.y, h, [&](int p, int& e, float& w) {
+      e = a.idx[p];
+      w = a.gate[p];
+    });
 }
 
 // ---------------------------------------------------------------- host side
@@ -891,8 +934,8 @@ DecWs decode_ws(int T, int H, int I, int E, int k) {
   DecWs w;
   const size_t rows = (size_t)T * k + T;
   // 16 ints for the two scalars, one per expert of the window and the shared
-  // one, one per column block
-  w.n_count = 16 + E + 1 + H / DEC_DN;
+  // one, one per column block, a cache line per workgroup
+  w.n_count = (16 + E + 1 + H / DEC_DN + 31) / 32 * 32 + 32 * moe_cu_count();
   w.count = 0;
   w.part = w.count + round256((size_t)w.n_count * 4);
   w.act = w.part + round256((size_t)router_slices(H, E) * T * E * 8);
@@ -940,12 +983,17 @@ int decode_launch(const DecArgs& a, hipStream_t s, const char* fn) {
   const long long units = experts * (a.I / DEC_GU + a.H / DEC_DN) + a.H / DEC_DN;
   const int cus = moe_cu_count();
   const dim3 grid((unsigned)(units < cus ? units : cus)), block(DEC_NT);
-  switch (route_width(a.E)) {
-    case 1: hipLaunchKernelGGL((decode_kernel<T, 1>), grid, block, 0, s, a); break;
-    case 2: hipLaunchKernelGGL((decode_kernel<T, 2>), grid, block, 0, s, a); break;
-    case 4: hipLaunchKernelGGL((decode_kernel<T, 4>), grid, block, 0, s, a); break;
-    default: hipLaunchKernelGGL((decode_kernel<T, 16>), grid, block, 0, s, a); break;
-  }
+  auto launch = [&](auto own) {
+    constexpr bool OWN = decltype(own)::value;
+    switch (route_width(a.E)) {
+      case 1: hipLaunchKernelGGL((decode_kernel<T, 1, OWN>), grid, block, 0, s, a); break;
+      case 2: hipLaunchKernelGGL((decode_kernel<T, 2, OWN>), grid, block, 0, s, a); break;
+      case 4: hipLaunchKernelGGL((decode_kernel<T, 4, OWN>), grid, block, 0, s, a); break;
+      default: hipLaunchKernelGGL((decode_kernel<T, 16, OWN>), grid, block, 0, s, a); break;
+    }
+  };
+  if (dec_own(a.T, a.k)) launch(std::true_type{});
+  else launch(std::false_type{});
   MOE_TRY(moe_check_launch(fn));
   if (a.T <= DEC_FUSED_T) return MOE_OK;
   hipLaunchKernelGGL(decode_sum_kernel<T>, dim3((a.H + 255) / 256, a.T), dim3(256), 0, s, a);
@@ -1009,6 +1057,7 @@ extern "C" int moe_decode(const void* x, int dt, const float* wg, const float* b
   a.routed = a.next + 8;
   a.act_done = a.next + 16;
   a.col_done = a.act_done + E + 1;
+  a.go = a.next + (16 + E + 1 + H / DEC_DN + 31) / 32 * 32;
   a.part = (double*)((char*)ws + w.part);
   a.act = (char*)ws + w.act;
   a.yp = (float*)((char*)ws + w.yp);

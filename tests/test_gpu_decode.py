@@ -66,9 +66,10 @@ CASES = [
     (64, 512, 64, 9, 3, {"g0": 2, "G": 4, "residual": True}),
     (65, 128, 128, 4, 4, {}),
     (128, 256, 192, 12, 6, {"shared": True, "residual": True}),
-    (128, 192, 64, 33, 32, {}),                       # the most pairs
+    (128, 192, 64, 33, 16, {}),                       # the most pairs
+    (8, 128, 64, 300, 256, {}),                       # as many of few tokens
     (100, 64, 64, 40, 2, {"dt": F32, "g0": 39, "G": 1}),
-    (4, 64, 64, 1024, 1024, {}),                      # every expert chosen
+    (2, 64, 64, 1024, 1024, {}),                      # every expert chosen
     (9, 128, 64, 1000, 7, {"g0": 0, "G": 1}),
     (3, 128, 64, 8, 2, {"G": 0, "shared": True}),     # no routed expert on this device
     (3, 128, 64, 8, 2, {"G": 0, "residual": True}),
