@@ -40,6 +40,7 @@ typedef double f64x4 __attribute__((ext_vector_type(4)));
 struct DecArgs {
   const void* x; const float* wg; const float* bias;
   int T, H, I, E, k, g0, G, shared;
+  int gu_tiles;       // row tiles of a gate/up unit: 1 or 2
   const void* w13; const void* w2; const void* ws13; const void* ws2; const void* residual;
   float* logits; int32_t* idx; float* gate; void* y;
   int S;              // K slices of the router product (0: logits are an input)
@@ -214,7 +215,8 @@ __device__ __forceinline__ void decode_route_token(const DecArgs& a, int t, bool
 // barrier, so the stream of weights does not stop between units.
 //
 // Streaming.  A unit is 32 weight rows (two 16-row tiles) times at most 16
-// rows of the other operand.  K runs in steps of 128 bytes of a row (64 bf16,
+// rows of the other operand (32 in the gate/up units of calls whose experts
+// have many rows: each unit reads its weights again).  K runs in steps of 128 bytes of a row (64 bf16,
 // 32 fp32) dealt to the four waves in turn; a step's weights and operand rows
 // go HBM -> LDS in 1 KB copies (lds_copy.hpp) into a ring that belongs to the
 // wave alone, several steps ahead.  A copy covers 8 whole 128-byte lines: read
@@ -239,7 +241,7 @@ __device__ __forceinline__ void decode_route_token(const DecArgs& a, int t, bool
 // lowest unfinished unit never waits: no residency of the grid is assumed.
 // For few tokens every workgroup routes them itself (they cost each about a
 // microsecond) instead of waiting for the one that would.
-constexpr int DEC_ROWS = 16;         // operand rows of a unit
+constexpr int DEC_ROWS = 16;         // operand rows of a tile; of a unit, but for gate/up ones of 32
 constexpr int DEC_DESCS = 4;
 constexpr int DEC_PAGE = 2048;       // a 16-row tile of a step
 constexpr int DEC_PAGES = 16;        // of a streaming wave's ring
@@ -249,34 +251,42 @@ constexpr unsigned long long DEC_WAIT_TICKS = 100000000ull;   // 1 s of the 100 
 
 enum { U_GATEUP = 0, U_DOWN = 1, U_ROUTE = 2, U_SUM = 3, U_EXIT = 4 };
 
+// words of a descriptor (a wave reads them all at once, one a lane)
+enum {
+  W_KIND = 0,
+  W_AT,                  // A tiles (operand copies of 16 rows)
+  W_MT,                  // row tiles of the result
+  W_PACKED,              // rows 8-15 are the low halves of rows 0-7
+  W_STEPS,               // K steps of 128 bytes
+  W_N,                   // rows
+  W_SLOT,                // counter the unit raises (expert, or column block)
+  W_COL,                 // first gate/up or output column
+  W_WLO, W_WHI, W_WBYTES,   // weights: address and extent
+  W_ALO, W_AHI, W_ABYTES,   // and the A operand's
+  W_LDW, W_TILE1,        // bytes of a weight row, and from the first tile to the second
+  W_WORDS = 16           // (all of them)
+};
+
 struct DecDesc {
-  int kind, at;                // A tiles (operand copies of 16 rows)
-  int packed;                  // rows 8-15 are the low halves of rows 0-7
-  int steps;                   // K steps of 128 bytes
-  int n;                       // rows
-  int slot;                    // counter the unit raises (expert, or column block)
-  int col;                     // first gate/up or output column
-  unsigned long long w, a;     // operand addresses
-  uint32_t wbytes, abytes;     // and extents
-  int ldw, tile1;              // bytes of a weight row, and from the first tile to the second
+  int word[W_WORDS];
   uint32_t arow[2 * 16];       // byte offset of each A row
-  int rows[DEC_ROWS];          // pair indices, or T k + token
+  int rows[2 * DEC_ROWS];      // pair indices, or T k + token
 };
 
 struct DecLds {
   char ring[DEC_SW][DEC_PAGES * DEC_PAGE];
-  float red[2][DEC_SW][2 * 256];   // partial tiles, of units of even and of odd number
+  float red[2][DEC_SW][2 * 256];   // partial tiles, of units of even and of odd number (units of
+                                   // two row tiles take both)
   int16_t order[DEC_MAX_PAIRS];    // pairs of the window, expert by expert
-  int cur[(MOE_MAX_E + 1) / 2];    // (while that is built: two counters a word)
+  int cur[(MOE_MAX_E + 3) / 2];    // while that is built: two counters a word; then pre_g
   int16_t list[MOE_MAX_E + 1];     // experts some token chose, ascending; the shared one first (-1)
   int16_t first[MOE_MAX_E + 2];    // their places in order
-  int16_t pre[MOE_MAX_E + 2];      // row blocks before each
+  int16_t pre[MOE_MAX_E + 2];      // row blocks before each, of second-product units
   int16_t own_idx[DEC_OWN_PAIRS];  // choices and gates, where every workgroup routes itself
   float own_gate[DEC_OWN_PAIRS];
   DecDesc desc[DEC_DESCS];
   // words the waves meet in
-  int ready;                       // descriptors written
-  int a_ready;                     // units whose A operand is there
+  int ready;                       // descriptors written, their A operands there
   int parts[DEC_SW];               // units whose partial tiles each streaming wave has left
   int taken;                       // units whose partial tiles were read
   int done;                        // units finished
@@ -303,8 +313,10 @@ __device__ __forceinline__ void vm_drain() {    // all but n of its memory opera
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(n) : "memory");
 }
 
-// row blocks of an expert with m rows
-__device__ __forceinline__ int row_blocks(int m) { return (m + DEC_ROWS - 1) / DEC_ROWS; }
+// row blocks of an expert with m rows, in units of `tiles` row tiles
+__device__ __forceinline__ int row_blocks(int m, int tiles) {
+  return (m + DEC_ROWS * tiles - 1) >> (tiles == 2 ? 5 : 4);
+}
 
 template <typename T> constexpr int DEC_PLANES = sizeof(T) == 2 ? 2 : 1;
 
@@ -356,13 +368,13 @@ __device__ __forceinline__ int decode_tables(DecConst& a, DecLds& l) {
       l.pre[0] = 0;
     }
     n = 1;
-    blocks = row_blocks(a.T);
+    blocks = row_blocks(a.T, 1);
   }
   for (int g0 = 0; g0 < a.G; g0 += 64) {
     const int g = g0 + lane;
     const int m = g < a.G ? (l.cur[g >> 1] >> ((g & 1) * 16)) & 0xffff : 0;
     const unsigned long long b = __ballot(m > 0);
-    int incl = m | row_blocks(m) << 16;   // both sums at once
+    int incl = m | row_blocks(m, 1) << 16;   // both sums at once
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
       const int v = __shfl_up(incl, o, 64);
@@ -372,7 +384,7 @@ __device__ __forceinline__ int decode_tables(DecConst& a, DecLds& l) {
       const int at = n + __popcll(b & ((1ull << lane) - 1));
       l.list[at] = (int16_t)g;
       l.first[at] = (int16_t)(rows + (incl & 0xffff) - m);
-      l.pre[at] = (int16_t)(blocks + (incl >> 16) - row_blocks(m));
+      l.pre[at] = (int16_t)(blocks + (incl >> 16) - row_blocks(m, 1));
       add(g, rows + (incl & 0xffff) - 2 * m);   // m counted there -> its first place
     }
     const int all = __shfl(incl, 63, 64);
@@ -387,6 +399,22 @@ __device__ __forceinline__ int decode_tables(DecConst& a, DecLds& l) {
   }
   lds_drain();
   pairs([&](int p, int g) { l.order[add(g, 1)] = (int16_t)p; });
+  // row blocks of gate/up units before each (the counters are done with)
+  int16_t* const pre_g = (int16_t*)l.cur;
+  int before = 0;
+  for (int s0 = 0; s0 <= n; s0 += 64) {
+    const int s = s0 + lane;
+    const int m = s >= n ? 0 : (a.shared && s == 0) ? a.T : l.first[s + 1] - l.first[s];
+    int incl = row_blocks(m, a.gu_tiles);
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(incl, o, 64);
+      if (lane >= o) incl += v;
+    }
+    if (s <= n) pre_g[s] = (int16_t)(before + incl - row_blocks(m, a.gu_tiles));
+    before += __shfl(incl, 63, 64);
+  }
+  lds_drain();
   return n;
 }
 
@@ -395,7 +423,8 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
   constexpr int ES = sizeof(T), PL = DEC_PLANES<T>;
   const int lane = threadIdx.x & 63;
   DecConst* args = (DecConst*)__builtin_amdgcn_kernarg_segment_ptr();
-  int n_list = -1, blocks = 0;
+  int n_list = -1, n_gu = 0, n_dn = 0;
+  const int16_t* const pre_g = (const int16_t*)l.cur;
   bool go = false;       // the activations are complete
   bool lost = false;     // a wait took a second (calls that share a workspace): wait no more
   auto draw = [&]() {
@@ -418,7 +447,7 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
     const int P = a.T * a.k;
     const int n_route = dec_own(a.T, a.k) ? 0 : (a.T + DEC_SW - 1) / DEC_SW;
     const int per_g = a.I / DEC_GU, per_d = a.H / DEC_DN;
-    const int n_shared = a.shared ? row_blocks(a.T) * per_g : 0;
+    const int n_shared = a.shared ? row_blocks(a.T, a.gu_tiles) * per_g : 0;
     lds_wait(&l.done, seq - DEC_DESCS + 1);   // the descriptor's last user is through
     DecDesc& d = l.desc[seq % DEC_DESCS];
     int kind, g = -2, s = 0, rb = 0, col = 0;
@@ -427,7 +456,7 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
       col = u * DEC_SW;
     } else if (u < n_route + n_shared) {
       // (the shared expert needs no routing)
-      const int v = u - n_route, nb = row_blocks(a.T);
+      const int v = u - n_route, nb = row_blocks(a.T, a.gu_tiles);
       kind = U_GATEUP;
       g = -1;
       rb = v % nb;
@@ -443,26 +472,27 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
           __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
         }
         n_list = decode_tables(a, l);
-        blocks = lds_peek(&l.per_col);
+        n_gu = pre_g[n_list] * per_g;
+        n_dn = l.pre[n_list] * per_d;
       }
       int v = u - n_route;
-      const int n_gu = blocks * per_g, n_dn = blocks * per_d;
       if (v < n_gu + n_dn) {
         kind = v < n_gu ? U_GATEUP : U_DOWN;
         const int per = v < n_gu ? per_g : per_d;
+        const int16_t* const pre = v < n_gu ? pre_g : l.pre;
         if (v >= n_gu) v -= n_gu;
         // place in the list: the last with pre * per <= v
         for (int s0 = 0; s0 < n_list; s0 += 64) {
           const unsigned long long le =
-              __ballot(s0 + lane < n_list && l.pre[s0 + lane] * per <= v);
+              __ballot(s0 + lane < n_list && pre[s0 + lane] * per <= v);
           if (le) s = s0 + 63 - __builtin_clzll(le);
         }
         g = l.list[s];
-        const int nb = l.pre[s + 1] - l.pre[s];
-        v -= l.pre[s] * per;
+        const int nb = pre[s + 1] - pre[s];
+        v -= pre[s] * per;
         rb = v % nb;
         col = v / nb * (kind == U_GATEUP ? DEC_GU : DEC_DN);
-      } else if (blocks == 0 && v < per_d && a.T <= DEC_FUSED_T) {
+      } else if (n_dn == 0 && v < per_d && a.T <= DEC_FUSED_T) {
         kind = U_SUM;    // nothing but the residual
         col = v * DEC_DN;
       } else {
@@ -470,26 +500,26 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
       }
     }
     if (kind <= U_DOWN) {
-      const int r0 = rb * DEC_ROWS;
+      const bool down = kind == U_DOWN;
+      const int mt = down ? 1 : a.gu_tiles, most = DEC_ROWS * mt, r0 = rb * most;
       int n, row = 0;
       if (g < 0) {
-        n = min(DEC_ROWS, a.T - r0);
+        n = min(most, a.T - r0);
         row = P + r0 + min(lane, n - 1);
       } else {
         const int f = l.first[s] + r0;
-        n = min(DEC_ROWS, l.first[s + 1] - f);
+        n = min(most, l.first[s + 1] - f);
         row = l.order[f + min(lane, n - 1)];
       }
       if (lane < n) d.rows[lane] = row;
-      const bool down = kind == U_DOWN;
       // (packed or not goes by the call: one number of tiles all through a phase)
       const bool two = down && PL == 2;
       const bool packed = two && a.T <= 8;
-      const int at = two && !packed ? 2 : 1;
+      const int at = two && !packed ? 2 : mt;
       const uint32_t plane = (uint32_t)(P + a.T) * (uint32_t)(a.I * ES);
       // A row `lane`: packed tiles hold the high halves in rows 0-7 and the low
       // ones in rows 8-15; else the tile of the low halves follows
-      const int per_plane = packed ? 8 : 16;
+      const int per_plane = packed ? 8 : 16 * mt;
       // (padding rows lie out of range: they read as zeros and move nothing)
       const int mine = __shfl(row, min(lane % per_plane, n - 1), 64);
       const int tok = mine >= P ? mine - P : mine / a.k;
@@ -497,30 +527,36 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
         d.arow[lane] = lane % per_plane >= n ? STREAM_OOB
                        : down ? (uint32_t)mine * (uint32_t)(a.I * ES) + lane / per_plane * plane
                               : (uint32_t)tok * (uint32_t)(a.H * ES);
+      const long long ld = (long long)(down ? a.I : a.H) * ES;
+      const char* base =
+          down ? (g < 0 ? (const char*)a.ws2 : (const char*)a.w2 + (long long)g * a.H * ld)
+               : (g < 0 ? (const char*)a.ws13 : (const char*)a.w13 + (long long)g * 2 * a.I * ld);
+      const unsigned long long w = (unsigned long long)(base + col * ld);
+      const unsigned long long x = (unsigned long long)(down ? a.act : a.x);
       if (lane == 0) {
-        d.at = at;
-        d.packed = packed;
-        d.n = n;
-        const long long ld = (long long)(down ? a.I : a.H) * ES;
-        d.steps = (int)(ld / 128);
-        d.slot = down ? col / DEC_DN : (g < 0 ? a.G : g);
-        const char* base =
-            down ? (g < 0 ? (const char*)a.ws2 : (const char*)a.w2 + (long long)g * a.H * ld)
-                 : (g < 0 ? (const char*)a.ws13 : (const char*)a.w13 + (long long)g * 2 * a.I * ld);
-        d.w = (unsigned long long)(base + col * ld);
-        d.tile1 = (int)((down ? 16 : a.I) * ld);
-        d.wbytes = (uint32_t)((down ? DEC_DN : a.I + DEC_GU) * ld);
-        d.ldw = (int)ld;
-        d.a = (unsigned long long)(down ? a.act : a.x);
-        d.abytes = down ? plane * PL : (uint32_t)(a.T * a.H * ES);
+        d.word[W_AT] = at;
+        d.word[W_MT] = mt;
+        d.word[W_PACKED] = packed;
+        d.word[W_STEPS] = (int)(ld / 128);
+        d.word[W_N] = n;
+        d.word[W_SLOT] = down ? col / DEC_DN : (g < 0 ? a.G : g);
+        d.word[W_WLO] = (int)(uint32_t)w;
+        d.word[W_WHI] = (int)(w >> 32) & 0xffff;
+        d.word[W_WBYTES] = (int)((down ? DEC_DN : a.I + DEC_GU) * ld);
+        d.word[W_ALO] = (int)(uint32_t)x;
+        d.word[W_AHI] = (int)(x >> 32) & 0xffff;
+        d.word[W_ABYTES] = (int)(down ? plane * PL : (uint32_t)(a.T * a.H * ES));
+        d.word[W_LDW] = (int)ld;
+        d.word[W_TILE1] = (int)((down ? 16 : a.I) * ld);
       }
     }
     if (lane == 0) {
-      d.kind = kind;
-      d.col = col;
+      d.word[W_KIND] = kind;
+      d.word[W_COL] = col;
     }
     lds_drain();
-    if (lane == 0) lds_post(&l.ready, seq + 1);
+    const bool wait = kind == U_DOWN && !go;
+    if (lane == 0 && !wait) lds_post(&l.ready, seq + 1);
     if (uniform(kind) == U_EXIT) break;
     held = seq == 0 ? draw() : held2;
     held2 = draw();
@@ -529,16 +565,16 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
     // at a look) and tells each of the others on a line of its own: 256 of them
     // watching the same lines took so long for every look that the copies
     // queued behind it in their CUs' memory pipelines stood still.
-    if (kind == U_DOWN && !go) {
+    if (wait) {
       const unsigned long long t0 = wall_clock64();
-      if (u == n_route + blocks * per_g) {
+      if (u == n_route + n_gu) {
         int known = 0;
         while (known < n_list && !lost) {
           const int q = known + lane;
           bool there = false;
           if (q < n_list) {
             const int gq = l.list[q];
-            there = dev_load(a.act_done + (gq < 0 ? a.G : gq)) >= (l.pre[q + 1] - l.pre[q]) * per_g;
+            there = dev_load(a.act_done + (gq < 0 ? a.G : gq)) >= (pre_g[q + 1] - pre_g[q]) * per_g;
           }
           const unsigned long long no = ~__ballot(there);
           known += no ? __builtin_ctzll(no) : 64;
@@ -553,25 +589,12 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
       go = true;
+      if (lane == 0) lds_post(&l.ready, seq + 1);
     }
-    if (lane == 0) lds_post(&l.a_ready, seq + 1);
   }
 }
 
 // ---- the streaming waves
-
-// descriptor words of an operand (the last one is the same for all)
-struct StreamBase {
-  int lo, hi, bytes;
-  __device__ __forceinline__ void set(unsigned long long p, uint32_t n) {
-    lo = uniform((int)(uint32_t)p);
-    hi = uniform((int)((p >> 32) & 0xffffu));
-    bytes = uniform((int)n);
-  }
-  __device__ __forceinline__ i32x4 rsrc() const {
-    return i32x4{uniform(lo), uniform(hi), uniform(bytes), MOE_RSRC_DW3};
-  }
-};
 
 // 1 KB of a step, W with the streaming policy: it is read once
 __device__ __forceinline__ void dma16_nt(const i32x4& rs, uint32_t lds, uint32_t voff, int soff) {
@@ -582,11 +605,12 @@ __device__ __forceinline__ void dma16_nt(const i32x4& rs, uint32_t lds, uint32_t
 }
 
 // The flat stream of one streaming wave over the units from seq on that have AT
-// A tiles each; returns the number of the first unit that has not.  Steps are
+// A tiles each, feeding MT row tiles of the result (A tile i adds to row tile
+// i % MT); returns the number of the first unit that has not.  Steps are
 // counted as they are copied (`put`) and read (`got`); a unit's tile is complete
 // when got reaches the put at which its last step was copied.  The copies are
 // at most one unit ahead.
-template <typename T, int AT>
+template <typename T, int AT, int MT>
 __device__ __forceinline__ int stream_units(DecLds& l, int seq) {
   constexpr int SIZE = 2 + AT, OPS = 4 + 2 * AT, D = DEC_PAGES / SIZE;
   constexpr int NEVER = 0x7fffffff;
@@ -596,7 +620,7 @@ __device__ __forceinline__ int stream_units(DecLds& l, int seq) {
   // the unit being copied
   int at_unit = seq - 1, left = 0, end = NEVER;
   bool stop = false;
-  StreamBase bw = {0, 0, 0}, ba = {0, 0, 0};
+  int wlo = 0, whi = 0, wbytes = 0, alo = 0, ahi = 0, abytes = 0;
   uint32_t wo[2] = {0, 0}, ao[2 * AT];
 #pragma unroll
   for (int j = 0; j < 2 * AT; ++j) ao[j] = 0;
@@ -612,27 +636,31 @@ __device__ __forceinline__ int stream_units(DecLds& l, int seq) {
     if (u > seq + 1 || stop || uniform(lds_peek(&l.ready)) <= u) return;
     asm volatile("" ::: "memory");
     const DecDesc& d = l.desc[u % DEC_DESCS];
-    if (uniform(d.kind) > U_DOWN || uniform(d.at) != AT) {
-      stop = true;
-      return;
-    }
-    if (uniform(lds_peek(&l.a_ready)) <= u) return;
-    asm volatile("" ::: "memory");
-    bw.set(d.w, d.wbytes);
-    ba.set(d.a, d.abytes);
-    tile1 = uniform(d.tile1);
-    left = (uniform(d.steps) - wave + DEC_SW - 1) / DEC_SW;
-    k = wave * 128;
-    const int ldw = uniform(d.ldw);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int r = 8 * j + (lane >> 3);
-      wo[j] = (uint32_t)(r * ldw + (((lane & 7) ^ ((r >> 1) & 7)) << 4));
-    }
+    const int word = d.word[lane % W_WORDS];
 #pragma unroll
     for (int j = 0; j < 2 * AT; ++j) {
       const int r = 8 * j + (lane >> 3);
       ao[j] = d.arow[r] + (uint32_t)(((lane & 7) ^ ((r >> 1) & 7)) << 4);
+    }
+    auto w = [&](int i) { return __builtin_amdgcn_readlane(word, i); };
+    if (w(W_KIND) > U_DOWN || w(W_AT) != AT || w(W_MT) != MT) {
+      stop = true;
+      return;
+    }
+    wlo = w(W_WLO);
+    whi = w(W_WHI);
+    wbytes = w(W_WBYTES);
+    alo = w(W_ALO);
+    ahi = w(W_AHI);
+    abytes = w(W_ABYTES);
+    tile1 = w(W_TILE1);
+    left = uniform((w(W_STEPS) - wave + DEC_SW - 1) / DEC_SW);
+    k = wave * 128;
+    const int ldw = w(W_LDW);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int r = 8 * j + (lane >> 3);
+      wo[j] = (uint32_t)(r * ldw + (((lane & 7) ^ ((r >> 1) & 7)) << 4));
     }
     at_unit = u;
     end = put + left;
@@ -641,8 +669,8 @@ __device__ __forceinline__ int stream_units(DecLds& l, int seq) {
   auto copy = [&]() {
     if (left == 0) bind();
     const int live = uniform(left > 0 ? -1 : 0);
-    const i32x4 rw = {uniform(bw.lo), uniform(bw.hi), uniform(bw.bytes & live), MOE_RSRC_DW3};
-    const i32x4 ra = {uniform(ba.lo), uniform(ba.hi), uniform(ba.bytes & live), MOE_RSRC_DW3};
+    const i32x4 rw = {uniform(wlo), uniform(whi), uniform(wbytes & live), MOE_RSRC_DW3};
+    const i32x4 ra = {uniform(alo), uniform(ahi), uniform(abytes & live), MOE_RSRC_DW3};
     const uint32_t p = (uint32_t)uniform((int)(lds + wslot));
     const int k0 = uniform(k & live), k1 = uniform((k + tile1) & live);
     dma16_nt(rw, p, wo[0], k0);
@@ -657,8 +685,10 @@ __device__ __forceinline__ int stream_units(DecLds& l, int seq) {
     left = uniform(left + live);
     ++put;
   };
-  f32x4 acc[2];
-  acc[0] = acc[1] = f32x4{0, 0, 0, 0};
+  f32x4 acc[MT][2];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = f32x4{0, 0, 0, 0};
+  lds_wait(&l.taken, seq);         // (units of another kind may have used all of red)
   // byte of this lane's 16 in a page, for the two halves of a step
   const int r = lane & 15, kg = lane >> 4;
   const int f0 = r * 128 + (((kg) ^ ((r >> 1) & 7)) << 4);
@@ -687,19 +717,22 @@ __device__ __forceinline__ int stream_units(DecLds& l, int seq) {
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int t = 0; t < AT; ++t) {
-        acc[0] = stream_mma(x[h][t], w[h][0], acc[0], T());
-        acc[1] = stream_mma(x[h][t], w[h][1], acc[1], T());
+        acc[t % MT][0] = stream_mma(x[h][t], w[h][0], acc[t % MT][0], T());
+        acc[t % MT][1] = stream_mma(x[h][t], w[h][1], acc[t % MT][1], T());
       }
     lds_drain();                   // the slot is read
     if (got >= got_end) {
       // (>: a unit without steps of this wave ends where it was bound)
-      lds_wait(&l.taken, seq - 1);
-      float* red = l.red[seq & 1][wave];
+      lds_wait(&l.taken, MT == 2 ? seq : seq - 1);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+      for (int m = 0; m < MT; ++m) {
+        float* red = l.red[MT == 2 ? m : seq & 1][wave];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) red[t * 256 + q * 64 + lane] = acc[t][q];
-        acc[t] = f32x4{0, 0, 0, 0};
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) red[t * 256 + q * 64 + lane] = acc[m][t][q];
+          acc[m][t] = f32x4{0, 0, 0, 0};
+        }
       }
       lds_drain();
       if (lane == 0) lds_post(&l.parts[wave], seq + 1);
@@ -718,20 +751,25 @@ __device__ __forceinline__ void decode_stream(const DecArgs& a, DecLds& l) {
   for (int seq = 0;;) {
     lds_wait(&l.ready, seq + 1);
     const DecDesc& d = l.desc[seq % DEC_DESCS];
-    const int kind = uniform(d.kind);
+    const int kind = uniform(d.word[W_KIND]);
     if (kind == U_EXIT) break;
     if (kind <= U_DOWN) {
-      if constexpr (DEC_PLANES<T> == 2 && !OWN) {
-        if (uniform(d.at) == 2) {
-          seq = stream_units<T, 2>(l, seq);
+      if constexpr (!OWN) {
+        if (uniform(d.word[W_MT]) == 2) {
+          seq = stream_units<T, 2, 2>(l, seq);
           continue;
         }
+        if constexpr (DEC_PLANES<T> == 2)
+          if (uniform(d.word[W_AT]) == 2) {
+            seq = stream_units<T, 2, 1>(l, seq);
+            continue;
+          }
       }
-      seq = stream_units<T, 1>(l, seq);
+      seq = stream_units<T, 1, 1>(l, seq);
       continue;
     }
     if constexpr (!OWN) {
-      const int t = uniform(d.col) + wave;
+      const int t = uniform(d.word[W_COL]) + wave;
       if (kind == U_ROUTE && t < a.T)
         decode_route_token<V>(a, t, true, [&](int slot, int e, float gate) {
           dev_store(a.idx + (long long)t * a.k + slot, e);
@@ -804,60 +842,71 @@ __device__ __forceinline__ void decode_finish(const DecArgs& a, DecLds& l) {
   for (int seq = 0;; ++seq) {
     lds_wait(&l.ready, seq + 1);
     const DecDesc& d = l.desc[seq % DEC_DESCS];
-    const int kind = uniform(d.kind), col = uniform(d.col);
+    const int word = d.word[lane % W_WORDS];
+    auto w = [&](int i) { return __builtin_amdgcn_readlane(word, i); };
+    const int kind = w(W_KIND), col = w(W_COL);
     if (kind == U_EXIT) break;
 #pragma unroll
     for (int w = 0; w < DEC_SW; ++w) lds_wait(&l.parts[w], seq + 1);
     if (kind <= U_DOWN) {
-      const int n = uniform(d.n);
-      const bool packed = uniform(d.packed);
-      float v[2][4];   // [weight tile][register]
+      const int n = w(W_N);
+      const bool packed = w(W_PACKED);
+      const int mt = w(W_MT);
+      float v[2][2][4];   // [row tile][weight tile][register]
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int m = 0; m < 2; ++m)
+        if (m < mt) {
+          const int b = mt == 2 ? m : seq & 1;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float s = l.red[seq & 1][0][t * 256 + q * 64 + lane];
+          for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int w = 1; w < DEC_SW; ++w) s += l.red[seq & 1][w][t * 256 + q * 64 + lane];
-          v[t][q] = s;
+            for (int q = 0; q < 4; ++q) {
+              float s = l.red[b][0][t * 256 + q * 64 + lane];
+#pragma unroll
+              for (int z = 1; z < DEC_SW; ++z) s += l.red[b][z][t * 256 + q * 64 + lane];
+              v[m][t][q] = s;
+            }
         }
       lds_drain();
       if (lane == 0) lds_post(&l.taken, seq + 1);
       // register q: row 4 (lane / 16) + q, column lane % 16
       const int c = lane & 15;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float s0 = v[0][q], s1 = v[1][q];
-        if (packed) {   // rows 8-15: the low halves' part of rows 0-7
-          s0 += __shfl_xor(s0, 32, 64);
-          s1 += __shfl_xor(s1, 32, 64);
-        }
-        const int r = 4 * (lane >> 4) + q;
-        if (r >= n || (packed && lane >= 32)) continue;
-        const int row = d.rows[r];
-        if (kind == U_GATEUP) {
-          const float s = decode_swiglu(s0, s1);
-          const long long at = (long long)row * a.I + col + c;
-          if constexpr (sizeof(T) == 2) {
-            const uint32_t hi = f32_to_bf16(s);
-            dev_store((bf16_t*)a.act + at, hi);
-            dev_store((bf16_t*)a.act + plane + at, f32_to_bf16(s - bf16_to_f32(hi)));
-          } else {
-            dev_store((float*)a.act + at, s);
+      for (int m = 0; m < 2; ++m)
+        if (m < mt)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float s0 = v[m][0][q], s1 = v[m][1][q];
+            if (packed) {   // rows 8-15: the low halves' part of rows 0-7
+              s0 += __shfl_xor(s0, 32, 64);
+              s1 += __shfl_xor(s1, 32, 64);
+            }
+            const int r = 16 * m + 4 * (lane >> 4) + q;
+            if (r >= n || (packed && lane >= 32)) continue;
+            const int row = d.rows[r];
+            if (kind == U_GATEUP) {
+              const float s = decode_swiglu(s0, s1);
+              const long long at = (long long)row * a.I + col + c;
+              if constexpr (sizeof(T) == 2) {
+                const uint32_t hi = f32_to_bf16(s);
+                dev_store((bf16_t*)a.act + at, hi);
+                dev_store((bf16_t*)a.act + plane + at, f32_to_bf16(s - bf16_to_f32(hi)));
+              } else {
+                dev_store((float*)a.act + at, s);
+              }
+            } else {
+              float* out = a.yp + (long long)row * a.H + col + c;
+              dev_store(out, s0);
+              dev_store(out + 16, s1);
+            }
           }
-        } else {
-          float* out = a.yp + (long long)row * a.H + col + c;
-          dev_store(out, s0);
-          dev_store(out + 16, s1);
-        }
-      }
       vm_drain<0>();   // the stores are out: the unit counts
       if (kind == U_GATEUP) {
-        if (lane == 0) dev_add(a.act_done + uniform(d.slot), 1);
+        if (lane == 0) dev_add(a.act_done + w(W_SLOT), 1);
       } else if (fused) {
         int before = 0;
         if (lane == 0)
-          before = __hip_atomic_fetch_add(a.col_done + uniform(d.slot), 1, __ATOMIC_RELAXED,
+          before = __hip_atomic_fetch_add(a.col_done + w(W_SLOT), 1, __ATOMIC_RELAXED,
                                           __HIP_MEMORY_SCOPE_AGENT);
         if (uniform(before) == uniform(lds_peek(&l.per_col)) - 1) {
           __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
@@ -880,7 +929,7 @@ template <typename T, int V, bool OWN>
 __global__ __launch_bounds__(DEC_NT) void decode_kernel(DecArgs a) {
   __shared__ __attribute__((aligned(1024))) DecLds l;
   if (threadIdx.x < DEC_SW) l.parts[threadIdx.x] = 0;
-  if (threadIdx.x == 0) l.ready = l.a_ready = l.taken = l.done = 0;
+  if (threadIdx.x == 0) l.ready = l.taken = l.done = 0;
   const int wave = uniform((int)(threadIdx.x >> 6));
   if (OWN && wave < DEC_SW) {
     const bool keep = blockIdx.x == 0;   // (one of them writes the choices out)
@@ -896,8 +945,11 @@ __global__ __launch_bounds__(DEC_NT) void decode_kernel(DecArgs a) {
       });
   }
   __syncthreads();
-  if (wave < DEC_SW) decode_stream<T, V, OWN>(a, l);
-  else if (wave == DEC_SW) decode_schedule<T>(l);
+  if (wave < DEC_SW) {
+    decode_stream<T, V, OWN>(a, l);
+    return;
+  }
+  if (wave == DEC_SW) decode_schedule<T>(l);
   else decode_finish<T>(a, l);
 }
 
@@ -922,6 +974,16 @@ int router_slices(int H, int E) {
   const int most = (H / 32 + RT_NW - 1) / RT_NW;
   s = s < most ? s : most;
   return s < RT_MAX_S ? s : RT_MAX_S;
+}
+
+// Row tiles of the gate/up units: two where an expert is likely to have more
+// rows than one tile holds (its mean over 8, or the shared expert's all).
+// Measured: see there.
+#ifndef GU_RULE
+#define GU_RULE 8
+#endif
+int gateup_tiles(bool shared, int T, int E, int k) {
+  return T > 16 && (shared || T * k > GU_RULE * E) ? 2 : 1;
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -1052,6 +1114,7 @@ extern "C" int moe_decode(const void* x, int dt, const float* wg, const float* b
   a.w13 = w13; a.w2 = w2; a.ws13 = ws13; a.ws2 = ws2; a.residual = residual;
   a.logits = logits; a.idx = idx; a.gate = gate; a.y = y;
   a.S = wg != nullptr ? router_slices(H, E) : 0;
+  a.gu_tiles = gateup_tiles(a.shared != 0, T, E, k);
   a.n_count = w.n_count;
   a.next = (int*)((char*)ws + w.count);
   a.routed = a.next + 8;
