@@ -218,12 +218,8 @@ __device__ __forceinline__ void decode_route_token(const DecArgs& a, int t, bool
 // rows of the other operand (32 in the gate/up units of calls whose experts
 // have many rows: each unit reads its weights again).  K runs in steps of 128 bytes of a row (64 bf16,
 // 32 fp32) dealt to the four waves in turn; a step's weights and operand rows
-// go HBM -> LDS in 1 KB copies (lds_copy.hpp) into a ring that belongs to the
-// wave alone, several steps ahead.  A copy covers 8 whole 128-byte lines: read
-// that way with the streaming policy HBM gives 7.0 TB/s here, against 5.1 TB/s
-// for loads straight into the MFMA's operand layout (16 rows x 64 bytes).
-// 16-byte chunk c of row r sits in slot c ^ ((r >> 1) & 7) of its row, so the
-// 16 rows of a fragment read hit all banks.  The stream is one flat sequence of
+// go HBM -> LDS in copies of whole lines (stream.hpp) into a ring that belongs
+// to the wave alone, several steps ahead.  The stream is one flat sequence of
 // steps, unit after unit: at the end of a unit the waves leave their partial
 // tiles in LDS while the next one's steps are on their way.  A wave has a SIMD
 // to itself, so a branch costs it as much as a dozen instructions, and a step
@@ -305,14 +301,6 @@ __device__ __forceinline__ void lds_wait(const int* p, int v) {
   while (uniform(lds_peek(p)) < v) __builtin_amdgcn_s_sleep(1);
   asm volatile("" ::: "memory");
 }
-__device__ __forceinline__ void lds_drain() {   // this wave's LDS accesses have happened
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-}
-template <int n>
-__device__ __forceinline__ void vm_drain() {    // all but n of its memory operations have
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(n) : "memory");
-}
-
 // row blocks of an expert with m rows, in units of `tiles` row tiles
 __device__ __forceinline__ int row_blocks(int m, int tiles) {
   return (m + DEC_ROWS * tiles - 1) >> (tiles == 2 ? 5 : 4);
@@ -596,14 +584,6 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
 
 // ---- the streaming waves
 
-// 1 KB of a step, W with the streaming policy: it is read once
-__device__ __forceinline__ void dma16_nt(const i32x4& rs, uint32_t lds, uint32_t voff, int soff) {
-  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
-               :
-               : "v"(voff), "s"(rs), "s"(uniform(soff)), "s"(uniform((int)lds))
-               : "memory", "m0");
-}
-
 // The flat stream of one streaming wave over the units from seq on that have AT
 // A tiles each, feeding MT row tiles of the result (A tile i adds to row tile
 // i % MT); returns the number of the first unit that has not.  Steps are
@@ -639,8 +619,8 @@ __device__ __forceinline__ int stream_units(DecLds& l, int seq) {
     const int word = d.word[lane % W_WORDS];
 #pragma unroll
     for (int j = 0; j < 2 * AT; ++j) {
-      const int r = 8 * j + (lane >> 3);
-      ao[j] = d.arow[r] + (uint32_t)(((lane & 7) ^ ((r >> 1) & 7)) << 4);
+      const int r = stream_row(j);
+      ao[j] = d.arow[r] + stream_chunk(j);
     }
     auto w = [&](int i) { return __builtin_amdgcn_readlane(word, i); };
     if (w(W_KIND) > U_DOWN || w(W_AT) != AT || w(W_MT) != MT) {
@@ -659,8 +639,7 @@ __device__ __forceinline__ int stream_units(DecLds& l, int seq) {
     const int ldw = w(W_LDW);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int r = 8 * j + (lane >> 3);
-      wo[j] = (uint32_t)(r * ldw + (((lane & 7) ^ ((r >> 1) & 7)) << 4));
+      wo[j] = (uint32_t)(stream_row(j) * ldw) + stream_chunk(j);
     }
     at_unit = u;
     end = put + left;
@@ -689,10 +668,7 @@ __device__ __forceinline__ int stream_units(DecLds& l, int seq) {
 #pragma unroll
   for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = f32x4{0, 0, 0, 0};
   lds_wait(&l.taken, seq);         // (units of another kind may have used all of red)
-  // byte of this lane's 16 in a page, for the two halves of a step
-  const int r = lane & 15, kg = lane >> 4;
-  const int f0 = r * 128 + (((kg) ^ ((r >> 1) & 7)) << 4);
-  const int f1 = r * 128 + (((4 + kg) ^ ((r >> 1) & 7)) << 4);
+  const int f0 = stream_frag(0), f1 = stream_frag(1);
 #pragma unroll 1
   for (int d = 0; d < D - 1; ++d) copy();
   for (;;) {

@@ -15,12 +15,19 @@
 
 namespace {
 
-constexpr int LIN_FEW_ROWS = 64;    // most rows of the streaming kernel
+// Rows of the streaming kernel, at most: up to 16 it always runs; up to 64 but
+// where N is short and K long, for then its workgroups, one per 16 columns, are
+// few and read for long, and the K slices of dense.hip end sooner (37 x 2048 x
+// 7680: 18.3 us streaming, 12.6 in slices; 64 x 4096 x 4096: 13.8 and 14.7; 33 x
+// 2048 x 2048 fp32: 12.1 and 13.1; 17 x 1024 x 1024: 7.8 and 11.6).
+bool few_rows(int M, int N, int K, int dt) {
+  return M <= 16 || (M <= 64 && (N >= 4096 || (long long)K * moe_dt_bytes(dt) <= 8192));
+}
 #ifndef LIN_TILES
 #define LIN_TILES 192
 #endif
 constexpr int LIN_BIG_TILES = LIN_TILES;   // 256 x 256 tiles from which the large-tile kernels run
-constexpr int LIN_NW = 8;
+constexpr int LIN_NW = 4;
 constexpr int LIN_NT = 64 * LIN_NW;
 
 struct LinArgs {
@@ -40,46 +47,129 @@ __device__ __forceinline__ void lin_store(void* p, long long i, float v) {
   else ((T*)p)[i] = v;
 }
 
-// 16 output columns per workgroup, all rows (at most 16 MT): every weight is
-// read once.
-template <typename T, int MT>
+// NT x 16 output columns per workgroup and all rows, at most 8 AC: every weight
+// is read once.  The four waves split K (stream.hpp) and keep D steps of copies
+// in flight each, AC of them for the rows' operand; their partial tiles are
+// summed through LDS in wave order (the same bits on every run).  Rows of a
+// 16-row tile beyond 8 AC hold whatever the LDS held: their results are dropped.
+template <typename T, int AC, int NT, int D>
 __global__ __launch_bounds__(LIN_NT) void linear_rows_kernel(LinArgs a) {
-  constexpr int ES = sizeof(T);
-  __shared__ float red[LIN_NW * 256];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int n0 = blockIdx.x * 16;
-  const uint32_t rowb = (uint32_t)(a.K * ES), k16 = (uint32_t)(lane >> 4) * 16u;
-  const __amdgpu_buffer_rsrc_t wr =
-      make_rsrc((const char*)a.w + (long long)n0 * a.K * ES, 16u * rowb);
-  const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x, (uint32_t)a.M * rowb);
-  const uint32_t woff[1] = {(uint32_t)(lane & 15) * rowb + k16};
-  uint32_t aoff[1][MT];
+  constexpr int ES = sizeof(T), MT = (AC + 1) / 2, OPS = 2 * NT + AC;
+  constexpr int SLOT = (NT + MT) * STREAM_TILE;
+  __shared__ __attribute__((aligned(1024))) char smem[LIN_NW * D * SLOT];
+  const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
+  const int n0 = blockIdx.x * 16 * NT;
+  const int ld = a.K * ES, steps = (ld / STREAM_STEP - wave + LIN_NW - 1) / LIN_NW;
+  const i32x4 rw = raw_rsrc((const char*)a.w + (long long)n0 * ld, 16u * NT * (uint32_t)ld);
+  const i32x4 rx = raw_rsrc(a.x, (uint32_t)a.M * (uint32_t)ld);
+  uint32_t wo[2], xo[AC];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) wo[j] = (uint32_t)(stream_row(j) * ld) + stream_chunk(j);
+#pragma unroll
+  for (int j = 0; j < AC; ++j)
+    xo[j] = stream_row(j) < a.M ? (uint32_t)(stream_row(j) * ld) + stream_chunk(j & 1) : STREAM_OOB;
+  char* const ring = smem + wave * D * SLOT;
+  const uint32_t lds = lds_addr(ring);
+  int k = wave * STREAM_STEP, left = steps;
+  uint32_t slot = 0;
+  // (steps past the last go through an empty range, so that every step waits
+  // for the same number of copies)
+  auto copy = [&]() {
+    const int live = uniform(left > 0 ? -1 : 0);
+    const i32x4 w = {uniform(rw.x), uniform(rw.y), uniform(rw.z & live), MOE_RSRC_DW3};
+    const i32x4 x = {uniform(rx.x), uniform(rx.y), uniform(rx.z & live), MOE_RSRC_DW3};
+    const uint32_t p = (uint32_t)uniform((int)(lds + slot));
+    const int k0 = uniform(k & live);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        dma16_nt(w, p + t * STREAM_TILE + j * 1024, wo[j], (k0 + t * 16 * ld) & live);
+#pragma unroll
+    for (int j = 0; j < AC; ++j) dma16(x, p + NT * STREAM_TILE + j * 1024, xo[j], k0);
+    slot = (uint32_t)uniform((int)(slot + SLOT == D * SLOT ? 0 : slot + SLOT));
+    k = uniform(k + LIN_NW * STREAM_STEP);
+    left = uniform(left + live);
+  };
+  f32x4 acc[MT][NT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
-    aoff[0][m] = (uint32_t)min(m * 16 + (lane & 15), a.M - 1) * rowb + k16;
-  f32x4 acc[MT][1];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) acc[m][0] = f32x4{0, 0, 0, 0};
-  stream_product<T, MT, 1, 1, STREAM_CS<MT>, LIN_NW, 2>(acc, wr, woff, xr, aoff, a.K * ES, wave);
-  stream_reduce<MT, 1, LIN_NW>(acc, red, [&](int mt, int m, int c, const float* v) {
-    const int r = mt * 16 + m, n = n0 + c;
-    if (r >= a.M) return;
+    for (int t = 0; t < NT; ++t) acc[m][t] = f32x4{0, 0, 0, 0};
+  const int f[2] = {stream_frag(0), stream_frag(1)};
+#pragma unroll
+  for (int d = 0; d < D - 1; ++d) copy();
+  uint32_t rs = 0;
+  for (int i = 0; i < steps; ++i) {
+    copy();                        // into the slot read last
+    vm_drain<(D - 1) * OPS>();
+    const char* p = ring + rs;
+    rs = (uint32_t)uniform((int)(rs + SLOT == D * SLOT ? 0 : rs + SLOT));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      u32x4 w[NT], x[MT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) w[t] = *(const u32x4*)(p + t * STREAM_TILE + f[h]);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) x[m] = *(const u32x4*)(p + (NT + m) * STREAM_TILE + f[h]);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[m][t] = stream_mma(x[m], w[t], acc[m][t], T());
+    }
+    lds_drain();                   // the slot is read
+  }
+  vm_drain<0>();                   // (empty copies)
+  __syncthreads();
+  // partial tiles: [wave][tile][register][lane]
+  float* const red = (float*)smem;
+  static_assert(MT * NT * 1024 <= D * SLOT, "partial tiles fit the ring");
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        red[((wave * MT + m) * NT + t) * 256 + q * 64 + lane] = acc[m][t][q];
+  __syncthreads();
+  for (int i = threadIdx.x; i < MT * NT * 256; i += LIN_NT) {
+    float v = red[i];
+#pragma unroll
+    for (int w = 1; w < LIN_NW; ++w) v += red[w * MT * NT * 256 + i];
+    // register q of lane l: row 4 (l / 16) + q, column l % 16
+    const int tile = i >> 8, q = (i >> 6) & 3, l = i & 63;
+    const int r = tile / NT * 16 + 4 * (l >> 4) + q, n = n0 + tile % NT * 16 + (l & 15);
+    if (r >= a.M) continue;
     const long long at = (long long)r * a.N + n;
-    const float z = a.bias != nullptr ? v[0] + a.bias[n] : v[0];
+    const float z = a.bias != nullptr ? v + a.bias[n] : v;
     if (a.z != nullptr) lin_store<T>(a.z, at, z);
     float y = act_value(z, a.act);
     if (a.residual != nullptr) y += lin_load<T>(a.residual, at);
     lin_store<T>(a.y, at, y);
-  });
+  }
 }
 
-template <typename T>
+template <typename T, int AC, int NT, int D>
 int launch_rows(const LinArgs& a, hipStream_t s, const char* fn) {
-  const dim3 grid(a.N / 16), block(LIN_NT);
-  if (a.M <= 16) hipLaunchKernelGGL((linear_rows_kernel<T, 1>), grid, block, 0, s, a);
-  else if (a.M <= 32) hipLaunchKernelGGL((linear_rows_kernel<T, 2>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((linear_rows_kernel<T, 4>), grid, block, 0, s, a);
+  hipLaunchKernelGGL((linear_rows_kernel<T, AC, NT, D>), dim3(a.N / (16 * NT)), dim3(LIN_NT), 0, s,
+                     a);
   return moe_check_launch(fn);
+}
+
+// Two 16-column tiles per workgroup halve what is read of x, once there are
+// columns enough to fill most of the chip that way (24 x 7680 x 7680: 23.8 us,
+// one tile 29.7; 64 x 4096 x 4096: 17.9, one tile 13.8).
+constexpr int LIN_TWO_N = 6144;
+template <typename T>
+int linear_rows(const LinArgs& a, hipStream_t s, const char* fn) {
+  const bool two = a.M > 16 && a.N >= LIN_TWO_N;
+  if (a.M <= 8) return launch_rows<T, 1, 1, 5>(a, s, fn);
+  if (a.M <= 16) return launch_rows<T, 2, 1, 5>(a, s, fn);
+  if (a.M <= 32)
+    return two ? launch_rows<T, 4, 2, 4>(a, s, fn) : launch_rows<T, 4, 1, 3>(a, s, fn);
+  if (a.M <= 48)
+    return two ? launch_rows<T, 6, 2, 3>(a, s, fn) : launch_rows<T, 6, 1, 2>(a, s, fn);
+  return two ? launch_rows<T, 8, 2, 3>(a, s, fn) : launch_rows<T, 8, 1, 2>(a, s, fn);
 }
 
 // ---------------------------------------------------------------- dz and db
@@ -156,7 +246,7 @@ bool fwd_big(int M, int N) { return big_tiles(M, N) >= LIN_BIG_TILES; }
 bool bwd_big(int M, int N, int K) { return big_tiles(M, K) + big_tiles(N, K) >= LIN_BIG_TILES; }
 
 size_t fwd_ws(int M, int N, int K, int dt) {
-  return M <= LIN_FEW_ROWS || fwd_big(M, N) ? 0 : round256(moe_dense_fwd_bytes(M, N, K, dt));
+  return few_rows(M, N, K, dt) || fwd_big(M, N) ? 0 : round256(moe_dense_fwd_bytes(M, N, K, dt));
 }
 
 struct BwdWs {
@@ -222,9 +312,9 @@ extern "C" int moe_linear(const void* x, int dt, int M, int N, int K, const void
     return moe_fail(MOE_ERR_INVALID_ARG, "%s: y and z need buffers of their own (y may be residual's)",
                     fn);
   hipStream_t s = (hipStream_t)stream;
-  if (M <= LIN_FEW_ROWS) {
+  if (few_rows(M, N, K, dt)) {
     LinArgs a = {x, w, bias, residual, z, y, M, N, K, act};
-    return dt == MOE_BF16 ? launch_rows<bf16_t>(a, s, fn) : launch_rows<float>(a, s, fn);
+    return dt == MOE_BF16 ? linear_rows<bf16_t>(a, s, fn) : linear_rows<float>(a, s, fn);
   }
   MOE_TRY(lin_tile_checks(fn, dt, M, N, K));
   const size_t need = fwd_ws(M, N, K, dt);

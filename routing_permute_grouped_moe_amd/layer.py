@@ -319,36 +319,34 @@ class MoeLayer:
 # ---------------------------------------------------------------------- checked calls
 def _check(name, t, dtype, device, *shape):
     """A tensor the kernels can read as it lies: dense, of this shape, type and device."""
+    if (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}, not {dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the weights are on {device}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} is not contiguous")
+    raise ValueError(f"{name} is not contiguous")
 
 
-class _On:
-    """The device of a call's tensors, and its stream as torch's current one, so
-    that outputs and workspaces allocated inside belong to that stream."""
-    __slots__ = ("guards",)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    def __init__(self, device, stream):
-        self.guards = []
-        if torch.cuda.current_device() != device.index:
-            self.guards.append(torch.cuda.device(device))
-        if stream is not None:
-            self.guards.append(torch.cuda.stream(stream))
 
-    def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+def _on(device, stream, call):
+    """call(raw stream) with the device of a call's tensors current, and the
+    given stream too (None: the device's current one), so that outputs and
+    workspaces allocated inside belong to it."""
+    if stream is None:
+        if torch.cuda.current_device() == device.index:
+            return call(_raw_stream(device.index))
+        with torch.cuda.device(device):
+            return call(_raw_stream(device.index))
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the weights are on {device}")
+    with torch.cuda.stream(stream):   # (makes the stream's device current too)
+        return call(stream.cuda_stream)
 
 
 def _device(t):
@@ -418,26 +416,26 @@ class MoeDecode:
             raise ValueError("logits come with the call if, and only if, there is no router")
         if logits is not None:
             _check("logits", logits, torch.float32, dev, T, s.E)
-        with _On(dev, stream) as st:
-            f32 = torch.float32
-            if out is None:
-                out = torch.empty_like(x)
-            else:
-                _check("out", out, s.dtype, dev, T, s.H)
-            if logits is None:
-                logits = torch.empty((T, s.E), dtype=f32, device=dev)
-            idx = torch.empty((T, s.k), dtype=torch.int32, device=dev)
-            gate = torch.empty((T, s.k), dtype=f32, device=dev)
-            if T not in self._ws_bytes:
-                self._ws_bytes[T] = abi.moe_decode_workspace_bytes(T, s.H, s.I, s.E, s.k, self.dt)
-            n = self._ws_bytes[T]
+        if out is not None:
+            _check("out", out, s.dtype, dev, T, s.H)
+
+        def call(st):
+            n = self._ws_bytes.get(T)
+            if n is None:
+                n = abi.moe_decode_workspace_bytes(T, s.H, s.I, s.E, s.k, self.dt)
+                self._ws_bytes[T] = n
+            y = torch.empty_like(x) if out is None else out
+            lg = x.new_empty((T, s.E), dtype=torch.float32) if logits is None else logits
+            idx = x.new_empty((T, s.k), dtype=torch.int32)
+            gate = x.new_empty((T, s.k), dtype=torch.float32)
             # a workspace per call, from the stream's own pool: calls on several
             # streams, or captured into several graphs, never share one
-            ws = torch.empty(n, dtype=torch.uint8, device=dev)
+            ws = x.new_empty(n, dtype=torch.uint8)
             abi.moe_decode(x, self.dt, self.wg, self.bias, T, s.H, s.I, s.E, s.k, s.g0, s.groups,
-                           self.w13, self.w2, self.ws13, self.ws2, residual, logits, idx, gate,
-                           out, ws, n, st)
-        return Decoded(out, idx, gate, logits)
+                           self.w13, self.w2, self.ws13, self.ws2, residual, lg, idx, gate, y, ws,
+                           n, st)
+            return Decoded(y, idx, gate, lg)
+        return _on(dev, stream, call)
 
 
 ACTS = {"none": abi.MOE_ACT_NONE, "relu": abi.MOE_ACT_RELU, "silu": abi.MOE_ACT_SILU,
@@ -460,6 +458,7 @@ class Linear:
         if act not in ACTS:
             raise ValueError(f"act {act!r} is none of {', '.join(ACTS)}")
         self.w, self.bias, self.act = w, bias, ACTS[act]
+        self._ws_bytes = {}
 
     def forward(self, x, residual=None, save_z=False, out=None, stream=None):
         """``x`` [M, K] -> y [M, N], or (y, z) with ``save_z``.  ``out``: y's
@@ -468,17 +467,20 @@ class Linear:
         _check("x", x, self.dtype, dev, M, self.K)
         if residual is not None:
             _check("residual", residual, self.dtype, dev, M, self.N)
-        with _On(dev, stream) as st:
-            if out is None:
-                out = torch.empty((M, self.N), dtype=self.dtype, device=dev)
-            else:
-                _check("out", out, self.dtype, dev, M, self.N)
-            z = torch.empty((M, self.N), dtype=self.dtype, device=dev) if save_z else None
-            n = abi.moe_linear_workspace_bytes(M, self.N, self.K, self.dt)
-            ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        if out is not None:
+            _check("out", out, self.dtype, dev, M, self.N)
+
+        def call(st):
+            n = self._ws_bytes.get(M)
+            if n is None:
+                n = self._ws_bytes[M] = abi.moe_linear_workspace_bytes(M, self.N, self.K, self.dt)
+            y = x.new_empty((M, self.N)) if out is None else out
+            z = x.new_empty((M, self.N)) if save_z else None
+            ws = x.new_empty(n, dtype=torch.uint8) if n else None
             abi.moe_linear(x, self.dt, M, self.N, self.K, self.w, self.bias, self.act, residual,
-                           z, out, ws, n, st)
-        return (out, z) if save_z else out
+                           z, y, ws, n, st)
+            return (y, z) if save_z else y
+        return _on(dev, stream, call)
 
     def backward(self, dy, x, z=None, bias_grad=None, stream=None):
         """(dx, dw, db) of ``dy`` [M, N], the forward's ``x`` and the ``z`` it
@@ -493,12 +495,13 @@ class Linear:
             _check("z", z, self.dtype, dev, M, self.N)
         if bias_grad is None:
             bias_grad = self.bias is not None
-        with _On(dev, stream) as st:
-            dx = torch.empty_like(x)
-            dw = torch.empty_like(self.w)
-            db = torch.empty(self.N, dtype=torch.float32, device=dev) if bias_grad else None
+
+        def call(st):
+            dx, dw = torch.empty_like(x), torch.empty_like(self.w)
+            db = x.new_empty(self.N, dtype=torch.float32) if bias_grad else None
             n = abi.moe_linear_bwd_workspace_bytes(M, self.N, self.K, self.dt, self.act)
-            ws = torch.empty(n, dtype=torch.uint8, device=dev)
+            ws = x.new_empty(n, dtype=torch.uint8)
             abi.moe_linear_bwd(dy, z, x, self.w, self.dt, M, self.N, self.K, self.act, dx, dw, db,
                                ws, n, st)
-        return dx, dw, db
+            return dx, dw, db
+        return _on(dev, stream, call)
