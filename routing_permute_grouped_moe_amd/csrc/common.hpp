@@ -177,11 +177,14 @@ int moe_gmm_linear_fwd(const void* x, int dt, int M, int N, int K, const void* w
                        const float* bias, int act, const void* residual, void* z, void* y,
                        hipStream_t s);
 int moe_gmm_linear_bwd(const void* dz, const void* x, const void* w, int dt, int M, int N, int K,
-                       void* dx, void* dw, hipStream_t s);
+                       void* dx, void* dw, int S, float* part, hipStream_t s);
+// out[MN] (dt) = sum of S fp32 partials, in order
+int moe_dense_sum(const float* part, int S, int M, int N, int dt, void* out, hipStream_t s);
 // the same on smaller tiles, in K slices (dense.hip); *_bytes: partial sums in ws
 size_t moe_dense_fwd_bytes(int M, int N, int K, int dt);
-size_t moe_dense_bwd_bytes(int M, int N, int K, int dt);
+// dx_only: planned for dx alone (dw null)
+size_t moe_dense_bwd_bytes(int M, int N, int K, int dt, bool dx_only);
 int moe_dense_fwd(const void* x, int dt, int M, int N, int K, const void* w, const float* bias,
                   int act, const void* residual, void* z, void* y, void* ws, hipStream_t s);
 int moe_dense_bwd(const void* dz, const void* x, const void* w, int dt, int M, int N, int K,
-                  void* dx, void* dw, void* ws, hipStream_t s);
+                  void* dx, void* dw, bool dx_only, void* ws, hipStream_t s);

@@ -39,7 +39,10 @@ struct DenseArgs {
 };
 
 // Per tile size: stages of the ring
-template <int BT> constexpr int D_STAGES = BT == 128 ? 3 : 4;
+// (two workgroups of 64 KB fit a CU, and one multiplies while the other waits
+// for its copies: with three stages, one to a CU, 2000 x 8192 x 2048 took 116 us
+// instead of 83)
+template <int BT> constexpr int D_STAGES = BT == 128 ? 2 : 4;
 template <int BT> constexpr int D_OPB = BT * D_ROWB;      // bytes of an operand's stage
 template <int BT> constexpr int D_RING = D_STAGES<BT> * 2 * D_OPB<BT>;
 
@@ -193,18 +196,35 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int m0, int n0, i
     __syncthreads();   // step kt has landed for every wave; step kt - 1's stage is free
     issue(kt + NS - 1);
     const char* st = smem + (kt % NS) * (2 * OPB);
+    // two sets of fragments in turn: a group's reads go between the MFMAs of the
+    // group before (pinned by scheduling barriers), so that only the first
+    // group of a step waits for its own
+    u32x4 fa[2][F], fb[2][F];
+    auto load = [&](int g, int q) {   // read q of group g: A fragments, then B
+      if (q < F) fa[g & 1][q] = dense_frag<T, A_MN, BT>(st, wm + 32 * q, g);
+      else fb[g & 1][q - F] = dense_frag<T, B_MN, BT>(st + OPB, wn + 32 * (q - F), g);
+    };
 #pragma unroll
-    for (int g = 0; g < D_GROUPS; ++g) {
-      u32x4 fa[F], fb[F];
+    for (int q = 0; q < 2 * F; ++q) load(0, q);
 #pragma unroll
-      for (int i = 0; i < F; ++i) fa[i] = dense_frag<T, A_MN, BT>(st, wm + 32 * i, g);
-#pragma unroll
-      for (int i = 0; i < F; ++i) fb[i] = dense_frag<T, B_MN, BT>(st + OPB, wn + 32 * i, g);
+    for (int g = 0; g < D_GROUPS; ++g)
 #pragma unroll
       for (int i = 0; i < F; ++i)
 #pragma unroll
-        for (int j = 0; j < F; ++j) acc[i][j] = dense_mma(fb[j], fa[i], acc[i][j], T());
-    }
+        for (int j = 0; j < F; ++j) {
+          acc[i][j] = dense_mma(fb[g & 1][j], fa[g & 1][i], acc[i][j], T());
+          __builtin_amdgcn_sched_barrier(0);
+          const int q = i * F + j;    // F^2 MFMAs carry the next group's 2 F reads
+          if (g + 1 < D_GROUPS) {
+            if constexpr (F == 1) {
+              load(g + 1, 0);
+              load(g + 1, 1);
+            } else if (q < 2 * F) {
+              load(g + 1, q);
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
   }
   wait_vm<0>();
   __syncthreads();   // the ring is free: each wave turns its tile through its own part of it
@@ -290,18 +310,24 @@ __global__ __launch_bounds__(256) void dense_sum_kernel(DenseArgs a, DenseArgs b
 
 constexpr int D_MAX_S = 16;
 
-// Tile size and slices: 128 x 128 tiles move half the bytes per flop of
-// 64 x 64 ones, so they are taken as soon as they, in slices of at least 512
-// of K, fill half the chip.
+// Tile size: 128 x 128 tiles move half the bytes per flop of 64 x 64 ones, so
+// they are taken as soon as there are 32 of them.  Slices: as many as give the
+// chip two workgroups a CU while each keeps 1024 of K (419 x 2048 x 8192: 28 us
+// with 8 slices, 30 with 4), else one a CU while each keeps 256 (128 x 8192 x
+// 2048: 17 us with 4 slices, 21 with 8: more partial sums to write and read).
+// fp32's matrix rate is a sixteenth, so its slices are never short of loads.
 struct Plan {
   int bt;
-  void slices(DenseArgs& a, int es, int target) const {
+  void slices(DenseArgs& a, int es, int wgs) const {
     a.mt = (a.M + bt - 1) / bt;
     a.nt = (a.N + bt - 1) / bt;
-    const int bk = D_ROWB / es, tiles = a.mt * a.nt;
+    const int bk = D_ROWB / es, tiles = a.mt * a.nt > 0 ? a.mt * a.nt : 1;
     const int least = es == 2 ? 256 : 64;          // K of the shortest slice
-    int s = target / (tiles > 0 ? tiles : 1);
-    s = s < a.K / least ? s : a.K / least;
+    int s = 2 * wgs / tiles;
+    if (es == 4 || (long long)s * 4 * least > a.K) {
+      s = wgs / tiles;
+      s = s < a.K / least ? s : a.K / least;
+    }
     s = s < D_MAX_S ? s : D_MAX_S;
     s = s > 1 ? s : 1;
     a.kslice = ((a.K + s - 1) / s + bk - 1) / bk * bk;
@@ -325,14 +351,14 @@ struct BwdPlan {
   int bt;
   DenseArgs dx, dw;
 };
-BwdPlan bwd_args(int M, int N, int K, int dt) {
+BwdPlan bwd_args(int M, int N, int K, int dt, bool dx_only) {
   BwdPlan p = {};
-  p.bt = plan_tile(M + N, K);
+  p.bt = plan_tile(dx_only ? M : M + N, K);
   p.dx.M = M; p.dx.N = K; p.dx.K = N; p.dx.lda = N; p.dx.ldb = K;
   p.dw.M = N; p.dw.N = K; p.dw.K = M; p.dw.lda = N; p.dw.ldb = K;
   const int es = moe_dt_bytes(dt);
   // the two products share the chip by their work, 2 M N K each
-  Plan{p.bt}.slices(p.dx, es, 128);
+  Plan{p.bt}.slices(p.dx, es, dx_only ? 256 : 128);
   Plan{p.bt}.slices(p.dw, es, 128);
   return p;
 }
@@ -347,9 +373,9 @@ size_t moe_dense_fwd_bytes(int M, int N, int K, int dt) {
   return part_bytes(fwd_args(M, N, K, dt));
 }
 
-size_t moe_dense_bwd_bytes(int M, int N, int K, int dt) {
-  const BwdPlan p = bwd_args(M, N, K, dt);
-  return part_bytes(p.dx) + part_bytes(p.dw);
+size_t moe_dense_bwd_bytes(int M, int N, int K, int dt, bool dx_only) {
+  const BwdPlan p = bwd_args(M, N, K, dt, dx_only);
+  return part_bytes(p.dx) + (dx_only ? 0 : part_bytes(p.dw));
 }
 
 int moe_dense_fwd(const void* x, int dt, int M, int N, int K, const void* w, const float* bias,
@@ -378,9 +404,9 @@ int moe_dense_fwd(const void* x, int dt, int M, int N, int K, const void* w, con
 }
 
 int moe_dense_bwd(const void* dz, const void* x, const void* w, int dt, int M, int N, int K,
-                  void* dx, void* dw, void* ws, hipStream_t s) {
+                  void* dx, void* dw, bool dx_only, void* ws, hipStream_t s) {
   const char* fn = "moe_linear_bwd";
-  BwdPlan p = bwd_args(M, N, K, dt);
+  BwdPlan p = bwd_args(M, N, K, dt, dx_only);
   DenseArgs &a = p.dx, &b = p.dw;
   a.A = dz; a.B = w; a.C = dx; a.part = (float*)ws;
   b.A = dz; b.B = x; b.C = dw; b.part = (float*)((char*)ws + part_bytes(a));
@@ -406,4 +432,15 @@ int moe_dense_bwd(const void* dz, const void* x, const void* w, int dt, int M, i
   else
     hipLaunchKernelGGL(dense_sum_kernel<float>, dim3(n0 + n1), block, 0, s, a, b, n0);
   return moe_check_launch(fn);
+}
+
+int moe_dense_sum(const float* part, int S, int M, int N, int dt, void* out, hipStream_t s) {
+  DenseArgs a = {};
+  a.M = M; a.N = N; a.S = S; a.part = const_cast<float*>(part); a.C = out;
+  const int n0 = (int)(((long long)M * N / 4 + 255) / 256);
+  if (dt == MOE_BF16)
+    hipLaunchKernelGGL(dense_sum_kernel<bf16_t>, dim3(n0), dim3(256), 0, s, a, a, n0);
+  else
+    hipLaunchKernelGGL(dense_sum_kernel<float>, dim3(n0), dim3(256), 0, s, a, a, n0);
+  return moe_check_launch("moe_linear_bwd");
 }

@@ -96,6 +96,7 @@ struct GmmArgs {
   // dense groups: all G groups have rows [0, shT) and their own operands at
   // X + g*x_gs, W + g*w_gs, C + g*c_gs (elements); no offsets table
   int dense; long long x_gs;
+  int rows_all;   // dense, > 0: the groups are runs of shT rows of rows_all, the last ones short
   int krep;      // > 1: each A K step serves krep consecutive K steps, whose
                  // B rows differ (the parts of a split fp32 operand)
   int out_f32;   // plain-store epilogue writes fp32 whatever T is
@@ -377,6 +378,7 @@ __device__ __forceinline__ void load_groups(const GmmArgs& a, GroupLds& gl) {
     } else {
       lo = 0;
       hi = a.shT;
+      if (a.rows_all > 0) hi = min(max(a.rows_all - g * a.shT, 0), a.shT);
     }
     gl.lo[g] = lo;
     gl.hi[g] = hi;
@@ -1273,37 +1275,56 @@ __device__ __forceinline__ void run_tile(const GmmArgs& a, const GroupLds& gl, c
           return (uint32_t)(m * a.ldc + n);
         };
         if constexpr (MODE == LIN) {
+          // Every thread keeps to one chunk of 8 columns (256 threads walk rows of
+          // 16 chunks), so its bias is read once; the residual's chunks are
+          // requested four at a time, ahead of the LDS reads they meet.
+          static_assert(NT % 16 == 0, "a thread keeps its columns");
           const __amdgpu_buffer_rsrc_t br = make_rsrc(a.bias, (uint32_t)a.N * 4u);
           const __amdgpu_buffer_rsrc_t rr =
               make_rsrc((const char*)a.res + (long long)rows0 * a.ldc * ES, clamp_bytes(cbytes));
           const __amdgpu_buffer_rsrc_t zr =
               make_rsrc((char*)a.C2 + (long long)rows0 * a.ldc * ES, out_bytes(cbytes));
-          emit(hc, [&](int row, int c, const float* v) {
-            bool ok;
-            const uint32_t e = place(row, c, ok);
-            const uint32_t n = (uint32_t)(n0 + (c / HW) * (2 * HW) + HW * h + (c % HW));
-            float o[8];
+          const int cc = (etid & 15) * 8;
+          const int n = n0 + (cc / HW) * (2 * HW) + HW * h + (cc % HW);
+          float b[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) o[q] = v[q];
-            if (a.bias != nullptr) {
-              float b[8];
-              unpack16(buf_load16(br, n * 4u), b, 0.f);
-              unpack16(buf_load16(br, n * 4u + 16u), b + 4, 0.f);
-#pragma unroll
-              for (int q = 0; q < 8; ++q) o[q] += b[q];
-            }
-            if (a.C2 != nullptr) store8(zr, ok, e, o);
-            if (a.act != MOE_ACT_NONE)
-#pragma unroll
-              for (int q = 0; q < 8; ++q) o[q] = act_value(o[q], a.act);
+          for (int q = 0; q < 8; ++q) b[q] = 0.f;
+          if (a.bias != nullptr) {   // (columns past N are read as the last ones, and dropped)
+            unpack16(buf_load16(br, (uint32_t)min(n, a.N - 8) * 4u), b, 0.f);
+            unpack16(buf_load16(br, (uint32_t)min(n, a.N - 8) * 4u + 16u), b + 4, 0.f);
+          }
+          put(std::integral_constant<int, h * (FN / 2)>{}, acc_of);
+          constexpr int CH = BMT * 16 / NT, PFR = 4;
+#pragma unroll 1
+          for (int it0 = 0; it0 < CH; it0 += PFR) {
+            float res[PFR][8];
             if (a.res != nullptr) {
-              float r[8];
-              load8(rr, ok, e, r);
 #pragma unroll
-              for (int q = 0; q < 8; ++q) o[q] += r[q];
+              for (int p = 0; p < PFR; ++p) {
+                const int row = ((it0 + p) * NT + etid) >> 4;
+                load8(rr, row < rows && n < a.N, (uint32_t)(row * a.ldc + n), res[p]);
+              }
             }
-            store8(cr, ok, e, o);
-          });
+#pragma unroll
+            for (int p = 0; p < PFR; ++p) {
+              const int row = ((it0 + p) * NT + etid) >> 4, sw = row & 31;
+              const f32x4 lo = *(const f32x4*)(ep + row * EP_PITCH + (((cc >> 2) ^ sw) << 2));
+              const f32x4 hi = *(const f32x4*)(ep + row * EP_PITCH + ((((cc >> 2) + 1) ^ sw) << 2));
+              float o[8] = {lo.x + b[0], lo.y + b[1], lo.z + b[2], lo.w + b[3],
+                            hi.x + b[4], hi.y + b[5], hi.z + b[6], hi.w + b[7]};
+              const bool ok = row < rows && n < a.N;
+              const uint32_t e = (uint32_t)(row * a.ldc + n);
+              if (a.C2 != nullptr) store8(zr, ok, e, o);
+              if (a.act != MOE_ACT_NONE)
+#pragma unroll
+                for (int q = 0; q < 8; ++q) o[q] = act_value(o[q], a.act);
+              if (a.res != nullptr)
+#pragma unroll
+                for (int q = 0; q < 8; ++q) o[q] += res[p][q];
+              store8(cr, ok, e, o);
+            }
+          }
+          __syncthreads();
         } else if (a.out_f32) {
           emit(hc, [&](int row, int c, const float* v) {
             bool ok;
@@ -2285,21 +2306,25 @@ int moe_gmm_linear_fwd(const void* x, int dt, int M, int N, int K, const void* w
   return launch_dt<LIN>(dt, a, s, "moe_linear");
 }
 
-// dx = dz . W (W stored [K = N][N = K]) and dW = dz^T . x in one launch
+// dx = dz . W (W stored [K = N][N = K]) and dW = dz^T . x in one launch.  With
+// S > 1 the rows are taken in S runs, each with a partial dW of its own in part
+// (fp32, [S][N][K]), for the caller to add.
 int moe_gmm_linear_bwd(const void* dz, const void* x, const void* w, int dt, int M, int N, int K,
-                       void* dx, void* dw, hipStream_t s) {
+                       void* dx, void* dw, int S, float* part, hipStream_t s) {
   const char* fn = "moe_linear_bwd";
   GmmArgs a1 = {};
-  a1.dense = 1; a1.G = 1; a1.shT = M; a1.R = M;
+  a1.dense = 1; a1.G = S; a1.shT = S > 1 ? (M + S - 1) / S : M; a1.R = M;
+  a1.rows_all = S > 1 ? M : 0;
   GmmArgs a2 = a1;
   a1.N = K; a1.K = N;
-  a1.X = dz; a1.ldx = N;
+  a1.X = dz; a1.ldx = N; a1.x_gs = (long long)a1.shT * N;
   a1.W = w; a1.ldw = K;
-  a1.C = dx; a1.ldc = K;
+  a1.C = dx; a1.ldc = K; a1.c_gs = (long long)a1.shT * K;
   a2.M = N; a2.N = K;
-  a2.X = dz; a2.ldx = N;
-  a2.W = x; a2.ldw = K;
-  a2.C = dw; a2.ldc = K;
+  a2.X = dz; a2.ldx = N; a2.x_gs = (long long)a2.shT * N;
+  a2.W = x; a2.ldw = K; a2.w_gs = (long long)a2.shT * K;
+  a2.C = S > 1 ? part : dw; a2.ldc = K; a2.c_gs = (long long)N * K;
+  a2.out_f32 = S > 1;
   if (dx != nullptr && dw != nullptr && M > 0) {
     GmmArgs none = {};
     none.M = -1;

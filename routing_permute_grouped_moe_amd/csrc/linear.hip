@@ -23,10 +23,6 @@ namespace {
 bool few_rows(int M, int N, int K, int dt) {
   return M <= 16 || (M <= 64 && (N >= 4096 || (long long)K * moe_dt_bytes(dt) <= 8192));
 }
-#ifndef LIN_TILES
-#define LIN_TILES 192
-#endif
-constexpr int LIN_BIG_TILES = LIN_TILES;   // 256 x 256 tiles from which the large-tile kernels run
 constexpr int LIN_NW = 4;
 constexpr int LIN_NT = 64 * LIN_NW;
 
@@ -179,9 +175,14 @@ int linear_rows(const LinArgs& a, hipStream_t s, const char* fn) {
 constexpr int DZ_COLS = 256;   // columns of a workgroup: 32 threads of 8
 constexpr int DZ_MAX_PARTS = 128;
 
-int dz_rows(int M) {           // rows of a block: at least 64, at most 128 blocks
-  const int r = (M + DZ_MAX_PARTS - 1) / DZ_MAX_PARTS;
-  return r < 64 ? 64 : (r + 7) / 8 * 8;
+// Rows of a block, a multiple of the 8 threads that share a column chunk: as few
+// as give 512 workgroups work, at most 128 blocks.
+int dz_rows(int M, int N) {
+  const int cols = (N + DZ_COLS - 1) / DZ_COLS;
+  const int want = (512 + cols - 1) / cols;               // blocks
+  const int parts = want < DZ_MAX_PARTS ? want : DZ_MAX_PARTS;
+  const int r = (M + parts - 1) / parts;
+  return r < 8 ? 8 : (r + 7) / 8 * 8;
 }
 
 template <typename T>
@@ -228,39 +229,75 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const T* __restrict__ dy
   }
 }
 
-// db = sum of the blocks' column sums, in block order
+// db = sum of the blocks' column sums: four threads a column, each over a
+// quarter of the blocks in order, then the four in order
 __global__ __launch_bounds__(256) void linear_db_kernel(const float* __restrict__ part, int parts,
                                                         int N, float* __restrict__ db) {
-  const int n = blockIdx.x * 256 + threadIdx.x;
-  if (n >= N) return;
+  __shared__ double red[4][64];
+  const int c = threadIdx.x & 63, q = threadIdx.x >> 6;
+  const int n = blockIdx.x * 64 + c;       // (N is a multiple of 64)
+  const int per = (parts + 3) / 4, p1 = min(parts, (q + 1) * per);
   double s = 0;
-  for (int p = 0; p < parts; ++p) s += part[(long long)p * N + n];
-  db[n] = (float)s;
+#pragma unroll 8
+  for (int p = q * per; p < p1; ++p) s += part[(long long)p * N + n];
+  red[q][c] = s;
+  __syncthreads();
+  if (q == 0) db[n] = (float)(((red[0][c] + red[1][c]) + red[2][c]) + red[3][c]);
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-// 256 x 256 tiles of an M x N product
+// The 256 x 256 tiles of the grouped GEMM (bf16; in fp32 the smaller ones are
+// faster throughout) pay once there are enough of them for the 256 CUs.
+// Measured, smaller tiles against these: 2048 x 4096 x 4096 (128 tiles) 73 and
+// 137 us, 2000 x 8192 x 2048 (256) 83 and 83, 4096^3 (256) 146 and 135, 8191 x
+// 2048 x 7680 (256) 308 and 236.
+constexpr int LIN_BIG_TILES = 192;
 long long big_tiles(long long M, long long N) { return ((M + 255) / 256) * ((N + 255) / 256); }
-bool fwd_big(int M, int N) { return big_tiles(M, N) >= LIN_BIG_TILES; }
-bool bwd_big(int M, int N, int K) { return big_tiles(M, K) + big_tiles(N, K) >= LIN_BIG_TILES; }
+bool fwd_big(int M, int N, int dt) {
+  return dt == MOE_BF16 && big_tiles(M, N) >= LIN_BIG_TILES;
+}
+
+// The backward's two products share a launch, so what counts is their tiles
+// together.  Where a dx tile (N deep) would take more than 3 times a workgroup's
+// share of the work, dx goes to the smaller tiles in slices, in a launch of its
+// own (1000 x 7680 x 2048: 100 us, 203 together, 177 all in smaller tiles; 200 x
+// 8192 x 8192: 122, 236 and 324), and where a dW tile (M deep) would take more than its share,
+// M is cut into `runs` (8192 x 2048 x 2048: 228 us, 302 in one run).
+struct BwdBig {
+  bool dx, dw;    // these tiles for this product
+  int runs;
+};
+BwdBig bwd_big(int M, int N, int K, int dt) {
+  const long long tx = big_tiles(M, K), tw = big_tiles(N, K);
+  const double share = ((double)tx * N + (double)tw * M) / 256;   // in K elements
+  BwdBig b = {false, false, 1};
+  if (dt != MOE_BF16 || tx + tw < LIN_BIG_TILES) return b;
+  b.dx = N <= 3 * share;
+  b.dw = b.dx || tw >= LIN_BIG_TILES;
+  while (b.dx && b.runs < 8 && M / b.runs > 1.3 * share && M / b.runs >= 1024) b.runs *= 2;
+  return b;
+}
 
 size_t fwd_ws(int M, int N, int K, int dt) {
-  return few_rows(M, N, K, dt) || fwd_big(M, N) ? 0 : round256(moe_dense_fwd_bytes(M, N, K, dt));
+  return few_rows(M, N, K, dt) || fwd_big(M, N, dt) ? 0 : round256(moe_dense_fwd_bytes(M, N, K, dt));
 }
 
 struct BwdWs {
   size_t part, dz, dense, total;
   int rows, parts;
+  BwdBig big;
 };
 BwdWs bwd_ws(int M, int N, int K, int dt, int act) {
   BwdWs w;
-  w.rows = dz_rows(M);
+  w.rows = dz_rows(M, N);
   w.parts = (M + w.rows - 1) / w.rows;
   w.part = 0;
   w.dz = round256((size_t)w.parts * N * 4);
   w.dense = w.dz + (act == MOE_ACT_NONE ? 0 : round256((size_t)M * N * moe_dt_bytes(dt)));
-  w.total = w.dense + (bwd_big(M, N, K) ? 0 : round256(moe_dense_bwd_bytes(M, N, K, dt)));
+  w.big = bwd_big(M, N, K, dt);
+  w.total = w.dense + round256(!w.big.dx ? moe_dense_bwd_bytes(M, N, K, dt, w.big.dw)
+                               : w.big.runs > 1 ? (size_t)w.big.runs * N * K * 4 : 0);
   if (w.total == 0) w.total = 256;
   return w;
 }
@@ -321,7 +358,7 @@ extern "C" int moe_linear(const void* x, int dt, int M, int N, int K, const void
   if (need > 0) MOE_TRY(moe_need_ptr(ws, fn, "ws", 256));
   if (ws_bytes < need)
     return moe_fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", fn, ws_bytes, need);
-  if (!fwd_big(M, N))
+  if (!fwd_big(M, N, dt))
     return moe_dense_fwd(x, dt, M, N, K, w, bias, act, residual, z, y, ws, s);
   return moe_gmm_linear_fwd(x, dt, M, N, K, w, bias, act, residual, z, y, s);
 }
@@ -371,11 +408,19 @@ extern "C" int moe_linear_bwd(const void* dy, const void* z, const void* x, cons
     if (out != nullptr) dz = out;
   }
   if (db != nullptr) {
-    hipLaunchKernelGGL(linear_db_kernel, dim3((N + 255) / 256), dim3(256), 0, s,
+    hipLaunchKernelGGL(linear_db_kernel, dim3(N / 64), dim3(256), 0, s,
                        (const float*)((char*)ws + lay.part), M > 0 ? lay.parts : 0, N, db);
     MOE_TRY(moe_check_launch(fn));
   }
-  if (M > 0 && !bwd_big(M, N, K))
-    return moe_dense_bwd(dz, x, w, dt, M, N, K, dx, dw, (char*)ws + lay.dense, s);
-  return moe_gmm_linear_bwd(dz, x, w, dt, M, N, K, dx, dw, s);
+  char* const dense = (char*)ws + lay.dense;
+  if (M > 0 && !lay.big.dx) {
+    MOE_TRY(moe_dense_bwd(dz, x, w, dt, M, N, K, dx, lay.big.dw ? nullptr : dw, lay.big.dw, dense,
+                          s));
+    if (!lay.big.dw) return MOE_OK;
+    dx = nullptr;
+  }
+  const int runs = M > 0 ? lay.big.runs : 1;
+  MOE_TRY(moe_gmm_linear_bwd(dz, x, w, dt, M, N, K, dx, dw, runs, (float*)dense, s));
+  return runs > 1 && dw != nullptr ? moe_dense_sum((const float*)dense, runs, N, K, dt, dw, s)
+                                   : MOE_OK;
 }

@@ -66,6 +66,10 @@ BWD = [
     (257, 256, 576, "gelu_tanh", BF), (333, 512, 256, "gelu", F32), (300, 1024, 64, "none", F32),
     (1031, 192, 320, "gelu", BF), (700, 768, 1024, "silu", BF), (2050, 64, 64, "relu", BF),
     (9000, 64, 128, "silu", BF),
+    # the large tiles: for both products, rows cut into runs (the last one
+    # short), and for dW alone
+    (700, 2048, 7680, "gelu_tanh", BF), (7000, 2048, 2048, "silu", BF),
+    (300, 7680, 2048, "none", BF),
 ]
 
 
