@@ -283,6 +283,7 @@ struct DecLds {
   DecDesc desc[DEC_DESCS];
   // words the waves meet in
   int ready;                       // descriptors written, their A operands there
+  int early;                       // one written whose A operand is not there yet: its number + 1
   int parts[DEC_SW];               // units whose partial tiles each streaming wave has left
   int taken;                       // units whose partial tiles were read
   int done;                        // units finished
@@ -325,6 +326,46 @@ typedef const __attribute__((address_space(4))) DecArgs DecConst;
 __device__ __forceinline__ int decode_tables(DecConst& a, DecLds& l) {
   const int lane = threadIdx.x & 63, P = a.T * a.k;
   const bool own = dec_own(a.T, a.k);
+  if (P <= 64 && a.T <= DEC_ROWS) {
+    // a pair a lane, sorted by counting; an expert has one row block at most
+    // (0.4 us, the general way below 2.4)
+    constexpr int NONE = 0x7fff;
+    int g = NONE, rank = lane;
+    if (lane < P) {
+      g = (own ? (int)l.own_idx[lane] : a.idx[lane]) - a.g0;
+      if (g < 0 || g >= a.G) g = NONE;
+      rank = 0;
+    }
+    for (int j = 0; j < P; ++j) {
+      const int o = __builtin_amdgcn_readlane(g, j);
+      rank += lane < P && (o < g || (o == g && j < lane)) ? 1 : 0;
+    }
+    const int n_in = __popcll(__ballot(g != NONE));
+    if (g != NONE) l.order[rank] = (int16_t)lane;
+    const int sorted = __builtin_amdgcn_ds_permute(rank * 4, g);
+    const int left = __shfl_up(sorted, 1, 64);
+    const bool head = sorted != NONE && (lane == 0 || left != sorted);
+    const unsigned long long b = __ballot(head);
+    const int n0 = a.shared ? 1 : 0, n = n0 + __popcll(b);
+    int16_t* const pre_g = (int16_t*)l.cur;
+    if (a.shared && lane == 0) {
+      l.list[0] = -1;
+      l.first[0] = l.pre[0] = pre_g[0] = 0;
+    }
+    if (head) {
+      const int at = n0 + __popcll(b & ((1ull << lane) - 1));
+      l.list[at] = (int16_t)sorted;
+      l.first[at] = (int16_t)lane;
+      l.pre[at] = pre_g[at] = (int16_t)at;
+    }
+    if (lane == 0) {
+      l.first[n] = (int16_t)n_in;
+      l.pre[n] = pre_g[n] = (int16_t)n;
+      l.per_col = n;
+    }
+    lds_drain();
+    return n;
+  }
   for (int g = lane; g < (a.G + 1) / 2; g += 64) l.cur[g] = 0;
   lds_drain();
   // counter of expert g: a half of a word (at most 2048 pairs in all)
@@ -414,6 +455,7 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
   int n_list = -1, n_gu = 0, n_dn = 0;
   const int16_t* const pre_g = (const int16_t*)l.cur;
   bool go = false;       // the activations are complete
+  bool pending = false, watch = false;   // not yet, and units wait for them; this wave looks
   bool lost = false;     // a wait took a second (calls that share a workspace): wait no more
   auto draw = [&]() {
     int v = 0;
@@ -543,42 +585,57 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
       d.word[W_COL] = col;
     }
     lds_drain();
-    const bool wait = kind == U_DOWN && !go;
-    if (lane == 0 && !wait) lds_post(&l.ready, seq + 1);
-    if (uniform(kind) == U_EXIT) break;
-    held = seq == 0 ? draw() : held2;
-    held2 = draw();
+    // The first unit of the second product: for few tokens its weights may come
+    // in before the wait, as many as the rings hold, and the unit behind it is
+    // looked up (one token of 2048 x 1408, 6 experts: 49.2 us
+    // without either, 47.0 with them; 61 tokens of 7680 x 2048: 468 and 472, the
+    // streams run dry to be started anew)
+    const bool first = kind == U_DOWN && !go && !pending;
+    if (first) {
+      pending = true;
+      watch = u == n_route + n_gu;
+      if (n_route == 0 && lane == 0 && !watch) lds_post(&l.early, seq + 1);
+    }
+    if (lane == 0 && !pending) lds_post(&l.ready, seq + 1);
+    if (!pending && uniform(kind) == U_EXIT) break;
+    if (uniform(kind) != U_EXIT) {
+      held = seq == 0 ? draw() : held2;
+      held2 = draw();
+    }
+    if (!pending || (first && n_route == 0)) continue;
     // The second product begins when all activations are complete.  One
     // workgroup, whoever drew its first unit, watches the experts' counters (64
     // at a look) and tells each of the others on a line of its own: 256 of them
     // watching the same lines took so long for every look that the copies
-    // queued behind it in their CUs' memory pipelines stood still.
-    if (wait) {
-      const unsigned long long t0 = wall_clock64();
-      if (u == n_route + n_gu) {
-        int known = 0;
-        while (known < n_list && !lost) {
-          const int q = known + lane;
-          bool there = false;
-          if (q < n_list) {
-            const int gq = l.list[q];
-            there = dev_load(a.act_done + (gq < 0 ? a.G : gq)) >= (pre_g[q + 1] - pre_g[q]) * per_g;
-          }
-          const unsigned long long no = ~__ballot(there);
-          known += no ? __builtin_ctzll(no) : 64;
-          lost = wall_clock64() - t0 > DEC_WAIT_TICKS;
+    // queued behind it in their CUs' memory pipelines stood still.  (It copies
+    // no weights early: its looks would queue behind them.)
+    const unsigned long long t0 = wall_clock64();
+    if (watch) {
+      int known = 0;
+      while (known < n_list && !lost) {
+        const int q = known + lane;
+        bool there = false;
+        if (q < n_list) {
+          const int gq = l.list[q];
+          there = dev_load(args->act_done + (gq < 0 ? args->G : gq)) >=
+                  (pre_g[q + 1] - pre_g[q]) * (args->I / DEC_GU);
         }
-        for (int w = lane; w < (int)gridDim.x; w += 64) dev_store(a.go + w * 32, 1);
-      } else {
-        while (uniform(dev_load(a.go + blockIdx.x * 32)) == 0 && !lost) {
-          lost = wall_clock64() - t0 > DEC_WAIT_TICKS;
-          __builtin_amdgcn_s_sleep(2);
-        }
+        const unsigned long long no = ~__ballot(there);
+        known += no ? __builtin_ctzll(no) : 64;
+        lost = wall_clock64() - t0 > DEC_WAIT_TICKS;
       }
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-      go = true;
-      if (lane == 0) lds_post(&l.ready, seq + 1);
+      for (int w = lane; w < (int)gridDim.x; w += 64) dev_store(args->go + w * 32, 1);
+    } else {
+      while (uniform(dev_load(args->go + blockIdx.x * 32)) == 0 && !lost) {
+        lost = wall_clock64() - t0 > DEC_WAIT_TICKS;
+        __builtin_amdgcn_s_sleep(2);
+      }
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    go = true;
+    pending = false;
+    if (lane == 0) lds_post(&l.ready, seq + 1);
+    if (uniform(kind) == U_EXIT) break;
   }
 }
 
@@ -589,9 +646,9 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
 // i % MT); returns the number of the first unit that has not.  Steps are
 // counted as they are copied (`put`) and read (`got`); a unit's tile is complete
 // when got reaches the put at which its last step was copied.  The copies are
-// at most one unit ahead.
-template <typename T, int AT, int MT>
-__device__ __forceinline__ int stream_units(DecLds& l, int seq) {
+// at most one unit ahead.  early: the first unit's operand is not there yet.
+template <typename T, int AT, int MT, bool OWN>
+__device__ __forceinline__ int stream_units(DecLds& l, int seq, bool early) {
   constexpr int SIZE = 2 + AT, OPS = 4 + 2 * AT, D = DEC_PAGES / SIZE;
   constexpr int NEVER = 0x7fffffff;
   const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
@@ -611,9 +668,13 @@ __device__ __forceinline__ int stream_units(DecLds& l, int seq) {
   uint32_t wslot = 0, rslot = 0;   // byte of the ring
 
   // on to the next unit, if it is known and its operand is there
-  auto bind = [&]() {
+  auto bind = [&](bool early) {
     const int u = at_unit + 1;
-    if (u > seq + 1 || stop || uniform(lds_peek(&l.ready)) <= u) return;
+    if (u > seq + 1 || stop) return;
+    if (!early && uniform(lds_peek(&l.ready)) <= u) {
+      if constexpr (OWN) stop = uniform(lds_peek(&l.early)) == u + 1;   // (a stream of its own)
+      return;
+    }
     asm volatile("" ::: "memory");
     const DecDesc& d = l.desc[u % DEC_DESCS];
     const int word = d.word[lane % W_WORDS];
@@ -645,8 +706,9 @@ __device__ __forceinline__ int stream_units(DecLds& l, int seq) {
     end = put + left;
     if (u == seq) got_end = end;
   };
-  auto copy = [&]() {
-    if (left == 0) bind();
+  // a step's copies: its weights, and (not `early`) its A rows
+  auto copy = [&](auto with_a) {
+    if (with_a() && left == 0) bind(false);
     const int live = uniform(left > 0 ? -1 : 0);
     const i32x4 rw = {uniform(wlo), uniform(whi), uniform(wbytes & live), MOE_RSRC_DW3};
     const i32x4 ra = {uniform(alo), uniform(ahi), uniform(abytes & live), MOE_RSRC_DW3};
@@ -656,8 +718,9 @@ __device__ __forceinline__ int stream_units(DecLds& l, int seq) {
     dma16_nt(rw, p + 1024, wo[1], k0);
     dma16_nt(rw, p + 2048, wo[0], k1);
     dma16_nt(rw, p + 3072, wo[1], k1);
+    if constexpr (with_a())
 #pragma unroll
-    for (int j = 0; j < 2 * AT; ++j) dma16(ra, p + 4096 + j * 1024, ao[j], k0);
+      for (int j = 0; j < 2 * AT; ++j) dma16(ra, p + 4096 + j * 1024, ao[j], k0);
     wslot = (uint32_t)uniform((int)(wslot + SIZE * DEC_PAGE == D * SIZE * DEC_PAGE
                                         ? 0 : wslot + SIZE * DEC_PAGE));
     k = uniform(k + DEC_SW * 128);
@@ -667,12 +730,31 @@ __device__ __forceinline__ int stream_units(DecLds& l, int seq) {
   f32x4 acc[MT][2];
 #pragma unroll
   for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = f32x4{0, 0, 0, 0};
-  lds_wait(&l.taken, seq);         // (units of another kind may have used all of red)
   const int f0 = stream_frag(0), f1 = stream_frag(1);
+  if (OWN && early) {
+    // the weights of as many steps as the ring holds, then, when it is there,
+    // the operand; the loop below finds D steps copied either way
+    bind(true);
+    const int steps = left;
 #pragma unroll 1
-  for (int d = 0; d < D - 1; ++d) copy();
+    for (int d = 0; d < D; ++d) copy(std::false_type());
+    lds_wait(&l.ready, seq + 1);
+#pragma unroll 1
+    for (int d = 0; d < D; ++d) {
+      const int live = uniform(d < steps ? -1 : 0);
+      const i32x4 ra = {uniform(alo), uniform(ahi), uniform(abytes & live), MOE_RSRC_DW3};
+      const uint32_t p = (uint32_t)uniform((int)(lds + d * SIZE * DEC_PAGE + 4096));
+#pragma unroll
+      for (int j = 0; j < 2 * AT; ++j)
+        dma16(ra, p + j * 1024, ao[j], uniform((wave + d * DEC_SW) * 128 & live));
+    }
+    vm_drain<0>();
+  } else {
+#pragma unroll 1
+    for (int d = 0; d < D; ++d) copy(std::true_type());
+  }
+  lds_wait(&l.taken, seq);         // (units of another kind may have used all of red)
   for (;;) {
-    copy();                        // into the slot read last
     vm_drain<(D - 1) * OPS>();     // the oldest step has landed
     const char* p = ring + rslot;
     u32x4 w[2][2], x[2][AT];
@@ -716,6 +798,7 @@ __device__ __forceinline__ int stream_units(DecLds& l, int seq) {
       got_end = at_unit == seq ? end : NEVER;
     }
     if (stop && at_unit < seq) break;
+    copy(std::true_type());        // into the slot read last
   }
   vm_drain<0>();                   // (empty copies)
   return seq;
@@ -725,23 +808,30 @@ template <typename T, int V, bool OWN>
 __device__ __forceinline__ void decode_stream(const DecArgs& a, DecLds& l) {
   const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
   for (int seq = 0;;) {
-    lds_wait(&l.ready, seq + 1);
+    bool early = false;
+    for (;;) {
+      if (uniform(lds_peek(&l.ready)) > seq) break;
+      if constexpr (OWN) early = uniform(lds_peek(&l.early)) == seq + 1;
+      if (early) break;
+      __builtin_amdgcn_s_sleep(1);
+    }
+    asm volatile("" ::: "memory");
     const DecDesc& d = l.desc[seq % DEC_DESCS];
     const int kind = uniform(d.word[W_KIND]);
     if (kind == U_EXIT) break;
     if (kind <= U_DOWN) {
       if constexpr (!OWN) {
         if (uniform(d.word[W_MT]) == 2) {
-          seq = stream_units<T, 2, 2>(l, seq);
+          seq = stream_units<T, 2, 2, false>(l, seq, early);
           continue;
         }
         if constexpr (DEC_PLANES<T> == 2)
           if (uniform(d.word[W_AT]) == 2) {
-            seq = stream_units<T, 2, 1>(l, seq);
+            seq = stream_units<T, 2, 1, false>(l, seq, early);
             continue;
           }
       }
-      seq = stream_units<T, 1, 1>(l, seq);
+      seq = stream_units<T, 1, 1, OWN>(l, seq, early);
       continue;
     }
     if constexpr (!OWN) {
@@ -777,29 +867,28 @@ __device__ __forceinline__ void elem_store(void* p, long long i, float v) {
   else ((T*)p)[i] = v;
 }
 
-// y[t, h] = residual + shared + sum_j gate yp[t, j], in that order; pair(p)
-// gives a pair's expert and gate
+// residual + shared + sum_j gate yp[t, j], in that order; pair(p) gives a
+// pair's expert and gate.  (For a pair outside the window row 0 is read, and not
+// added: a branch for each would have every load waited for in turn.)
 template <typename T, typename Pair>
-__device__ __forceinline__ void decode_sum(const DecArgs& a, int t, int h, Pair&& pair) {
-  const long long at = (long long)t * a.H + h;
-  float s = a.residual != nullptr ? elem_load<T>(a.residual, at) : 0.f;
+__device__ __forceinline__ float decode_sum(const DecArgs& a, int t, int h, Pair&& pair) {
+  float s = a.residual != nullptr ? elem_load<T>(a.residual, (long long)t * a.H + h) : 0.f;
   if (a.shared) s += a.yp[((long long)a.T * a.k + t) * a.H + h];
   for (int j0 = 0; j0 < a.k; j0 += 8) {
     float gate[8], v[8];
+    bool in[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       const int p = t * a.k + min(j0 + q, a.k - 1);
       int e;
-      float w;
-      pair(p, e, w);
-      const bool in = j0 + q < a.k && e >= a.g0 && e - a.g0 < a.G;
-      gate[q] = in ? w : 0.f;
-      v[q] = in ? a.yp[(long long)p * a.H + h] : 0.f;
+      pair(p, e, gate[q]);
+      in[q] = j0 + q < a.k && e >= a.g0 && e - a.g0 < a.G;
+      v[q] = a.yp[(long long)(in[q] ? p : 0) * a.H + h];
     }
 #pragma unroll
-    for (int q = 0; q < 8; ++q) s += gate[q] * v[q];
+    for (int q = 0; q < 8; ++q) s += in[q] ? gate[q] * v[q] : 0.f;
   }
-  elem_store<T>(a.y, at, s);
+  return s;
 }
 
 template <typename T>
@@ -808,13 +897,20 @@ __device__ __forceinline__ void decode_finish(const DecArgs& a, DecLds& l) {
   const bool fused = a.T <= DEC_FUSED_T;
   const long long plane = (long long)(P + a.T) * a.I;
   const bool own = dec_own(a.T, a.k);
-  auto sum_block = [&](int col) {
-    for (int t = lane >> 5; t < a.T; t += 2)
-      decode_sum<T>(a, t, col + (lane & 31), [&](int p, int& e, float& w) {
+  auto sum_block = [&](int col, int n) {
+#pragma unroll 1
+    for (int t0 = 0; t0 < a.T; t0 += 2) {
+      const int t = t0 + (lane >> 5), h = col + (lane & 31);
+      const float s = decode_sum<T>(a, min(t, a.T - 1), h, [&](int p, int& e, float& w) {
         e = own ? (int)l.own_idx[p & (DEC_OWN_PAIRS - 1)] : a.idx[p];
         w = own ? l.own_gate[p & (DEC_OWN_PAIRS - 1)] : a.gate[p];
       });
+      if (t < n) elem_store<T>(a.y, (long long)t * a.H + h, s);
+    }
   };
+  // Once for nothing, while the first unit streams: a first pass through this
+  // code waits for every line of it, 4 us that would end the call.
+  if (fused && own) sum_block(0, 0);
   for (int seq = 0;; ++seq) {
     lds_wait(&l.ready, seq + 1);
     const DecDesc& d = l.desc[seq % DEC_DESCS];
@@ -886,7 +982,7 @@ __device__ __forceinline__ void decode_finish(const DecArgs& a, DecLds& l) {
                                           __HIP_MEMORY_SCOPE_AGENT);
         if (uniform(before) == uniform(lds_peek(&l.per_col)) - 1) {
           __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-          sum_block(col);
+          sum_block(col, a.T);
         }
       }
     } else {
@@ -894,7 +990,7 @@ __device__ __forceinline__ void decode_finish(const DecArgs& a, DecLds& l) {
       if (kind == U_ROUTE) {
         if (lane == 0) dev_add(a.routed, min(DEC_SW, a.T - col));
       } else {
-        sum_block(col);
+        sum_block(col, a.T);
       }
     }
     if (lane == 0) lds_post(&l.done, seq + 1);
@@ -905,11 +1001,11 @@ template <typename T, int V, bool OWN>
 __global__ __launch_bounds__(DEC_NT) void decode_kernel(DecArgs a) {
   __shared__ __attribute__((aligned(1024))) DecLds l;
   if (threadIdx.x < DEC_SW) l.parts[threadIdx.x] = 0;
-  if (threadIdx.x == 0) l.ready = l.taken = l.done = 0;
+  if (threadIdx.x == 0) l.ready = l.early = l.taken = l.done = 0;
   const int wave = uniform((int)(threadIdx.x >> 6));
-  if (OWN && wave < DEC_SW) {
+  if constexpr (OWN) {
     const bool keep = blockIdx.x == 0;   // (one of them writes the choices out)
-    for (int t = wave; t < a.T; t += DEC_SW)
+    for (int t = wave; t < a.T; t += DEC_SW + 2)
       decode_route_token<V>(a, t, keep, [&](int slot, int e, float gate) {
         const int p = t * a.k + slot;
         l.own_idx[p & (DEC_OWN_PAIRS - 1)] = (int16_t)e;
@@ -933,11 +1029,12 @@ __global__ __launch_bounds__(DEC_NT) void decode_kernel(DecArgs a) {
 template <typename T>
 __global__ __launch_bounds__(256) void decode_sum_kernel(DecArgs a) {
   const int h = blockIdx.x * 256 + threadIdx.x;
-  if (h < a.H)
-    decode_sum<T>(a, blockIdx.y, h, [&](int p, int& e, float& w) {
-      e = a.idx[p];
-      w = a.gate[p];
-    });
+  if (h >= a.H) return;
+  const float s = decode_sum<T>(a, blockIdx.y, h, [&](int p, int& e, float& w) {
+    e = a.idx[p];
+    w = a.gate[p];
+  });
+  elem_store<T>(a.y, (long long)blockIdx.y * a.H + h, s);
 }
 
 // ---------------------------------------------------------------- host side
