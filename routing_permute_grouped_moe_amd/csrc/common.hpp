@@ -186,5 +186,8 @@ size_t moe_dense_fwd_bytes(int M, int N, int K, int dt);
 size_t moe_dense_bwd_bytes(int M, int N, int K, int dt, bool dx_only);
 int moe_dense_fwd(const void* x, int dt, int M, int N, int K, const void* w, const float* bias,
                   int act, const void* residual, void* z, void* y, void* ws, hipStream_t s);
+// and db (if not null) from `parts` rows of column sums of dz
+int moe_dense_db(const float* sums, int parts, int N, float* db, hipStream_t s);
 int moe_dense_bwd(const void* dz, const void* x, const void* w, int dt, int M, int N, int K,
-                  void* dx, void* dw, bool dx_only, void* ws, hipStream_t s);
+                  void* dx, void* dw, bool dx_only, const float* sums,
+                  int parts, float* db, void* ws, hipStream_t s);

@@ -281,12 +281,38 @@ __global__ __launch_bounds__(256) void dense_fwd_kernel(DenseArgs a) {
   dense_unit<T, false, false, BT>(a, xcd_unit(blockIdx.x, gridDim.x), smem);
 }
 
+// db = sum of the blocks' column sums of dz: four threads a column, each over a
+// quarter of the blocks in order, then the four in order.  Workgroup b takes 64
+// columns (N is a multiple of 64).
+struct DbArgs {
+  const float* sums; int parts, N; float* db;
+};
+__device__ __forceinline__ void dense_db(const DbArgs& a, int b, double* red) {
+  const int c = threadIdx.x & 63, q = threadIdx.x >> 6, n = b * 64 + c;
+  const int per = (a.parts + 3) / 4, p1 = min(a.parts, (q + 1) * per);
+  double s = 0;
+#pragma unroll 8
+  for (int p = q * per; p < p1; ++p) s += a.sums[(long long)p * a.N + n];
+  red[q * 64 + c] = s;
+  __syncthreads();
+  if (q == 0) a.db[n] = (float)(((red[c] + red[64 + c]) + red[128 + c]) + red[192 + c]);
+}
+__global__ __launch_bounds__(256) void dense_db_kernel(DbArgs a) {
+  __shared__ double red[256];
+  dense_db(a, blockIdx.x, red);
+}
+
 // dx (A = dz K-contiguous, B = W with rows along K) and dW (both operands
-// with rows along K): units of dx first
+// with rows along K): units of dx first; then the bias gradient
 template <typename T, int BT>
-__global__ __launch_bounds__(256) void dense_bwd_kernel(DenseArgs dx, DenseArgs dw) {
+__global__ __launch_bounds__(256) void dense_bwd_kernel(DenseArgs dx, DenseArgs dw, DbArgs db) {
   __shared__ __attribute__((aligned(1024))) char smem[D_RING<BT>];
-  const int u = xcd_unit(blockIdx.x, gridDim.x), n = dx.S * dx.mt * dx.nt;
+  const int n = dx.S * dx.mt * dx.nt, units = n + dw.S * dw.mt * dw.nt;
+  if ((int)blockIdx.x >= units) {
+    dense_db(db, blockIdx.x - units, (double*)smem);
+    return;
+  }
+  const int u = xcd_unit(blockIdx.x, units);
   if (u < n) dense_unit<T, false, true, BT>(dx, u, smem);
   else dense_unit<T, true, true, BT>(dw, u - n, smem);
 }
@@ -403,8 +429,14 @@ int moe_dense_fwd(const void* x, int dt, int M, int N, int K, const void* w, con
   return moe_check_launch(fn);
 }
 
+int moe_dense_db(const float* sums, int parts, int N, float* db, hipStream_t s) {
+  hipLaunchKernelGGL(dense_db_kernel, dim3(N / 64), dim3(256), 0, s, DbArgs{sums, parts, N, db});
+  return moe_check_launch("moe_linear_bwd");
+}
+
 int moe_dense_bwd(const void* dz, const void* x, const void* w, int dt, int M, int N, int K,
-                  void* dx, void* dw, bool dx_only, void* ws, hipStream_t s) {
+                  void* dx, void* dw, bool dx_only, const float* sums,
+                  int parts, float* db, void* ws, hipStream_t s) {
   const char* fn = "moe_linear_bwd";
   BwdPlan p = bwd_args(M, N, K, dt, dx_only);
   DenseArgs &a = p.dx, &b = p.dw;
@@ -412,14 +444,15 @@ int moe_dense_bwd(const void* dz, const void* x, const void* w, int dt, int M, i
   b.A = dz; b.B = x; b.C = dw; b.part = (float*)((char*)ws + part_bytes(a));
   if (dx == nullptr) a.mt = a.nt = 0;   // no units, no sums
   if (dw == nullptr) b.mt = b.nt = 0;
-  const dim3 grid(a.S * a.mt * a.nt + b.S * b.mt * b.nt), block(256);
+  const DbArgs c = {sums, parts, N, db};
+  const dim3 grid(a.S * a.mt * a.nt + b.S * b.mt * b.nt + (db != nullptr ? N / 64 : 0)), block(256);
   if (grid.x == 0) return MOE_OK;
   if (dt == MOE_BF16) {
-    if (p.bt == 128) hipLaunchKernelGGL((dense_bwd_kernel<bf16_t, 128>), grid, block, 0, s, a, b);
-    else hipLaunchKernelGGL((dense_bwd_kernel<bf16_t, 64>), grid, block, 0, s, a, b);
+    if (p.bt == 128) hipLaunchKernelGGL((dense_bwd_kernel<bf16_t, 128>), grid, block, 0, s, a, b, c);
+    else hipLaunchKernelGGL((dense_bwd_kernel<bf16_t, 64>), grid, block, 0, s, a, b, c);
   } else {
-    if (p.bt == 128) hipLaunchKernelGGL((dense_bwd_kernel<float, 128>), grid, block, 0, s, a, b);
-    else hipLaunchKernelGGL((dense_bwd_kernel<float, 64>), grid, block, 0, s, a, b);
+    if (p.bt == 128) hipLaunchKernelGGL((dense_bwd_kernel<float, 128>), grid, block, 0, s, a, b, c);
+    else hipLaunchKernelGGL((dense_bwd_kernel<float, 64>), grid, block, 0, s, a, b, c);
   }
   MOE_TRY(moe_check_launch(fn));
   auto blocks = [](const DenseArgs& q) {

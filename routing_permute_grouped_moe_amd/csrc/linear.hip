@@ -229,22 +229,6 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const T* __restrict__ dy
   }
 }
 
-// db = sum of the blocks' column sums: four threads a column, each over a
-// quarter of the blocks in order, then the four in order
-__global__ __launch_bounds__(256) void linear_db_kernel(const float* __restrict__ part, int parts,
-                                                        int N, float* __restrict__ db) {
-  __shared__ double red[4][64];
-  const int c = threadIdx.x & 63, q = threadIdx.x >> 6;
-  const int n = blockIdx.x * 64 + c;       // (N is a multiple of 64)
-  const int per = (parts + 3) / 4, p1 = min(parts, (q + 1) * per);
-  double s = 0;
-#pragma unroll 8
-  for (int p = q * per; p < p1; ++p) s += part[(long long)p * N + n];
-  red[q][c] = s;
-  __syncthreads();
-  if (q == 0) db[n] = (float)(((red[0][c] + red[1][c]) + red[2][c]) + red[3][c]);
-}
-
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 // The 256 x 256 tiles of the grouped GEMM (bf16; in fp32 the smaller ones are
@@ -407,17 +391,16 @@ extern "C" int moe_linear_bwd(const void* dy, const void* z, const void* x, cons
     MOE_TRY(moe_check_launch(fn));
     if (out != nullptr) dz = out;
   }
-  if (db != nullptr) {
-    hipLaunchKernelGGL(linear_db_kernel, dim3(N / 64), dim3(256), 0, s,
-                       (const float*)((char*)ws + lay.part), M > 0 ? lay.parts : 0, N, db);
-    MOE_TRY(moe_check_launch(fn));
-  }
+  const float* const sums = (const float*)((char*)ws + lay.part);
+  const int parts = M > 0 ? lay.parts : 0;
   char* const dense = (char*)ws + lay.dense;
   if (M > 0 && !lay.big.dx) {
-    MOE_TRY(moe_dense_bwd(dz, x, w, dt, M, N, K, dx, lay.big.dw ? nullptr : dw, lay.big.dw, dense,
-                          s));
+    MOE_TRY(moe_dense_bwd(dz, x, w, dt, M, N, K, dx, lay.big.dw ? nullptr : dw, lay.big.dw, sums,
+                          parts, db, dense, s));
     if (!lay.big.dw) return MOE_OK;
     dx = nullptr;
+  } else if (db != nullptr) {
+    MOE_TRY(moe_dense_db(sums, parts, N, db, s));
   }
   const int runs = M > 0 ? lay.big.runs : 1;
   MOE_TRY(moe_gmm_linear_bwd(dz, x, w, dt, M, N, K, dx, dw, runs, (float*)dense, s));
