@@ -337,39 +337,48 @@ __global__ __launch_bounds__(256) void dense_sum_kernel(DenseArgs a, DenseArgs b
 constexpr int D_MAX_S = 16;
 
 // Tile size: 128 x 128 tiles move half the bytes per flop of 64 x 64 ones, so
-// they are taken as soon as there are 32 of them.  Slices: as many as give the
-// chip two workgroups a CU while each keeps 1024 of K (419 x 2048 x 8192: 28 us
-// with 8 slices, 30 with 4), else one a CU while each keeps 256 (128 x 8192 x
-// 2048: 17 us with 4 slices, 21 with 8: more partial sums to write and read).
-// fp32's matrix rate is a sixteenth, so its slices are never short of loads.
-struct Plan {
-  int bt;
-  void slices(DenseArgs& a, int es, int wgs) const {
-    a.mt = (a.M + bt - 1) / bt;
-    a.nt = (a.N + bt - 1) / bt;
-    const int bk = D_ROWB / es, tiles = a.mt * a.nt > 0 ? a.mt * a.nt : 1;
-    const int least = es == 2 ? 256 : 64;          // K of the shortest slice
-    int s = 2 * wgs / tiles;
-    if (es == 4 || (long long)s * 4 * least > a.K) {
-      s = wgs / tiles;
-      s = s < a.K / least ? s : a.K / least;
-    }
-    s = s < D_MAX_S ? s : D_MAX_S;
-    s = s > 1 ? s : 1;
-    a.kslice = ((a.K + s - 1) / s + bk - 1) / bk * bk;
-    if (a.kslice < bk) a.kslice = bk;              // (no rows: K = 0)
-    a.S = a.K > 0 ? (a.K + a.kslice - 1) / a.kslice : 1;
-  }
-};
+// bf16 takes them as soon as there are 32.  In fp32, at a sixteenth of the
+// matrix rate, the bytes matter less than an even share of the work: 1000 x 1024
+// x 1024 (64 large tiles) takes 31 us on small ones and 34 on large, 600 x 2048 x
+// 1600 (80) takes 60 and 48.
+int plan_tile(long long M, long long N, int es) {
+  return ((M + 127) / 128) * ((N + 127) / 128) >= (es == 4 ? 72 : 32) ? 128 : 64;
+}
 
-int plan_tile(long long M, long long N) {
-  return ((M + 127) / 128) * ((N + 127) / 128) >= 32 ? 128 : 64;
+// tiles of a product; returns their number times K
+double plan_tiles(DenseArgs& a, int bt) {
+  a.mt = (a.M + bt - 1) / bt;
+  a.nt = (a.N + bt - 1) / bt;
+  return (double)a.mt * a.nt * a.K;
+}
+// K of a slice, for a launch of `work` tiles times K in all: 512 slices, two
+// workgroups a CU, while they stay long enough to be worth their ramp and their
+// partial sums (419 x 2048 x 8192: 28 us with 8 slices a tile, 30 with 4), else
+// one a CU (128 x 8192 x 2048: 17 us with 4 slices, 21 with 8).  Both products
+// of a backward are cut to the same length: 700 x 2048 x 1600 in fp32 takes 98
+// us so, 248 when each is given half of the chip.
+double plan_length(double work, int es) {
+  const double two = es == 2 ? 640 : 256, least = es == 2 ? 256 : 64;
+  double l = work / 512;
+  if (l < two) l = work / 256;
+  return l > least ? l : least;
+}
+void plan_slices(DenseArgs& a, int es, double length, double round) {
+  const int bk = D_ROWB / es;
+  int s = (int)(a.K / length + round);
+  s = s < D_MAX_S ? s : D_MAX_S;
+  s = s > 1 ? s : 1;
+  a.kslice = ((a.K + s - 1) / s + bk - 1) / bk * bk;
+  if (a.kslice < bk) a.kslice = bk;              // (no rows: K = 0)
+  a.S = a.K > 0 ? (a.K + a.kslice - 1) / a.kslice : 1;
 }
 
 DenseArgs fwd_args(int M, int N, int K, int dt) {
   DenseArgs a = {};
   a.M = M; a.N = N; a.K = K; a.lda = K; a.ldb = K;
-  Plan{plan_tile(M, N)}.slices(a, moe_dt_bytes(dt), 256);
+  const int es = moe_dt_bytes(dt);
+  const double work = plan_tiles(a, plan_tile(M, N, es));
+  plan_slices(a, es, plan_length(work, es), 1e-6);   // (no more than that)
   return a;
 }
 
@@ -379,13 +388,15 @@ struct BwdPlan {
 };
 BwdPlan bwd_args(int M, int N, int K, int dt, bool dx_only) {
   BwdPlan p = {};
-  p.bt = plan_tile(dx_only ? M : M + N, K);
+  const int es = moe_dt_bytes(dt);
+  p.bt = plan_tile(dx_only ? M : M + N, K, es);
   p.dx.M = M; p.dx.N = K; p.dx.K = N; p.dx.lda = N; p.dx.ldb = K;
   p.dw.M = N; p.dw.N = K; p.dw.K = M; p.dw.lda = N; p.dw.ldb = K;
-  const int es = moe_dt_bytes(dt);
-  // the two products share the chip by their work, 2 M N K each
-  Plan{p.bt}.slices(p.dx, es, dx_only ? 256 : 128);
-  Plan{p.bt}.slices(p.dw, es, 128);
+  double work = plan_tiles(p.dx, p.bt);
+  if (!dx_only) work += plan_tiles(p.dw, p.bt);
+  const double length = plan_length(work, es);
+  plan_slices(p.dx, es, length, 0.5);
+  plan_slices(p.dw, es, length, 0.5);
   return p;
 }
 
@@ -411,7 +422,7 @@ int moe_dense_fwd(const void* x, int dt, int M, int N, int K, const void* w, con
   a.A = x; a.B = w; a.C = y; a.part = (float*)ws;
   a.bias = bias; a.res = residual; a.z = z; a.act = act;
   const dim3 grid(a.S * a.mt * a.nt), block(256);
-  const bool big = plan_tile(M, N) == 128;
+  const bool big = plan_tile(M, N, moe_dt_bytes(dt)) == 128;
   if (dt == MOE_BF16) {
     if (big) hipLaunchKernelGGL((dense_fwd_kernel<bf16_t, 128>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((dense_fwd_kernel<bf16_t, 64>), grid, block, 0, s, a);
