@@ -1052,7 +1052,7 @@ int router_slices(int H, int E) {
 // Row tiles of the gate/up units: two where an expert is likely to have more
 // rows than one tile holds (its mean over 8, or the shared expert's all): its
 // weights are then read once, not once a tile.  Measured, one tile and two:
-// 128 tokens of 64 experts, 8 each (mean 16) 300 and 273 us; 61 tokens and the
+// 128 tokens of 64 experts, 6 each (mean 12) 300 and 273 us; 61 tokens and the
 // shared expert 485 and 473 us.
 constexpr int GU_MEAN = 8;
 int gateup_tiles(bool shared, int T, int E, int k) {

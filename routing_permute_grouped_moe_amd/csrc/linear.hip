@@ -5,8 +5,9 @@
 // Few rows (decode batches) run as a stream of W (stream.hpp); large products
 // run on the grouped GEMM's 256 x 256 tiles (gmm.hip), those between on
 // smaller tiles (dense.hip).  The epilogues take the bias, activation and
-// residual, and the two products of the backward share one launch.  What is here: the few-row kernel, the elementwise half of the
-// backward, the checks and the choice between the kernels.
+// residual, and the two products of the backward share one launch.  What is
+// here: the few-row kernel, the elementwise half of the backward, the checks
+// and the choice between the kernels.
 #include <type_traits>
 
 #include "act.hpp"
@@ -246,8 +247,9 @@ bool fwd_big(int M, int N, int dt) {
 // together.  Where a dx tile (N deep) would take more than 3 times a workgroup's
 // share of the work, dx goes to the smaller tiles in slices, in a launch of its
 // own (1000 x 7680 x 2048: 100 us, 203 together, 177 all in smaller tiles; 200 x
-// 8192 x 8192: 122, 236 and 324), and where a dW tile (M deep) would take more than its share,
-// M is cut into `runs` (8192 x 2048 x 2048: 228 us, 302 in one run).
+// 8192 x 8192: 122, 236 and 324), and where a dW tile (M deep) would take more
+// than its share, M is cut into `runs` (8192 x 2048 x 2048: 228 us, 302 in one
+// run).
 struct BwdBig {
   bool dx, dw;    // these tiles for this product
   int runs;
@@ -264,7 +266,8 @@ BwdBig bwd_big(int M, int N, int K, int dt) {
 }
 
 size_t fwd_ws(int M, int N, int K, int dt) {
-  return few_rows(M, N, K, dt) || fwd_big(M, N, dt) ? 0 : round256(moe_dense_fwd_bytes(M, N, K, dt));
+  return few_rows(M, N, K, dt) || fwd_big(M, N, dt) ? 0
+                                                    : round256(moe_dense_fwd_bytes(M, N, K, dt));
 }
 
 struct BwdWs {
