@@ -288,6 +288,7 @@ struct DecLds {
   int taken;                       // units whose partial tiles were read
   int done;                        // units finished
   int per_col;                     // units of a column block
+  int lost;                        // a wait was given up: what it waited for is not there
 };
 static_assert(sizeof(DecLds) <= 160 * 1024, "LDS of a CU");
 
@@ -456,7 +457,8 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
   const int16_t* const pre_g = (const int16_t*)l.cur;
   bool go = false;       // the activations are complete
   bool pending = false, watch = false;   // not yet, and units wait for them; this wave looks
-  bool lost = false;     // a wait took a second (calls that share a workspace): wait no more
+  bool lost = false;     // a wait took a second (calls that share a workspace): wait no more,
+                         // and what this workgroup adds to the result is NaN
   auto draw = [&]() {
     int v = 0;
     if (lane == 0)
@@ -500,6 +502,7 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
             __builtin_amdgcn_s_sleep(1);
           }
           __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+          if (lost && lane == 0) lds_post(&l.lost, 1);
         }
         n_list = decode_tables(a, l);
         n_gu = pre_g[n_list] * per_g;
@@ -634,6 +637,7 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
     go = true;
     pending = false;
+    if (lost && lane == 0) lds_post(&l.lost, 1);
     if (lane == 0) lds_post(&l.ready, seq + 1);
     if (uniform(kind) == U_EXIT) break;
   }
@@ -717,7 +721,7 @@ __device__ __forceinline__ int stream_units(DecLds& l, int seq, bool early) {
     dma16_nt(rw, p, wo[0], k0);
     dma16_nt(rw, p + 1024, wo[1], k0);
     dma16_nt(rw, p + 2048, wo[0], k1);
-    dma16_nt(rw, p + 3072, wo[1], k1);
+    dma16_nt(rw, p + 3 * 1024, wo[1], k1);
     if constexpr (with_a())
 #pragma unroll
       for (int j = 0; j < 2 * AT; ++j) dma16(ra, p + 4096 + j * 1024, ao[j], k0);
@@ -924,6 +928,7 @@ __device__ __forceinline__ void decode_finish(const DecArgs& a, DecLds& l) {
       const int n = w(W_N);
       const bool packed = w(W_PACKED);
       const int mt = w(W_MT);
+      const bool lost = uniform(lds_peek(&l.lost)) != 0;   // NaN, not a wrong answer
       float v[2][2][4];   // [row tile][weight tile][register]
 #pragma unroll
       for (int m = 0; m < 2; ++m)
@@ -967,6 +972,7 @@ __device__ __forceinline__ void decode_finish(const DecArgs& a, DecLds& l) {
                 dev_store((float*)a.act + at, s);
               }
             } else {
+              if (lost) s0 = s1 = __uint_as_float(0x7fc00000u);
               float* out = a.yp + (long long)row * a.H + col + c;
               dev_store(out, s0);
               dev_store(out + 16, s1);
@@ -1001,7 +1007,7 @@ template <typename T, int V, bool OWN>
 __global__ __launch_bounds__(DEC_NT) void decode_kernel(DecArgs a) {
   __shared__ __attribute__((aligned(1024))) DecLds l;
   if (threadIdx.x < DEC_SW) l.parts[threadIdx.x] = 0;
-  if (threadIdx.x == 0) l.ready = l.early = l.taken = l.done = 0;
+  if (threadIdx.x == 0) l.ready = l.early = l.taken = l.done = l.lost = 0;
   const int wave = uniform((int)(threadIdx.x >> 6));
   if constexpr (OWN) {
     const bool keep = blockIdx.x == 0;   // (one of them writes the choices out)

@@ -332,7 +332,7 @@ extern "C" int moe_linear(const void* x, int dt, int M, int N, int K, const void
   MOE_TRY(moe_opt_ptr(residual, fn, "residual"));
   MOE_TRY(moe_opt_ptr(z, fn, "z"));
   MOE_TRY(moe_need_ptr(y, fn, "y"));
-  if (y == x || z == x || (z != nullptr && (z == y || z == residual)))
+  if (y == x || y == w || z == x || (z != nullptr && z == w) || (z != nullptr && (z == y || z == residual)))
     return moe_fail(MOE_ERR_INVALID_ARG, "%s: y and z need buffers of their own (y may be residual's)",
                     fn);
   hipStream_t s = (hipStream_t)stream;
@@ -370,8 +370,13 @@ extern "C" int moe_linear_bwd(const void* dy, const void* z, const void* x, cons
     if (act != MOE_ACT_NONE) MOE_TRY(moe_need_ptr(z, fn, "z"));
     if (dw != nullptr) MOE_TRY(moe_need_ptr(x, fn, "x"));
     if (dx != nullptr) MOE_TRY(moe_need_ptr(w, fn, "w"));
-    if (dx != nullptr && (dx == dy || dx == z || dx == x))
-      return moe_fail(MOE_ERR_INVALID_ARG, "%s: dx needs a buffer of its own", fn);
+    // (both products read dy or dz, and x or W, to the end of the launch)
+    auto taken = [&](const void* p) {
+      return p != nullptr && (p == dy || p == z || p == x || p == w);
+    };
+    if (taken(dx) || taken(dw) || taken(db) || (dx != nullptr && dx == dw))
+      return moe_fail(MOE_ERR_INVALID_ARG, "%s: %s needs a buffer of its own", fn,
+                      taken(dx) ? "dx" : taken(db) ? "db" : "dw");
     MOE_TRY(moe_need_ptr(ws, fn, "ws", 256));
     if (ws_bytes < lay.total)
       return moe_fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", fn, ws_bytes,

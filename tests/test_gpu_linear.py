@@ -69,7 +69,7 @@ BWD = [
     # the large tiles: for both products, rows cut into runs (the last one
     # short), and for dW alone
     (700, 2048, 7680, "gelu_tanh", BF), (7000, 2048, 2048, "silu", BF),
-    (300, 7680, 2048, "none", BF),
+    (300, 7680, 2048, "none", BF), (30001, 256, 512, "relu", BF),
 ]
 
 
@@ -150,6 +150,32 @@ def test_parts_of_the_gradient_and_no_rows():
     assert dx0.shape == (0, K) and (dw0 == 0).all() and (db0 == 0).all()
     y, zz = op.forward(x[:0], save_z=True)
     assert y.shape == (0, N) and zz.shape == (0, N)
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 7680, 2048), (30001, 256, 512), (700, 2048, 7680)])
+def test_parts_of_the_gradient_of_large_products(M, N, K):
+    """dx in slices beside a dW of large tiles; dW in runs of rows; neither: each
+    gradient alone, and on a stream of its own, gives the bits it has with the
+    others."""
+    from routing_permute_grouped_moe_amd import abi
+    from routing_permute_grouped_moe_amd.layer import Linear
+    n = normal(9)
+    x, w, dy, z = n(M, K), n(N, K, std=0.05), n(M, N), n(M, N)
+    op = Linear(w, act="silu")
+    want = op.backward(dy, x, z=z, bias_grad=True)
+    ws = torch.empty(abi.moe_linear_bwd_workspace_bytes(M, N, K, op.dt, op.act),
+                     dtype=torch.uint8, device="cuda")
+    for part in range(3):
+        outs = [torch.full_like(t, 7.0) if i == part else None for i, t in enumerate(want)]
+        abi.moe_linear_bwd(dy, z, x, w, op.dt, M, N, K, op.act, *outs, ws, ws.numel())
+        assert torch.equal(outs[part], want[part])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    other = op.backward(dy, x, z=z, bias_grad=True, stream=side)
+    again = op.backward(dy, x, z=z, bias_grad=True)
+    torch.cuda.synchronize()
+    for a, b, c in zip(want, other, again):
+        assert torch.equal(a, b) and torch.equal(a, c)
 
 
 def test_extreme_pre_activations():

@@ -101,6 +101,7 @@ LINEAR = dict(x=P, dt=1, M=4, N=128, K=64, w=P, bias=None, act=0, residual=None,
     ({"y": None}, "INVALID_ARG", "y is NULL"),
     ({"y": P}, "INVALID_ARG", "buffers of their own"),
     ({"z": 2 * P}, "INVALID_ARG", "buffers of their own"),
+    ({"w": 2 * P}, "INVALID_ARG", "buffers of their own"),
     ({"z": 3 * P, "residual": 3 * P}, "INVALID_ARG", "buffers of their own"),
     ({"M": 100, "K": 4096}, "INVALID_ARG", "ws is NULL"),
     ({"M": 100, "K": 4096, "ws": P, "ws_bytes": 256}, "WORKSPACE", "workspace 256"),
@@ -129,6 +130,9 @@ BWD = dict(dy=P, z=P, x=P, w=P, dt=1, M=4, N=128, K=64, act=2, dx=2 * P, dw=3 * 
     ({"dw": ODD}, "INVALID_ARG", "dw"),
     ({"db": ODD}, "INVALID_ARG", "db"),
     ({"dx": P}, "INVALID_ARG", "buffer of its own"),
+    ({"dw": P}, "INVALID_ARG", "dw needs a buffer of its own"),
+    ({"db": P}, "INVALID_ARG", "db needs a buffer of its own"),
+    ({"dw": 2 * P}, "INVALID_ARG", "dw needs a buffer of its own"),
     ({"ws": None}, "INVALID_ARG", "ws"),
     ({"ws_bytes": 64}, "WORKSPACE", "workspace 64"),
     ({"M": 1 << 15, "K": 1 << 15}, "UNSUPPORTED", "2 GiB"),
