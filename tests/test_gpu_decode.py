@@ -89,6 +89,40 @@ def test_layer(T, H, I, E, k, extra):
     check(op, x, r, residual=res)
 
 
+@pytest.mark.parametrize("T,E,k,g0,G,shared", [
+    (8, 20, 8, 0, 20, False),      # 64 pairs, as many as lanes
+    (13, 5, 5, 0, 5, True),        # 65: one more
+    (16, 9, 4, 0, 9, True), (16, 9, 4, 3, 5, False), (12, 4, 4, 3, 1, True),
+    (9, 1000, 7, 990, 10, False), (6, 64, 1, 0, 64, True), (16, 1, 1, 0, 1, False),
+])
+def test_few_pairs(T, E, k, g0, G, shared):
+    """Calls of about 64 pairs, whose experts' rows are found in another way."""
+    op, n = make(T, 192, 128, E, k, g0=g0, G=G, shared=shared, router=False, seed=E)
+    x, lg = n(T, 192), n(T, E, d=F32)
+    r = op.forward(x, logits=lg)
+    torch.cuda.synchronize()
+    check(op, x, r, logits=lg)
+
+
+def test_inputs_dropped_behind_another_stream():
+    """Inputs that the caller drops while the call still waits on its stream are
+    not handed out again before it has read them."""
+    op, n = make(4, 1024, 512, 16, 4)
+    x, res = n(4, 1024), n(4, 1024)
+    want = op.forward(x, residual=res)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    x1, res1 = x.clone(), res.clone()
+    torch.cuda.current_stream().synchronize()
+    got = op.forward(x1, residual=res1, stream=side)
+    del x1, res1
+    junk = [torch.full_like(x, float("nan")) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got)) and len(junk) == 8
+
+
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("T", [1, 18, 70, 128])
 def test_masked_and_hot_experts(T, dt):

@@ -178,6 +178,27 @@ def test_parts_of_the_gradient_of_large_products(M, N, K):
         assert torch.equal(a, b) and torch.equal(a, c)
 
 
+def test_inputs_dropped_behind_another_stream():
+    from routing_permute_grouped_moe_amd.layer import Linear
+    n = normal(11)
+    x, w, dy, z = n(200, 320), n(192, 320), n(200, 192), n(200, 192)
+    op = Linear(w, act="silu")
+    y, grads = op.forward(x), op.backward(dy, x, z=z, bias_grad=True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    x1, dy1, z1 = x.clone(), dy.clone(), z.clone()
+    torch.cuda.current_stream().synchronize()
+    got_y = op.forward(x1, stream=side)
+    got = op.backward(dy1, x1, z=z1, bias_grad=True, stream=side)
+    del x1, dy1, z1
+    junk = [torch.full_like(t, float("nan")) for t in (x, dy, z) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(y, got_y) and all(torch.equal(a, b) for a, b in zip(grads, got))
+    assert len(junk) == 12
+
+
 def test_extreme_pre_activations():
     """Large |z|, infinities and NaN: slopes and values at their limits, a NaN
     stays in its own row and column."""
