@@ -49,7 +49,10 @@ struct DecArgs {
   float* yp;          // [T k + T][H] expert outputs
   // counters, zero when the second launch starts: the next unit, tokens
   // routed, finished gate/up units of each expert (window index; the shared
-  // expert last), finished units of each block of DEC_DN output columns
+  // expert last), finished units of each block of DEC_DN output columns.  Those
+  // of the first three lie a cache line apart: on one line with the others, a
+  // look at an expert's counter waited for everyone's draws (128 tokens: 323 us
+  // so, 267 apart)
   int* next; int* routed; int* act_done; int* col_done;
   int* go;            // one word a cache line for each workgroup: the activations are complete
   int n_count;        // all of them, from next on
@@ -588,18 +591,33 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
       d.word[W_COL] = col;
     }
     lds_drain();
-    // The first unit of the second product: for few tokens its weights may come
-    // in before the wait, as many as the rings hold, and the unit behind it is
-    // looked up (one token of 2048 x 1408, 6 experts: 49.2 us
+    // A unit of the second product needs its expert's activations, and those of
+    // the experts at the head of the list are long there when its last gate/up
+    // units still run: one look at the expert's counter (and at this workgroup's
+    // word, below) lets such a unit go ahead (one token of 7680 x 2048, 8 experts
+    // and the shared one: 174 us without, 162 with it; 61 tokens: 460 and 447).
+    const bool ask = kind == U_DOWN && !go && !pending;
+    bool there = false;
+    if (uniform(ask)) {
+      const int v = dev_load(lane == 1 ? a.go + blockIdx.x * 32 : a.act_done + 32 * (g < 0 ? a.G : g));
+      const int need = lane == 1 ? 1 : (pre_g[s + 1] - pre_g[s]) * per_g;
+      const unsigned long long ok = __ballot(lane < 2 && v >= need);
+      there = ok != 0;
+      go = (ok & 2) != 0;
+      if (there) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    }
+    // The first one whose expert is not there waits for all of them: for few
+    // tokens its weights may come in before that, as many as the rings hold, and
+    // the unit behind it is looked up (one token of 2048 x 1408, 6 experts: 49.2 us
     // without either, 47.0 with them; 61 tokens of 7680 x 2048: 468 and 472, the
     // streams run dry to be started anew)
-    const bool first = kind == U_DOWN && !go && !pending;
+    const bool first = uniform(ask && (!there || u == n_route + n_gu));
     if (first) {
       pending = true;
       watch = u == n_route + n_gu;
       if (n_route == 0 && lane == 0 && !watch) lds_post(&l.early, seq + 1);
     }
-    if (lane == 0 && !pending) lds_post(&l.ready, seq + 1);
+    if (lane == 0 && (!pending || (first && there))) lds_post(&l.ready, seq + 1);
     if (!pending && uniform(kind) == U_EXIT) break;
     if (uniform(kind) != U_EXIT) {
       held = seq == 0 ? draw() : held2;
@@ -620,7 +638,7 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
         bool there = false;
         if (q < n_list) {
           const int gq = l.list[q];
-          there = dev_load(args->act_done + (gq < 0 ? args->G : gq)) >=
+          there = dev_load(args->act_done + 32 * (gq < 0 ? args->G : gq)) >=
                   (pre_g[q + 1] - pre_g[q]) * (args->I / DEC_GU);
         }
         const unsigned long long no = ~__ballot(there);
@@ -980,7 +998,7 @@ __device__ __forceinline__ void decode_finish(const DecArgs& a, DecLds& l) {
           }
       vm_drain<0>();   // the stores are out: the unit counts
       if (kind == U_GATEUP) {
-        if (lane == 0) dev_add(a.act_done + w(W_SLOT), 1);
+        if (lane == 0) dev_add(a.act_done + 32 * w(W_SLOT), 1);
       } else if (fused) {
         int before = 0;
         if (lane == 0)
@@ -1074,9 +1092,9 @@ struct DecWs {
 DecWs decode_ws(int T, int H, int I, int E, int k) {
   DecWs w;
   const size_t rows = (size_t)T * k + T;
-  // 16 ints for the two scalars, one per expert of the window and the shared
-  // one, one per column block, a cache line per workgroup
-  w.n_count = (16 + E + 1 + H / DEC_DN + 31) / 32 * 32 + 32 * moe_cu_count();
+  // a cache line for each of the two scalars and each expert of the window and
+  // the shared one, an int per column block, a cache line per workgroup
+  w.n_count = (64 + 32 * (E + 1) + H / DEC_DN + 31) / 32 * 32 + 32 * moe_cu_count();
   w.count = 0;
   w.part = w.count + round256((size_t)w.n_count * 4);
   w.act = w.part + round256((size_t)router_slices(H, E) * T * E * 8);
@@ -1196,10 +1214,10 @@ extern "C" int moe_decode(const void* x, int dt, const float* wg, const float* b
   a.gu_tiles = gateup_tiles(a.shared != 0, T, E, k);
   a.n_count = w.n_count;
   a.next = (int*)((char*)ws + w.count);
-  a.routed = a.next + 8;
-  a.act_done = a.next + 16;
-  a.col_done = a.act_done + E + 1;
-  a.go = a.next + (16 + E + 1 + H / DEC_DN + 31) / 32 * 32;
+  a.routed = a.next + 32;
+  a.act_done = a.next + 64;
+  a.col_done = a.act_done + 32 * (E + 1);
+  a.go = a.next + (64 + 32 * (E + 1) + H / DEC_DN + 31) / 32 * 32;
   a.part = (double*)((char*)ws + w.part);
   a.act = (char*)ws + w.act;
   a.yp = (float*)((char*)ws + w.yp);
