@@ -195,13 +195,15 @@ __device__ __forceinline__ void decode_route_token(const DecArgs& a, int t, bool
       v[i] = e < a.E ? a.logits[(long long)t * a.E + e] : -INFINITY;
     }
   }
+  bool masked = true;   // (fmaxf passes NaN over: m alone does not tell)
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     key[i] = lane + i * MOE_WAVE < a.E ? route_key(v[i]) : 0u;
     m = fmaxf(m, v[i]);
+    masked = masked && v[i] == -INFINITY;
   }
   m = wave_max(m);
-  const bool none = m == -INFINITY;   // every expert masked: gates of zero, not NaN
+  const bool none = __all(masked);   // every expert masked: gates of zero, not NaN
   float s = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i) s += lane + i * MOE_WAVE < a.E ? expf(v[i] - m) : 0.f;

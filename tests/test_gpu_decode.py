@@ -279,3 +279,57 @@ def test_block_of_a_decoder():
     keep = r.y.clone()
     y = down.forward(f, residual=r.y, out=r.y)
     assert_within("down", y, ref_linear(f, down.w, None, "none", keep, BF)[0])
+
+
+def nan_of_either_sign(n):
+    return torch.tensor([0x7fc00000, -0x400000], dtype=torch.int32).view(F32).repeat(n)[:n].cuda()
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("T", [1, 6, 40])
+def test_nan_logits_are_no_mask(T, dt):
+    """A row of NaN, or of NaN and -inf, is not a row whose experts are masked:
+    its gates are NaN, as moe_route gives them, and so is its y; the other rows
+    do not see it."""
+    from routing_permute_grouped_moe_amd import abi
+    E, k, H, I = 70, 3, 128, 64
+    op, n = make(T, H, I, E, k, dt=dt, router=False, shared=True, seed=T)
+    lg = n(T, E, d=F32)
+    rows = [T // 2] if T < 6 else [1, 2, 4]
+    for i, r in enumerate(rows):
+        if i == 0:
+            lg[r] = nan_of_either_sign(E)
+        elif i == 1:
+            lg[r] = -float("inf")
+            lg[r, 66] = float("nan")
+        else:
+            lg[r, 7] = float("nan")                # among finite ones
+    x, res = n(T, H, d=dt), n(T, H, d=dt)
+    r = op.forward(x, residual=res, logits=lg)
+    idx = torch.empty(T, k, dtype=torch.int32, device="cuda")
+    gate = torch.empty(T, k, dtype=F32, device="cuda")
+    abi.moe_route(lg, T, E, k, idx, gate)
+    assert torch.equal(r.idx, idx) and torch.equal(torch.isnan(r.gate), torch.isnan(gate))
+    bad = torch.zeros(T, dtype=torch.bool)
+    bad[rows] = True
+    assert torch.isnan(r.gate[bad]).all() and torch.isnan(r.y[bad]).all()
+    if T > 1:
+        alone = op.forward(x[~bad].contiguous(), residual=res[~bad].contiguous(),
+                           logits=lg[~bad].contiguous())
+        assert_within("gate", r.gate[~bad], ref_route(lg[~bad].cpu(), k)[1:])
+        assert torch.equal(r.y[~bad], alone.y) and torch.isfinite(alone.y).all()
+
+
+@pytest.mark.parametrize("T", [2, 30])
+def test_nan_in_the_router_reaches_y(T):
+    """A NaN in a row of Wg makes every logit NaN, one in x a token's: no finite y."""
+    op, n = make(T, 128, 64, 9, 2, seed=3)
+    x, res = n(T, 128), n(T, 128)
+    wg = op.wg.clone()
+    x[0, 5] = float("nan")
+    r = op.forward(x, residual=res)
+    assert torch.isnan(r.y[0]).all() and torch.isfinite(r.y[1:]).all()
+    op.wg[77] = float("nan")
+    r = op.forward(x, residual=res)
+    assert torch.isnan(r.logits).all() and torch.isnan(r.gate).all() and torch.isnan(r.y).all()
+    op.wg.copy_(wg)
