@@ -30,8 +30,8 @@
  *    buffers have R = T*k rows (dropless, [Pangu-QA]), or R = E*C in the
  *    drop-and-pad variant (moe_permute_capacity).
  *  - The caller owns every buffer, including workspaces.  The library keeps no
- *    device memory; its only global state is the per-device CU count and the
- *    thread-local text of the last error.
+ *    device memory; its only global state is the per-device CU count and, for
+ *    each host thread, the text of the last error and moe_decode_wait_limit.
  *  - Arguments are validated on the host before any launch.  Errors:
  *    MOE_ERR_INVALID_ARG (null pointer, misalignment, negative or
  *    inconsistent size), MOE_ERR_UNSUPPORTED (outside the supported shapes:
@@ -383,12 +383,19 @@ int moe_grouped_gemm_bwd_dw_recompute(const void* x, const int32_t* src_token, i
  * the faster one there), one expert's w13 and the call's rows below 2 GiB.
  * ws: moe_decode_workspace_bytes bytes (256-byte aligned, contents scratch),
  * not shared by calls that may overlap.
+ * Workgroups of the call wait for each other's work.  Such a wait always ends
+ * in a call that has its workspace for itself; it is bounded all the same, by
+ * moe_decode_wait_limit, and where it is given up y holds NaN in place of what
+ * was not computed, never a finite wrong value.
  */
 size_t moe_decode_workspace_bytes(int T, int H, int I, int E, int k, int dt);
 int moe_decode(const void* x, int dt, const float* wg, const float* bias, int T, int H, int I,
                int E, int k, int g0, int G, const void* w13, const void* w2, const void* ws13,
                const void* ws2, const void* residual, float* logits, int32_t* idx, float* gate,
                void* y, void* ws, size_t ws_bytes, moe_stream_t stream);
+/* Longest wait, in microseconds, within the moe_decode calls that this host
+ * thread makes (or captures) from now on; 1000000 at first. */
+void moe_decode_wait_limit(unsigned us);
 
 /* ---------------------------------------------------------------- fused linear product
  * The dense products beside the expert layer (projections onto the residual

@@ -81,6 +81,7 @@ _SIGS = {
     "moe_decode_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "moe_decode": (_I, [_P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P,
                         _P, _P, _P, _SZ, _P]),
+    "moe_decode_wait_limit": (None, [ctypes.c_uint]),
     "moe_linear_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
     "moe_linear": (_I, [_P, _I, _I, _I, _I, _P, _P, _I, _P, _P, _P, _P, _SZ, _P]),
     "moe_linear_bwd_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
@@ -281,6 +282,12 @@ def moe_decode(x, dt, wg, bias, T, H, I, E, k, g0, G, w13, w2, ws13, ws2, residu
     _call("moe_decode", addr(x), dt, addr(wg), addr(bias), T, H, I, E, k, g0, G, addr(w13),
           addr(w2), addr(ws13), addr(ws2), addr(residual), addr(logits), addr(idx), addr(gate),
           addr(y), addr(ws), ws_bytes, _stream(stream))
+
+
+def moe_decode_wait_limit(us: int):
+    """Longest wait, in microseconds, within this host thread's moe_decode calls
+    from now on (1000000 at first)."""
+    _lib.moe_decode_wait_limit(us)
 
 
 def moe_linear_workspace_bytes(M, N, K, dt) -> int:

@@ -54,8 +54,9 @@ struct DecArgs {
   // look at an expert's counter waited for everyone's draws (128 tokens: 323 us
   // so, 267 apart)
   int* next; int* routed; int* act_done; int* col_done;
-  int* go;            // one word a cache line for each workgroup: the activations are complete
+  int* go;            // one word a cache line for each workgroup: 0, DEC_GO or DEC_GO_LOST
   int n_count;        // all of them, from next on
+  unsigned long long wait_ticks;   // after which a wait is given up
 };
 
 // 8 elements of T as fp32, from byte offset off
@@ -248,7 +249,9 @@ constexpr int DEC_PAGE = 2048;       // a 16-row tile of a step
 constexpr int DEC_PAGES = 16;        // of a streaming wave's ring
 constexpr int DEC_OWN_T = 8;         // tokens, and pairs, that every workgroup routes itself
 constexpr int DEC_OWN_PAIRS = 256;
-constexpr unsigned long long DEC_WAIT_TICKS = 100000000ull;   // 1 s of the 100 MHz clock
+constexpr unsigned DEC_WAIT_US = 1000000;   // a wait longer than this is given up (moe_decode_wait_limit)
+constexpr unsigned DEC_TICKS_PER_US = 100;   // of the constant 100 MHz clock
+constexpr int DEC_GO = 1, DEC_GO_LOST = 2;   // a workgroup's word: activations complete, or given up
 
 enum { U_GATEUP = 0, U_DOWN = 1, U_ROUTE = 2, U_SUM = 3, U_EXIT = 4 };
 
@@ -503,7 +506,7 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
         if (n_route > 0) {
           const unsigned long long t0 = wall_clock64();
           while (uniform(dev_load(a.routed)) < a.T && !lost) {
-            lost = wall_clock64() - t0 > DEC_WAIT_TICKS;
+            lost = wall_clock64() - t0 > args->wait_ticks;
             __builtin_amdgcn_s_sleep(1);
           }
           __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
@@ -606,6 +609,10 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
       const unsigned long long ok = __ballot(lane < 2 && v >= need);
       there = ok != 0;
       go = (ok & 2) != 0;
+      if (__ballot(lane == 1 && v == DEC_GO_LOST)) {
+        lost = true;
+        if (lane == 0) lds_post(&l.lost, 1);   // (before this unit is)
+      }
       if (there) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
     }
     // The first one whose expert is not there waits for all of them: for few
@@ -645,14 +652,18 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
         }
         const unsigned long long no = ~__ballot(there);
         known += no ? __builtin_ctzll(no) : 64;
-        lost = wall_clock64() - t0 > DEC_WAIT_TICKS;
+        lost = wall_clock64() - t0 > args->wait_ticks;
       }
-      for (int w = lane; w < (int)gridDim.x; w += 64) dev_store(args->go + w * 32, 1);
+      // (given up: the others must not take incomplete activations for whole ones)
+      const int word = lost ? DEC_GO_LOST : DEC_GO;
+      for (int w = lane; w < (int)gridDim.x; w += 64) dev_store(args->go + w * 32, word);
     } else {
-      while (uniform(dev_load(args->go + blockIdx.x * 32)) == 0 && !lost) {
-        lost = wall_clock64() - t0 > DEC_WAIT_TICKS;
+      int word;
+      while ((word = uniform(dev_load(args->go + blockIdx.x * 32))) == 0 && !lost) {
+        lost = wall_clock64() - t0 > args->wait_ticks;
         __builtin_amdgcn_s_sleep(2);
       }
+      lost = lost || word == DEC_GO_LOST;
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
     go = true;
@@ -1163,6 +1174,10 @@ int decode_launch(const DecArgs& a, hipStream_t s, const char* fn) {
 
 }  // namespace
 
+static thread_local unsigned g_wait_us = DEC_WAIT_US;
+
+extern "C" void moe_decode_wait_limit(unsigned us) { g_wait_us = us; }
+
 extern "C" size_t moe_decode_workspace_bytes(int T, int H, int I, int E, int k, int dt) {
   if (decode_shape("moe_decode_workspace_bytes", T, H, I, E, k, dt) != MOE_OK) return 0;
   return decode_ws(T, H, I, E, k).total;
@@ -1215,6 +1230,7 @@ extern "C" int moe_decode(const void* x, int dt, const float* wg, const float* b
   a.S = wg != nullptr ? router_slices(H, E) : 0;
   a.gu_tiles = gateup_tiles(a.shared != 0, T, E, k);
   a.n_count = w.n_count;
+  a.wait_ticks = (unsigned long long)g_wait_us * DEC_TICKS_PER_US;
   a.next = (int*)((char*)ws + w.count);
   a.routed = a.next + 32;
   a.act_done = a.next + 64;

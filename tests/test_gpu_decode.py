@@ -333,3 +333,44 @@ def test_nan_in_the_router_reaches_y(T):
     r = op.forward(x, residual=res)
     assert torch.isnan(r.logits).all() and torch.isnan(r.gate).all() and torch.isnan(r.y).all()
     op.wg.copy_(wg)
+
+
+@pytest.fixture
+def no_patience():
+    """Every wait within a call that finds its work missing is given up."""
+    from routing_permute_grouped_moe_amd import abi
+    abi.moe_decode_wait_limit(0)
+    yield
+    abi.moe_decode_wait_limit(1000000)
+
+
+def nan_or_right(op, x, wanted, calls, **kw):
+    """Calls whose every value is NaN or the right one; how many held a NaN."""
+    held = 0
+    for _ in range(calls):
+        r = op.forward(x, **kw)
+        torch.cuda.synchronize()
+        nan = torch.isnan(r.y)
+        assert torch.equal(torch.where(nan, wanted.y, r.y), wanted.y)
+        assert torch.equal(r.idx, wanted.idx) and torch.equal(r.gate, wanted.gate)
+        held += bool(nan.any())
+    return held
+
+
+@pytest.mark.parametrize("T,H,I,E,k,shared", [(1, 2048, 1408, 64, 6, False),
+                                              (8, 512, 256, 16, 4, True),
+                                              (3, 256, 512, 8, 8, False)])
+def test_a_wait_given_up_is_nan_for_few_tokens(T, H, I, E, k, shared, no_patience):
+    """The wait between the products, given up at once: what is not right is NaN,
+    and the next call, with patience, is right again."""
+    from routing_permute_grouped_moe_amd import abi
+    op, n = make(T, H, I, E, k, shared=shared)
+    x, res = n(T, H), n(T, H)
+    abi.moe_decode_wait_limit(1000000)
+    want = op.forward(x, residual=res)
+    check(op, x, want, residual=res)
+    abi.moe_decode_wait_limit(0)
+    assert nan_or_right(op, x, want, 20, residual=res) > 0
+    abi.moe_decode_wait_limit(1000000)
+    r = op.forward(x, residual=res)
+    assert all(torch.equal(a, b) for a, b in zip(want, r))
