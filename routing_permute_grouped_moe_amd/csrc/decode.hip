@@ -30,7 +30,6 @@ constexpr int DEC_SW = 4;            // streaming waves of a workgroup of the se
 constexpr int DEC_NT = 64 * (DEC_SW + 2);   // and one that schedules, one that finishes tiles
 constexpr int DEC_GU = 16;           // gate/up columns of a unit (16 gate and 16 up rows of W13)
 constexpr int DEC_DN = 32;           // output columns of a unit of the second product
-constexpr int DEC_FUSED_T = 8;       // tokens up to which the last unit of a column block sums it
 constexpr int RT_NW = 4;             // waves of a router workgroup
 constexpr int RT_COLS = 16;          // experts of a router workgroup
 constexpr int RT_MAX_S = 32;         // K slices of the router product
@@ -48,12 +47,12 @@ struct DecArgs {
   void* act;          // [planes][T k + T][I] activations, shared rows last
   float* yp;          // [T k + T][H] expert outputs
   // counters, zero when the second launch starts: the next unit, tokens
-  // routed, finished gate/up units of each expert (window index; the shared
-  // expert last), finished units of each block of DEC_DN output columns.  Those
-  // of the first three lie a cache line apart: on one line with the others, a
+  // routed, whether a wait for that was given up, finished gate/up units of each
+  // expert (window index; the shared expert last), finished units of each block of
+  // DEC_DN output columns.  All but the last lie a cache line apart: on one line with the others, a
   // look at an expert's counter waited for everyone's draws (128 tokens: 323 us
   // so, 267 apart)
-  int* next; int* routed; int* act_done; int* col_done;
+  int* next; int* routed; int* unrouted; int* act_done; int* col_done;
   int* go;            // one word a cache line for each workgroup: 0, DEC_GO or DEC_GO_LOST
   int n_count;        // all of them, from next on
   unsigned long long wait_ticks;   // after which a wait is given up
@@ -510,14 +509,21 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
             __builtin_amdgcn_s_sleep(1);
           }
           __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-          if (lost && lane == 0) lds_post(&l.lost, 1);
+          if (lost && lane == 0) dev_store(a.unrouted, 1);
         }
-        n_list = decode_tables(a, l);
-        n_gu = pre_g[n_list] * per_g;
-        n_dn = l.pre[n_list] * per_d;
+        if (!lost) {
+          n_list = decode_tables(a, l);
+          n_gu = pre_g[n_list] * per_g;
+          n_dn = l.pre[n_list] * per_d;
+        }
       }
       int v = u - n_route;
-      if (v < n_gu + n_dn) {
+      if (lost && n_list < 0) {
+        // Without every token's choices the numbers mean nothing: this workgroup
+        // does no more, whoever waits for its units gives up in turn, and the
+        // sum's launch makes all of y NaN.
+        kind = U_EXIT;
+      } else if (v < n_gu + n_dn) {
         kind = v < n_gu ? U_GATEUP : U_DOWN;
         const int per = v < n_gu ? per_g : per_d;
         const int16_t* const pre = v < n_gu ? pre_g : l.pre;
@@ -533,7 +539,7 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
         v -= pre[s] * per;
         rb = v % nb;
         col = v / nb * (kind == U_GATEUP ? DEC_GU : DEC_DN);
-      } else if (n_dn == 0 && v < per_d && a.T <= DEC_FUSED_T) {
+      } else if (n_dn == 0 && v < per_d && n_route == 0) {
         kind = U_SUM;    // nothing but the residual
         col = v * DEC_DN;
       } else {
@@ -929,23 +935,24 @@ __device__ __forceinline__ float decode_sum(const DecArgs& a, int t, int h, Pair
 template <typename T>
 __device__ __forceinline__ void decode_finish(const DecArgs& a, DecLds& l) {
   const int lane = threadIdx.x & 63, P = a.T * a.k;
-  const bool fused = a.T <= DEC_FUSED_T;
+  // the last unit of a column block sums it, where no wait precedes the tables
+  // and the choices are at hand; else the sum is a launch of its own
+  const bool fused = dec_own(a.T, a.k);
   const long long plane = (long long)(P + a.T) * a.I;
-  const bool own = dec_own(a.T, a.k);
   auto sum_block = [&](int col, int n) {
 #pragma unroll 1
     for (int t0 = 0; t0 < a.T; t0 += 2) {
       const int t = t0 + (lane >> 5), h = col + (lane & 31);
       const float s = decode_sum<T>(a, min(t, a.T - 1), h, [&](int p, int& e, float& w) {
-        e = own ? (int)l.own_idx[p & (DEC_OWN_PAIRS - 1)] : a.idx[p];
-        w = own ? l.own_gate[p & (DEC_OWN_PAIRS - 1)] : a.gate[p];
+        e = l.own_idx[p & (DEC_OWN_PAIRS - 1)];
+        w = l.own_gate[p & (DEC_OWN_PAIRS - 1)];
       });
       if (t < n) elem_store<T>(a.y, (long long)t * a.H + h, s);
     }
   };
   // Once for nothing, while the first unit streams: a first pass through this
   // code waits for every line of it, 4 us that would end the call.
-  if (fused && own) sum_block(0, 0);
+  if (fused) sum_block(0, 0);
   for (int seq = 0;; ++seq) {
     lds_wait(&l.ready, seq + 1);
     const DecDesc& d = l.desc[seq % DEC_DESCS];
@@ -1062,7 +1069,8 @@ __global__ __launch_bounds__(DEC_NT) void decode_kernel(DecArgs a) {
   else decode_finish<T>(a, l);
 }
 
-// the sum as a launch of its own, for more tokens than one wave should add
+// the sum as a launch of its own, for more tokens than one wave should add; NaN
+// where some workgroup gave up its wait for the routing
 template <typename T>
 __global__ __launch_bounds__(256) void decode_sum_kernel(DecArgs a) {
   const int h = blockIdx.x * 256 + threadIdx.x;
@@ -1071,7 +1079,8 @@ __global__ __launch_bounds__(256) void decode_sum_kernel(DecArgs a) {
     e = a.idx[p];
     w = a.gate[p];
   });
-  elem_store<T>(a.y, (long long)blockIdx.y * a.H + h, s);
+  elem_store<T>(a.y, (long long)blockIdx.y * a.H + h,
+                *a.unrouted == 0 ? s : __uint_as_float(0x7fc00000u));
 }
 
 // ---------------------------------------------------------------- host side
@@ -1105,9 +1114,9 @@ struct DecWs {
 DecWs decode_ws(int T, int H, int I, int E, int k) {
   DecWs w;
   const size_t rows = (size_t)T * k + T;
-  // a cache line for each of the two scalars and each expert of the window and
+  // a cache line for each of the three scalars and each expert of the window and
   // the shared one, an int per column block, a cache line per workgroup
-  w.n_count = (64 + 32 * (E + 1) + H / DEC_DN + 31) / 32 * 32 + 32 * moe_cu_count();
+  w.n_count = (96 + 32 * (E + 1) + H / DEC_DN + 31) / 32 * 32 + 32 * moe_cu_count();
   w.count = 0;
   w.part = w.count + round256((size_t)w.n_count * 4);
   w.act = w.part + round256((size_t)router_slices(H, E) * T * E * 8);
@@ -1167,7 +1176,7 @@ int decode_launch(const DecArgs& a, hipStream_t s, const char* fn) {
   if (dec_own(a.T, a.k)) launch(std::true_type{});
   else launch(std::false_type{});
   MOE_TRY(moe_check_launch(fn));
-  if (a.T <= DEC_FUSED_T) return MOE_OK;
+  if (dec_own(a.T, a.k)) return MOE_OK;
   hipLaunchKernelGGL(decode_sum_kernel<T>, dim3((a.H + 255) / 256, a.T), dim3(256), 0, s, a);
   return moe_check_launch(fn);
 }
@@ -1233,9 +1242,10 @@ extern "C" int moe_decode(const void* x, int dt, const float* wg, const float* b
   a.wait_ticks = (unsigned long long)g_wait_us * DEC_TICKS_PER_US;
   a.next = (int*)((char*)ws + w.count);
   a.routed = a.next + 32;
-  a.act_done = a.next + 64;
+  a.unrouted = a.next + 64;
+  a.act_done = a.next + 96;
   a.col_done = a.act_done + 32 * (E + 1);
-  a.go = a.next + (64 + 32 * (E + 1) + H / DEC_DN + 31) / 32 * 32;
+  a.go = a.next + (96 + 32 * (E + 1) + H / DEC_DN + 31) / 32 * 32;
   a.part = (double*)((char*)ws + w.part);
   a.act = (char*)ws + w.act;
   a.yp = (float*)((char*)ws + w.yp);

@@ -7,7 +7,9 @@ ahead once their expert's activations are there; the first one whose are not
 waits for all of them: whoever drew the first of them watches the experts'
 counters and tells every other workgroup on a word of its own.  Every wait is
 bounded: one that takes too long is given up, and what a workgroup adds to the
-result from then on is NaN.
+result from then on is NaN.  A workgroup that gives up waiting for the routing
+does no more and says so in a word that has the sum's launch (calls with routing
+units have one) write NaN throughout.
 
 The model replays that protocol (the scheduling wave's decisions, a queue of
 descriptors, the draws held ahead) with random durations and workgroups that
@@ -36,7 +38,7 @@ class Call:
         self.next = self.routed = 0
         self.act = {}                        # finished gate/up units of an expert
         self.go = [0] * nwg                  # 1: the activations are complete, 2: given up
-        self.gave_up = 0
+        self.unrouted = False
         self.per_col = sum(blocks)
         self.col_done = [0] * per_d
         self.yp = {}                         # (expert, row block, column): ok, wrong, nan
@@ -77,12 +79,15 @@ class Call:
             else:
                 if self.n_route and not wg.get("tables"):
                     over = self.waiter()
-                    while self.routed < self.tokens:
+                    while self.routed < self.tokens and not lost:
                         yield 1
-                        assert not over(), "no test of this wait here"
-                wg["tables"] = True
+                        lost = over()
+                    self.unrouted = self.unrouted or lost
+                wg["tables"] = wg.get("tables") or not lost
                 v = u - self.n_route
-                if v < len(self.gus):
+                if not wg["tables"]:
+                    unit = (EXIT, None)
+                elif v < len(self.gus):
                     unit = (GATEUP, self.gus[v])
                 elif v < len(self.gus) + len(self.downs):
                     unit = (DOWN, self.downs[v - len(self.gus)])
@@ -142,7 +147,7 @@ class Call:
                 self.yp[unit] = "nan" if wg["lost"] else "ok" if seen else "wrong"
                 c = unit[2]
                 self.col_done[c] += 1
-                if self.col_done[c] == self.per_col:
+                if self.col_done[c] == self.per_col and not self.n_route:
                     self.sum(c)
             seq += 1
             wg["done"] = seq
@@ -168,6 +173,11 @@ class Call:
                     except StopIteration:
                         del gens[i]
             assert self.now < 10 ** 6, "the run does not end"
+        if self.n_route:
+            for c in range(self.per_d):
+                self.sum(c)
+                if self.unrouted:
+                    self.y[c] = "nan"
         return self.y
 
 
@@ -175,9 +185,10 @@ SHAPES = [([1], 4, 2, 4), ([1, 1, 1], 8, 6, 16), ([1] * 7, 20, 12, 64), ([1, 2, 
 
 
 @pytest.mark.parametrize("blocks,per_g,per_d,nwg", SHAPES)
-def test_with_patience_every_block_is_right(blocks, per_g, per_d, nwg):
+@pytest.mark.parametrize("tokens", [0, 10, 61])
+def test_with_patience_every_block_is_right(blocks, per_g, per_d, nwg, tokens):
     for seed in range(10):
-        y = Call(0, blocks, per_g, per_d, nwg, seed, 10 ** 5, late=1).run()
+        y = Call(tokens, blocks, per_g, per_d, nwg, seed, 10 ** 5, late=1).run()
         assert y == ["ok"] * per_d
 
 
@@ -188,6 +199,18 @@ def test_a_watch_given_up_ends_in_nan(blocks, per_g, per_d, nwg):
     for seed in range(10):
         for patience in (0, 5, 20):
             y = Call(0, blocks, per_g, per_d, nwg, seed, patience, late=1).run()
+            assert set(y) <= {"ok", "nan"}, (seed, patience, y)
+            seen |= set(y)
+    assert "nan" in seen
+
+
+@pytest.mark.parametrize("tokens", [9, 61, 128])
+@pytest.mark.parametrize("blocks,per_g,per_d,nwg", SHAPES)
+def test_a_wait_for_the_routing_given_up_ends_in_nan(blocks, per_g, per_d, nwg, tokens):
+    seen = set()
+    for seed in range(10):
+        for patience in (0, 5, 20, 60):
+            y = Call(tokens, blocks, per_g, per_d, nwg, seed, patience, late=1).run()
             assert set(y) <= {"ok", "nan"}, (seed, patience, y)
             seen |= set(y)
     assert "nan" in seen

@@ -374,3 +374,22 @@ def test_a_wait_given_up_is_nan_for_few_tokens(T, H, I, E, k, shared, no_patienc
     abi.moe_decode_wait_limit(1000000)
     r = op.forward(x, residual=res)
     assert all(torch.equal(a, b) for a, b in zip(want, r))
+
+
+@pytest.mark.parametrize("T,H,I,E,k,shared", [(9, 512, 256, 16, 4, False), (40, 512, 256, 16, 4, True),
+                                              (128, 256, 128, 24, 6, False),
+                                              (8, 128, 64, 300, 256, False)])
+def test_a_wait_given_up_is_nan_throughout(T, H, I, E, k, shared, no_patience):
+    """Calls whose tokens are routed in units of their own: a workgroup that gives
+    up waiting for them leaves units undone, and no value of y is taken for right."""
+    from routing_permute_grouped_moe_amd import abi
+    op, n = make(T, H, I, E, k, shared=shared)
+    x, res = n(T, H), n(T, H)
+    abi.moe_decode_wait_limit(1000000)
+    want = op.forward(x, residual=res)
+    check(op, x, want, residual=res)
+    abi.moe_decode_wait_limit(0)
+    assert nan_or_right(op, x, want, 20, residual=res) > 0
+    abi.moe_decode_wait_limit(1000000)
+    r = op.forward(x, residual=res)
+    assert all(torch.equal(a, b) for a, b in zip(want, r))
