@@ -394,7 +394,8 @@ int moe_decode(const void* x, int dt, const float* wg, const float* bias, int T,
                const void* ws2, const void* residual, float* logits, int32_t* idx, float* gate,
                void* y, void* ws, size_t ws_bytes, moe_stream_t stream);
 /* Longest wait, in microseconds, within the moe_decode calls that this host
- * thread makes (or captures) from now on; 1000000 at first. */
+ * thread makes (or captures) from now on; 1000000 at first.  Time in which the
+ * GPU ran something else in the waiting kernel's place does not count. */
 void moe_decode_wait_limit(unsigned us);
 
 /* ---------------------------------------------------------------- fused linear product

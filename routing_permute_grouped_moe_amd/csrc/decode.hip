@@ -250,6 +250,7 @@ constexpr int DEC_OWN_T = 8;         // tokens, and pairs, that every workgroup 
 constexpr int DEC_OWN_PAIRS = 256;
 constexpr unsigned DEC_WAIT_US = 1000000;   // a wait longer than this is given up (moe_decode_wait_limit)
 constexpr unsigned DEC_TICKS_PER_US = 100;   // of the constant 100 MHz clock
+constexpr unsigned DEC_STEP_US = 100;        // most that a look of a wait counts for
 constexpr int DEC_GO = 1, DEC_GO_LOST = 2;   // a workgroup's word: activations complete, or given up
 
 enum { U_GATEUP = 0, U_DOWN = 1, U_ROUTE = 2, U_SUM = 3, U_EXIT = 4 };
@@ -313,6 +314,24 @@ __device__ __forceinline__ void lds_wait(const int* p, int v) {
 // row blocks of an expert with m rows, in units of `tiles` row tiles
 __device__ __forceinline__ int row_blocks(int m, int tiles) {
   return (m + DEC_ROWS * tiles - 1) >> (tiles == 2 ? 5 : 4);
+}
+
+// A wait for other workgroups, bounded by the time that this one ran: a step from
+// look to look counts DEC_STEP_US at most, so that the time in which the whole
+// queue was suspended does not (looks are a few microseconds apart).
+struct DecWait {
+  unsigned long long last = wall_clock64(), spent = 0;
+  bool late = false;
+};
+// After a look that found nothing: give up?  Only if the look before was late
+// already, so that one look at least follows the last of the time.
+__device__ __forceinline__ bool dec_give_up(DecWait& w, unsigned long long limit) {
+  if (w.late) return true;
+  const unsigned long long now = wall_clock64(), step = now - w.last;
+  w.last = now;
+  w.spent += step < DEC_STEP_US * DEC_TICKS_PER_US ? step : DEC_STEP_US * DEC_TICKS_PER_US;
+  w.late = w.spent >= limit;
+  return false;
 }
 
 template <typename T> constexpr int DEC_PLANES = sizeof(T) == 2 ? 2 : 1;
@@ -464,7 +483,7 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
   const int16_t* const pre_g = (const int16_t*)l.cur;
   bool go = false;       // the activations are complete
   bool pending = false, watch = false;   // not yet, and units wait for them; this wave looks
-  bool lost = false;     // a wait took a second (calls that share a workspace): wait no more,
+  bool lost = false;     // a wait was given up (calls that share a workspace): wait no more,
                          // and what this workgroup adds to the result is NaN
   auto draw = [&]() {
     int v = 0;
@@ -503,9 +522,10 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
     } else {
       if (n_list < 0) {
         if (n_route > 0) {
-          const unsigned long long t0 = wall_clock64();
-          while (uniform(dev_load(a.routed)) < a.T && !lost) {
-            lost = wall_clock64() - t0 > args->wait_ticks;
+          DecWait w;
+          while (uniform(dev_load(a.routed)) < a.T) {
+            lost = dec_give_up(w, args->wait_ticks);
+            if (lost) break;
             __builtin_amdgcn_s_sleep(1);
           }
           __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
@@ -645,10 +665,10 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
     // watching the same lines took so long for every look that the copies
     // queued behind it in their CUs' memory pipelines stood still.  (It copies
     // no weights early: its looks would queue behind them.)
-    const unsigned long long t0 = wall_clock64();
+    DecWait wait;
     if (watch) {
       int known = 0;
-      while (known < n_list && !lost) {
+      while (known < n_list) {
         const int q = known + lane;
         bool there = false;
         if (q < n_list) {
@@ -658,7 +678,8 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
         }
         const unsigned long long no = ~__ballot(there);
         known += no ? __builtin_ctzll(no) : 64;
-        lost = wall_clock64() - t0 > args->wait_ticks;
+        if (known < n_list && !lost) lost = dec_give_up(wait, args->wait_ticks);
+        if (lost) break;
       }
       // (given up: the others must not take incomplete activations for whole ones)
       const int word = lost ? DEC_GO_LOST : DEC_GO;
@@ -666,7 +687,7 @@ __device__ __forceinline__ void decode_schedule(DecLds& l) {
     } else {
       int word;
       while ((word = uniform(dev_load(args->go + blockIdx.x * 32))) == 0 && !lost) {
-        lost = wall_clock64() - t0 > args->wait_ticks;
+        lost = dec_give_up(wait, args->wait_ticks);
         __builtin_amdgcn_s_sleep(2);
       }
       lost = lost || word == DEC_GO_LOST;

@@ -23,18 +23,21 @@ import pytest
 
 DESCS = 4
 ROUTE, GATEUP, DOWN, EXIT = range(4)
+CLAMP = 5
 
 
 class Call:
     """One call: ``tokens`` (0: every workgroup routes them all itself), row
     blocks of each chosen expert, gate/up and output column blocks."""
 
-    def __init__(self, tokens, blocks, per_g, per_d, nwg, seed, patience, late=0):
+    def __init__(self, tokens, blocks, per_g, per_d, nwg, seed, patience, late=0,
+                 sleep_at=None):
         self.rnd = random.Random(seed)
         self.n_route, self.tokens = (tokens + 3) // 4, tokens
         self.blocks, self.per_g, self.per_d = blocks, per_g, per_d
         self.nwg, self.patience = nwg, patience
-        self.now = 0
+        self.now = self.asleep = 0           # (time in which nothing of the call ran)
+        self.sleep_at = sleep_at
         self.next = self.routed = 0
         self.act = {}                        # finished gate/up units of an expert
         self.go = [0] * nwg                  # 1: the activations are complete, 2: given up
@@ -57,12 +60,19 @@ class Call:
         return self.act.get(e, 0) >= self.blocks[e] * self.per_g
 
     def waiter(self):
-        """Time spent waiting, and whether that is too long."""
-        t0 = self.now
+        """Asked after a look that found nothing: is the wait given up?  A step of
+        the clock counts at most CLAMP, and a look follows the last of them."""
+        last, spent, late = self.now + self.asleep, 0, False
 
-        def over():
-            return self.now - t0 > self.patience
-        return over
+        def give_up():
+            nonlocal last, spent, late
+            if late:
+                return True
+            now = self.now + self.asleep
+            spent, last = spent + min(now - last, CLAMP), now
+            late = spent >= self.patience
+            return False
+        return give_up
 
     def schedule(self, b, wg):
         """The scheduling wave of workgroup b; wg: queue, done, lost."""
@@ -78,10 +88,10 @@ class Call:
                 unit = (ROUTE, u)
             else:
                 if self.n_route and not wg.get("tables"):
-                    over = self.waiter()
+                    give_up = self.waiter()
                     while self.routed < self.tokens and not lost:
+                        lost = give_up()
                         yield 1
-                        lost = over()
                     self.unrouted = self.unrouted or lost
                 wg["tables"] = wg.get("tables") or not lost
                 v = u - self.n_route
@@ -110,17 +120,17 @@ class Call:
             if not pending:
                 yield self.rnd.randint(1, 2)
                 continue
-            over = self.waiter()
+            give_up = self.waiter()
             if u == first_down:
                 while not all(self.complete(e) for e in range(len(self.blocks))) and not lost:
+                    lost = give_up()
                     yield 1
-                    lost = over()
                 for w in range(self.nwg):
                     self.go[w] = 2 if lost else 1
             else:
                 while self.go[b] == 0 and not lost:
+                    lost = give_up()
                     yield 1
-                    lost = over()
                 lost = lost or self.go[b] == 2
             go = True
             wg["lost"] = wg["lost"] or lost
@@ -166,6 +176,8 @@ class Call:
                 wake[len(wake)] = t0
         while gens:
             self.now += 1
+            if self.now == self.sleep_at:
+                self.asleep = 10 ** 9
             for i in list(gens):
                 if wake[i] <= self.now:
                     try:
@@ -193,6 +205,17 @@ def test_with_patience_every_block_is_right(blocks, per_g, per_d, nwg, tokens):
 
 
 @pytest.mark.parametrize("blocks,per_g,per_d,nwg", SHAPES)
+@pytest.mark.parametrize("tokens", [0, 61])
+def test_a_suspended_call_is_right(blocks, per_g, per_d, nwg, tokens):
+    """The clock goes on while the GPU runs something else for long; the call's
+    waits do not end by that."""
+    for seed in range(4):
+        for at in (2, 5, 20, 50, 100, 200):
+            y = Call(tokens, blocks, per_g, per_d, nwg, seed, 10 ** 5, late=1, sleep_at=at).run()
+            assert y == ["ok"] * per_d, (seed, at)
+
+
+@pytest.mark.parametrize("blocks,per_g,per_d,nwg", SHAPES)
 def test_a_watch_given_up_ends_in_nan(blocks, per_g, per_d, nwg):
     """Whoever gives up watching tells the others so, not that all is there."""
     seen = set()
@@ -214,3 +237,13 @@ def test_a_wait_for_the_routing_given_up_ends_in_nan(blocks, per_g, per_d, nwg, 
             assert set(y) <= {"ok", "nan"}, (seed, patience, y)
             seen |= set(y)
     assert "nan" in seen
+
+
+@pytest.mark.parametrize("impatient", [1, 2, 5])
+def test_one_workgroup_that_gives_up_the_routing(impatient):
+    """It alone: the others find its units missing, and give up in turn."""
+    for seed in range(20):
+        c = Call(61, [1, 1, 1], 8, 6, 16, seed, 3000)
+        waiter, asked = c.waiter, iter(range(1000))
+        c.waiter = lambda: (lambda: True) if next(asked) == impatient else waiter()
+        assert set(c.run()) <= {"ok", "nan"}
