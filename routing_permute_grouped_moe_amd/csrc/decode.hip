@@ -912,6 +912,8 @@ __device__ __forceinline__ void decode_stream(const DecArgs& a, DecLds& l) {
 
 // ---- the finishing wave
 
+constexpr float BF16_MAX = 0x1.fep127f;
+
 // silu(g) u; the sum of two bf16 that the second product reads carries 16
 // bits of it, so its rounding does not show beside that of the result
 __device__ __forceinline__ float decode_swiglu(float g, float u) {
@@ -1024,7 +1026,9 @@ __device__ __forceinline__ void decode_finish(const DecArgs& a, DecLds& l) {
               const float s = decode_swiglu(s0, s1);
               const long long at = (long long)row * a.I + col + c;
               if constexpr (sizeof(T) == 2) {
-                const uint32_t hi = f32_to_bf16(s);
+                // (held to the finite values: with hi an infinity, s - hi would be NaN or
+                // the opposite one; so an infinite s is lo's, and NaN too)
+                const uint32_t hi = f32_to_bf16(fminf(fmaxf(s, -BF16_MAX), BF16_MAX));
                 dev_store((bf16_t*)a.act + at, hi);
                 dev_store((bf16_t*)a.act + plane + at, f32_to_bf16(s - bf16_to_f32(hi)));
               } else {

@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from decode_util import (U, assert_within, ref_decode, ref_linear, ref_logits, ref_route)
+from decode_util import (U, assert_within, f64, ref_decode, ref_linear, ref_logits, ref_route)
 from gpu_util import have_gpu
 
 pytestmark = [pytest.mark.gpu,
@@ -393,3 +393,33 @@ def test_a_wait_given_up_is_nan_throughout(T, H, I, E, k, shared, no_patience):
     abi.moe_decode_wait_limit(1000000)
     r = op.forward(x, residual=res)
     assert all(torch.equal(a, b) for a, b in zip(want, r))
+
+
+@pytest.mark.parametrize("T", [1, 12, 20])
+def test_activations_beyond_bf16(T):
+    """An activation that overflows fp32 is an infinity in y (not NaN); one that is
+    finite but above the largest bf16 counts as it is."""
+    H = I = 64
+    op, n = make(T, H, I, 2, 1, router=False, seed=T)
+    lg = torch.zeros(T, 2, device="cuda")
+    lg[:, 0] = 1.0
+    x = torch.zeros(T, H, dtype=BF, device="cuda")
+    x[:, :2] = 1.0
+    for t in (op.w13, op.w2):
+        t.zero_()
+    # gate 1.99997 x 2^63 (the sum of two bf16), up 2^64
+    op.w13[0, :2, 0] = 1.9921875 * 2.0 ** 63
+    op.w13[0, :2, 1] = 1.9921875 * 2.0 ** 55
+    op.w13[0, I, 0], op.w13[0, I + 1, 0] = 2.0 ** 64, -(2.0 ** 64)
+    op.w2[0, 0, 0] = op.w2[0, 1, 1] = 2.0 ** -10
+    y = f64(op.forward(x, logits=lg).y)
+    s = torch.softmax(f64(lg), dim=1)[:, 0] * (1.9921875 + 1.9921875 / 256) * 2.0 ** 117
+    # (within bf16's half step, and the 16 bits of the activation)
+    assert ((y[:, 0] - s).abs() <= 1.01 * 2.0 ** -8 * s).all(), y[0, :2]
+    assert ((y[:, 1] + s).abs() <= 1.01 * 2.0 ** -8 * s).all(), y[0, :2]
+    # up 2^66: infinities, all of them, against weights without a zero
+    op.w13[0, :I, :2] = op.w13[0, :1, :2].clone()
+    op.w13[0, I:, 0] = 2.0 ** 66
+    op.w2[0, 2], op.w2[0, 3] = 2.0 ** -10, -(2.0 ** -10)
+    y = op.forward(x, logits=lg).y
+    assert (y[:, 2] == float("inf")).all() and (y[:, 3] == -float("inf")).all(), y[0, :4]
