@@ -406,9 +406,10 @@ void moe_decode_wait_limit(unsigned us);
  * be its buffer), z [M,N] (nullable: kept for the backward).  Products and the
  * epilogue are fp32; z and y are each rounded once (act sees the unrounded z).
  * act: MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU (z sigma(z)), MOE_ACT_GELU
- * (z Phi(z)) or MOE_ACT_GELU_TANH (its tanh form).  N and K are multiples of
- * 64; M is any number; x, w, y are below 2 GiB each.  ws: scratch of
- * moe_linear_workspace_bytes bytes, 256-byte aligned (NULL where that is 0).
+ * (z Phi(z)) or MOE_ACT_GELU_TANH (its tanh form); at infinities these and
+ * their derivatives are their limits, and a NaN gives NaN.  N and K are
+ * multiples of 64; M is any number; x, w, y are below 2 GiB each.  ws: scratch
+ * of moe_linear_workspace_bytes bytes, 256-byte aligned (NULL where that is 0).
  */
 enum {
   MOE_ACT_NONE = 0,

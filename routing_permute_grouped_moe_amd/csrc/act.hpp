@@ -36,16 +36,21 @@ __device__ __forceinline__ float act_phi(float z, float& gauss) {
 
 // gelu is z Phi(z); its tanh form is z s(2 u), u = c (z + q z^3), since (1 +
 // tanh u) / 2 = s(2 u).
+// z p for a p that falls to 0 faster than z grows: 0 at z = -infinity too
+__device__ __forceinline__ float act_times(float z, float p) {
+  return p == 0.f ? 0.f : z * p;
+}
+
 __device__ __forceinline__ float act_value(float z, int act) {
   switch (act) {
     case MOE_ACT_RELU: return z < 0.f ? 0.f : z;   // (a NaN stays one)
-    case MOE_ACT_SILU: return z * act_sigmoid(z);
+    case MOE_ACT_SILU: return act_times(z, act_sigmoid(z));
     case MOE_ACT_GELU: {
       float gauss;
-      return z * act_phi(z, gauss);
+      return act_times(z, act_phi(z, gauss));
     }
     case MOE_ACT_GELU_TANH:
-      return z * act_sigmoid(2.0f * ACT_GELU_C * (z + ACT_GELU_Q * z * z * z));
+      return act_times(z, act_sigmoid(2.0f * ACT_GELU_C * (z + ACT_GELU_Q * z * z * z)));
     default: return z;
   }
 }
@@ -54,6 +59,7 @@ __device__ __forceinline__ float act_slope(float z, int act) {
   switch (act) {
     case MOE_ACT_RELU: return z > 0.f ? 1.f : (z != z ? z : 0.f);
     case MOE_ACT_SILU: {
+      if (fabsf(z) > 100.f) return z > 0.f ? 1.f : 0.f;   // its limits, ahead of infinity times 0
       const float s = act_sigmoid(z);
       return s * (1.0f + z * (1.0f - s));
     }

@@ -260,3 +260,32 @@ def test_backward_replays_from_a_graph():
             assert torch.equal(a, b)
         for a, b in zip(step(), want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("M", [9, 100])
+def test_infinite_pre_activations(M, dt):
+    """At infinities the activations and their slopes are their limits; a NaN
+    stays one."""
+    from routing_permute_grouped_moe_amd.layer import Linear
+    inf, N, K = float("inf"), 128, 64
+    n = normal(8)
+    x, w, dy = n(M, K, d=dt), n(N, K, std=1 / 8, d=dt), n(M, N, d=dt)
+    b = torch.zeros(N, device="cuda")
+    b[3], b[5], b[7] = inf, -inf, float("nan")
+    eye = torch.zeros(N, N, dtype=dt, device="cuda")
+    eye.fill_diagonal_(1.0)
+    for act in ACTS:
+        y, z = Linear(w, bias=b, act=act).forward(x, save_z=True)
+        assert (z[:, 3] == inf).all() and (z[:, 5] == -inf).all() and torch.isnan(z[:, 7]).all()
+        assert (y[:, 3] == inf).all() and torch.isnan(y[:, 7]).all(), act
+        assert (y[:, 5] == (-inf if act == "none" else 0)).all(), (act, y[0, 5])
+        rest = [i for i in range(N) if i not in (3, 5, 7)]
+        assert torch.isfinite(y[:, rest]).all(), act
+        if act == "none":
+            continue
+        # the slopes, by db of one row at a time's worth: a column of db sums its own
+        _, _, db = Linear(eye, act=act).backward(dy, dy, z=z, bias_grad=True)
+        s = dy[:, 3].double().sum()
+        assert abs(db[3].double() - s) <= (M + 2) * 2.0 ** -24 * dy[:, 3].double().abs().sum(), act
+        assert db[5] == 0 and torch.isnan(db[7]) and torch.isfinite(db[rest]).all(), (act, db[:8])
