@@ -374,11 +374,12 @@ int moe_grouped_gemm_bwd_dw_recompute(const void* x, const int32_t* src_token, i
  * of other experts add nothing: they are another device's part of the sum).
  * Router ([H,E] fp32): the logits are exact sums rounded once to fp32, and
  * idx / gate follow from them ([T,E], [T,k], [T,k] outputs).  With wg NULL
- * logits is an input (bias must be NULL).  A logit of -inf masks an expert; a
- * token whose logits are all -inf gets gates of zero; one with a NaN among
- * them gets gates of NaN.  Shared expert: ws13 [2I,H] and ws2 [H,I], both or
- * neither.  residual [T,H] is nullable, and y may be its buffer.  Gate/up
- * values, expert outputs and the sum stay in fp32; y is rounded once.
+ * logits is an input (bias must be NULL).  A logit of -inf masks an expert: a
+ * pair whose gate is zero adds nothing, whatever the expert holds.  A token
+ * whose logits are all -inf gets gates of zero; one with a NaN among them gets
+ * gates of NaN.  Shared expert: ws13 [2I,H] and ws2 [H,I], both or neither.
+ * residual [T,H] is nullable, and y may be its buffer.  Gate/up values, expert
+ * outputs and the sum stay in fp32; y is rounded once.
  * T <= 128 and T k <= 2048 (MOE_ERR_UNSUPPORTED beyond: the grouped path is
  * the faster one there), one expert's w13 and the call's rows below 2 GiB.
  * ws: moe_decode_workspace_bytes bytes (256-byte aligned, contents scratch),

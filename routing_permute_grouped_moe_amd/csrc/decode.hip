@@ -933,7 +933,9 @@ __device__ __forceinline__ void elem_store(void* p, long long i, float v) {
 
 // residual + shared + sum_j gate yp[t, j], in that order; pair(p) gives a
 // pair's expert and gate.  (For a pair outside the window row 0 is read, and not
-// added: a branch for each would have every load waited for in turn.)
+// added: a branch for each would have every load waited for in turn.)  A gate of
+// zero adds nothing either: a masked expert, there to fill the k slots, may hold
+// infinities or NaN.
 template <typename T, typename Pair>
 __device__ __forceinline__ float decode_sum(const DecArgs& a, int t, int h, Pair&& pair) {
   float s = a.residual != nullptr ? elem_load<T>(a.residual, (long long)t * a.H + h) : 0.f;
@@ -950,7 +952,7 @@ __device__ __forceinline__ float decode_sum(const DecArgs& a, int t, int h, Pair
       v[q] = a.yp[(long long)(in[q] ? p : 0) * a.H + h];
     }
 #pragma unroll
-    for (int q = 0; q < 8; ++q) s += in[q] ? gate[q] * v[q] : 0.f;
+    for (int q = 0; q < 8; ++q) s += in[q] && gate[q] != 0.f ? gate[q] * v[q] : 0.f;
   }
   return s;
 }

@@ -423,3 +423,26 @@ def test_activations_beyond_bf16(T):
     op.w2[0, 2], op.w2[0, 3] = 2.0 ** -10, -(2.0 ** -10)
     y = op.forward(x, logits=lg).y
     assert (y[:, 2] == float("inf")).all() and (y[:, 3] == -float("inf")).all(), y[0, :4]
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("T", [1, 8, 40])
+def test_a_masked_expert_adds_nothing_whatever_it_holds(T, dt):
+    """Experts masked by -inf that fill a token's last slots (fewer are left than
+    k), or all slots of a token without any: their weights, or the token's own x,
+    may hold infinities and NaN."""
+    E, k, H, I = 5, 4, 128, 64
+    op, n = make(T, H, I, E, k, dt=dt, router=False, seed=T)
+    lg = n(T, E, d=F32)
+    lg[:, 2:4] = -float("inf")
+    x, res = n(T, H, d=dt), n(T, H, d=dt)
+    want = op.forward(x, residual=res, logits=lg)
+    assert torch.isfinite(want.y).all()
+    op.w13[2] = float("nan")
+    op.w2[3] = float("inf")
+    r = op.forward(x, residual=res, logits=lg)
+    assert all(torch.equal(a, b) for a, b in zip(want, r))
+    lg[0] = -float("inf")
+    x[0] = float("nan")
+    r = op.forward(x, residual=res, logits=lg)
+    assert torch.equal(r.y[0], res[0]) and torch.equal(r.y[1:], want.y[1:])
