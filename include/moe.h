@@ -378,8 +378,9 @@ int moe_grouped_gemm_bwd_dw_recompute(const void* x, const int32_t* src_token, i
  * pair whose gate is zero adds nothing, whatever the expert holds.  A token
  * whose logits are all -inf gets gates of zero; one with a NaN among them gets
  * gates of NaN.  Shared expert: ws13 [2I,H] and ws2 [H,I], both or neither.
- * residual [T,H] is nullable, and y may be its buffer.  Gate/up values, expert
- * outputs and the sum stay in fp32; y is rounded once.
+ * residual [T,H] is nullable, and y may be its buffer; other than that no output
+ * shares memory with another operand (MOE_ERR_INVALID_ARG).  Gate/up values,
+ * expert outputs and the sum stay in fp32; y is rounded once.
  * T <= 128 and T k <= 2048 (MOE_ERR_UNSUPPORTED beyond: the grouped path is
  * the faster one there), one expert's w13 and the call's rows below 2 GiB.
  * ws: moe_decode_workspace_bytes bytes (256-byte aligned, contents scratch),
@@ -404,7 +405,8 @@ void moe_decode_wait_limit(unsigned us);
  * stream, dense feed-forward layers):
  *   z = x W^T + bias,  y = act(z) + residual
  * x [M,K], w [N,K], bias [N] fp32 (nullable), residual [M,N] (nullable; y may
- * be its buffer), z [M,N] (nullable: kept for the backward).  Products and the
+ * be its buffer, and shares memory with nothing else), z [M,N] (nullable: kept
+ * for the backward; a buffer of its own).  Products and the
  * epilogue are fp32; z and y are each rounded once (act sees the unrounded z).
  * act: MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU (z sigma(z)), MOE_ACT_GELU
  * (z Phi(z)) or MOE_ACT_GELU_TANH (its tanh form); at infinities these and
@@ -428,7 +430,7 @@ int moe_linear(const void* x, int dt, int M, int N, int K, const void* w, const 
  * MOE_ACT_NONE):
  *   dz = dy * act'(z),  dx = dz W,  dw = dz^T x,  db = sum_m dz
  * dx [M,K], dw [N,K] and db [N] (fp32) are each written if not NULL, into
- * buffers that are none of the inputs'; the gradient of the residual is dy
+ * buffers that share no memory with each other or an input; the gradient of the residual is dy
  * itself.  dz is rounded to the storage type for the two products (they read it
  * on the matrix cores); db sums it unrounded.  M == 0 writes zeros to dw and db.  ws: scratch of
  * moe_linear_bwd_workspace_bytes bytes, 256-byte aligned.

@@ -1250,13 +1250,25 @@ extern "C" int moe_decode(const void* x, int dt, const float* wg, const float* b
   MOE_TRY(moe_need_ptr(idx, fn, "idx", 4));
   MOE_TRY(moe_need_ptr(gate, fn, "gate", 4));
   MOE_TRY(moe_need_ptr(y, fn, "y"));
-  if (y == x)
-    return moe_fail(MOE_ERR_INVALID_ARG, "%s: y is x's buffer (it may be residual's)", fn);
   MOE_TRY(moe_need_ptr(ws, fn, "ws", 256));
   const DecWs w = decode_ws(T, H, I, E, k);
   if (ws_bytes < w.total)
     return moe_fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", fn, ws_bytes,
                     w.total);
+  const long long es = moe_dt_bytes(dt), th = (long long)T * H * es, ih = (long long)I * H * es;
+  const MoeRange rx = {x, th, "x"}, rg = {wg, 4LL * H * E, "wg"}, rb = {bias, 4LL * E, "bias"},
+                 r13 = {w13, 2 * G * ih, "w13"}, r2 = {w2, G * ih, "w2"},
+                 rs13 = {ws13, 2 * ih, "ws13"}, rs2 = {ws2, ih, "ws2"}, rr = {residual, th, "residual"},
+                 outs[] = {{y, th, "y"}, {logits, 4LL * T * E, "logits"}, {idx, 4LL * T * k, "idx"},
+                           {gate, 4LL * T * k, "gate"}, {ws, (long long)w.total, "ws"}};
+  for (int i = 0; i < 5; ++i) {
+    const char* with = moe_shares(outs[i], {rx, rg, rb, r13, r2, rs13, rs2, rr},
+                                  i == 0 ? residual : nullptr);
+    for (int j = 0; j < i && with == nullptr; ++j) with = moe_shares(outs[i], {outs[j]});
+    if (with != nullptr)
+      return moe_fail(MOE_ERR_INVALID_ARG, "%s: %s overlaps %s's buffer (y may be residual's)", fn,
+                      outs[i].name, with);
+  }
   DecArgs a = {};
   a.x = x; a.wg = wg; a.bias = bias;
   a.T = T; a.H = H; a.I = I; a.E = E; a.k = k; a.g0 = g0; a.G = G;

@@ -332,19 +332,37 @@ extern "C" int moe_linear(const void* x, int dt, int M, int N, int K, const void
   MOE_TRY(moe_opt_ptr(residual, fn, "residual"));
   MOE_TRY(moe_opt_ptr(z, fn, "z"));
   MOE_TRY(moe_need_ptr(y, fn, "y"));
-  if (y == x || y == w || z == x || (z != nullptr && z == w) || (z != nullptr && (z == y || z == residual)))
-    return moe_fail(MOE_ERR_INVALID_ARG, "%s: y and z need buffers of their own (y may be residual's)",
-                    fn);
-  hipStream_t s = (hipStream_t)stream;
-  if (few_rows(M, N, K, dt)) {
-    LinArgs a = {x, w, bias, residual, z, y, M, N, K, act};
-    return dt == MOE_BF16 ? linear_rows<bf16_t>(a, s, fn) : linear_rows<float>(a, s, fn);
-  }
-  MOE_TRY(lin_tile_checks(fn, dt, M, N, K));
+  const bool few = few_rows(M, N, K, dt);
+  if (!few) MOE_TRY(lin_tile_checks(fn, dt, M, N, K));
   const size_t need = fwd_ws(M, N, K, dt);
   if (need > 0) MOE_TRY(moe_need_ptr(ws, fn, "ws", 256));
   if (ws_bytes < need)
     return moe_fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", fn, ws_bytes, need);
+  // (the products read x and W to the end of the launch; a residual that y is
+  // written over is read by the thread that writes, so only element for element)
+  const long long es = moe_dt_bytes(dt), mn = (long long)M * N * es;
+  const MoeRange rx = {x, (long long)M * K * es, "x"}, rw = {w, (long long)N * K * es, "w"},
+                 rb = {bias, 4LL * N, "bias"}, rr = {residual, mn, "residual"}, rz = {z, mn, "z"},
+                 ry = {y, mn, "y"}, rs = {need > 0 ? ws : nullptr, (long long)need, "ws"};
+  const char* with = moe_shares(ry, {rx, rw, rb, rr, rz, rs}, residual);
+  const char* out = "y";
+  if (with == nullptr) {
+    with = moe_shares(rz, {rx, rw, rb, rr, rs});
+    out = "z";
+  }
+  if (with == nullptr) {
+    with = moe_shares(rs, {rx, rw, rb, rr});
+    out = "ws";
+  }
+  if (with != nullptr)
+    return moe_fail(MOE_ERR_INVALID_ARG,
+                    "%s: %s overlaps %s (y and z need buffers of their own; y may be residual's)", fn,
+                    out, with);
+  hipStream_t s = (hipStream_t)stream;
+  if (few) {
+    LinArgs a = {x, w, bias, residual, z, y, M, N, K, act};
+    return dt == MOE_BF16 ? linear_rows<bf16_t>(a, s, fn) : linear_rows<float>(a, s, fn);
+  }
   if (!fwd_big(M, N, dt))
     return moe_dense_fwd(x, dt, M, N, K, w, bias, act, residual, z, y, ws, s);
   return moe_gmm_linear_fwd(x, dt, M, N, K, w, bias, act, residual, z, y, s);
@@ -370,17 +388,28 @@ extern "C" int moe_linear_bwd(const void* dy, const void* z, const void* x, cons
     if (act != MOE_ACT_NONE) MOE_TRY(moe_need_ptr(z, fn, "z"));
     if (dw != nullptr) MOE_TRY(moe_need_ptr(x, fn, "x"));
     if (dx != nullptr) MOE_TRY(moe_need_ptr(w, fn, "w"));
-    // (both products read dy or dz, and x or W, to the end of the launch)
-    auto taken = [&](const void* p) {
-      return p != nullptr && (p == dy || p == z || p == x || p == w);
-    };
-    if (taken(dx) || taken(dw) || taken(db) || (dx != nullptr && dx == dw))
-      return moe_fail(MOE_ERR_INVALID_ARG, "%s: %s needs a buffer of its own", fn,
-                      taken(dx) ? "dx" : taken(db) ? "db" : "dw");
+    // (both products read dy or dz, and x or W, to the end of the launch, and
+    // the outputs are written side by side)
+    const long long es = moe_dt_bytes(dt), mn = (long long)M * N * es, mk = (long long)M * K * es,
+                    nk = (long long)N * K * es;
+    const MoeRange rdy = {dy, mn, "dy"}, rz = {z, mn, "z"}, rx = {x, mk, "x"}, rw = {w, nk, "w"},
+                   outs[] = {{dx, mk, "dx"}, {dw, nk, "dw"}, {db, 4LL * N, "db"}};
+    for (int i = 0; i < 3; ++i) {
+      const char* with = moe_shares(outs[i], {rdy, rz, rx, rw});
+      for (int j = 0; j < i && with == nullptr; ++j) with = moe_shares(outs[i], {outs[j]});
+      if (with != nullptr)
+        return moe_fail(MOE_ERR_INVALID_ARG, "%s: %s needs a buffer of its own, it overlaps %s", fn,
+                        outs[i].name, with);
+    }
     MOE_TRY(moe_need_ptr(ws, fn, "ws", 256));
     if (ws_bytes < lay.total)
       return moe_fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", fn, ws_bytes,
                       lay.total);
+    const bool any = dx != nullptr || dw != nullptr || db != nullptr;
+    const char* with = any ? moe_shares({ws, (long long)lay.total, "ws"},
+                                        {rdy, rz, rx, rw, outs[0], outs[1], outs[2]}) : nullptr;
+    if (with != nullptr)
+      return moe_fail(MOE_ERR_INVALID_ARG, "%s: ws overlaps %s", fn, with);
   }
   if (dx == nullptr && dw == nullptr && db == nullptr) return MOE_OK;
   hipStream_t s = (hipStream_t)stream;

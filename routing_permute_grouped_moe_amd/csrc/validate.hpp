@@ -4,6 +4,8 @@
 
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "common.hpp"
 
 #define MOE_MAX_E 1024
@@ -62,4 +64,22 @@ static inline int moe_need_elems(long long rows, long long cols, int bytes, cons
     return moe_fail(MOE_ERR_UNSUPPORTED, "%s: %s has %lld x %lld elements, above the limit", fn,
                     name, rows, cols);
   return MOE_OK;
+}
+
+// Memory of a call's operand (p nullable).
+struct MoeRange {
+  const void* p; long long bytes; const char* name;
+};
+
+// The one of `others` that shares memory with `out`, or null.  same: an operand
+// that may be out's very buffer (but not a shifted one).
+static inline const char* moe_shares(const MoeRange& out, std::initializer_list<MoeRange> others,
+                                     const void* same = nullptr) {
+  const uintptr_t a = (uintptr_t)out.p;
+  for (const MoeRange& o : others) {
+    const uintptr_t b = (uintptr_t)o.p;
+    if (a == 0 || b == 0 || out.bytes <= 0 || o.bytes <= 0 || (o.p == same && o.p == out.p)) continue;
+    if (a < b + (uintptr_t)o.bytes && b < a + (uintptr_t)out.bytes) return o.name;
+  }
+  return nullptr;
 }

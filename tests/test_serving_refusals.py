@@ -195,3 +195,65 @@ def test_tensors_are_checked(abi):
         _check("t", torch.zeros(8, 4).t(), torch.float32, cpu, 4, 8)
     with pytest.raises(ValueError, match="the weights are on"):
         _check("t", t, torch.float32, torch.device("cuda", 0), 4, 8)
+
+
+# ranges that do not meet; y may be residual's very buffer and nothing else
+APART = dict(DECODE, w13=0x1000000, w2=0x2000000, wg=0x3000000, logits=0x40000, idx=0x50000,
+             gate=0x60000, ws=0x10000000, residual=0x70000, y=0x80000)
+
+
+@pytest.mark.parametrize("change,text", [
+    ({"y": P + 16}, "y overlaps x"),                        # x is 4 x 128 bf16: 1024 bytes
+    ({"y": P - 1008}, "y overlaps x"),
+    ({"y": 0x70000 + 256}, "y overlaps residual"),          # the residual's, shifted by a row
+    ({"y": 0x70000 - 256}, "y overlaps residual"),
+    ({"y": 0x1000000 + 4096}, "y overlaps w13"),
+    ({"y": 0x2000000 + 8 * 128 * 64 * 2 - 16}, "y overlaps w2"),
+    ({"y": 0x3000000}, "y overlaps wg"),
+    ({"logits": P}, "logits overlaps x"),
+    ({"idx": 0x40000 + 64}, "idx overlaps logits"),
+    ({"gate": 0x50000 + 16}, "gate overlaps idx"),
+    ({"gate": 0x80000}, "gate overlaps y"),
+    ({"ws": 0x80000 - 0x10000}, "ws overlaps"),
+    ({"wg": None, "bias": None, "logits": 0x80000}, "logits overlaps y"),
+    ({"ws13": 0x4000000, "ws2": 0x5000000, "y": 0x4000000 + 128}, "y overlaps ws13"),
+])
+def test_decode_refuses_outputs_over_operands(abi, change, text):
+    st = abi._lib.moe_decode(*{**APART, **change}.values())
+    assert st == abi.MOE_ERR_INVALID_ARG and text in abi.moe_last_error(), abi.moe_last_error()
+
+
+@pytest.mark.parametrize("change,text", [
+    ({"y": P + 16}, "y overlaps x"),
+    ({"y": P - 512}, "y overlaps x"),                       # y is 4 x 128 bf16
+    ({"w": 0x400000, "y": 0x400000 + 128 * 64 * 2 - 16}, "y overlaps w"),
+    ({"residual": 2 * P + 256}, "y overlaps residual"),
+    ({"residual": 2 * P - 256}, "y overlaps residual"),
+    ({"bias": 2 * P + 64}, "y overlaps bias"),
+    ({"z": 2 * P + 1008}, "y overlaps z"),
+    ({"z": P + 16}, "z overlaps x"),
+    ({"z": 3 * P, "residual": 3 * P - 16}, "z overlaps residual"),
+    ({"z": 3 * P, "bias": 3 * P}, "z overlaps bias"),
+    ({"M": 100, "K": 4096, "x": 0x1000000, "w": 0x2000000, "ws": 0x1000100, "ws_bytes": 1 << 30},
+     "ws overlaps x"),
+    ({"M": 100, "K": 4096, "x": 0x1000000, "w": 0x2000000, "ws": 2 * P - 256, "ws_bytes": 1 << 30},
+     "y overlaps ws"),
+])
+def test_linear_refuses_outputs_over_operands(abi, change, text):
+    st = abi._lib.moe_linear(*{**LINEAR, **change}.values())
+    assert st == abi.MOE_ERR_INVALID_ARG and text in abi.moe_last_error(), abi.moe_last_error()
+
+
+@pytest.mark.parametrize("change,text", [
+    ({"db": 2 * P}, "db needs a buffer of its own, it overlaps dx"),
+    ({"db": 3 * P}, "db needs a buffer of its own, it overlaps dw"),
+    ({"db": 3 * P + 128 * 64 * 2 - 16}, "db needs a buffer of its own, it overlaps dw"),
+    ({"dx": 3 * P + 64}, "dw needs a buffer of its own, it overlaps dx"),
+    ({"dx": P + 128}, "overlaps dy"),
+    ({"dw": P - 128 * 64 * 2 + 16}, "dw needs a buffer of its own"),
+    ({"ws": 2 * P}, "ws overlaps dx"),
+    ({"ws": P}, "ws overlaps dy"),
+])
+def test_linear_bwd_refuses_outputs_over_operands(abi, change, text):
+    st = abi._lib.moe_linear_bwd(*{**BWD, "ws": 0x1000000, **change}.values())
+    assert st == abi.MOE_ERR_INVALID_ARG and text in abi.moe_last_error(), abi.moe_last_error()
