@@ -337,8 +337,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 def _on(device, stream, call, *inputs):
     """call(raw stream) with the device of a call's tensors current, and the
     given stream too (None: the device's current one), so that outputs and
-    workspaces allocated inside belong to it; the inputs, which may not, are
-    kept from reuse until the stream has passed."""
+    workspaces allocated inside belong to it; the inputs and weights, which may
+    not, are kept from reuse until the stream has passed."""
     if stream is None:
         if torch.cuda.current_device() == device.index:
             return call(_raw_stream(device.index))
@@ -439,7 +439,8 @@ class MoeDecode:
                            self.w13, self.w2, self.ws13, self.ws2, residual, lg, idx, gate, y, ws,
                            n, st)
             return Decoded(y, idx, gate, lg)
-        return _on(dev, stream, call, x, residual, logits, out)
+        return _on(dev, stream, call, x, residual, logits, out, self.w13, self.w2, self.wg,
+                   self.bias, self.ws13, self.ws2)
 
 
 ACTS = {"none": abi.MOE_ACT_NONE, "relu": abi.MOE_ACT_RELU, "silu": abi.MOE_ACT_SILU,
@@ -484,7 +485,7 @@ class Linear:
             abi.moe_linear(x, self.dt, M, self.N, self.K, self.w, self.bias, self.act, residual,
                            z, y, ws, n, st)
             return (y, z) if save_z else y
-        return _on(dev, stream, call, x, residual, out)
+        return _on(dev, stream, call, x, residual, out, self.w, self.bias)
 
     def backward(self, dy, x, z=None, bias_grad=None, stream=None):
         """(dx, dw, db) of ``dy`` [M, N], the forward's ``x`` and the ``z`` it
@@ -508,4 +509,4 @@ class Linear:
             abi.moe_linear_bwd(dy, z, x, self.w, self.dt, M, self.N, self.K, self.act, dx, dw, db,
                                ws, n, st)
             return dx, dw, db
-        return _on(dev, stream, call, dy, x, z)
+        return _on(dev, stream, call, dy, x, z, self.w)

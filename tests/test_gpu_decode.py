@@ -446,3 +446,24 @@ def test_a_masked_expert_adds_nothing_whatever_it_holds(T, dt):
     x[0] = float("nan")
     r = op.forward(x, residual=res, logits=lg)
     assert torch.equal(r.y[0], res[0]) and torch.equal(r.y[1:], want.y[1:])
+
+
+def test_weights_dropped_behind_another_stream():
+    """Weights that the caller drops, layer and all, while the call still waits on
+    its stream are not handed out again before it has read them."""
+    from routing_permute_grouped_moe_amd.layer import MoeDecode
+    op, n = make(4, 1024, 512, 16, 4, shared=True)
+    x = n(4, 1024)
+    want = op.forward(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(40_000_000)
+    names = ("w13", "w2", "wg", "bias", "ws13", "ws2")
+    other = MoeDecode(op.s, **{m: getattr(op, m).clone() for m in names})
+    torch.cuda.current_stream().synchronize()
+    got = other.forward(x, stream=side)
+    del other
+    junk = [torch.full_like(getattr(op, m), float("nan")) for m in names for _ in range(3)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got)) and len(junk) == 18

@@ -289,3 +289,25 @@ def test_infinite_pre_activations(M, dt):
         s = dy[:, 3].double().sum()
         assert abs(db[3].double() - s) <= (M + 2) * 2.0 ** -24 * dy[:, 3].double().abs().sum(), act
         assert db[5] == 0 and torch.isnan(db[7]) and torch.isfinite(db[rest]).all(), (act, db[:8])
+
+
+def test_weights_dropped_behind_another_stream():
+    from routing_permute_grouped_moe_amd.layer import Linear
+    n = normal(12)
+    x, w, dy, z = n(200, 1024), n(640, 1024), n(200, 640), n(200, 640)
+    b = n(640, d=F32)
+    op = Linear(w, bias=b, act="silu")
+    y, grads = op.forward(x), op.backward(dy, x, z=z)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(40_000_000)
+    other, last = (Linear(w.clone(), bias=b.clone(), act="silu") for _ in range(2))
+    torch.cuda.current_stream().synchronize()
+    got_y = other.forward(x, stream=side)
+    got = last.backward(dy, x, z=z, stream=side)
+    del other, last
+    junk = [torch.full_like(t, float("nan")) for t in (w, b) for _ in range(6)]
+    torch.cuda.synchronize()
+    assert torch.equal(y, got_y) and all(torch.equal(p, q) for p, q in zip(grads, got))
+    assert len(junk) == 12
