@@ -381,6 +381,8 @@ class MoeDecode:
             raise ValueError("the few-token layer drops no pairs: capacity must be None")
         if s.router != (wg is not None):
             raise ValueError("wg comes with shape.router, and only with it")
+        if bias is not None and wg is None:
+            raise ValueError("bias comes with wg, and only with it")
         if s.shared != (ws13 is not None) or s.shared != (ws2 is not None):
             raise ValueError("ws13 and ws2 come with shape.shared, and only with it")
         dev = self.device = _device(w13)

@@ -257,3 +257,11 @@ def test_linear_refuses_outputs_over_operands(abi, change, text):
 def test_linear_bwd_refuses_outputs_over_operands(abi, change, text):
     st = abi._lib.moe_linear_bwd(*{**BWD, "ws": 0x1000000, **change}.values())
     assert st == abi.MOE_ERR_INVALID_ARG and text in abi.moe_last_error(), abi.moe_last_error()
+
+
+def test_a_bias_without_a_router_is_refused_when_the_layer_is_made(abi):
+    from routing_permute_grouped_moe_amd.layer import LayerShape, MoeDecode
+    s = LayerShape(T=4, H=64, I=64, E=2, k=1, dtype=torch.bfloat16, router=False)
+    w = torch.zeros(2, 128, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="bias comes with wg"):
+        MoeDecode(s, w, w, bias=torch.zeros(2))
