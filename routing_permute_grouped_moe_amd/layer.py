@@ -489,10 +489,12 @@ class Linear:
             return (y, z) if save_z else y
         return _on(dev, stream, call, x, residual, out, self.w, self.bias)
 
-    def backward(self, dy, x, z=None, bias_grad=None, stream=None):
+    def backward(self, dy, x, z=None, bias_grad=None, stream=None, x_grad=True, w_grad=True):
         """(dx, dw, db) of ``dy`` [M, N], the forward's ``x`` and the ``z`` it
-        kept (None without an activation).  db is None unless ``bias_grad``
-        (by default: unless there is a bias).  The residual's gradient is dy."""
+        kept (None without an activation).  Each is computed, or None, as
+        ``x_grad`` (a first layer needs none), ``w_grad`` (frozen weights) and
+        ``bias_grad`` (by default: whether there is a bias) say.  The residual's
+        gradient is dy."""
         M, dev = dy.shape[0], self.device
         _check("dy", dy, self.dtype, dev, M, self.N)
         _check("x", x, self.dtype, dev, M, self.K)
@@ -504,7 +506,8 @@ class Linear:
             bias_grad = self.bias is not None
 
         def call(st):
-            dx, dw = torch.empty_like(x), torch.empty_like(self.w)
+            dx = torch.empty_like(x) if x_grad else None
+            dw = torch.empty_like(self.w) if w_grad else None
             db = x.new_empty(self.N, dtype=torch.float32) if bias_grad else None
             n = abi.moe_linear_bwd_workspace_bytes(M, self.N, self.K, self.dt, self.act)
             ws = x.new_empty(n, dtype=torch.uint8)

@@ -311,3 +311,19 @@ def test_weights_dropped_behind_another_stream():
     torch.cuda.synchronize()
     assert torch.equal(y, got_y) and all(torch.equal(p, q) for p, q in zip(grads, got))
     assert len(junk) == 12
+
+
+@pytest.mark.parametrize("M", [40, 700])
+def test_only_the_gradients_asked_for(M):
+    """A first layer needs no dx, frozen weights no dW: the products that are not
+    asked for are not made, and the others keep their bits."""
+    from routing_permute_grouped_moe_amd.layer import Linear
+    n = normal(13)
+    x, w, dy, z = n(M, 320), n(192, 320), n(M, 192), n(M, 192)
+    op = Linear(w, act="gelu")
+    want = op.backward(dy, x, z=z, bias_grad=True)
+    for asked in range(8):
+        on = [bool(asked >> i & 1) for i in range(3)]
+        got = op.backward(dy, x, z=z, x_grad=on[0], w_grad=on[1], bias_grad=on[2])
+        for i in range(3):
+            assert torch.equal(got[i], want[i]) if on[i] else got[i] is None, (on, i)
