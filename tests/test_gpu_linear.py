@@ -327,3 +327,31 @@ def test_only_the_gradients_asked_for(M):
         got = op.backward(dy, x, z=z, x_grad=on[0], w_grad=on[1], bias_grad=on[2])
         for i in range(3):
             assert torch.equal(got[i], want[i]) if on[i] else got[i] is None, (on, i)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_activations_over_their_range(act):
+    """fp32 activations of z in [-20, 20], through the identity, against 64 bits.
+
+    In units of u = 2^-24: an exp is off by its argument's error (the product with
+    log2 e: 1 for the rounding, 0.3 for the constant; before it nothing for silu,
+    1 for z z in gelu, 5 for the cubic and its factors in the tanh form) times the
+    argument, and 2 for the exp2; then the sum 1, the reciprocal 2, the product 1.
+    gelu's polynomial adds 1.3 for its fit, 8 for t through its slope and 4 for its
+    own roundings.  Results near 2^-126 are 0."""
+    from routing_permute_grouped_moe_amd.layer import Linear
+    gen = torch.Generator().manual_seed(21)
+    z = (torch.rand(1024, 64, generator=gen) * 40 - 20).cuda()
+    y, kept = Linear(torch.eye(64, device="cuda"), act=act).forward(z, save_z=True)
+    assert torch.equal(kept, z)
+    zz = f64(z)
+    want = ref_act(zz, act)[0]
+    if act == "gelu_tanh":       # (its tanh loses all digits of 1 + tanh for z << 0)
+        arg = 2 * (2 / torch.pi) ** 0.5 * (zz + 0.044715 * zz ** 3)
+        want = zz / (1 + torch.exp(-arg))
+        bound = 8 + 6.3 * arg.abs()
+    elif act == "gelu":
+        bound = 20 + 2.3 * zz * zz / 2
+    else:
+        bound = 7 + 1.3 * zz.abs()
+    assert_within("y", y, (want, bound * 2.0 ** -24 * want.abs() + 4 * zz.abs() * 2.0 ** -126))
