@@ -19,7 +19,7 @@ __device__ __forceinline__ float act_sigmoid(float z) {
 // E(x) / 2 with x = |z| / sqrt 2 and E(x) = e^(x^2) erfc(x), and Phi(z) = 1 -
 // Phi(-z).  E is smooth and falls like 1/x, so it is a polynomial in t = 1 / (1
 // + 0.39 x); these coefficients are a weighted least-squares fit made minimax in
-// the relative error by reweighting (7.4e-8 on [0, 14]; beyond, the exponential
+// the relative error by reweighting (7e-8 on [0, 14]; beyond, the exponential
 // is zero).  In fp32 gelu was off by 5.5 x 2^-24 of its value at most for z > 0 and
 // by (8 + 0.75 z^2) 2^-24 below, where the exp's rounded argument is most of it.
 // gauss: e^(-z^2 / 2), which the slope needs too.  (erfcf took 39 us of the

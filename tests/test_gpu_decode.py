@@ -467,3 +467,14 @@ def test_weights_dropped_behind_another_stream():
     junk = [torch.full_like(getattr(op, m), float("nan")) for m in names for _ in range(3)]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, got)) and len(junk) == 18
+
+
+@pytest.mark.parametrize("T", [9, 40, 128])
+@pytest.mark.parametrize("shared", [False, True])
+def test_no_expert_on_this_device(T, shared):
+    """More tokens than every workgroup routes itself, and an empty window."""
+    op, n = make(T, 128, 64, 8, 2, G=0, shared=shared, seed=T)
+    x, res = n(T, 128), n(T, 128)
+    r = op.forward(x, residual=res)
+    check(op, x, r, residual=res)
+    assert shared or torch.equal(r.y, res)

@@ -355,3 +355,22 @@ def test_activations_over_their_range(act):
     else:
         bound = 7 + 1.3 * zz.abs()
     assert_within("y", y, (want, bound * 2.0 ** -24 * want.abs() + 4 * zz.abs() * 2.0 ** -126))
+
+
+@pytest.mark.parametrize("M,N,K,act,dt,bias,residual,z", [
+    # two column tiles a workgroup, of each row count
+    (24, 6208, 128, "silu", BF, True, True, True), (32, 6144, 64, "gelu", F32, True, True, False),
+    (40, 6144, 192, "none", BF, True, False, True), (48, 6208, 64, "relu", F32, False, True, True),
+    (49, 6208, 320, "gelu_tanh", BF, True, True, True), (64, 6144, 64, "none", F32, True, True, False),
+    # one column tile, 49 to 64 rows; short and long K either side of the slices
+    (64, 4096, 64, "silu", BF, True, True, True), (50, 128, 4160, "gelu", BF, True, True, True),
+    (50, 128, 2112, "silu", F32, True, True, True),
+    # the large tiles, ragged in rows and columns, and one column of them
+    (3100, 4160, 64, "gelu_tanh", BF, True, True, True), (3100, 4160, 64, "none", BF, False, False, False),
+    (3329, 4096, 192, "relu", BF, True, False, False), (49100, 64, 64, "silu", BF, False, True, True),
+    # 128 x 128 tiles in fp32
+    (1000, 1536, 192, "gelu", F32, True, True, True),
+])
+def test_forward_of_every_form(M, N, K, act, dt, bias, residual, z):
+    """Forms that only wide or large products take."""
+    test_forward(M, N, K, act, dt, bias, residual, z)
