@@ -3,18 +3,22 @@
 // gate-weighted sum and the residual.
 //
 // For at most 128 tokens the layer is a stream of the chosen experts' weights,
-// every byte read once, with the multiplications in its shade (2 m flops per
-// weight for m rows, far below the 300 flops per byte at which the matrix
-// cores and HBM balance).  Sorting rows into groups, as the training path
-// does, would be latency only: the rows of an expert are found from the
-// tokens' choices directly and the products read tokens in place.  Two
-// launches:
+// with the multiplications in its shade (2 m flops per weight for m rows, far
+// below the 300 flops per byte at which the matrix cores and HBM balance).  An
+// expert's weights are read once for every block of its rows: 16 or 32 rows of
+// W13 (gateup_tiles below), 16 of W2, so once where it serves at most 16 tokens;
+// the shared expert's W2 is asked for 8 times at 128 tokens.  (128 tokens of 64
+// experts, 6 each: 1.31 GB from the fabric, 1.11 without re-reads.)  Sorting rows
+// into groups, as the training path does, would be latency only: the rows of an
+// expert are found from the tokens' choices directly and the products read tokens
+// in place.  Two launches up to 8 tokens, three above:
 //  1. the router product in K slices (and the second launch's counters set
 //     to zero);
 //  2. everything else in one persistent launch of one workgroup per CU, whose
 //     units of work -- route a few tokens, 16 gate/up columns of an expert, 32
 //     output columns of an expert -- are drawn from one counter in an order in
-//     which a unit depends on earlier ones only.
+//     which a unit depends on earlier ones only;
+//  3. above 8 tokens (or 256 pairs), the gate-weighted sum.
 #include <type_traits>
 
 #include "lds_copy.hpp"
@@ -49,9 +53,9 @@ struct DecArgs {
   // counters, zero when the second launch starts: the next unit, tokens
   // routed, whether a wait for that was given up, finished gate/up units of each
   // expert (window index; the shared expert last), finished units of each block of
-  // DEC_DN output columns.  All but the last lie a cache line apart: on one line with the others, a
-  // look at an expert's counter waited for everyone's draws (128 tokens: 323 us
-  // so, 267 apart)
+  // DEC_DN output columns.  All but the last lie a cache line apart: on one line
+  // with the others, a look at an expert's counter waited for everyone's draws
+  // (128 tokens: 323 us so, 267 apart)
   int* next; int* routed; int* unrouted; int* act_done; int* col_done;
   int* go;            // one word a cache line for each workgroup: 0, DEC_GO or DEC_GO_LOST
   int n_count;        // all of them, from next on
@@ -1124,9 +1128,15 @@ int router_slices(int H, int E) {
 
 // Row tiles of the gate/up units: two where an expert is likely to have more
 // rows than one tile holds (its mean over 8, or the shared expert's all): its
-// weights are then read once, not once a tile.  Measured, one tile and two:
-// 128 tokens of 64 experts, 6 each (mean 12) 300 and 273 us; 61 tokens and the
-// shared expert 485 and 473 us.
+// weights are then read once, not once a tile.  us with one tile and with two
+// (bf16; H x I, experts, k):
+//   shared expert    7680 x 2048, 32 of 256, 8: 17 tokens 253, 248; 64 462, 450; 128 574, 548
+//                    7168 x 2048, 16 of 256, 8: 17 tokens 122, 115; 128 335, 313
+//                    4096 x 1024, 16, 2: 24 tokens 88.0, 89.5; 64 103, 102; 128 146, 128
+//                    1024 x 512, 128, 8: 17 tokens 98, 98.5; 128 140.7, 142.8
+//   mean of 8        4096 x 2048, 8, 2: 99.6, 101.6; 4096 x 1024, 16, 2: 100.4, 103.6
+//   12               105.7, 108.5 (4096 x 1024, 16, 2); 4096 x 2048, 32, 4: 322, 303
+//   16               4096 x 2048, 8, 2: 125, 120; 32, 4: 398, 340; 4096 x 1024, 16, 2: 128, 125
 constexpr int GU_MEAN = 8;
 int gateup_tiles(bool shared, int T, int E, int k) {
   return T > 16 && (shared || T * k > GU_MEAN * E) ? 2 : 1;
