@@ -430,10 +430,11 @@ int moe_linear(const void* x, int dt, int M, int N, int K, const void* w, const 
  * MOE_ACT_NONE):
  *   dz = dy * act'(z),  dx = dz W,  dw = dz^T x,  db = sum_m dz
  * dx [M,K], dw [N,K] and db [N] (fp32) are each written if not NULL, into
- * buffers that share no memory with each other or an input; the gradient of the residual is dy
- * itself.  dz is rounded to the storage type for the two products (they read it
- * on the matrix cores); db sums it unrounded.  M == 0 writes zeros to dw and db.  ws: scratch of
- * moe_linear_bwd_workspace_bytes bytes, 256-byte aligned.
+ * buffers that share no memory with each other or an input; the gradient of
+ * the residual is dy itself.  dz is rounded to the storage type for the two
+ * products (they read it on the matrix cores); db sums it unrounded.  M == 0
+ * writes zeros to dw and db.  ws: scratch of moe_linear_bwd_workspace_bytes
+ * bytes, 256-byte aligned.
  */
 size_t moe_linear_bwd_workspace_bytes(int M, int N, int K, int dt, int act);
 int moe_linear_bwd(const void* dy, const void* z, const void* x, const void* w, int dt, int M,

@@ -1272,8 +1272,10 @@ extern "C" int moe_decode(const void* x, int dt, const float* wg, const float* b
                  outs[] = {{y, th, "y"}, {logits, 4LL * T * E, "logits"}, {idx, 4LL * T * k, "idx"},
                            {gate, 4LL * T * k, "gate"}, {ws, (long long)w.total, "ws"}};
   for (int i = 0; i < 5; ++i) {
-    const char* with = moe_shares(outs[i], {rx, rg, rb, r13, r2, rs13, rs2, rr},
-                                  i == 0 ? residual : nullptr);
+    // (given logits are an input: apart from the outputs only; y may be residual's very buffer)
+    const bool out = i != 1 || wg != nullptr;
+    const char* with = out ? moe_shares(outs[i], {rx, rg, rb, r13, r2, rs13, rs2}) : nullptr;
+    if (with == nullptr && out && !(i == 0 && residual == y)) with = moe_shares(outs[i], {rr});
     for (int j = 0; j < i && with == nullptr; ++j) with = moe_shares(outs[i], {outs[j]});
     if (with != nullptr)
       return moe_fail(MOE_ERR_INVALID_ARG, "%s: %s overlaps %s's buffer (y may be residual's)", fn,

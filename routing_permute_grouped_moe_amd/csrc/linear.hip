@@ -349,7 +349,8 @@ extern "C" int moe_linear(const void* x, int dt, int M, int N, int K, const void
   const MoeRange rx = {x, (long long)M * K * es, "x"}, rw = {w, (long long)N * K * es, "w"},
                  rb = {bias, 4LL * N, "bias"}, rr = {residual, mn, "residual"}, rz = {z, mn, "z"},
                  ry = {y, mn, "y"}, rs = {need > 0 ? ws : nullptr, (long long)need, "ws"};
-  const char* with = moe_shares(ry, {rx, rw, rb, rr, rz, rs}, residual);
+  const char* with = moe_shares(ry, {rx, rw, rb, rz, rs});
+  if (with == nullptr && residual != y) with = moe_shares(ry, {rr});
   const char* out = "y";
   if (with == nullptr) {
     with = moe_shares(rz, {rx, rw, rb, rr, rs});

@@ -71,14 +71,12 @@ struct MoeRange {
   const void* p; long long bytes; const char* name;
 };
 
-// The one of `others` that shares memory with `out`, or null.  same: an operand
-// that may be out's very buffer (but not a shifted one).
-static inline const char* moe_shares(const MoeRange& out, std::initializer_list<MoeRange> others,
-                                     const void* same = nullptr) {
+// The one of `others` that shares memory with `out`, or null.
+static inline const char* moe_shares(const MoeRange& out, std::initializer_list<MoeRange> others) {
   const uintptr_t a = (uintptr_t)out.p;
   for (const MoeRange& o : others) {
     const uintptr_t b = (uintptr_t)o.p;
-    if (a == 0 || b == 0 || out.bytes <= 0 || o.bytes <= 0 || (o.p == same && o.p == out.p)) continue;
+    if (a == 0 || b == 0 || out.bytes <= 0 || o.bytes <= 0) continue;
     if (a < b + (uintptr_t)o.bytes && b < a + (uintptr_t)out.bytes) return o.name;
   }
   return nullptr;

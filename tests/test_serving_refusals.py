@@ -265,3 +265,17 @@ def test_a_bias_without_a_router_is_refused_when_the_layer_is_made(abi):
     w = torch.zeros(2, 128, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="bias comes with wg"):
         MoeDecode(s, w, w, bias=torch.zeros(2))
+
+
+def test_y_over_a_residual_that_is_x(abi):
+    """y may be the residual's buffer, but not x's, also where x is the residual."""
+    st = abi._lib.moe_decode(*{**APART, "residual": P, "y": P}.values())
+    assert st == abi.MOE_ERR_INVALID_ARG and "y overlaps x" in abi.moe_last_error()
+    st = abi._lib.moe_linear(*{**LINEAR, "N": 64, "residual": P, "y": P}.values())
+    assert st == abi.MOE_ERR_INVALID_ARG and "y overlaps x" in abi.moe_last_error()
+
+
+def test_given_logits_are_an_input(abi):
+    """Inputs may share memory: given logits with x (the refusal is of gate, here)."""
+    st = abi._lib.moe_decode(*{**APART, "wg": None, "logits": P, "gate": 0x50000}.values())
+    assert st == abi.MOE_ERR_INVALID_ARG and "gate overlaps idx" in abi.moe_last_error()
