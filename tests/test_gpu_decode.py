@@ -2,7 +2,8 @@
 import pytest
 import torch
 
-from decode_util import (U, assert_within, f64, ref_decode, ref_linear, ref_logits, ref_route)
+from decode_util import (U, assert_within, ref_decode, ref_linear, ref_logits, ref_route)
+from decode_util import f64
 from gpu_util import have_gpu
 
 pytestmark = [pytest.mark.gpu,
