@@ -1,0 +1,445 @@
+"""The operators around the expert layer in a training step, as they are measured.
+
+* ``balance`` -- the router's balance and z losses with per-expert counts, per
+  sequence (``fwd``), and their gradient, together with the gates' (``bwd``).
+* ``norm`` -- layer norm or RMS norm of rows, with the residual sum in front
+  (``fwd``), and its gradients, with the reductions of the weight's and the
+  bias's (``bwd``).
+* ``grad`` -- the norm of all gradients together and of each (``norm``), and
+  clipping by it (``clip``: into other buffers; ``keep``: in place, gradients
+  short of the limit, as in most steps).
+
+``run`` computes them in plain torch operations, or with ``own`` through the
+framework's calls; ``exact`` states their definition in 64 bits.
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+_DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+_WEIGHTS = (0.01, 0.001)     # of the balance loss and of the z loss
+_EPS = {"layer": 1e-5, "rms": 1e-6}
+
+
+# ---------------------------------------------------------------- cases
+
+def _balance(way, T, E, k, S=1, keep=False, gates=False, dead=0, **name):
+    return {**name, "op": "balance", "way": way, "T": T, "E": E, "k": k, "S": S, "keep": keep,
+            "gates": gates and way == "bwd", "dead": dead}
+
+
+def _norm(way, M, H, kind="layer", dt="bf16", residual=False, bias=True, **name):
+    return {**name, "op": "norm", "way": way, "M": M, "H": H, "kind": kind, "dt": dt,
+            "residual": residual, "bias": bias}
+
+
+def _layer_grads(way, G, H, I, E, dt="bf16", shared=False, wide=False, **name):
+    return {**name, "op": "grad", "way": way, "set": "layer", "G": G, "H": H, "I": I, "E": E,
+            "dt": dt, "shared": shared, "wide": wide}
+
+
+def _many_grads(way, count, mean, sizes, kind="l2", wide=False, **name):
+    return {**name, "op": "grad", "way": way, "set": "many", "count": count, "mean": mean,
+            "sizes": sizes, "kind": kind, "wide": wide}
+
+
+def listed():
+    return [
+        # the smallest layer's router: what a call costs that moves nothing to speak of
+        _balance("fwd", 256, 8, 2, name="balance_256_e8"),
+        # a training batch of one device, packed sequences with padding between them
+        _balance("fwd", 8192, 256, 8, S=13, keep=True, name="balance_8192_e256"),
+        # the same batch back: the losses' gradient and the gates' into one dlogits
+        _balance("bwd", 8192, 256, 8, S=13, keep=True, gates=True, name="balance_bwd_8192_e256"),
+        # a long batch, one run of tokens, a few experts switched off
+        _balance("fwd", 65521, 256, 8, dead=5, name="balance_65521_e256"),
+        # one token in serving, onto the residual stream
+        _norm("fwd", 1, 7680, kind="rms", residual=True, bias=False, name="norm_1_h7680"),
+        # a training batch in front of the layer
+        _norm("fwd", 8192, 7680, residual=True, name="norm_8192_h7680"),
+        # its gradients, with the residual stream's own added
+        _norm("bwd", 8192, 7680, residual=True, name="norm_bwd_8192_h7680"),
+        # fp32, a ragged batch of a smaller model
+        _norm("bwd", 4095, 2048, dt="f32", name="norm_bwd_4095_f32"),
+        # many short rows, as a norm of each head has them
+        _norm("bwd", 131071, 128, kind="rms", bias=False, name="norm_bwd_heads"),
+        # every gradient of the smallest layer, short of the limit: in place, nothing to scale
+        _layer_grads("keep", 8, 128, 64, 8, dt="f32", name="clip_keep_tiny"),
+        # every gradient of one device's share of a large layer, clipped into the optimizer's fp32
+        _layer_grads("clip", 8, 7680, 2048, 256, shared=True, wide=True, name="clip_h7680"),
+        # the norms of a whole model's worth of small and large tensors
+        _many_grads("norm", 700, 40000, 5, name="grad_norm_700"),
+    ]
+
+
+def _log(rng, lo, hi):
+    """A whole number in [lo, hi], its logarithm spread evenly."""
+    return min(hi, max(lo, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    what = rng.random()
+    if what < 0.34:
+        E = _log(rng, 2, 1024)
+        T = min(_log(rng, 1, 65536), (1 << 24) // E)
+        return _balance(rng.choice(("fwd", "bwd")), T, E, min(E, rng.randint(1, 10)),
+                        S=_log(rng, 1, 64), keep=rng.random() < 0.5, gates=rng.random() < 0.7,
+                        dead=rng.choice((0, 0, E // 10)) if E >= 20 else 0)
+    if what < 0.68:
+        way, dt = rng.choice(("fwd", "bwd")), "f32" if rng.random() < 0.3 else "bf16"
+        H = 8 * _log(rng, 1, 2048 if dt == "bf16" else 1024)
+        M = min(_log(rng, 1, 262144), (1 << 26 if dt == "bf16" else 1 << 25) // H)
+        return _norm(way, max(1, M), H, kind=rng.choice(("layer", "rms")), dt=dt,
+                     residual=rng.random() < 0.5, bias=rng.random() < 0.6)
+    way = rng.choice(("norm", "clip", "keep"))
+    if rng.random() < 0.5:
+        dt = "f32" if rng.random() < 0.3 else "bf16"
+        H, I, E = 64 * _log(rng, 2, 120), 64 * _log(rng, 1, 32), _log(rng, 2, 256)
+        G = min(E, max(1, int(3e8 / (3 * H * I))), 64)
+        return _layer_grads(way, G, H, I, E, dt=dt, shared=rng.random() < 0.5,
+                            wide=way == "clip" and dt == "bf16" and rng.random() < 0.5)
+    mean = _log(rng, 10, 4_000_000)
+    count = min(_log(rng, 1, 1000 if way == "norm" else 60), max(1, 100_000_000 // mean))
+    return _many_grads(way, count, mean, rng.randrange(1 << 30),
+                       kind="max" if rng.random() < 0.25 else "l2",
+                       wide=way == "clip" and rng.random() < 0.3)
+
+
+# ---------------------------------------------------------------- inputs
+
+def _grad_shapes(c):
+    """(elements, type) of each gradient."""
+    if c["set"] == "layer":
+        G, H, I, E, dt = c["G"], c["H"], c["I"], c["E"], _DT[c["dt"]]
+        got = [(G * 2 * I * H, dt), (G * H * I, dt)]
+        if c["shared"]:
+            got += [(2 * I * H, dt), (H * I, dt)]
+        return got + [(H * E, torch.float32), (E, torch.float32)]
+    r = random.Random(c["sizes"])     # a few large ones, many small, odd lengths
+    return [(max(1, int(c["mean"] * math.exp(r.gauss(-0.72, 1.2)))),
+             torch.float32 if r.random() < 0.4 else torch.bfloat16) for _ in range(c["count"])]
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    rng = random.Random(seed)
+    f32 = torch.float32
+
+    def normal(*shape, std=1.0, mean=0.0, dtype=f32):
+        return torch.empty(shape, dtype=dtype, device="cuda").normal_(mean, std, generator=gen)
+
+    s = {"case": case}
+    if case["op"] == "balance":
+        T, E, k, S = (case[n] for n in ("T", "E", "k", "S"))
+        logits = normal(T, E, std=1.8) + normal(E, std=0.5)
+        if case["dead"]:
+            off = rng.sample(range(E), min(case["dead"], E - k))
+            logits[:, off] = -math.inf
+        s["logits"] = logits
+        s["idx"] = torch.topk(logits, k, dim=1).indices.int()
+        s["keep"] = s["seq"] = None
+        if case["keep"]:
+            s["keep"] = (torch.rand(T, device="cuda", generator=gen) < 0.9).to(torch.uint8)
+        if S > 1:     # sequences of any length, also none; what is behind the last is padding
+            end = T - rng.randint(0, T // 10)
+            cuts = sorted(rng.randint(0, end) for _ in range(S - 1))
+            s["seq"] = torch.tensor([0, *cuts, end], dtype=torch.int32, device="cuda")
+        if case["way"] == "bwd":
+            s["counts"], s["tokens"] = _count(s, _members(s))
+            s["dgate"] = normal(T, k, std=0.1) if case["gates"] else None
+            s["dloss"] = normal(1).abs() + 0.5
+        return s
+    if case["op"] == "norm":
+        M, H, dt = case["M"], case["H"], _DT[case["dt"]]
+        s["w"] = normal(H, std=0.2, mean=1.0)
+        s["b"] = normal(H, std=0.1) if case["bias"] else None
+        s["x"] = normal(M, H, std=0.7, mean=0.1, dtype=dt)
+        other = normal(M, H, std=1.5, dtype=dt) if case["residual"] else None
+        if case["way"] == "fwd":
+            s["residual"] = other
+            return s
+        s["dh"] = other
+        s["dy"] = normal(M, H, dtype=dt)
+        mean, rstd = _row_stats(s["x"].float(), case["kind"])
+        s["mean"] = mean[:, 0].contiguous() if case["kind"] == "layer" else None
+        s["rstd"] = rstd[:, 0].contiguous()
+        return s
+    s["grads"] = [normal(n, std=0.02 * math.exp(rng.gauss(0, 0.5)), dtype=dt)
+                  for n, dt in _grad_shapes(case)]
+    # the norm is near 0.02 times the root of their number, a largest value near 0.1
+    near = 0.02 * math.sqrt(sum(g.numel() for g in s["grads"]))
+    s["max_norm"] = 100 * near + 10 if case["way"] == "keep" else 0.03 * min(near, 1.0)
+    if case["way"] == "clip":
+        s["outs"] = [torch.empty_like(g, dtype=f32 if case["wide"] else g.dtype)
+                     for g in s["grads"]]
+    return s
+
+
+# ---------------------------------------------------------------- one pass
+
+def run(state):
+    if own:
+        return _own(state)
+    return {"balance": _plain_balance, "norm": _plain_norm,
+            "grad": _plain_grad}[state["case"]["op"]](state)
+
+
+def _members(s):
+    """[S, T], in 64 bits: 1 where a token counts in a sequence, else 0."""
+    logits, S = s["logits"], s["case"]["S"]
+    t = torch.arange(logits.shape[0], device=logits.device)
+    used = logits.amax(dim=1) > -math.inf
+    if s["keep"] is not None:
+        used = used & (s["keep"] != 0)
+    if s["seq"] is None:
+        return used[None].double()
+    return ((t >= s["seq"][:-1, None]) & (t < s["seq"][1:, None]) & used).double()
+
+
+def _sums(of, v):
+    """[S, E]: v [T, E] over the tokens of each sequence."""
+    return (of.t() * v).sum(dim=0)[None] if of.shape[0] == 1 else of @ v
+
+
+def _count(s, of):
+    """counts [S, E] and tokens [S+1], the last their sum."""
+    chosen = torch.zeros_like(s["logits"], dtype=torch.float64).scatter(1, s["idx"].long(), 1.0)
+    n = of.sum(dim=1)
+    return _sums(of, chosen).int(), torch.cat([n, n.sum()[None]]).int()
+
+
+def _plain_balance(s):
+    c, logits = s["case"], s["logits"]
+    S, E, k = c["S"], c["E"], c["k"]
+    m = logits.amax(dim=1, keepdim=True)
+    m = torch.where(m > -math.inf, m, 0.0)
+    p = torch.exp(logits - m)
+    total = p.sum(dim=1, keepdim=True)
+    p = p / total
+    lse = m + torch.log(total)
+    if c["way"] == "fwd":
+        of = _members(s)
+        counts, tokens = _count(s, of)
+        some = tokens.double().clamp(min=1)
+        sums = _sums(of, p.double())                   # (in 64 bits: long sums)
+        frac = counts.double() * E / (k * some[:S, None])
+        n = some[S]
+        balance = (frac * sums).sum() / n
+        z = torch.where(of.sum(dim=0) > 0, lse[:, 0].double().square(), 0.0).sum() / n
+        loss = torch.stack([balance, z, _WEIGHTS[0] * balance + _WEIGHTS[1] * z])
+        return {"loss": loss.float(), "counts": counts, "tokens": tokens,
+                "prob": (sums / some[:S, None]).float()}
+    of = _members(s).float()
+    tokens = s["tokens"].float().clamp(min=1)
+    frac = s["counts"].float() * E / (k * tokens[:S, None])
+    scale = s["dloss"] / tokens[S]
+    g = of.t() @ (frac * (_WEIGHTS[0] * scale))
+    add = torch.where(of.sum(dim=0)[:, None] > 0, 2 * _WEIGHTS[1] * scale * lse, 0.0)
+    if s["dgate"] is not None:
+        g = g.scatter_add(1, s["idx"].long(), s["dgate"])
+    return {"dlogits": p * (g - (p * g).sum(dim=1, keepdim=True) + add)}
+
+
+def _row_stats(x, kind):
+    if kind == "rms":
+        return 0.0, torch.rsqrt((x * x).mean(dim=1, keepdim=True) + _EPS[kind])
+    mean = x.mean(dim=1, keepdim=True)
+    d = x - mean
+    return mean, torch.rsqrt((d * d).mean(dim=1, keepdim=True) + _EPS[kind])
+
+
+def _plain_norm(s):
+    c = s["case"]
+    dt, kind, x = s["x"].dtype, c["kind"], s["x"].float()
+    if c["way"] == "fwd":
+        out = {}
+        if s["residual"] is not None:
+            out["h"] = (x + s["residual"].float()).to(dt)
+            x = out["h"].float()        # the norm of the sum as it is stored
+        mean, rstd = _row_stats(x, kind)
+        y = (x - mean) * rstd * s["w"]
+        if s["b"] is not None:
+            y = y + s["b"]
+        out["y"], out["rstd"] = y.to(dt), rstd[:, 0]
+        if kind == "layer":
+            out["mean"] = mean[:, 0]
+        return out
+    rstd, dy = s["rstd"][:, None], s["dy"].float()
+    xh = (x - s["mean"][:, None]) * rstd if kind == "layer" else x * rstd
+    g = dy * s["w"]
+    dx = g - xh * (g * xh).mean(dim=1, keepdim=True)
+    if kind == "layer":
+        dx = dx - g.mean(dim=1, keepdim=True)
+    dx = dx * rstd
+    if s["dh"] is not None:
+        dx = dx + s["dh"].float()
+    out = {"dx": dx.to(dt), "dw": (dy * xh).double().sum(dim=0).float()}   # long sums
+    if c["bias"]:
+        out["db"] = dy.double().sum(dim=0).float()
+    return out
+
+
+def _plain_grad(s):
+    c, grads = s["case"], s["grads"]
+    if c.get("kind", "l2") == "max":
+        each = torch.stack([g.float().abs().amax() for g in grads])
+        norm = each.amax()
+    else:
+        squares = torch.stack([g.double().square().sum() for g in grads])
+        each, norm = squares.sqrt().float(), squares.sum().sqrt().float()
+    if c["way"] == "norm":
+        return {"norm": norm, "norms": each}
+    scale = torch.clamp(s["max_norm"] / (norm + 1e-6), max=1.0)
+    if c["way"] == "keep":
+        return {"norm": norm, "grads": [g.copy_(g.float() * scale) for g in grads]}
+    return {"norm": norm, "grads": [o.copy_(g.float() * scale)
+                                    for g, o in zip(grads, s["outs"])]}
+
+
+def _own(s):
+    c = s["case"]
+    if c["op"] == "grad":
+        from routing_permute_grouped_moe_amd.layer import clip_grads, grad_norm
+        kind = c.get("kind", "l2")
+        if c["way"] == "norm":
+            norm, norms = grad_norm(s["grads"], kind=kind, each=True)
+            return {"norm": norm, "norms": norms}
+        outs = s["grads"] if c["way"] == "keep" else s["outs"]
+        norm = clip_grads(s["grads"], s["max_norm"], kind=kind, outs=outs)
+        return {"norm": norm, "grads": outs}
+    op = s.get("op")
+    if op is None:   # what a program builds once for its weights
+        from routing_permute_grouped_moe_amd.layer import BalanceLoss, Norm
+        if c["op"] == "balance":
+            op = BalanceLoss(weight=_WEIGHTS[0], z_weight=_WEIGHTS[1])
+        else:
+            op = Norm(s["w"], bias=s["b"], kind=c["kind"], eps=_EPS[c["kind"]])
+        s["op"] = op
+    if c["op"] == "balance":
+        if c["way"] == "fwd":
+            r = op.forward(s["logits"], s["idx"], seq=s["seq"], keep=s["keep"])
+            return {"loss": r.loss, "counts": r.counts, "tokens": r.tokens, "prob": r.prob}
+        return {"dlogits": op.backward(s["logits"], s["idx"], s["counts"], s["tokens"],
+                                       seq=s["seq"], keep=s["keep"], dgate=s["dgate"],
+                                       dloss=s["dloss"])}
+    if c["way"] == "fwd":
+        r = op.forward(s["x"], residual=s["residual"], save=True)
+        out = {"y": r.y, "rstd": r.rstd}
+        if c["residual"]:
+            out["h"] = r.h
+        if c["kind"] == "layer":
+            out["mean"] = r.mean
+        return out
+    dx, dw, db = op.backward(s["dy"], s["x"], s["rstd"], mean=s["mean"], dh=s["dh"],
+                             bias_grad=c["bias"])
+    return {"dx": dx, "dw": dw, "db": db} if c["bias"] else {"dx": dx, "dw": dw}
+
+
+# ---------------------------------------------------------------- what a pass cannot do without
+
+def work(case):
+    c = case
+    if c["op"] == "balance":
+        T, E, k, S = (c[n] for n in ("T", "E", "k", "S"))
+        moved = 4.0 * T * E + 4 * T * k + (T if c["keep"] else 0) + 8 * S * E
+        if c["way"] == "bwd":
+            moved += 4.0 * T * E - 4 * S * E + (4 * T * k if c["gates"] else -4 * T * k)
+        return {"bytes": moved, "flops": 8.0 * T * E}
+    if c["op"] == "norm":
+        M, H, b = c["M"], c["H"], 4 if c["dt"] == "f32" else 2
+        rows = (2 + 2 * c["residual"]) if c["way"] == "fwd" else (3 + c["residual"])
+        small = 4 * H * (1 + c["bias"]) * (1 if c["way"] == "fwd" else 2)
+        return {"bytes": float(M) * H * b * rows + small + 4 * M * (2 if c["kind"] == "layer" else 1),
+                "flops": (8.0 if c["way"] == "fwd" else 14.0) * M * H}
+    shapes = _grad_shapes(c)
+    size = lambda dt: 4 if dt is torch.float32 else 2
+    moved = float(sum(n * size(dt) for n, dt in shapes))
+    if c["way"] == "clip":
+        moved += sum(n * (4 if c["wide"] else size(dt)) for n, dt in shapes)
+    return {"bytes": moved + 4, "flops": (2.0 if c["way"] == "norm" else 3.0) * sum(n for n, _ in shapes)}
+
+
+# ---------------------------------------------------------------- the definition, in 64 bits
+
+def exact(case, seed):
+    c, s = case, prepare(case, seed)
+    if c["op"] == "grad":
+        flat = [g.double() for g in s["grads"]]
+        if c.get("kind", "l2") == "max":
+            norms = torch.stack([torch.linalg.vector_norm(g, ord=math.inf) for g in flat])
+            norm = norms.max()
+        else:
+            norms = torch.stack([torch.linalg.vector_norm(g) for g in flat])
+            norm = torch.linalg.vector_norm(norms)
+        if c["way"] == "norm":
+            return {"norm": norm, "norms": norms}
+        scale = min(1.0, s["max_norm"] / (norm.item() + 1e-6))
+        return {"norm": norm, "grads": [g.mul_(scale) for g in flat]}
+    if c["op"] == "norm":
+        x = s["x"].double()
+        if c["way"] == "fwd" and s["residual"] is not None:
+            x = x + s["residual"].double()
+        whole = x
+        if c["way"] == "fwd":
+            x = x.to(s["x"].dtype).double()
+        mean = x.mean(1, True) if c["kind"] == "layer" else torch.zeros_like(x[:, :1])
+        rstd = ((x - mean).square().mean(1, True) + _EPS[c["kind"]]).pow(-0.5)
+        n = (x - mean) * rstd
+        if c["way"] == "fwd":
+            y = torch.addcmul(s["b"].double() if c["bias"] else torch.zeros_like(n[:1]), n, s["w"].double())
+            out = {"y": y, "rstd": rstd.flatten()}
+            if c["residual"]:
+                out["h"] = whole
+            if c["kind"] == "layer":
+                out["mean"] = mean.flatten()
+            return out
+        # d/dx of <dy, y>: the projection of w dy orthogonal to what the norm removes
+        dy = s["dy"].double()
+        v = dy * s["w"].double()
+        dx = v - n * torch.linalg.vecdot(v, n).unsqueeze(1) / c["H"]
+        if c["kind"] == "layer":
+            dx -= v.sum(1, True) / c["H"]
+        dx *= rstd
+        if s["dh"] is not None:
+            dx += s["dh"].double()
+        out = {"dx": dx, "dw": torch.linalg.vecdot(dy, n, dim=0)}
+        return {**out, "db": dy.sum(0)} if c["bias"] else out
+    # each sequence by itself, one after the other
+    z, idx = s["logits"].double(), s["idx"].long()
+    T, E, k, S = c["T"], c["E"], c["k"], c["S"]
+    bounds = [0, T] if s["seq"] is None else s["seq"].tolist()
+    live = torch.isfinite(z).any(1)
+    if s["keep"] is not None:
+        live &= s["keep"].bool()
+    p, lse = torch.softmax(z, 1), torch.logsumexp(z, 1)
+    counts = torch.zeros(S, E, dtype=torch.int32, device=z.device)
+    prob = torch.zeros(S, E, dtype=torch.float64, device=z.device)
+    each, balance, z2, slope = [], 0.0, 0.0, torch.zeros_like(z)
+    for i in range(S):
+        rows = torch.nonzero(live[bounds[i]:bounds[i + 1]]).flatten() + bounds[i]
+        each.append(rows.numel())
+        if not each[-1]:
+            continue
+        counts[i] = torch.bincount(idx[rows].flatten(), minlength=E).int()
+        prob[i] = p[rows].mean(0)
+        frac = counts[i].double() * (E / (k * each[-1]))
+        balance += each[-1] * torch.dot(frac, prob[i]).item()
+        z2 += lse[rows].square().sum().item()
+        slope[rows] = _WEIGHTS[0] * frac + 2 * _WEIGHTS[1] * lse[rows, None]
+        slope[rows] -= _WEIGHTS[0] * (p[rows] @ frac)[:, None]
+    n = max(1, sum(each))
+    if c["way"] == "fwd":
+        loss = [balance / n, z2 / n, _WEIGHTS[0] * balance / n + _WEIGHTS[1] * z2 / n]
+        tokens = torch.tensor(each + [sum(each)], dtype=torch.int32, device=z.device)
+        return {"loss": torch.tensor(loss, dtype=torch.float64, device=z.device), "counts": counts,
+                "tokens": tokens, "prob": prob}
+    out = p * slope * (s["dloss"].double() / n)
+    if s["dgate"] is not None:
+        chosen = torch.zeros_like(z)
+        chosen[torch.arange(T, device=z.device)[:, None], idx] = s["dgate"].double()
+        inner = (p * chosen).sum(1, True)
+        out = out + p * (chosen - inner)
+    return {"dlogits": out}
