@@ -301,23 +301,21 @@ def _plain_grad(s):
 
 def _own(s):
     c = s["case"]
-    if c["op"] == "grad":
-        from routing_permute_grouped_moe_amd.layer import clip_grads, grad_norm
-        kind = c.get("kind", "l2")
-        if c["way"] == "norm":
-            norm, norms = grad_norm(s["grads"], kind=kind, each=True)
-            return {"norm": norm, "norms": norms}
-        outs = s["grads"] if c["way"] == "keep" else s["outs"]
-        norm = clip_grads(s["grads"], s["max_norm"], kind=kind, outs=outs)
-        return {"norm": norm, "grads": outs}
     op = s.get("op")
-    if op is None:   # what a program builds once for its weights
-        from routing_permute_grouped_moe_amd.layer import BalanceLoss, Norm
+    if op is None:   # what a program builds once for its weights and gradients
+        from routing_permute_grouped_moe_amd.layer import BalanceLoss, GradClip, Norm
         if c["op"] == "balance":
             op = BalanceLoss(weight=_WEIGHTS[0], z_weight=_WEIGHTS[1])
+        elif c["op"] == "grad":
+            op = GradClip(s["grads"], outs=s.get("outs"), kind=c.get("kind", "l2"))
         else:
             op = Norm(s["w"], bias=s["b"], kind=c["kind"], eps=_EPS[c["kind"]])
         s["op"] = op
+    if c["op"] == "grad":
+        if c["way"] == "norm":
+            norm, norms = op.norm(each=True)
+            return {"norm": norm, "norms": norms}
+        return {"norm": op.clip(s["max_norm"]), "grads": s.get("outs", s["grads"])}
     if c["op"] == "balance":
         if c["way"] == "fwd":
             r = op.forward(s["logits"], s["idx"], seq=s["seq"], keep=s["keep"])
