@@ -441,6 +441,117 @@ int moe_linear_bwd(const void* dy, const void* z, const void* x, const void* w, 
                    int N, int K, int act, void* dx, void* dw, float* db, void* ws,
                    size_t ws_bytes, moe_stream_t stream);
 
+/* ---------------------------------------------------------------- losses of the router
+ * The auxiliary losses of a training step on the router's logits, per-expert
+ * counts, and their gradients.  Tokens lie in S sequences, runs of tokens
+ * [seq[s], seq[s+1]) (int32 [S+1], ascending, on the device; NULL with S == 1:
+ * all T); sequences may be empty, S is at most 65535.  A token counts if it lies in one, keep[t]
+ * is not 0 (uint8 [T], NULL: all are kept) and one of its logits is not -inf.
+ * n_s tokens of s count, N in all; p = softmax(logits[t,:]); c_se is the
+ * number of times that idx names e in the tokens of s that count.
+ *   balance = 1/N sum_s n_s sum_e f_se P_se,  f_se = c_se E / (k n_s),
+ *             P_se = the mean of p_te over the tokens of s that count
+ *   z       = 1/N sum_t log(sum_e exp(logits[t,e]))^2 over the tokens that count
+ * (balance is 1 where each expert is chosen alike or has the same P; every
+ * token weighs the same, whatever its sequence's length).  Outputs:
+ *   loss [3] fp32      balance, z, and w_balance balance + w_z z (zeros if N = 0)
+ *   counts [S,E] int32 c_se;  tokens [S+1] int32: n_s, then N
+ *   prob [S,E] fp32    P_se (nullable; a statistic, zeros where n_s = 0)
+ * A logit of -inf masks an expert; NaN or +inf in a token that counts gives
+ * NaN losses.  idx entries outside [0, E) are not counted.  T == 0 writes zeros.  ws:
+ * scratch of moe_balance_loss_workspace_bytes bytes, 256-byte aligned, not
+ * shared by calls that may overlap.  Outputs share memory with nothing else.
+ */
+size_t moe_balance_loss_workspace_bytes(int T, int E, int k, int S);
+int moe_balance_loss(const float* logits, const int32_t* idx, const uint8_t* keep,
+                     const int32_t* seq, int T, int E, int k, int S, float w_balance, float w_z,
+                     float* loss, int32_t* counts, int32_t* tokens, float* prob, void* ws,
+                     size_t ws_bytes, moe_stream_t stream);
+
+/* The gradient of dloss[0] * loss[2] (dloss on the device; NULL: 1) and, with
+ * dgate [T,k], of the gates too -- moe_route_bwd's, in the same pass:
+ *   dlogits[t,e] = p_te (g_te - sum_e' p_te' g_te' + 2 w_z dloss/N lse_t)
+ *   g_te = w_balance dloss/N f_se + (dgate[t,j] where idx[t,j] = e)
+ * The first and the last term are zero for a token that does not count, f is a
+ * constant (counts have no gradient).  counts and tokens are the forward's.
+ * dgate is nullable; with it idx names a token's experts once each (as
+ * moe_route does), without it idx is not read and may be NULL.  dlogits [T,E]
+ * is written whole.  With w_balance = w_z = 0 and finite logits it holds
+ * moe_route_bwd's values.
+ */
+int moe_balance_loss_bwd(const float* logits, const int32_t* idx, const float* dgate,
+                         const uint8_t* keep, const int32_t* seq, const int32_t* counts,
+                         const int32_t* tokens, int T, int E, int k, int S, float w_balance,
+                         float w_z, const float* dloss, float* dlogits, moe_stream_t stream);
+
+/* ---------------------------------------------------------------- norm of rows
+ * Layer norm, or RMS norm, of the rows of x [M,H], with a residual in front:
+ *   h = x + residual, rounded to dt             (h = x without a residual)
+ *   layer: m = mean(h), v = mean((h - m)^2);  RMS: m = 0, v = mean(h^2)
+ *   rstd = 1 / sqrt(v + eps);  y = (h - m) rstd w + bias
+ * of the values of h as they are stored.  w and bias are [H] fp32 (bias
+ * nullable).  h [M,H] is written if not NULL and only with a residual; it may
+ * be the residual's buffer or x's.  mean and rstd [M] fp32 are nullable, what
+ * the backward needs (mean is not written for RMS).  Statistics and products
+ * are fp32, y is rounded once.  H is a multiple of 8, at most 16384; eps > 0;
+ * rows whose sum of squares passes fp32's range give wrong numbers, a NaN or
+ * an infinity in a row NaN in that row alone.
+ */
+enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 };
+int moe_norm(const void* x, const void* residual, int dt, int M, int H, int kind, float eps,
+             const float* w, const float* bias, void* h, void* y, float* mean, float* rstd,
+             moe_stream_t stream);
+
+/* Its gradients, given dy [M,H], the h it took the norm of (x without a
+ * residual) and the mean (layer norm; NULL for RMS) and rstd it wrote:
+ *   g = dy w,  q = (h - mean) rstd
+ *   dx = rstd (g - mean(g) - q mean(g q)) + dh     (RMS: without mean(g))
+ *   dw = sum_m dy q,  db = sum_m dy
+ * dh [M,H] (nullable) is the gradient that reaches h besides, from the residual
+ * stream: dx is then the gradient of x and of the residual both.  dx [M,H], dw
+ * and db [H] fp32 are each written if not NULL; dx may be dh's buffer, and
+ * shares memory with nothing else.  M == 0 writes zeros to dw and db.  ws:
+ * scratch of moe_norm_bwd_workspace_bytes bytes, 256-byte aligned.
+ */
+size_t moe_norm_bwd_workspace_bytes(int M, int H, int dt);
+int moe_norm_bwd(const void* dy, const void* h, const void* dh, int dt, int M, int H, int kind,
+                 const float* w, const float* mean, const float* rstd, void* dx, float* dw,
+                 float* db, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------- norm of all gradients, clipping
+ * Gradients g_0 .. g_{count-1} of any sizes, fp32 and bf16 mixed, given by a
+ * host array that is read before the call returns.  A gradient is dense and
+ * aligned to its elements (a view into a flat buffer will do); n may pass 2^31,
+ * n == 0 is skipped and g may be NULL then.
+ *   kind MOE_GRAD_L2:  norms[i] = sqrt(sum g_i^2),  norm = sqrt(sum of all squares)
+ *   kind MOE_GRAD_MAX: norms[i] = max |g_i|,        norm = the largest
+ * Squares and sums are fp64: no finite gradient overflows, and a NaN gives NaN.
+ * norm [1] and norms [count] (nullable) are fp32; total [1] fp64 (nullable) is
+ * the sum of all squares, or the maximum: what ranks that hold parts of a model
+ * reduce before they clip.  Without a gradient all are 0.  out and out_dt are
+ * not used.  ws: scratch of moe_grad_norm_workspace_bytes bytes, 256-byte
+ * aligned.
+ */
+typedef struct moe_grad {
+  const void* g;
+  void* out;
+  long long n;   /* elements */
+  int dt, out_dt;
+} moe_grad;
+enum { MOE_GRAD_L2 = 0, MOE_GRAD_MAX = 1 };
+size_t moe_grad_norm_workspace_bytes(const moe_grad* grads, int count);
+int moe_grad_norm(const moe_grad* grads, int count, int kind, float* norm, float* norms,
+                  double* total, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* out_i = c g_i with c = min(1, max_norm / (norm[0] + 1e-6)), rounded once; norm
+ * is read on the device.  out is g's own buffer with g's type (then nothing is
+ * moved where c is 1), or a buffer that overlaps no gradient and no other out,
+ * of type g's or MOE_F32.  In place a gradient is given once.  max_norm >= 0.  A
+ * NaN norm gives c = NaN, an infinite one c = 0, as the formula does.
+ */
+int moe_grad_clip(const moe_grad* grads, int count, const float* norm, float max_norm,
+                  moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -24,10 +24,13 @@ _lib = ctypes.CDLL(LIB_PATH)
 MOE_F32, MOE_BF16 = 0, 1
 MOE_ROUTER_WG_SPLIT = 1          # moe_router_logits_bwd: reuse the forward's split of wg
 MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH = range(5)
+MOE_NORM_LAYER, MOE_NORM_RMS = 0, 1
+MOE_GRAD_L2, MOE_GRAD_MAX = 0, 1
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_LAUNCH = range(5)
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_F = ctypes.c_float
 _SZ = ctypes.c_size_t
 
 
@@ -42,6 +45,11 @@ class SharedExpert(ctypes.Structure):
     """``moe_shared_expert``: the always-on shared expert run as one more group."""
     _fields_ = [("T", _I), ("x", _P), ("w13", _P), ("w2", _P), ("h13", _P), ("act", _P),
                 ("y", _P), ("dy", _P), ("dh13", _P), ("dx", _P), ("dw13", _P), ("dw2", _P)]
+
+
+class Grad(ctypes.Structure):
+    """``moe_grad``: one gradient, and where it goes scaled."""
+    _fields_ = [("g", _P), ("out", _P), ("n", ctypes.c_longlong), ("dt", _I), ("out_dt", _I)]
 
 
 _SIGS = {
@@ -86,6 +94,17 @@ _SIGS = {
     "moe_linear": (_I, [_P, _I, _I, _I, _I, _P, _P, _I, _P, _P, _P, _P, _SZ, _P]),
     "moe_linear_bwd_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
     "moe_linear_bwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
+    "moe_balance_loss_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "moe_balance_loss": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _F, _F, _P, _P, _P, _P, _P, _SZ,
+                              _P]),
+    "moe_balance_loss_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _F, _P, _P,
+                                  _P]),
+    "moe_norm": (_I, [_P, _P, _I, _I, _I, _I, _F, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_norm_bwd_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "moe_norm_bwd": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_grad_norm_workspace_bytes": (_SZ, [ctypes.POINTER(Grad), _I]),
+    "moe_grad_norm": (_I, [ctypes.POINTER(Grad), _I, _I, _P, _P, _P, _P, _SZ, _P]),
+    "moe_grad_clip": (_I, [ctypes.POINTER(Grad), _I, _P, _F, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -306,3 +325,58 @@ def moe_linear_bwd_workspace_bytes(M, N, K, dt, act) -> int:
 def moe_linear_bwd(dy, z, x, w, dt, M, N, K, act, dx, dw, db, ws, ws_bytes, stream=None):
     _call("moe_linear_bwd", addr(dy), addr(z), addr(x), addr(w), dt, M, N, K, act, addr(dx),
           addr(dw), addr(db), addr(ws), ws_bytes, _stream(stream))
+
+
+def moe_balance_loss_workspace_bytes(T, E, k, S) -> int:
+    return _lib.moe_balance_loss_workspace_bytes(T, E, k, S)
+
+
+def moe_balance_loss(logits, idx, keep, seq, T, E, k, S, w_balance, w_z, loss, counts, tokens,
+                     prob, ws, ws_bytes, stream=None):
+    _call("moe_balance_loss", addr(logits), addr(idx), addr(keep), addr(seq), T, E, k, S,
+          w_balance, w_z, addr(loss), addr(counts), addr(tokens), addr(prob), addr(ws), ws_bytes,
+          _stream(stream))
+
+
+def moe_balance_loss_bwd(logits, idx, dgate, keep, seq, counts, tokens, T, E, k, S, w_balance, w_z,
+                         dloss, dlogits, stream=None):
+    _call("moe_balance_loss_bwd", addr(logits), addr(idx), addr(dgate), addr(keep), addr(seq),
+          addr(counts), addr(tokens), T, E, k, S, w_balance, w_z, addr(dloss), addr(dlogits),
+          _stream(stream))
+
+
+def moe_norm(x, residual, dt, M, H, kind, eps, w, bias, h, y, mean, rstd, stream=None):
+    _call("moe_norm", addr(x), addr(residual), dt, M, H, kind, eps, addr(w), addr(bias), addr(h),
+          addr(y), addr(mean), addr(rstd), _stream(stream))
+
+
+def moe_norm_bwd_workspace_bytes(M, H, dt) -> int:
+    return _lib.moe_norm_bwd_workspace_bytes(M, H, dt)
+
+
+def moe_norm_bwd(dy, h, dh, dt, M, H, kind, w, mean, rstd, dx, dw, db, ws, ws_bytes, stream=None):
+    _call("moe_norm_bwd", addr(dy), addr(h), addr(dh), dt, M, H, kind, addr(w), addr(mean),
+          addr(rstd), addr(dx), addr(dw), addr(db), addr(ws), ws_bytes, _stream(stream))
+
+
+def grads(tensors, outs=None):
+    """A ``moe_grad`` array of tensors, and of the tensors they go to scaled (None:
+    to themselves)."""
+    arr = (Grad * max(1, len(tensors)))()
+    for a, g, o in zip(arr, tensors, tensors if outs is None else outs):
+        a.g, a.out, a.n = g.data_ptr(), o.data_ptr(), g.numel()
+        a.dt, a.out_dt = dtype_code(g), dtype_code(o)
+    return arr
+
+
+def moe_grad_norm_workspace_bytes(grads, count) -> int:
+    return _lib.moe_grad_norm_workspace_bytes(grads, count)
+
+
+def moe_grad_norm(grads, count, kind, norm, norms, total, ws, ws_bytes, stream=None):
+    _call("moe_grad_norm", grads, count, kind, addr(norm), addr(norms), addr(total), addr(ws),
+          ws_bytes, _stream(stream))
+
+
+def moe_grad_clip(grads, count, norm, max_norm, stream=None):
+    _call("moe_grad_clip", grads, count, addr(norm), max_norm, _stream(stream))

@@ -9,7 +9,7 @@
 
 #include "common.hpp"
 
-#define MOE_ABI_VERSION 13
+#define MOE_ABI_VERSION 14
 
 static thread_local char g_last_error[512];
 

@@ -1,0 +1,350 @@
+// The norm of many gradients together and of each, and clipping by it.
+//   norm = sqrt(sum g^2) or max |g|;  out = min(1, max_norm / (norm + 1e-6)) g
+//
+// Gradients are cut into chunks of one length; a workgroup takes one.  Which
+// chunk belongs to which gradient stands in a table that travels with the
+// launch's arguments (no copy to the device, and a captured launch keeps its
+// own); where the gradients are more than a table holds there are several
+// launches.  A chunk's sum is kept in fp64 -- squares of every fp32 value are
+// in its range -- and a second launch adds the chunks in order.
+#include <algorithm>
+#include <new>
+
+#include "validate.hpp"
+
+namespace {
+
+constexpr int CLIP_NT = 256;
+constexpr int CLIP_WAVES = CLIP_NT / MOE_WAVE;
+constexpr int CLIP_SUM_NT = 1024;
+constexpr int NORM_TABLE = 176;      // gradients of one launch: tables below 4 KB
+constexpr int CLIP_TABLE = 128;
+constexpr long long CLIP_CHUNK = 16384;   // elements of a chunk, at least
+constexpr long long CLIP_CHUNKS = 8192;   // chunks, at most, but for one a gradient
+
+struct NormTable {
+  const void* g[NORM_TABLE];
+  unsigned long long n[NORM_TABLE];   // elements; top bit: bf16
+  int first[NORM_TABLE + 1];          // first chunk, within this launch
+  int count;
+};
+struct ClipTable {
+  const void* g[CLIP_TABLE];
+  void* out[CLIP_TABLE];
+  unsigned long long n[CLIP_TABLE];   // elements; top bits: g is bf16, out is bf16
+  int first[CLIP_TABLE + 1];
+  int count;
+};
+constexpr unsigned long long G_BF16 = 1ull << 63, OUT_BF16 = 1ull << 62,
+                             N_MASK = OUT_BF16 - 1;
+
+// 16 bytes, aligned to an element only
+typedef unsigned int u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef unsigned int u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+__device__ __forceinline__ u32x4 load16(const float* p) { return *(const u32x4_a4*)p; }
+__device__ __forceinline__ u32x4 load16(const bf16_t* p) { return *(const u32x4_a2*)p; }
+__device__ __forceinline__ void store16(float* p, u32x4 v) { *(u32x4_a4*)p = v; }
+__device__ __forceinline__ void store16(bf16_t* p, u32x4 v) { *(u32x4_a2*)p = v; }
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ float load1(const bf16_t* p) { return bf16_to_f32(*p); }
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store1(bf16_t* p, float v) { *p = (bf16_t)f32_to_bf16(v); }
+
+// The gradient that chunk c belongs to.
+__device__ __forceinline__ int grad_of(const int* first, int count, int c) {
+  int lo = 0, hi = count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first[mid] <= c) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// (a NaN is larger than any number)
+__device__ __forceinline__ double max_nan(double a, double b) { return a >= b || a != a ? a : b; }
+
+template <bool MAX>
+__device__ __forceinline__ double join(double a, double b) { return MAX ? max_nan(a, b) : a + b; }
+template <bool MAX>
+__device__ __forceinline__ double wave_join(double v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v = join<MAX>(v, __shfl_xor(v, o, MOE_WAVE));
+  return v;
+}
+template <bool MAX>
+__device__ __forceinline__ double take(double acc, float v) {
+  return MAX ? max_nan(acc, fabs((double)v)) : fma((double)v, (double)v, acc);
+}
+
+template <bool MAX, typename T>
+__device__ __forceinline__ double chunk_sum(const T* g, long long n) {
+  constexpr int VEC = Elem<T>::VEC;
+  double acc = 0;
+  const long long whole = n / VEC * VEC;
+  for (long long i = (long long)threadIdx.x * VEC; i < whole; i += CLIP_NT * VEC) {
+    float v[VEC];
+    unpack16(load16(g + i), v, T());
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) acc = take<MAX>(acc, v[j]);
+  }
+  if (whole + threadIdx.x < n) acc = take<MAX>(acc, load1(g + whole + threadIdx.x));
+  return acc;
+}
+
+template <bool MAX>
+__global__ __launch_bounds__(CLIP_NT) void grad_part_kernel(NormTable t, long long chunk, int base,
+                                                            int grad0, double* part, int* starts) {
+  __shared__ double red[CLIP_WAVES];
+  const int c = blockIdx.x, i = grad_of(t.first, t.count, c);
+  if (c == 0)
+    for (int j = threadIdx.x; j <= t.count; j += CLIP_NT) starts[grad0 + j] = base + t.first[j];
+  const unsigned long long word = t.n[i];
+  const long long n = (long long)(word & N_MASK), at = (long long)(c - t.first[i]) * chunk;
+  const long long len = n - at < chunk ? n - at : chunk;
+  double v = word & G_BF16 ? chunk_sum<MAX>((const bf16_t*)t.g[i] + at, len)
+                           : chunk_sum<MAX>((const float*)t.g[i] + at, len);
+  v = wave_join<MAX>(v);
+  if (threadIdx.x % MOE_WAVE == 0) red[threadIdx.x / MOE_WAVE] = v;
+  __syncthreads();
+  if (threadIdx.x == 0 && c < t.first[t.count]) {
+    v = red[0];
+#pragma unroll
+    for (int w = 1; w < CLIP_WAVES; ++w) v = join<MAX>(v, red[w]);
+    part[base + c] = v;
+  }
+}
+
+template <bool MAX>
+__global__ __launch_bounds__(CLIP_SUM_NT) void grad_norm_kernel(const double* part,
+                                                                const int* starts, int count,
+                                                                float* norm, float* norms,
+                                                                double* total) {
+  constexpr int WAVES = CLIP_SUM_NT / MOE_WAVE;
+  __shared__ double red[WAVES];
+  const int lane = threadIdx.x % MOE_WAVE, wave = threadIdx.x / MOE_WAVE;
+  double all = 0;
+  for (int i = wave; i < count; i += WAVES) {
+    double v = 0;
+    for (int c = starts[i] + lane; c < starts[i + 1]; c += MOE_WAVE) v = join<MAX>(v, part[c]);
+    v = wave_join<MAX>(v);
+    all = join<MAX>(all, v);
+    if (norms && lane == 0) norms[i] = (float)(MAX ? v : sqrt(v));
+  }
+  if (lane == 0) red[wave] = all;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    all = red[0];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) all = join<MAX>(all, red[w]);
+    norm[0] = (float)(MAX ? all : sqrt(all));
+    if (total) total[0] = all;
+  }
+}
+
+template <typename G, typename O>
+__device__ __forceinline__ void scale_chunk(const G* g, O* out, long long n, float c) {
+  constexpr int VEC = 8;
+  const long long whole = n / VEC * VEC;
+  for (long long i = (long long)threadIdx.x * VEC; i < whole; i += CLIP_NT * VEC) {
+    float v[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; j += Elem<G>::VEC) unpack16(load16(g + i + j), v + j, G());
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) v[j] *= c;
+#pragma unroll
+    for (int j = 0; j < VEC; j += Elem<O>::VEC) store16(out + i + j, pack16(v + j, O()));
+  }
+  if (whole + threadIdx.x < n)
+    store1(out + whole + threadIdx.x, load1(g + whole + threadIdx.x) * c);
+}
+
+__global__ __launch_bounds__(CLIP_NT) void grad_clip_kernel(ClipTable t, long long chunk,
+                                                            const float* norm, float max_norm) {
+  const int b = blockIdx.x, i = grad_of(t.first, t.count, b);
+  float c = max_norm / (norm[0] + 1e-6f);
+  c = c > 1.f ? 1.f : c;        // (a NaN stays one)
+  if (c == 1.f && t.out[i] == t.g[i]) return;
+  const unsigned long long word = t.n[i];
+  const long long n = (long long)(word & N_MASK), at = (long long)(b - t.first[i]) * chunk;
+  const long long len = n - at < chunk ? n - at : chunk;
+  if (!(word & G_BF16))
+    scale_chunk((const float*)t.g[i] + at, (float*)t.out[i] + at, len, c);
+  else if (word & OUT_BF16)
+    scale_chunk((const bf16_t*)t.g[i] + at, (bf16_t*)t.out[i] + at, len, c);
+  else
+    scale_chunk((const bf16_t*)t.g[i] + at, (float*)t.out[i] + at, len, c);
+}
+
+// Elements of a chunk: a whole number of all lanes' loads.
+long long chunk_of(const moe_grad* g, int count) {
+  long long n = 0;
+  for (int i = 0; i < count; ++i) n += g[i].n;
+  long long c = (n + CLIP_CHUNKS - 1) / CLIP_CHUNKS;
+  c = (c + 2047) / 2048 * 2048;
+  return c < CLIP_CHUNK ? CLIP_CHUNK : c;
+}
+long long chunks_of(const moe_grad* g, int count, long long chunk) {
+  long long c = 0;
+  for (int i = 0; i < count; ++i) c += (g[i].n + chunk - 1) / chunk;
+  return c;
+}
+
+int grad_checks(const char* fn, const moe_grad* g, int count, bool outs) {
+  MOE_TRY(moe_need_nonneg(count, fn, "count"));
+  if (count > 0 && g == nullptr) return moe_fail(MOE_ERR_INVALID_ARG, "%s: grads is NULL", fn);
+  if (count > (1 << 20))
+    return moe_fail(MOE_ERR_UNSUPPORTED, "%s: %d gradients, above the limit", fn, count);
+  for (int i = 0; i < count; ++i) {
+    if (g[i].n < 0 || g[i].n >= (1LL << 40))
+      return moe_fail(MOE_ERR_INVALID_ARG, "%s: gradient %d has %lld elements", fn, i, g[i].n);
+    MOE_TRY(moe_need_dt(g[i].dt, fn));
+    if (outs && g[i].out_dt != MOE_F32 && g[i].out_dt != g[i].dt)
+      return moe_fail(MOE_ERR_INVALID_ARG,
+                      "%s: out %d has dtype %d, neither its gradient's nor MOE_F32", fn, i,
+                      g[i].out_dt);
+    if (g[i].n == 0) continue;
+    MOE_TRY(moe_need_ptr(g[i].g, fn, "a gradient", moe_dt_bytes(g[i].dt)));
+    if (outs) {
+      MOE_TRY(moe_need_ptr(g[i].out, fn, "an out", moe_dt_bytes(g[i].out_dt)));
+      if (g[i].out == g[i].g && g[i].out_dt != g[i].dt)
+        return moe_fail(MOE_ERR_INVALID_ARG, "%s: out %d overlaps its gradient, of another type",
+                        fn, i);
+    }
+  }
+  return MOE_OK;
+}
+
+// An out that shares memory with another gradient or out (in place: its own).
+struct Span {
+  uintptr_t lo, hi;
+  int i;
+  bool written;
+  bool operator<(const Span& o) const { return lo < o.lo; }
+};
+int clip_overlaps(const char* fn, const moe_grad* g, int count) {
+  Span* s = new (std::nothrow) Span[2 * (size_t)count];
+  if (s == nullptr) return moe_fail(MOE_ERR_UNSUPPORTED, "%s: no host memory", fn);
+  int m = 0;
+  for (int i = 0; i < count; ++i) {
+    if (g[i].n == 0) continue;
+    const uintptr_t p = (uintptr_t)g[i].g, o = (uintptr_t)g[i].out;
+    s[m++] = {o, o + (uintptr_t)g[i].n * moe_dt_bytes(g[i].out_dt), i, true};
+    if (o != p) s[m++] = {p, p + (uintptr_t)g[i].n * moe_dt_bytes(g[i].dt), i, false};
+  }
+  std::sort(s, s + m);
+  uintptr_t any = 0, written = 0;     // ends of what began before
+  int st = MOE_OK;
+  for (int j = 0; j < m && st == MOE_OK; ++j) {
+    if (s[j].lo < (s[j].written ? any : written))
+      st = moe_fail(MOE_ERR_INVALID_ARG, "%s: the memory of %s %d is also another's", fn,
+                    s[j].written ? "out" : "gradient", s[j].i);
+    any = std::max(any, s[j].hi);
+    if (s[j].written) written = std::max(written, s[j].hi);
+  }
+  delete[] s;
+  return st;
+}
+
+}  // namespace
+
+extern "C" size_t moe_grad_norm_workspace_bytes(const moe_grad* grads, int count) {
+  if (grad_checks("moe_grad_norm_workspace_bytes", grads, count, false) != MOE_OK) return 0;
+  const size_t part = (size_t)chunks_of(grads, count, chunk_of(grads, count)) * 8;
+  return (part + 255) / 256 * 256 + ((size_t)(count + 1) * 4 + 255) / 256 * 256;
+}
+
+extern "C" int moe_grad_norm(const moe_grad* grads, int count, int kind, float* norm, float* norms,
+                             double* total, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  const char* fn = "moe_grad_norm";
+  MOE_TRY(grad_checks(fn, grads, count, false));
+  if (kind != MOE_GRAD_L2 && kind != MOE_GRAD_MAX)
+    return moe_fail(MOE_ERR_INVALID_ARG, "%s: kind %d is none of the MOE_GRAD values", fn, kind);
+  MOE_TRY(moe_need_ptr(norm, fn, "norm", 4));
+  MOE_TRY(moe_opt_ptr(norms, fn, "norms", 4));
+  MOE_TRY(moe_opt_ptr(total, fn, "total", 8));
+  MOE_TRY(moe_need_ptr(ws, fn, "ws", 256));
+  const size_t need = moe_grad_norm_workspace_bytes(grads, count);
+  if (ws_bytes < need)
+    return moe_fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", fn, ws_bytes, need);
+  const MoeRange outs[] = {{norm, 4, "norm"}, {norms, 4LL * count, "norms"}, {total, 8, "total"},
+                           {ws, (long long)need, "ws"}};
+  for (int i = 0; i < 4; ++i) {
+    const char* with = nullptr;
+    for (int j = 0; j < i && with == nullptr; ++j) with = moe_shares(outs[i], {outs[j]});
+    for (int j = 0; j < count && with == nullptr; ++j)
+      with = moe_shares(outs[i], {{grads[j].g, grads[j].n * moe_dt_bytes(grads[j].dt),
+                                   "a gradient"}});
+    if (with != nullptr)
+      return moe_fail(MOE_ERR_INVALID_ARG, "%s: %s needs a buffer of its own, it overlaps %s", fn,
+                      outs[i].name, with);
+  }
+  hipStream_t s = (hipStream_t)stream;
+  const long long chunk = chunk_of(grads, count);
+  const long long chunks = chunks_of(grads, count, chunk);
+  double* const part = (double*)ws;
+  int* const starts = (int*)((char*)ws + ((size_t)chunks * 8 + 255) / 256 * 256);
+  int base = 0;
+  for (int g0 = 0; g0 < count; g0 += NORM_TABLE) {
+    NormTable t;
+    t.count = std::min(NORM_TABLE, count - g0);
+    t.first[0] = 0;
+    for (int i = 0; i < t.count; ++i) {
+      const moe_grad& g = grads[g0 + i];
+      t.g[i] = g.g;
+      t.n[i] = (unsigned long long)g.n | (g.dt == MOE_BF16 ? G_BF16 : 0);
+      t.first[i + 1] = t.first[i] + (int)((g.n + chunk - 1) / chunk);
+    }
+    const int blocks = t.first[t.count];
+    // (a launch of gradients that are all empty has a block for their starts)
+    const dim3 grid(blocks > 0 ? blocks : 1);
+    if (kind == MOE_GRAD_MAX)
+      hipLaunchKernelGGL(grad_part_kernel<true>, grid, dim3(CLIP_NT), 0, s, t, chunk, base, g0,
+                         part, starts);
+    else
+      hipLaunchKernelGGL(grad_part_kernel<false>, grid, dim3(CLIP_NT), 0, s, t, chunk, base, g0,
+                         part, starts);
+    MOE_TRY(moe_check_launch(fn));
+    base += blocks;
+  }
+  if (kind == MOE_GRAD_MAX)
+    hipLaunchKernelGGL(grad_norm_kernel<true>, dim3(1), dim3(CLIP_SUM_NT), 0, s, part, starts,
+                       count, norm, norms, total);
+  else
+    hipLaunchKernelGGL(grad_norm_kernel<false>, dim3(1), dim3(CLIP_SUM_NT), 0, s, part, starts,
+                       count, norm, norms, total);
+  return moe_check_launch(fn);
+}
+
+extern "C" int moe_grad_clip(const moe_grad* grads, int count, const float* norm, float max_norm,
+                             moe_stream_t stream) {
+  const char* fn = "moe_grad_clip";
+  MOE_TRY(grad_checks(fn, grads, count, true));
+  if (!(max_norm >= 0.f))
+    return moe_fail(MOE_ERR_INVALID_ARG, "%s: max_norm = %g is negative or NaN", fn, max_norm);
+  MOE_TRY(moe_need_ptr(norm, fn, "norm", 4));
+  for (int i = 0; i < count; ++i)
+    if (moe_shares({grads[i].out, grads[i].n * moe_dt_bytes(grads[i].out_dt), "out"},
+                   {{norm, 4, "norm"}}))
+      return moe_fail(MOE_ERR_INVALID_ARG, "%s: out %d overlaps norm", fn, i);
+  MOE_TRY(clip_overlaps(fn, grads, count));
+  hipStream_t s = (hipStream_t)stream;
+  const long long chunk = chunk_of(grads, count);
+  for (int g0 = 0; g0 < count; g0 += CLIP_TABLE) {
+    ClipTable t;
+    t.count = std::min(CLIP_TABLE, count - g0);
+    t.first[0] = 0;
+    for (int i = 0; i < t.count; ++i) {
+      const moe_grad& g = grads[g0 + i];
+      t.g[i] = g.g;
+      t.out[i] = g.out;
+      t.n[i] = (unsigned long long)g.n | (g.dt == MOE_BF16 ? G_BF16 : 0) |
+               (g.out_dt == MOE_BF16 ? OUT_BF16 : 0);
+      t.first[i + 1] = t.first[i] + (int)((g.n + chunk - 1) / chunk);
+    }
+    if (t.first[t.count] == 0) continue;
+    hipLaunchKernelGGL(grad_clip_kernel, dim3(t.first[t.count]), dim3(CLIP_NT), 0, s, t, chunk,
+                       norm, max_norm);
+    MOE_TRY(moe_check_launch(fn));
+  }
+  return MOE_OK;
+}

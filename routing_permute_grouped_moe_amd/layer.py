@@ -67,9 +67,13 @@ class MoeLayer:
     """Device buffers of one layer plus the forward/backward call sequences."""
 
     def __init__(self, shape: LayerShape, device="cuda", overlap: bool = False,
-                 recompute: bool = False):
+                 recompute: bool = False, balance: "Optional[BalanceLoss]" = None):
         s = self.s = shape
         self.overlap = overlap
+        # auxiliary losses of the router, over packed sequences ``seq`` and the
+        # tokens to ``keep`` (set by the caller; None: one sequence, all tokens)
+        self.balance = balance
+        self.seq = self.keep = self.losses = None
         # recompute: no permuted copy of x (the grouped GEMMs gather token
         # rows through src_token) and act is recomputed from h13 for dW
         self.recompute = recompute
@@ -168,6 +172,12 @@ class MoeLayer:
         s = self.s
         abi.moe_route(self.logits, s.T, s.E, s.k, self.idx, self.gate, stream)
 
+    def balance_loss(self, stream=None):
+        """``losses`` (a :class:`Balance`): read its ``loss`` after the forward; the
+        backward takes the gradient of ``loss[2]`` into dlogits."""
+        self.losses = self.balance.forward(self.logits, self.idx, seq=self.seq, keep=self.keep,
+                                           stream=stream)
+
     def permute(self, stream=None):
         s = self.s
         if s.capacity is not None:
@@ -257,6 +267,11 @@ class MoeLayer:
 
     def route_bwd(self, stream=None):
         s = self.s
+        if self.balance is not None:      # the gates' and the losses' gradient in one pass
+            self.balance.backward(self.logits, self.idx, self.losses.counts, self.losses.tokens,
+                                  seq=self.seq, keep=self.keep, dgate=self.dgate,
+                                  out=self.dlogits, stream=stream)
+            return
         abi.moe_route_bwd(self.logits, self.idx, self.dgate, s.T, s.E, s.k, self.dlogits, stream)
 
     def router_bwd(self, stream=None):
@@ -284,6 +299,8 @@ class MoeLayer:
         if s.router:
             self.router_fwd(stream)
         self.route(stream)
+        if self.balance is not None:
+            self.balance_loss(stream)
         self.permute(stream)
         self.load_stats(stream)
         self.gmm_fwd(stream)
@@ -315,16 +332,31 @@ class MoeLayer:
         self.forward(stream)
         self.backward(stream)
 
+    def grads(self):
+        """The gradients of the layer's parameters, in their buffers."""
+        g = [self.dw13, self.dw2]
+        if self.s.shared:
+            g += [self.dws13, self.dws2]
+        if self.s.router:
+            g += [self.dwg] if self.bias is None else [self.dwg, self.dbias]
+        return g
+
+    def clip_grads(self, max_norm: float, stream=None):
+        """Clips the layer's gradients by their norm together, in place; returns the
+        norm (:class:`GradClip` takes the gradients of several layers)."""
+        return GradClip(self.grads()).clip(max_norm, stream=stream)
+
 
 # ---------------------------------------------------------------------- checked calls
-def _check(name, t, dtype, device, *shape):
-    """A tensor the kernels can read as it lies: dense, of this shape, type and device."""
+def _check(name, t, dtype, device, *shape, beside="the weights are"):
+    """A tensor the kernels can read as it lies: dense, of this shape, type and device
+    (that of ``beside``)."""
     if (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
         return
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}, not {dtype}")
     if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the weights are on {device}")
+        raise ValueError(f"{name} is on {t.device}, {beside} on {device}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
     raise ValueError(f"{name} is not contiguous")
@@ -345,7 +377,7 @@ def _on(device, stream, call, *inputs):
         with torch.cuda.device(device):
             return call(_raw_stream(device.index))
     if stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the weights are on {device}")
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
     with torch.cuda.stream(stream):   # (makes the stream's device current too)
         for x in inputs:
             if x is not None:
@@ -353,9 +385,9 @@ def _on(device, stream, call, *inputs):
         return call(stream.cuda_stream)
 
 
-def _device(t):
+def _device(t, what="weights are"):
     if not t.is_cuda:
-        raise ValueError(f"weights are on {t.device}, not on a GPU")
+        raise ValueError(f"{what} on {t.device}, not on a GPU")
     return t.device
 
 
@@ -515,3 +547,260 @@ class Linear:
                                ws, n, st)
             return dx, dw, db
         return _on(dev, stream, call, dy, x, z, self.w)
+
+
+class Balance(NamedTuple):
+    """The losses of :class:`BalanceLoss` and what its backward needs."""
+    loss: torch.Tensor             # [3] fp32: balance, z, and their weighted sum
+    counts: torch.Tensor           # [S, E] int32, choices of each expert
+    tokens: torch.Tensor           # [S + 1] int32, tokens that count of each sequence, and of all
+    prob: torch.Tensor             # [S, E] fp32, mean probabilities (a statistic)
+
+
+class BalanceLoss:
+    """``weight`` times the balance loss of a routing step and ``z_weight`` times
+    its z loss (defined at ``moe_balance_loss`` in ``include/moe.h``), with
+    per-expert counts, and their gradient together with the gates'.
+
+    ``seq`` [S + 1] int32 are the ends of packed sequences (None: all tokens are
+    one), ``keep`` [T] uint8 or bool says which tokens count (None: all)."""
+
+    def __init__(self, weight: float = 0.01, z_weight: float = 0.0):
+        self.weight, self.z_weight = float(weight), float(z_weight)
+
+    @staticmethod
+    def _inputs(logits, idx, seq, keep):
+        dev = _device(logits, "logits are")
+        if logits.dim() != 2:
+            raise ValueError(f"logits have {logits.dim()} dimensions, not 2")
+        T, E = logits.shape
+        of = {"beside": "logits are"}
+        _check("logits", logits, torch.float32, dev, T, E)
+        if idx.dim() != 2:
+            raise ValueError(f"idx has {idx.dim()} dimensions, not 2")
+        k = idx.shape[1]
+        _check("idx", idx, torch.int32, dev, T, k, **of)
+        S = 1
+        if seq is not None:
+            if seq.dim() != 1 or seq.shape[0] < 2:
+                raise ValueError(f"seq has shape {tuple(seq.shape)}, not one of S + 1 >= 2 ends")
+            S = seq.shape[0] - 1
+            _check("seq", seq, torch.int32, dev, S + 1, **of)
+        if keep is not None:
+            _check("keep", keep, torch.bool if keep.dtype == torch.bool else torch.uint8, dev, T,
+                   **of)
+        return dev, T, E, k, S
+
+    def forward(self, logits, idx, seq=None, keep=None, stream=None) -> Balance:
+        """``logits`` [T, E] and the chosen ``idx`` [T, k] -> :class:`Balance`."""
+        dev, T, E, k, S = self._inputs(logits, idx, seq, keep)
+
+        def call(st):
+            n = abi.moe_balance_loss_workspace_bytes(T, E, k, S)
+            loss, prob = logits.new_empty(3), logits.new_empty((S, E))
+            counts, tokens = idx.new_empty((S, E)), idx.new_empty(S + 1)
+            # a workspace per call, from the stream's own pool: calls on several
+            # streams, or captured into several graphs, never share one
+            ws = logits.new_empty(n, dtype=torch.uint8)
+            abi.moe_balance_loss(logits, idx, keep, seq, T, E, k, S, self.weight, self.z_weight,
+                                 loss, counts, tokens, prob, ws, n, st)
+            return Balance(loss, counts, tokens, prob)
+        return _on(dev, stream, call, logits, idx, seq, keep)
+
+    def backward(self, logits, idx, counts, tokens, seq=None, keep=None, dgate=None, dloss=None,
+                 out=None, stream=None):
+        """dlogits [T, E] (into ``out``, if given) of ``dloss`` (one fp32 value;
+        None: 1) times the weighted sum of the losses and, with ``dgate`` [T, k],
+        of the gates too.  ``counts`` and ``tokens`` are the forward's."""
+        dev, T, E, k, S = self._inputs(logits, idx, seq, keep)
+        f32, of = torch.float32, {"beside": "logits are"}
+        _check("counts", counts, torch.int32, dev, S, E, **of)
+        _check("tokens", tokens, torch.int32, dev, S + 1, **of)
+        if dgate is not None:
+            _check("dgate", dgate, f32, dev, T, k, **of)
+        if dloss is not None:
+            if dloss.numel() != 1:
+                raise ValueError(f"dloss has {dloss.numel()} values, not 1")
+            _check("dloss", dloss, f32, dev, *dloss.shape, **of)
+        if out is not None:
+            _check("out", out, f32, dev, T, E, **of)
+
+        def call(st):
+            dlogits = torch.empty_like(logits) if out is None else out
+            abi.moe_balance_loss_bwd(logits, idx, dgate, keep, seq, counts, tokens, T, E, k, S,
+                                     self.weight, self.z_weight, dloss, dlogits, st)
+            return dlogits
+        return _on(dev, stream, call, logits, idx, counts, tokens, seq, keep, dgate, dloss, out)
+
+
+NORMS = {"layer": abi.MOE_NORM_LAYER, "rms": abi.MOE_NORM_RMS}
+
+
+class Normed(NamedTuple):
+    """One pass of :class:`Norm`."""
+    y: torch.Tensor                # [M, H]
+    h: torch.Tensor                # [M, H], x + residual (x itself without a residual)
+    mean: Optional[torch.Tensor]   # [M] fp32, with ``save`` and of a layer norm
+    rstd: Optional[torch.Tensor]   # [M] fp32, with ``save``
+
+
+class Norm:
+    """Layer norm (``kind="layer"``) or RMS norm (``"rms"``) of rows, with an
+    optional residual sum in front, and its gradients; ``w`` and ``bias`` are
+    [H] fp32."""
+
+    def __init__(self, w, bias=None, kind: str = "layer", eps: float = 1e-5):
+        self.device = _device(w)
+        if w.dim() != 1:
+            raise ValueError(f"w has {w.dim()} dimensions, not 1")
+        self.H = w.shape[0]
+        _check("w", w, torch.float32, self.device, self.H)
+        if bias is not None:
+            _check("bias", bias, torch.float32, self.device, self.H)
+        if kind not in NORMS:
+            raise ValueError(f"kind {kind!r} is none of {', '.join(NORMS)}")
+        if not 0.0 < eps < float("inf"):
+            raise ValueError(f"eps {eps} is not positive and finite")
+        self.w, self.bias, self.kind, self.eps = w, bias, NORMS[kind], float(eps)
+
+    def _rows(self, x):
+        if x.dim() != 2:
+            raise ValueError(f"x has {x.dim()} dimensions, not 2")
+        dt = abi.dtype_code(x)
+        _check("x", x, x.dtype, self.device, x.shape[0], self.H)
+        return dt, x.shape[0]
+
+    def forward(self, x, residual=None, save=False, out=None, h_out=None, stream=None) -> Normed:
+        """``x`` [M, H] -> :class:`Normed`; ``save``: with the statistics that the
+        backward needs.  ``out``: y's buffer; ``h_out``: that of x + residual (the
+        residual's will do, or x's)."""
+        dt, M = self._rows(x)
+        H, dev = self.H, self.device
+        for name, t in (("residual", residual), ("out", out), ("h_out", h_out)):
+            if t is not None:
+                _check(name, t, x.dtype, dev, M, H)
+        if h_out is not None and residual is None:
+            raise ValueError("h_out comes with a residual, and only with it")
+
+        def call(st):
+            y = torch.empty_like(x) if out is None else out
+            h = None if residual is None else torch.empty_like(x) if h_out is None else h_out
+            rstd = self.w.new_empty(M) if save else None
+            mean = self.w.new_empty(M) if save and self.kind == abi.MOE_NORM_LAYER else None
+            abi.moe_norm(x, residual, dt, M, H, self.kind, self.eps, self.w, self.bias, h, y, mean,
+                         rstd, st)
+            return Normed(y, x if h is None else h, mean, rstd)
+        return _on(dev, stream, call, x, residual, out, h_out, self.w, self.bias)
+
+    def backward(self, dy, h, rstd, mean=None, dh=None, x_grad=True, w_grad=True, bias_grad=None,
+                 out=None, stream=None):
+        """(dx, dw, db) of ``dy`` [M, H], the forward's ``h``, ``rstd`` and ``mean``
+        (None for RMS); ``dh``: the gradient that reaches h besides, added to dx,
+        which is that of x and of the residual.  Each is computed, or None, as
+        ``x_grad``, ``w_grad`` and ``bias_grad`` (by default: whether there is a
+        bias) say.  ``out``: dx's buffer (dh's will do)."""
+        dt, M = self._rows(h)
+        H, dev, f32 = self.H, self.device, torch.float32
+        for name, t in (("dy", dy), ("dh", dh), ("out", out)):
+            if t is not None:
+                _check(name, t, h.dtype, dev, M, H)
+        _check("rstd", rstd, f32, dev, M)
+        if (mean is None) != (self.kind == abi.MOE_NORM_RMS):
+            raise ValueError("mean comes with a layer norm, and only with it")
+        if mean is not None:
+            _check("mean", mean, f32, dev, M)
+        if bias_grad is None:
+            bias_grad = self.bias is not None
+
+        def call(st):
+            dx = None if not x_grad else torch.empty_like(h) if out is None else out
+            dw = torch.empty_like(self.w) if w_grad else None
+            db = torch.empty_like(self.w) if bias_grad else None
+            n = abi.moe_norm_bwd_workspace_bytes(M, H, dt) if w_grad or bias_grad else 0
+            ws = h.new_empty(n, dtype=torch.uint8) if n else None
+            abi.moe_norm_bwd(dy, h, dh, dt, M, H, self.kind, self.w, mean, rstd, dx, dw, db, ws, n,
+                             st)
+            return dx, dw, db
+        return _on(dev, stream, call, dy, h, rstd, mean, dh, out, self.w)
+
+
+GRAD_NORMS = {"l2": abi.MOE_GRAD_L2, "max": abi.MOE_GRAD_MAX}
+
+
+class GradClip:
+    """The norm of ``grads`` together (``kind``: ``"l2"``, the root of the sum of
+    all squares, or ``"max"``, the largest magnitude) and clipping by it.
+
+    ``grads`` are dense tensors of any shapes, fp32 or bf16, on one GPU; ``outs``:
+    where the clipped ones go, of the same sizes and of the same type or fp32
+    (None: in place).  The tensors stay the caller's; each call takes their
+    present contents, and their addresses as they are then."""
+
+    def __init__(self, grads, outs=None, kind: str = "l2"):
+        self.grads = list(grads)
+        self.outs = self.grads if outs is None else list(outs)
+        if not self.grads:
+            raise ValueError("no gradients")
+        if len(self.outs) != len(self.grads):
+            raise ValueError(f"{len(self.outs)} outs for {len(self.grads)} gradients")
+        if kind not in GRAD_NORMS:
+            raise ValueError(f"kind {kind!r} is none of {', '.join(GRAD_NORMS)}")
+        self.kind = GRAD_NORMS[kind]
+        self.device = _device(self.grads[0], "gradients are")
+        self._tensors = self.grads if outs is None else self.grads + self.outs
+        of = {"beside": "the first gradient is"}
+        for i, (g, o) in enumerate(zip(self.grads, self.outs)):
+            abi.dtype_code(g)
+            _check(f"gradient {i}", g, g.dtype, self.device, *g.shape, **of)
+            if o is not g:
+                _check(f"out {i}", o, o.dtype if o.dtype == torch.float32 else g.dtype, self.device,
+                       *g.shape, **of)
+        self._lay_out()
+
+    def _lay_out(self):
+        self._at = [t.data_ptr() for t in self._tensors]
+        self._arr = abi.grads(self.grads, self.outs)
+        self._ws_bytes = abi.moe_grad_norm_workspace_bytes(self._arr, len(self.grads))
+
+    def _array(self):
+        if [t.data_ptr() for t in self._tensors] != self._at:   # (storage that was replaced)
+            self.__init__(self.grads, None if self.outs is self.grads else self.outs,
+                          {v: k for k, v in GRAD_NORMS.items()}[self.kind])
+        return self._arr
+
+    def _norm(self, arr, st, each=False, total=False):
+        dev, n = self.device, len(self.grads)
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+        norms = torch.empty(n, dtype=torch.float32, device=dev) if each else None
+        whole = torch.empty((), dtype=torch.float64, device=dev) if total else None
+        ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=dev)
+        abi.moe_grad_norm(arr, n, self.kind, norm, norms, whole, ws, self._ws_bytes, st)
+        return norm, norms, whole
+
+    def norm(self, each=False, total=False, stream=None):
+        """The norm (fp32, no dimensions), with ``each`` also those of the
+        gradients one by one [n], with ``total`` also the sum of all squares in
+        64 bits (the maximum): what ranks that hold parts of a model reduce."""
+        arr = self._array()
+
+        def call(st):
+            norm, norms, whole = self._norm(arr, st, each, total)
+            more = tuple(t for t in (norms, whole) if t is not None)
+            return (norm, *more) if more else norm
+        return _on(self.device, stream, call, *self.grads)
+
+    def clip(self, max_norm: float, norm=None, stream=None):
+        """Scales the gradients by min(1, max_norm / (norm + 1e-6)); returns the
+        norm.  ``norm``: one fp32 value to take instead of the gradients' own."""
+        arr = self._array()
+        if norm is not None:
+            if norm.numel() != 1:
+                raise ValueError(f"norm has {norm.numel()} values, not 1")
+            _check("norm", norm, torch.float32, self.device, *norm.shape,
+                   beside="the gradients are")
+
+        def call(st):
+            by = self._norm(arr, st)[0] if norm is None else norm
+            abi.moe_grad_clip(arr, len(self.grads), by, max_norm, st)
+            return by
+        return _on(self.device, stream, call, norm, *self._tensors)
