@@ -2,80 +2,156 @@
 // gradients:
 //   h = x + residual,  q = (h - m) rstd,  y = q w + bias
 //   g = dy w,  dx = rstd (g - mean(g) - q mean(g q)) + dh,  dw = sum dy q,  db = sum dy
+#include "reduce.hpp"
 #include "validate.hpp"
 
 namespace {
 
-constexpr int NORM_NT = 256;
-constexpr int NORM_WAVES = NORM_NT / MOE_WAVE;
 constexpr int NORM_MAX_H = 16384;
-constexpr int NORM_PARTS = 256;   // row runs of the weight gradient, at most
+constexpr uint32_t NORM_OOB = 0x80000000u;   // past every row: reads zeros, stores are dropped
 
-template <typename T>
-__device__ __forceinline__ float norm_load(const void* p, long long i) {
-  if constexpr (sizeof(T) == 2) return bf16_to_f32(((const T*)p)[i]);
-  else return ((const T*)p)[i];
-}
-template <typename T>
-__device__ __forceinline__ float norm_store(void* p, long long i, float v) {
-  if constexpr (sizeof(T) == 2) {
-    const T b = (T)f32_to_bf16(v);
-    ((T*)p)[i] = b;
-    return bf16_to_f32(b);
-  } else {
-    ((T*)p)[i] = v;
-    return v;
+// TPR threads hold a row, C chunks of 16 bytes each; rows of less than a
+// workgroup share one.
+template <typename T, int TPR, int C, int THREADS>
+struct Rows {
+  static constexpr int VEC = Elem<T>::VEC;
+  static constexpr int NT = THREADS;
+  static constexpr int G = NT / TPR;         // rows at a time
+  static constexpr int WAVES = NT / MOE_WAVE;
+  static constexpr bool PRE = !(TPR == 1024 && C * VEC >= 16);
+};
+
+// The sums of two values over the threads of a row, in all of them; `turn` flips
+// from call to call, so that one barrier a call is enough.
+template <int TPR, int WAVES>
+__device__ __forceinline__ void row_sums(float& a, float& b, float2 (*red)[WAVES], int& turn) {
+  constexpr int N = TPR < MOE_WAVE ? TPR : MOE_WAVE;
+  a = lanes_sum<N>(a);
+  b = lanes_sum<N>(b);
+  if constexpr (TPR > MOE_WAVE) {
+    const int wave = threadIdx.x / MOE_WAVE, first = wave / (TPR / MOE_WAVE) * (TPR / MOE_WAVE);
+    if ((threadIdx.x & 63) == 0) red[turn][wave] = float2{a, b};
+    __syncthreads();
+    a = 0.f, b = 0.f;
+#pragma unroll
+    for (int w = 0; w < TPR / MOE_WAVE; ++w) {
+      a += red[turn][first + w].x;
+      b += red[turn][first + w].y;
+    }
+    turn ^= 1;
   }
 }
-
-__device__ __forceinline__ float block_sum(float v, float* red) {
-  v = wave_sum(v);
-  __syncthreads();
-  if (threadIdx.x % MOE_WAVE == 0) red[threadIdx.x / MOE_WAVE] = v;
-  __syncthreads();
-  float s = 0.f;
+template <int TPR, int WAVES>
+__device__ __forceinline__ float row_sum(float a, float2 (*red)[WAVES], int& turn) {
+  constexpr int N = TPR < MOE_WAVE ? TPR : MOE_WAVE;
+  a = lanes_sum<N>(a);
+  if constexpr (TPR > MOE_WAVE) {
+    const int wave = threadIdx.x / MOE_WAVE, first = wave / (TPR / MOE_WAVE) * (TPR / MOE_WAVE);
+    if ((threadIdx.x & 63) == 0) red[turn][wave].x = a;
+    __syncthreads();
+    a = 0.f;
 #pragma unroll
-  for (int w = 0; w < NORM_WAVES; ++w) s += red[w];
-  return s;
+    for (int w = 0; w < TPR / MOE_WAVE; ++w) a += red[turn][first + w].x;
+    turn ^= 1;
+  }
+  return a;
 }
 
 struct NormArgs {
   const void* x; const void* residual; const float* w; const float* bias;
   void* h; void* y; float* mean; float* rstd;
-  int M, H, rms;
-  float eps;
+  int M, H, rms, stream;
+  float eps, inv_h;
 };
 
-template <typename T>
-__global__ __launch_bounds__(NORM_NT) void norm_kernel(NormArgs a) {
-  __shared__ float red[NORM_WAVES];
-  const long long r0 = (long long)blockIdx.x * a.H;
-  auto at = [&](int i) {
-    float v = norm_load<T>(a.x, r0 + i);
-    if (a.residual) {
-      v += norm_load<T>(a.residual, r0 + i);
-      if constexpr (sizeof(T) == 2) v = bf16_to_f32(f32_to_bf16(v));
+template <typename T, int TPR, int C, int NT_>
+__global__ __launch_bounds__(NT_) void norm_kernel(NormArgs a) {
+  using R = Rows<T, TPR, C, NT_>;
+  constexpr int VEC = R::VEC, ES = sizeof(T);
+  __shared__ float2 red[2][R::WAVES];
+  const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+  const int n = a.H / VEC;                   // chunks of a row
+  const uint32_t rb = (uint32_t)a.H * ES;
+  uint32_t off[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int c = lane + i * TPR;
+    off[i] = c < n ? (uint32_t)grp * rb + (uint32_t)c * 16u : NORM_OOB;
+  }
+  float w[C][VEC], b[C][VEC];
+  const auto rw = make_rsrc(a.w, (uint32_t)a.H * 4u);
+  const auto rbias = make_rsrc(a.bias, a.bias ? (uint32_t)a.H * 4u : 0u);
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+#pragma unroll
+    for (int j = 0; j < VEC; j += 4) {
+      const uint32_t o = ((uint32_t)(lane + i * TPR) * VEC + j) * 4u;
+      unpack16(buf_load16(rw, o), &w[i][j], float());
+      unpack16(buf_load16(rbias, o), &b[i][j], float());
     }
-    return v;
+  auto rows = [&](const void* p, int r0) {   // the rows from r0 on (no memory: none)
+    const int m = r0 < a.M && p != nullptr ? (a.M - r0 < R::G ? a.M - r0 : R::G) : 0;
+    return make_rsrc((const char*)p + (m ? (long long)r0 * rb : 0), (uint32_t)m * rb);
   };
-  float s = 0.f;
-  for (int i = threadIdx.x; i < a.H; i += NORM_NT) s += at(i);
-  const float mean = a.rms ? 0.f : block_sum(s, red) / a.H;
-  float q = 0.f;
-  for (int i = threadIdx.x; i < a.H; i += NORM_NT) {
-    const float d = at(i) - mean;
-    q += d * d;
-  }
-  const float rstd = 1.0f / sqrtf(block_sum(q, red) / a.H + a.eps);
-  for (int i = threadIdx.x; i < a.H; i += NORM_NT) {
-    const float v = at(i);
-    if (a.h) norm_store<T>(a.h, r0 + i, v);
-    const float y = (v - mean) * rstd * a.w[i];
-    norm_store<T>(a.y, r0 + i, a.bias ? y + a.bias[i] : y);
-  }
-  if (threadIdx.x == 0) {
-    if (a.mean && !a.rms) a.mean[blockIdx.x] = mean;
-    if (a.rstd) a.rstd[blockIdx.x] = rstd;
+  u32x4 x[C], res[C];
+  auto fetch = [&](int r0) {
+    const auto rx = rows(a.x, r0), rr = rows(a.residual, r0);
+    if (a.stream) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) x[i] = buf_load16_nt(rx, off[i]), res[i] = buf_load16_nt(rr, off[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < C; ++i) x[i] = buf_load16(rx, off[i]), res[i] = buf_load16(rr, off[i]);
+    }
+  };
+  const int step = gridDim.x * R::G;
+  int turn = 0;
+  int r0 = blockIdx.x * R::G;
+  fetch(r0);
+  for (; r0 < a.M; r0 += step) {
+    u32x4 h[C];
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      float v[VEC], q[VEC];
+      unpack16(x[i], v, T());
+      unpack16(res[i], q, T());
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[j] += q[j];
+      h[i] = pack16(v, T());
+      unpack16(h[i], v, T());                // the norm of the sum as it is stored
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) s += v[j];
+    }
+    fetch(r0 + step);                        // in flight during the sums
+    const float mean = a.rms ? 0.f : row_sum<TPR>(s, red, turn) * a.inv_h;
+    float d2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      float v[VEC], e = 0.f;
+      unpack16(h[i], v, T());
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const float d = v[j] - mean;
+        e = fmaf(d, d, e);
+      }
+      d2 += off[i] != NORM_OOB ? e : 0.f;
+    }
+    const float rstd = 1.0f / sqrtf(row_sum<TPR>(d2, red, turn) * a.inv_h + a.eps);
+    const auto rh = rows(a.h, r0), ry = rows(a.y, r0);
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      float v[VEC];
+      unpack16(h[i], v, T());
+      buf_store16_nt(rh, off[i], h[i]);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[j] = fmaf((v[j] - mean) * rstd, w[i][j], b[i][j]);
+      buf_store16_nt(ry, off[i], pack16(v, T()));
+    }
+    if (lane == 0 && r0 + grp < a.M) {
+      if (a.mean && !a.rms) a.mean[r0 + grp] = mean;
+      if (a.rstd) a.rstd[r0 + grp] = rstd;
+    }
   }
 }
 
@@ -83,59 +159,267 @@ struct NormBwdArgs {
   const void* dy; const void* h; const void* dh; const float* w; const float* mean;
   const float* rstd;
   void* dx; float* dw; float* db; float* part;
-  int M, H, rms, parts;
+  int M, H, rms, stream, parts;
+  float inv_h;
 };
 
+template <typename T, int TPR, int C, int NT_>
+__global__ __launch_bounds__(NT_) void norm_bwd_kernel(NormBwdArgs a) {
+  using R = Rows<T, TPR, C, NT_>;
+  constexpr int VEC = R::VEC, ES = sizeof(T);
+  constexpr bool PRE = R::PRE;
+  __shared__ float2 red[2][R::WAVES];
+  const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+  const int n = a.H / VEC;
+  const uint32_t rb = (uint32_t)a.H * ES;
+  uint32_t off[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int c = lane + i * TPR;
+    off[i] = c < n ? (uint32_t)grp * rb + (uint32_t)c * 16u : NORM_OOB;
+  }
+  float w[PRE ? C : 1][VEC], dw[C][VEC], db[C][VEC];
+  const auto rw = make_rsrc(a.w, (uint32_t)a.H * 4u);
+  auto wo = [&](int i, int j) { return ((uint32_t)(lane + i * TPR) * VEC + j) * 4u; };
+  auto weight = [&](int i) -> const float (&)[VEC] {   // (where registers are short: read again)
+    if constexpr (PRE) {
+      return w[i];
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; j += 4) unpack16(buf_load16(rw, wo(i, j)), &w[0][j], float());
+      return w[0];
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+#pragma unroll
+    for (int j = 0; j < VEC; j += 4) {
+      if (PRE) unpack16(buf_load16(rw, wo(i, j)), &w[i][j], float());
+#pragma unroll
+      for (int l = 0; l < 4; ++l) dw[i][j + l] = 0.f, db[i][j + l] = 0.f;
+    }
+  auto rows = [&](const void* p, int r0) {
+    const int m = r0 < a.M && p != nullptr ? (a.M - r0 < R::G ? a.M - r0 : R::G) : 0;
+    return make_rsrc((const char*)p + (m ? (long long)r0 * rb : 0), (uint32_t)m * rb);
+  };
+  u32x4 y[C], x[C];
+  float mean, rstd;
+  auto fetch = [&](int r0) {
+    const auto ry = rows(a.dy, r0), rx = rows(a.h, r0);
+    if (a.stream) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) y[i] = buf_load16_nt(ry, off[i]), x[i] = buf_load16_nt(rx, off[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < C; ++i) y[i] = buf_load16(ry, off[i]), x[i] = buf_load16(rx, off[i]);
+    }
+    const int r = r0 + grp;
+    mean = !a.rms && r < a.M ? a.mean[r] : 0.f;
+    rstd = r < a.M ? a.rstd[r] : 0.f;
+  };
+  const int step = gridDim.x * R::G;
+  int turn = 0;
+  int r0 = blockIdx.x * R::G;
+  fetch(r0);
+  for (; r0 < a.M; r0 += step) {
+    float s1 = 0.f, s2 = 0.f;
+    u32x4 yc[C], xc[C], ac[C];
+    const float m = mean, rs = rstd;
+    const auto ra = rows(a.dx ? a.dh : nullptr, r0);
+    if (a.stream) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) ac[i] = buf_load16_nt(ra, off[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < C; ++i) ac[i] = buf_load16(ra, off[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      yc[i] = y[i], xc[i] = x[i];
+      float dy[VEC], q[VEC];
+      unpack16(yc[i], dy, T());
+      unpack16(xc[i], q, T());
+      const float(&wi)[VEC] = weight(i);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        q[j] = (q[j] - m) * rs;
+        const float g = dy[j] * wi[j];
+        s1 += g;
+        s2 = fmaf(g, q[j], s2);
+        dw[i][j] = fmaf(dy[j], q[j], dw[i][j]);
+        db[i][j] += dy[j];
+      }
+    }
+    if (PRE) fetch(r0 + step);               // in flight during the sums
+    row_sums<TPR>(s1, s2, red, turn);
+    s1 = a.rms ? 0.f : s1 * a.inv_h;
+    s2 *= a.inv_h;
+    const auto rx = rows(a.dx, r0);
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      float dy[VEC], q[VEC], v[VEC];
+      unpack16(yc[i], dy, T());
+      unpack16(xc[i], q, T());
+      unpack16(ac[i], v, T());
+      const float(&wi)[VEC] = weight(i);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        q[j] = (q[j] - m) * rs;
+        v[j] = fmaf(rs, dy[j] * wi[j] - s1 - q[j] * s2, v[j]);
+      }
+      buf_store16_nt(rx, off[i], pack16(v, T()));
+    }
+    if (!PRE) fetch(r0 + step);
+  }
+  if (a.part == nullptr) return;
+  float* const part = a.part + (long long)blockIdx.x * 2 * a.H;
+  const auto rp = make_rsrc(part, (uint32_t)a.H * 8u);
+  if constexpr (R::G > 1) {                  // rows side by side: lanes of a wave, then the waves
+    constexpr int PER = TPR < MOE_WAVE ? 1 : TPR / MOE_WAVE;   // waves of a row
+    __shared__ float sum[2][TPR * C * VEC];
+    if constexpr (TPR < MOE_WAVE) {
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+#pragma unroll
+          for (int o = TPR; o < MOE_WAVE; o *= 2) {
+            dw[i][j] += __shfl_xor(dw[i][j], o, MOE_WAVE);
+            db[i][j] += __shfl_xor(db[i][j], o, MOE_WAVE);
+          }
+    }
+    for (int v = 0; v < R::WAVES / PER; ++v) {
+      if ((int)(threadIdx.x / MOE_WAVE) / PER == v && (threadIdx.x & 63) < TPR) {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) {
+            const int c = (lane + i * TPR) * VEC + j;
+            sum[0][c] = v ? sum[0][c] + dw[i][j] : dw[i][j];
+            sum[1][c] = v ? sum[1][c] + db[i][j] : db[i][j];
+          }
+      }
+      __syncthreads();
+    }
+    for (int c = threadIdx.x; c < a.H; c += R::NT) {
+      part[c] = sum[0][c];
+      part[a.H + c] = sum[1][c];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      if (off[i] == NORM_OOB) continue;
+#pragma unroll
+      for (int j = 0; j < VEC; j += 4) {
+        const uint32_t o = ((uint32_t)(lane + i * TPR) * VEC + j) * 4u;
+        buf_store16(rp, o, pack16(&dw[i][j], float()));
+        buf_store16(rp, o + (uint32_t)a.H * 4u, pack16(&db[i][j], float()));
+      }
+    }
+  }
+}
+
+// The workgroups' sums, in their order: 32 columns a workgroup, a 32nd of the
+// rows a thread.
+constexpr int SUM_COLS = 32, SUM_ROWS = 32;
+__global__ __launch_bounds__(SUM_COLS* SUM_ROWS) void norm_sum_kernel(NormBwdArgs a) {
+  __shared__ double red[SUM_ROWS][SUM_COLS];
+  const int col = threadIdx.x % SUM_COLS, row = threadIdx.x / SUM_COLS;
+  const int c = blockIdx.x * SUM_COLS + col;   // of [dw | db]
+  double s = 0;
+  if (c < 2 * a.H)
+#pragma unroll 8
+    for (int p = row; p < a.parts; p += SUM_ROWS) s += a.part[(long long)p * 2 * a.H + c];
+  red[row][col] = s;
+  __syncthreads();
+  if (row != 0 || c >= 2 * a.H) return;
+#pragma unroll
+  for (int r = 1; r < SUM_ROWS; ++r) s += red[r][col];
+  if (c < a.H) {
+    if (a.dw) a.dw[c] = (float)s;
+  } else if (a.db) {
+    a.db[c - a.H] = (float)s;
+  }
+}
+
+// ---------------------------------------------------------------- host
+
+struct Shape {
+  int tpr, c, nt;   // as Rows
+  int waves;        // resident in a CU
+};
+
+// Threads of a row by its 16-byte chunks.  Rows that a wave can hold need no
+// barrier; longer ones have at most two chunks a thread where registers allow
+// two rows in flight and the weight besides.
+Shape norm_shape(int chunks, bool residual) {
+  if (chunks <= 8) return {8, 1, 256, 16};
+  if (chunks <= 16) return {16, 1, 256, 16};
+  if (chunks <= 32) return {32, 1, 256, 16};
+  if (chunks <= 64) return {64, 1, 256, 16};
+  if (chunks <= 128) return {64, 2, 256, 16};
+  const int waves = residual ? 8 : 16;
+  if (chunks <= 256) return {256, 1, 256, waves};
+  if (chunks <= 512) return {256, 2, 256, waves};
+  if (chunks <= 1024) return {512, 2, 512, waves};
+  if (chunks <= 2048) return {512, 4, 512, waves};
+  return {1024, 4, 1024, 16};
+}
+Shape norm_bwd_shape(int chunks) {
+  if (chunks <= 8) return {8, 1, 512, 16};
+  if (chunks <= 16) return {16, 1, 512, 16};
+  if (chunks <= 32) return {32, 1, 512, 16};
+  if (chunks <= 64) return {64, 1, 512, 16};
+  if (chunks <= 128) return {64, 2, 512, 8};
+  if (chunks <= 256) return {128, 2, 512, 8};
+  if (chunks <= 512) return {256, 2, 512, 8};
+  if (chunks <= 1024) return {512, 2, 512, 8};
+  if (chunks <= 2048) return {1024, 2, 1024, 16};
+  return {1024, 4, 1024, 16};
+}
+int norm_blocks(int M, Shape s) {
+  const long long G = s.nt / s.tpr, most = (long long)moe_cu_count() * s.waves * MOE_WAVE / s.nt;
+  const long long need = (M + G - 1) / G, per = (need + most - 1) / most;
+  return per ? (int)((need + per - 1) / per) : 0;
+}
+int norm_parts(int M, int H, int dt) {
+  return norm_blocks(M, norm_bwd_shape(H * moe_dt_bytes(dt) / 16));
+}
+
+#define NORM_SHAPES(X)                                                                    \
+  X(8, 1, 256) X(16, 1, 256) X(32, 1, 256) X(64, 1, 256) X(64, 2, 256) X(256, 1, 256)     \
+  X(256, 2, 256) X(512, 2, 512) X(512, 4, 512) X(1024, 4, 1024)
+#define NORM_BWD_SHAPES(X)                                                                \
+  X(8, 1, 512) X(16, 1, 512) X(32, 1, 512) X(64, 1, 512) X(64, 2, 512) X(128, 2, 512)     \
+  X(256, 2, 512) X(512, 2, 512) X(1024, 2, 1024) X(1024, 4, 1024)
+
+// (rows of bf16 end at 2048 chunks)
 template <typename T>
-__global__ __launch_bounds__(NORM_NT) void norm_dx_kernel(NormBwdArgs a) {
-  __shared__ float red[NORM_WAVES];
-  const long long r0 = (long long)blockIdx.x * a.H;
-  const float mean = a.rms ? 0.f : a.mean[blockIdx.x], rstd = a.rstd[blockIdx.x];
-  float s1 = 0.f, s2 = 0.f;
-  for (int i = threadIdx.x; i < a.H; i += NORM_NT) {
-    const float g = norm_load<T>(a.dy, r0 + i) * a.w[i];
-    s1 += g;
-    s2 += g * ((norm_load<T>(a.h, r0 + i) - mean) * rstd);
-  }
-  s1 = a.rms ? 0.f : block_sum(s1, red) / a.H;
-  s2 = block_sum(s2, red) / a.H;
-  for (int i = threadIdx.x; i < a.H; i += NORM_NT) {
-    const float g = norm_load<T>(a.dy, r0 + i) * a.w[i];
-    const float q = (norm_load<T>(a.h, r0 + i) - mean) * rstd;
-    float v = rstd * (g - s1 - q * s2);
-    if (a.dh) v += norm_load<T>(a.dh, r0 + i);
-    norm_store<T>(a.dx, r0 + i, v);
-  }
+int norm_launch(const NormArgs& a, Shape s, hipStream_t st) {
+  const dim3 grid(norm_blocks(a.M, s));
+#define X(P, N, TH)                                                                        \
+  if constexpr (P * N * Elem<T>::VEC <= NORM_MAX_H)                                        \
+    if (s.tpr == P && s.c == N)                                                            \
+      hipLaunchKernelGGL((norm_kernel<T, P, N, TH>), grid, dim3(TH), 0, st, a);
+  NORM_SHAPES(X)
+#undef X
+  return moe_check_launch("moe_norm");
 }
-
 template <typename T>
-__global__ __launch_bounds__(NORM_NT) void norm_dw_kernel(NormBwdArgs a) {
-  const int c = blockIdx.x * NORM_NT + threadIdx.x;
-  if (c >= a.H) return;
-  float dw = 0.f, db = 0.f;
-  for (int r = blockIdx.y; r < a.M; r += gridDim.y) {
-    const float d = norm_load<T>(a.dy, (long long)r * a.H + c);
-    const float m = a.rms ? 0.f : a.mean[r];
-    dw += d * ((norm_load<T>(a.h, (long long)r * a.H + c) - m) * a.rstd[r]);
-    db += d;
-  }
-  a.part[(long long)blockIdx.y * 2 * a.H + c] = dw;
-  a.part[((long long)blockIdx.y * 2 + 1) * a.H + c] = db;
+int norm_bwd_launch(const NormBwdArgs& a, Shape s, hipStream_t st) {
+  const dim3 grid(a.parts);
+#define X(P, N, TH)                                                                        \
+  if constexpr (P * N * Elem<T>::VEC <= NORM_MAX_H)                                        \
+    if (s.tpr == P && s.c == N)                                                            \
+      hipLaunchKernelGGL((norm_bwd_kernel<T, P, N, TH>), grid, dim3(TH), 0, st, a);
+  NORM_BWD_SHAPES(X)
+#undef X
+  return moe_check_launch("moe_norm_bwd");
 }
 
-__global__ __launch_bounds__(NORM_NT) void norm_dw_sum_kernel(NormBwdArgs a) {
-  const int c = blockIdx.x * NORM_NT + threadIdx.x;
-  if (c >= a.H) return;
-  double dw = 0, db = 0;
-  for (int p = 0; p < a.parts; ++p) {
-    dw += a.part[(long long)p * 2 * a.H + c];
-    db += a.part[((long long)p * 2 + 1) * a.H + c];
-  }
-  if (a.dw) a.dw[c] = (float)dw;
-  if (a.db) a.db[c] = (float)db;
-}
-
-int norm_parts(int M) { return M < NORM_PARTS ? M : NORM_PARTS; }
+// Rows beyond what the 256 MB memory-side cache holds are read with the
+// streaming policy.
+bool norm_streams(long long bytes) { return bytes > (256LL << 20); }
 
 int norm_checks(const char* fn, int dt, int M, int H, int kind) {
   MOE_TRY(moe_need_dt(dt, fn));
@@ -190,18 +474,16 @@ extern "C" int moe_norm(const void* x, const void* residual, int dt, int M, int 
     return moe_fail(MOE_ERR_INVALID_ARG,
                     "%s: %s overlaps %s (h alone may be x's or the residual's buffer)", fn, out,
                     with);
-  NormArgs a = {x, residual, w, bias, h, y, mean, rstd, M, H, kind == MOE_NORM_RMS, eps};
+  NormArgs a = {x, residual, w, bias, h, y, mean, rstd, M, H, kind == MOE_NORM_RMS,
+                norm_streams(mh * (residual ? 2 : 1)), eps, 1.0f / H};
   hipStream_t s = (hipStream_t)stream;
-  if (dt == MOE_BF16)
-    hipLaunchKernelGGL(norm_kernel<bf16_t>, dim3(M), dim3(NORM_NT), 0, s, a);
-  else
-    hipLaunchKernelGGL(norm_kernel<float>, dim3(M), dim3(NORM_NT), 0, s, a);
-  return moe_check_launch(fn);
+  const Shape shape = norm_shape(H * moe_dt_bytes(dt) / 16, residual != nullptr);
+  return dt == MOE_BF16 ? norm_launch<bf16_t>(a, shape, s) : norm_launch<float>(a, shape, s);
 }
 
 extern "C" size_t moe_norm_bwd_workspace_bytes(int M, int H, int dt) {
   if (norm_checks("moe_norm_bwd_workspace_bytes", dt, M, H, MOE_NORM_LAYER) != MOE_OK) return 0;
-  return ((size_t)norm_parts(M) * 2 * H * 4 + 255) / 256 * 256;
+  return ((size_t)norm_parts(M, H, dt) * 2 * H * 4 + 255) / 256 * 256;
 }
 
 extern "C" int moe_norm_bwd(const void* dy, const void* h, const void* dh, int dt, int M, int H,
@@ -244,26 +526,16 @@ extern "C" int moe_norm_bwd(const void* dy, const void* h, const void* dh, int d
       return moe_fail(MOE_ERR_INVALID_ARG, "%s: %s overlaps %s (dx alone may be dh's buffer)", fn,
                       outs[i].name, with);
   }
-  NormBwdArgs a = {dy, h, dh, w, mean, rstd, dx, dw, db, (float*)ws, M, H, kind == MOE_NORM_RMS,
-                   norm_parts(M)};
+  NormBwdArgs a = {dy, h, dh, w, mean, rstd, dx, dw, db, sums ? (float*)ws : nullptr, M, H,
+                   kind == MOE_NORM_RMS, norm_streams(2 * mh), norm_parts(M, H, dt), 1.0f / H};
   hipStream_t s = (hipStream_t)stream;
-  const int cols = (H + NORM_NT - 1) / NORM_NT;
-  if (M > 0 && sums) {
-    const dim3 grid(cols, a.parts);
-    if (dt == MOE_BF16)
-      hipLaunchKernelGGL(norm_dw_kernel<bf16_t>, grid, dim3(NORM_NT), 0, s, a);
-    else
-      hipLaunchKernelGGL(norm_dw_kernel<float>, grid, dim3(NORM_NT), 0, s, a);
-    MOE_TRY(moe_check_launch(fn));
+  if (M > 0 && (dx != nullptr || sums)) {
+    const Shape shape = norm_bwd_shape(H * moe_dt_bytes(dt) / 16);
+    MOE_TRY(dt == MOE_BF16 ? norm_bwd_launch<bf16_t>(a, shape, s)
+                           : norm_bwd_launch<float>(a, shape, s));
   }
-  if (sums) {
-    hipLaunchKernelGGL(norm_dw_sum_kernel, dim3(cols), dim3(NORM_NT), 0, s, a);
-    MOE_TRY(moe_check_launch(fn));
-  }
-  if (M == 0 || dx == nullptr) return MOE_OK;
-  if (dt == MOE_BF16)
-    hipLaunchKernelGGL(norm_dx_kernel<bf16_t>, dim3(M), dim3(NORM_NT), 0, s, a);
-  else
-    hipLaunchKernelGGL(norm_dx_kernel<float>, dim3(M), dim3(NORM_NT), 0, s, a);
+  if (!sums) return MOE_OK;
+  hipLaunchKernelGGL(norm_sum_kernel, dim3((2 * H + SUM_COLS - 1) / SUM_COLS),
+                     dim3(SUM_COLS * SUM_ROWS), 0, s, a);
   return moe_check_launch(fn);
 }

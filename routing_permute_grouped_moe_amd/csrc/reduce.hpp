@@ -1,0 +1,40 @@
+// Sums over lanes on the vector ALU alone: a shuffle goes through LDS and takes
+// some 60 cycles a step, a DPP or permlane step a few.
+#pragma once
+
+#include "common.hpp"
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xf,
+                                                               0xf, true));
+}
+// v of the lane 32 (16) away, added: the swap leaves a half's (row's) values in both.
+__device__ __forceinline__ float add_swap32(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float add_swap16(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// The sum over each N lanes in a row (8, 16, 32 or 64), in all of them.  For 64
+// the pairs are those of wave_sum, so the bits are the same.
+template <int N>
+__device__ __forceinline__ float lanes_sum(float v) {
+  static_assert(N == 8 || N == 16 || N == 32 || N == 64, "lanes");
+  if constexpr (N == 8) {
+    v += dpp<0x141>(v);               // row_half_mirror
+    v += dpp<0x4e>(v);                // quad_perm 2 3 0 1
+    v += dpp<0xb1>(v);                // quad_perm 1 0 3 2
+  } else {
+    if constexpr (N == 64) v = add_swap32(v);
+    if constexpr (N >= 32) v = add_swap16(v);
+    v += dpp<0x128>(v);               // row_ror 8, 4, 2, 1
+    v += dpp<0x124>(v);
+    v += dpp<0x122>(v);
+    v += dpp<0x121>(v);
+  }
+  return v;
+}
