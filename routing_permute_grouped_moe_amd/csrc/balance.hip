@@ -10,40 +10,52 @@
 // sequence's rows add up to is summed in fp64 in the order of the blocks, so the
 // bits are the same on every run.  Block b's row for sequence s is b + s: along
 // the tokens b and s only grow and one of them grows from row to row, so the rows
-// are distinct and at most blocks + S.
+// are distinct and at most blocks + S.  Few tokens are one block, which leaves
+// the outputs themselves.
+#include "reduce.hpp"
 #include "validate.hpp"
 
 namespace {
 
-constexpr int BAL_WAVES = 4;
-constexpr int BAL_NT = BAL_WAVES * MOE_WAVE;
+constexpr int BAL_NT = 1024;                  // forward
+constexpr int BAL_WAVES = BAL_NT / MOE_WAVE;
+constexpr int BAL_BWD_NT = 256;
 constexpr int BAL_MAX_S = 65535;              // sequences: a grid's second dimension
+constexpr uint32_t BAL_OOB = 0xffffffffu;     // past every tensor: reads zeros
 
-int bal_block_tokens(int T) {
-  const int most = 512;                       // blocks
-  int tb = BAL_WAVES;
-  while (((long long)T + tb - 1) / tb > most) tb *= 2;
-  return tb;
-}
-int bal_blocks(int T) {
-  const int tb = bal_block_tokens(T);
-  return (int)(((long long)T + tb - 1) / tb);
-}
+// Lanes of a token: a wave has one of many experts, or several of few.
+int bal_lanes(int E) { return E <= 16 ? 16 : E <= 32 ? 32 : 64; }
 int bal_width(int E) {
   int v = 1;
   while (v * MOE_WAVE < E) v *= 2;
   return v;
 }
+// Tokens of a block: at most 256 blocks, one for each CU, of whole rounds of its waves.
+int bal_block_tokens(int T, int E) {
+  const int round = BAL_NT / bal_lanes(E);
+  if (T <= 4 * round) return T > 0 ? T : 1;
+  const long long per = ((long long)T + 255) / 256;
+  return (int)((per + round - 1) / round * round);
+}
+int bal_blocks(int T, int E) {
+  const int tb = bal_block_tokens(T, E);
+  return T > 0 ? (int)(((long long)T + tb - 1) / tb) : 1;
+}
+bool bal_one(int T, int E, int S) { return bal_blocks(T, E) == 1 && S <= 16; }
 
 struct BalWs {
   size_t q, c, z, n, term, total;
 };
 BalWs bal_ws(int T, int E, int S) {
-  const size_t rows = (size_t)bal_blocks(T) + S, cg = (E + MOE_WAVE - 1) / MOE_WAVE;
-  BalWs w;
+  BalWs w = {};
+  if (bal_one(T, E, S)) {
+    w.total = 256;
+    return w;
+  }
+  const size_t rows = (size_t)bal_blocks(T, E) + S, cg = (E + MOE_WAVE - 1) / MOE_WAVE;
   auto up = [](size_t b) { return (b + 255) / 256 * 256; };
-  w.q = 0;
-  w.c = up(rows * E * 4);
+  w.q = 256;                                  // (in front: the count of workgroups that are done)
+  w.c = w.q + up(rows * E * 4);
   w.z = w.c + up(rows * E * 4);
   w.n = w.z + up(rows * 8);
   w.term = w.n + up(rows * 4);
@@ -53,8 +65,8 @@ BalWs bal_ws(int T, int E, int S) {
 
 struct BalArgs {
   const float* logits; const int32_t* idx; const uint8_t* keep; const int32_t* seq;
-  int T, E, k, S, tb;
-  float* q; int32_t* c; double* z; int32_t* n; double* term;
+  int T, E, k, S, tb, one;
+  int* done; float* q; int32_t* c; double* z; int32_t* n; double* term;
   float w_balance, w_z;
   float* loss; int32_t* counts; int32_t* tokens; float* prob;
 };
@@ -68,62 +80,81 @@ __device__ __forceinline__ double wave_sum64(double v) {
   for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, MOE_WAVE);
   return v;
 }
+__device__ __forceinline__ int wave_sum_int(int v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, MOE_WAVE);
+  return v;
+}
 
-// First sequence that ends behind token t (S if none does).
+// First sequence that ends behind token t (S if none does), by a whole wave: 64
+// ends at a time cut the range to a 64th, so that 64 sequences take one trip to
+// memory where halving takes six.
 __device__ __forceinline__ int bal_first(const int32_t* seq, int S, int T, int t) {
-  int lo = 0, hi = S;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (bal_seq(seq, mid + 1, T) > t) hi = mid; else lo = mid + 1;
+  const int lane = threadIdx.x % MOE_WAVE;
+  int lo = 0, len = S;                        // it is in [lo, lo + len]
+  while (len > 0) {
+    const int step = (len + MOE_WAVE - 1) / MOE_WAVE;
+    const int at = lo + (lane + 1) * step - 1;   // the last of the lane's run
+    const bool before = at < lo + len && bal_seq(seq, at + 1, T) <= t;
+    const int runs = __popcll(__ballot(before));
+    const int from = runs * step;             // runs that end before t are behind us
+    lo += from;
+    len = len - from < step - 1 ? len - from : step - 1;
   }
   return lo;
 }
 
-// One row's softmax: v <- exp(v - max), its sum's reciprocal (0 for a row of -inf
-// alone) and the log of the sum; whether one logit is not -inf.
-template <int V>
-__device__ __forceinline__ bool bal_softmax(const float* row, int E, float (&v)[V], float& inv,
-                                            float& lse) {
-  const int lane = threadIdx.x % MOE_WAVE;
+// A token's softmax over its lanes: v <- exp(v - max), the reciprocal of their
+// sum (0 where all logits are -inf) and the sum's log; whether one is not -inf.
+// (A NaN or +inf among them makes the sum NaN.)
+template <int TPR, int V>
+__device__ __forceinline__ bool bal_softmax(float (&v)[V], int E, float& inv, float& lse) {
+  const int lane = threadIdx.x % TPR;
   float m = -INFINITY;
-  bool some = false;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int e = lane + i * MOE_WAVE;
-    v[i] = e < E ? row[e] : -INFINITY;
-    some |= !(v[i] == -INFINITY);     // (a NaN is one)
+    v[i] = lane + i * TPR < E ? v[i] : -INFINITY;
     m = fmaxf(m, v[i]);
   }
-  some = __ballot(some) != 0;
-  m = some ? wave_max(m) : 0.f;
+  m = lanes_max<TPR>(m);
+  m = m == -INFINITY ? 0.f : m;
   float s = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    v[i] = lane + i * MOE_WAVE < E ? expf(v[i] - m) : 0.f;
+    v[i] = lane + i * TPR < E ? expf(v[i] - m) : 0.f;
     s += v[i];
   }
-  s = wave_sum(s);
+  s = lanes_sum<TPR>(s);
+  const bool some = !(s == 0.f);
   inv = some ? 1.0f / s : 0.f;
   lse = m + logf(s);
   return some;
 }
 
-template <int V>
+template <int TPR, int V>
 __global__ __launch_bounds__(BAL_NT) void balance_part_kernel(BalArgs a) {
-  __shared__ float q_s[BAL_WAVES][V * MOE_WAVE];
-  __shared__ int c_s[V * MOE_WAVE];
+  constexpr int G = BAL_NT / TPR;             // tokens at a time
+  constexpr int U = V >= 16 ? 1 : V >= 8 ? 2 : 4;
+  __shared__ float q_s[BAL_WAVES][V * TPR];
+  __shared__ int c_s[V * TPR];
   __shared__ double z_s[BAL_WAVES];
   __shared__ int n_s[BAL_WAVES];
-  const int lane = threadIdx.x % MOE_WAVE, wave = threadIdx.x / MOE_WAVE;
+  const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+  const int wave = uniform((int)(threadIdx.x / MOE_WAVE));
   const int E = a.E, b = blockIdx.x;
   const int t0 = b * a.tb, t1 = a.T - t0 < a.tb ? a.T : t0 + a.tb;
-  int s = a.seq ? bal_first(a.seq, a.S, a.T, t0) : 0;
+  const auto rl = make_rsrc(a.logits, clamp_bytes(4LL * a.T * E));
+  const auto ri = make_rsrc(a.idx, clamp_bytes(4LL * a.T * a.k));
+  if (b == 0 && threadIdx.x == 0 && !a.one) *a.done = 0;
+  double all_b = 0, all_z = 0;                // (one block: the losses)
+  int all_n = 0;
+  int s = a.one || !a.seq ? 0 : uniform(bal_first(a.seq, a.S, a.T, t0));
   for (; s < a.S; ++s) {
     int lo = a.seq ? bal_seq(a.seq, s, a.T) : 0, hi = a.seq ? bal_seq(a.seq, s + 1, a.T) : a.T;
-    if (lo >= t1) break;
+    if (lo >= t1 && !a.one) break;
     lo = lo < t0 ? t0 : lo;
     hi = hi > t1 ? t1 : hi;
-    if (lo >= hi) continue;
+    if (lo >= hi && !a.one) continue;
     for (int e = threadIdx.x; e < E; e += BAL_NT) c_s[e] = 0;
     __syncthreads();
     float acc[V];
@@ -131,110 +162,169 @@ __global__ __launch_bounds__(BAL_NT) void balance_part_kernel(BalArgs a) {
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
     double z = 0;
     int n = 0;
-    for (int t = lo + wave; t < hi; t += BAL_WAVES) {
-      if (a.keep && a.keep[t] == 0) continue;
-      float v[V], inv, lse;
-      if (!bal_softmax<V>(a.logits + (long long)t * E, E, v, inv, lse)) continue;
+    for (int base = lo; base < hi; base += G * U) {
+      float v[U][V];
+      int e0[U];
+      bool use[U];
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] += v[i] * inv;
-      z += (double)lse * lse;
-      ++n;
-      for (int j = lane; j < a.k; j += MOE_WAVE) {
-        const int e = a.idx[(long long)t * a.k + j];
-        if (e >= 0 && e < E) atomicAdd(&c_s[e], 1);
+      for (int u = 0; u < U; ++u) {
+        const int t = base + u * G + grp;
+        use[u] = t < hi && (!a.keep || a.keep[t] != 0);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int e = lane + i * TPR;
+          v[u][i] = __uint_as_float(
+              buf_load4(rl, use[u] && e < E ? ((uint32_t)t * (uint32_t)E + e) * 4u : BAL_OOB));
+        }
+        e0[u] = (int)buf_load4(
+            ri, use[u] && lane < a.k ? ((uint32_t)t * (uint32_t)a.k + lane) * 4u : BAL_OOB);
+        e0[u] = lane < a.k ? e0[u] : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float inv, lse;
+        use[u] = bal_softmax<TPR, V>(v[u], E, inv, lse) && use[u];
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] += use[u] ? v[u][i] * inv : 0.f;
+        z += use[u] ? (double)lse * lse : 0.0;
+        n += use[u];
+        if (use[u]) {
+          if (e0[u] >= 0 && e0[u] < E) atomicAdd(&c_s[e0[u]], 1);
+          const long long t = base + u * G + grp;
+          for (int j = lane + TPR; j < a.k; j += TPR) {
+            const int e = a.idx[t * a.k + j];
+            if (e >= 0 && e < E) atomicAdd(&c_s[e], 1);
+          }
+        }
       }
     }
+    // the tokens of a wave, then the waves
+    if constexpr (TPR < MOE_WAVE)
 #pragma unroll
-    for (int i = 0; i < V; ++i) q_s[wave][lane + i * MOE_WAVE] = acc[i];
-    if (lane == 0) { z_s[wave] = z; n_s[wave] = n; }
+      for (int o = TPR; o < MOE_WAVE; o *= 2) acc[0] += __shfl_xor(acc[0], o, MOE_WAVE);
+#pragma unroll
+    for (int i = 0; i < V; ++i) q_s[wave][lane + i * TPR] = acc[i];
+    z = wave_sum64(lane == 0 ? z : 0.0);
+    n = wave_sum_int(lane == 0 ? n : 0);
+    if (threadIdx.x % MOE_WAVE == 0) { z_s[wave] = z; n_s[wave] = n; }
     __syncthreads();
-    const long long row = b + s;
+    z = 0, n = 0;
+#pragma unroll
+    for (int w = 0; w < BAL_WAVES; ++w) { z += z_s[w]; n += n_s[w]; }
+    const long long row = a.one ? s : b + s;
+    double part = 0;
     for (int e = threadIdx.x; e < E; e += BAL_NT) {
       float q = 0.f;
 #pragma unroll
       for (int w = 0; w < BAL_WAVES; ++w) q += q_s[w][e];
-      a.q[row * E + e] = q;
-      a.c[row * E + e] = c_s[e];
+      const int c = c_s[e];
+      if (a.one) {
+        a.counts[row * E + e] = c;
+        if (a.prob) a.prob[row * E + e] = n > 0 ? (float)((double)q / n) : 0.f;
+        if (n > 0) part += (double)c * q / n;
+      } else {
+        a.q[row * E + e] = q;
+        a.c[row * E + e] = c;
+      }
     }
-    if (threadIdx.x == 0) {
-      double zz = 0;
-      int nn = 0;
-#pragma unroll
-      for (int w = 0; w < BAL_WAVES; ++w) { zz += z_s[w]; nn += n_s[w]; }
-      a.z[row] = zz;
-      a.n[row] = nn;
+    if (a.one) {
+      all_b += part;
+      all_z += z;
+      all_n += n;
+      if (threadIdx.x == 0) a.tokens[s] = n;
+    } else if (threadIdx.x == 0) {
+      a.z[row] = z;
+      a.n[row] = n;
     }
     __syncthreads();
   }
+  if (!a.one) return;
+  all_b = wave_sum64(all_b);
+  if (threadIdx.x % MOE_WAVE == 0) z_s[wave] = all_b;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  all_b = 0;
+#pragma unroll
+  for (int w = 0; w < BAL_WAVES; ++w) all_b += z_s[w];
+  const double d = all_n > 0 ? all_n : 1;
+  all_b *= a.E / (a.k * d);
+  all_z /= d;
+  a.loss[0] = (float)all_b;
+  a.loss[1] = (float)all_z;
+  a.loss[2] = (float)(a.w_balance * all_b + a.w_z * all_z);
+  a.tokens[a.S] = all_n;
 }
 
 // Rows of a sequence: counts, probabilities and its part of the losses, 64
-// experts a workgroup, a quarter of the rows a wave.
+// experts a workgroup, a 16th of the rows a wave.  The workgroup that is done
+// last adds the parts, in their order.
 __global__ __launch_bounds__(BAL_NT) void balance_sum_kernel(BalArgs a) {
-  __shared__ double q_s[BAL_WAVES][MOE_WAVE], z_s[BAL_WAVES];
-  __shared__ int c_s[BAL_WAVES][MOE_WAVE], n_s[BAL_WAVES];
+  __shared__ double q_s[BAL_WAVES][MOE_WAVE], z_s[BAL_WAVES], b_s[BAL_WAVES];
+  __shared__ int c_s[BAL_WAVES][MOE_WAVE];
+  __shared__ long long n_s[BAL_WAVES];
+  __shared__ int last;
   const int lane = threadIdx.x % MOE_WAVE, wave = threadIdx.x / MOE_WAVE;
-  const int s = blockIdx.y, E = a.E, e = blockIdx.x * MOE_WAVE + lane;
+  const int s = blockIdx.y, E = a.E, e = blockIdx.x * MOE_WAVE + lane, cg = gridDim.x;
   const int lo = a.seq ? bal_seq(a.seq, s, a.T) : 0, hi = a.seq ? bal_seq(a.seq, s + 1, a.T) : a.T;
   const int b0 = lo / a.tb, b1 = lo < hi ? (hi - 1) / a.tb + 1 : b0;
   double q = 0, z = 0;
-  int c = 0, n = 0;
-  for (int b = b0 + wave; b < b1; b += BAL_WAVES) {
-    const long long row = b + s;
-    if (e < E) {
-      q += a.q[row * E + e];
-      c += a.c[row * E + e];
+  int c = 0;
+  long long n = 0;
+  if (e < E)
+#pragma unroll 4
+    for (int b = b0 + wave; b < b1; b += BAL_WAVES) {
+      const long long at = (long long)(b + s) * E + e;
+      q += a.q[at];
+      c += a.c[at];
     }
-  }
   for (int b = b0 + threadIdx.x; b < b1; b += BAL_NT) {
     z += a.z[b + s];
     n += a.n[b + s];
   }
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) n += __shfl_xor(n, o, MOE_WAVE);
   z = wave_sum64(z);
+  n = wave_sum_int((int)n);
   q_s[wave][lane] = q;
   c_s[wave][lane] = c;
   if (lane == 0) { z_s[wave] = z; n_s[wave] = n; }
   __syncthreads();
-  if (wave != 0) return;
-  q = 0, z = 0, c = 0, n = 0;
+  if (wave == 0) {
+    q = 0, z = 0, c = 0, n = 0;
 #pragma unroll
-  for (int w = 0; w < BAL_WAVES; ++w) {
-    q += q_s[w][lane];
-    c += c_s[w][lane];
-    z += z_s[w];
-    n += n_s[w];
-  }
-  if (e < E) {
-    a.counts[(long long)s * E + e] = c;
-    if (a.prob) a.prob[(long long)s * E + e] = n > 0 ? (float)(q / n) : 0.f;
-  }
-  const double part = wave_sum64(e < E && n > 0 ? c * q / n : 0.0);
-  if (lane == 0) {
-    a.term[(long long)s * gridDim.x + blockIdx.x] = part;
-    if (blockIdx.x == 0) {
-      a.term[(long long)a.S * gridDim.x + s] = z;
-      a.tokens[s] = n;
+    for (int w = 0; w < BAL_WAVES; ++w) {
+      q += q_s[w][lane];
+      c += c_s[w][lane];
+      z += z_s[w];
+      n += n_s[w];
+    }
+    if (e < E) {
+      a.counts[(long long)s * E + e] = c;
+      if (a.prob) a.prob[(long long)s * E + e] = n > 0 ? (float)(q / n) : 0.f;
+    }
+    const double part = wave_sum64(e < E && n > 0 ? c * q / n : 0.0);
+    if (lane == 0) {
+      a.term[(long long)s * cg + blockIdx.x] = part;
+      if (blockIdx.x == 0) {
+        a.term[(long long)a.S * cg + s] = z;
+        a.tokens[s] = (int)n;
+      }
+      // what this workgroup wrote is seen by whoever sees the count
+      last = __hip_atomic_fetch_add(a.done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+             cg * a.S - 1;
     }
   }
-}
-
-__global__ __launch_bounds__(BAL_NT) void balance_loss_kernel(BalArgs a, int cg) {
-  __shared__ double b_s[BAL_WAVES], z_s[BAL_WAVES];
-  __shared__ long long n_s[BAL_WAVES];
-  const int lane = threadIdx.x % MOE_WAVE, wave = threadIdx.x / MOE_WAVE;
-  double b = 0, z = 0;
-  long long n = 0;
+  __syncthreads();
+  if (!last) return;
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+  double b = 0;
+  z = 0, n = 0;
   for (long long i = threadIdx.x; i < (long long)a.S * cg; i += BAL_NT) b += a.term[i];
-  for (int s = threadIdx.x; s < a.S; s += BAL_NT) {
-    z += a.term[(long long)a.S * cg + s];
-    n += a.tokens[s];
+  for (int i = threadIdx.x; i < a.S; i += BAL_NT) {
+    z += a.term[(long long)a.S * cg + i];
+    n += a.tokens[i];
   }
   b = wave_sum64(b);
   z = wave_sum64(z);
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) n += __shfl_xor(n, o, MOE_WAVE);
+  n = wave_sum_int((int)n);
   if (lane == 0) { b_s[wave] = b; z_s[wave] = z; n_s[wave] = n; }
   __syncthreads();
   if (threadIdx.x != 0) return;
@@ -242,8 +332,8 @@ __global__ __launch_bounds__(BAL_NT) void balance_loss_kernel(BalArgs a, int cg)
 #pragma unroll
   for (int w = 0; w < BAL_WAVES; ++w) { b += b_s[w]; z += z_s[w]; n += n_s[w]; }
   const double d = n > 0 ? (double)n : 1.0;
-  b = b * a.E / (a.k * d);
-  z = z / d;
+  b *= a.E / (a.k * d);
+  z /= d;
   a.loss[0] = (float)b;
   a.loss[1] = (float)z;
   a.loss[2] = (float)(a.w_balance * b + a.w_z * z);
@@ -258,67 +348,89 @@ struct BalBwd {
   float* dlogits;
 };
 
-template <int V>
-__global__ __launch_bounds__(BAL_NT) void balance_bwd_kernel(BalBwd a) {
-  __shared__ float dp_s[BAL_WAVES][V * MOE_WAVE];
-  const int lane = threadIdx.x % MOE_WAVE, wave = threadIdx.x / MOE_WAVE, E = a.E;
-  const int t = blockIdx.x * BAL_WAVES + wave;
-  if (t >= a.T) return;  // whole wave leaves together; no block barrier below
-  float* dp = dp_s[wave];
-  if (a.dgate) {
+template <int TPR, int V>
+__global__ __launch_bounds__(BAL_BWD_NT) void balance_bwd_kernel(BalBwd a) {
+  constexpr int G = BAL_BWD_NT / TPR;
+  __shared__ float dp_s[G][V * TPR];
+  const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR, E = a.E;
+  const int t = blockIdx.x * G + grp;
+  const bool in = t < a.T;                    // (lanes past the end go along with their wave)
+  const auto rl = make_rsrc(a.logits, clamp_bytes(4LL * a.T * E));
+  float v[V], g[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) dp[lane + i * MOE_WAVE] = 0.f;
-    __builtin_amdgcn_s_waitcnt(0);
-    __builtin_amdgcn_wave_barrier();
-    // chosen experts of a token are distinct, so these writes never collide
-    for (int j = lane; j < a.k; j += MOE_WAVE) {
-      const int e = a.idx[(long long)t * a.k + j];
-      if (e >= 0 && e < E) dp[e] = a.dgate[(long long)t * a.k + j];
-    }
-    __builtin_amdgcn_s_waitcnt(0);
-    __builtin_amdgcn_wave_barrier();
+  for (int i = 0; i < V; ++i) {
+    const int e = lane + i * TPR;
+    v[i] = __uint_as_float(
+        buf_load4(rl, in && e < E ? ((uint32_t)t * (uint32_t)E + e) * 4u : BAL_OOB));
   }
-  float v[V], inv, lse;
-  bool counts = bal_softmax<V>(a.logits + (long long)t * E, E, v, inv, lse);
-  if (a.keep && a.keep[t] == 0) counts = false;
+  bool counts = in && !(a.keep && a.keep[t] == 0);
   int s = 0;
   if (a.seq) {
-    s = bal_first(a.seq, a.S, a.T, t);
+#pragma unroll
+    for (int j = 0; j < MOE_WAVE / TPR; ++j) {   // the tokens of a wave
+      const int of = bal_first(a.seq, a.S, a.T, __builtin_amdgcn_readlane(t, j * TPR));
+      s = (int)(threadIdx.x % MOE_WAVE) / TPR == j ? of : s;
+    }
     counts = counts && s < a.S && bal_seq(a.seq, s, a.T) <= t;
+    s = s < a.S ? s : 0;
   }
   float fs = 0.f, zs = 0.f;
-  if (counts) {
+  {
     const float dl = a.dloss ? a.dloss[0] : 1.f;
     const int N = a.tokens[a.S], n = a.tokens[s];
     const float per = dl / (float)(N > 0 ? N : 1);
     fs = a.w_balance * per * ((float)E / ((float)a.k * (float)(n > 0 ? n : 1)));
-    zs = 2.f * a.w_z * per * lse;
+    zs = 2.f * a.w_z * per;
   }
-  const int32_t* c = a.counts + (long long)(counts ? s : 0) * E;
-  float g[V], acc = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int e = lane + i * MOE_WAVE;
-    g[i] = counts && e < E ? fs * (float)c[e] : 0.f;
-    if (a.dgate) g[i] += dp[e];
-    acc += v[i] * inv * g[i];
+    const int e = lane + i * TPR;
+    g[i] = counts && e < E ? fs * (float)a.counts[(long long)s * E + e] : 0.f;
   }
-  acc = wave_sum(acc);
+  if (a.dgate) {
+    float* const dp = dp_s[grp];
+#pragma unroll
+    for (int i = 0; i < V; ++i) dp[lane + i * TPR] = 0.f;
+    __builtin_amdgcn_s_waitcnt(0xc07f);       // (LDS alone)
+    __builtin_amdgcn_wave_barrier();
+    // chosen experts of a token are distinct, so these writes never collide
+    for (int j = lane; j < a.k; j += TPR) {
+      const long long at = (long long)t * a.k + j;
+      const int e = in ? a.idx[at] : -1;
+      if (e >= 0 && e < E) dp[e] = a.dgate[at];
+    }
+    __builtin_amdgcn_s_waitcnt(0xc07f);
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < V; ++i) g[i] += dp[lane + i * TPR];
+  }
+  float inv, lse;
+  const bool some = bal_softmax<TPR, V>(v, E, inv, lse);
+  if (!(counts && some)) {
+    zs = 0.f;
+  } else {
+    zs *= lse;
+  }
+  float acc = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc += v[i] * inv * g[i];
+  acc = lanes_sum<TPR>(acc);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int e = lane + i * MOE_WAVE;
-    if (e < E) a.dlogits[(long long)t * E + e] = v[i] * inv * (g[i] - acc + zs);
+    const int e = lane + i * TPR;
+    if (in && e < E) a.dlogits[(long long)t * E + e] = v[i] * inv * (g[i] - acc + zs);
   }
 }
 
-template <int V>
+template <int TPR, int V>
 void launch_part(const BalArgs& a, int blocks, hipStream_t s) {
-  hipLaunchKernelGGL(balance_part_kernel<V>, dim3(blocks), dim3(BAL_NT), 0, s, a);
+  hipLaunchKernelGGL((balance_part_kernel<TPR, V>), dim3(blocks), dim3(BAL_NT), 0, s, a);
 }
-template <int V>
+template <int TPR, int V>
 void launch_bwd(const BalBwd& a, hipStream_t s) {
-  hipLaunchKernelGGL(balance_bwd_kernel<V>, dim3((a.T + BAL_WAVES - 1) / BAL_WAVES), dim3(BAL_NT),
-                     0, s, a);
+  constexpr int G = BAL_BWD_NT / TPR;
+  hipLaunchKernelGGL((balance_bwd_kernel<TPR, V>), dim3((a.T + G - 1) / G), dim3(BAL_BWD_NT), 0, s,
+                     a);
 }
 
 int bal_checks(const char* fn, int T, int E, int k, int S) {
@@ -328,8 +440,8 @@ int bal_checks(const char* fn, int T, int E, int k, int S) {
   if (S > BAL_MAX_S)
     return moe_fail(MOE_ERR_UNSUPPORTED, "%s: S = %d above %d", fn, S, BAL_MAX_S);
   MOE_TRY(moe_need_elems(T, E, 4, fn, "logits"));
-  // (rows of partial sums: at most 512 and one a sequence)
-  MOE_TRY(moe_need_elems((long long)S + 512, E, 4, fn, "counts"));
+  // (rows of partial sums: at most 256 and one a sequence)
+  MOE_TRY(moe_need_elems((long long)S + 256, E, 4, fn, "counts"));
   return MOE_OK;
 }
 
@@ -375,26 +487,26 @@ extern "C" int moe_balance_loss(const float* logits, const int32_t* idx, const u
                       outs[i].name, with);
   }
   char* const w = (char*)ws;
-  BalArgs a = {logits, idx, keep, seq, T, E, k, S, bal_block_tokens(T),
+  const bool one = bal_one(T, E, S);
+  BalArgs a = {logits, idx, keep, seq, T, E, k, S, bal_block_tokens(T, E), one, (int*)w,
                (float*)(w + lay.q), (int32_t*)(w + lay.c), (double*)(w + lay.z),
                (int32_t*)(w + lay.n), (double*)(w + lay.term), w_balance, w_z,
                loss, counts, tokens, prob};
   hipStream_t s = (hipStream_t)stream;
-  const int blocks = bal_blocks(T);
-  if (blocks > 0) {
-    switch (bal_width(E)) {
-      case 1: launch_part<1>(a, blocks, s); break;
-      case 2: launch_part<2>(a, blocks, s); break;
-      case 4: launch_part<4>(a, blocks, s); break;
-      case 8: launch_part<8>(a, blocks, s); break;
-      default: launch_part<16>(a, blocks, s); break;
-    }
-    MOE_TRY(moe_check_launch(fn));
+  const int blocks = bal_blocks(T, E);
+  switch (bal_lanes(E) + bal_width(E)) {
+    case 17: launch_part<16, 1>(a, blocks, s); break;
+    case 33: launch_part<32, 1>(a, blocks, s); break;
+    case 65: launch_part<64, 1>(a, blocks, s); break;
+    case 66: launch_part<64, 2>(a, blocks, s); break;
+    case 68: launch_part<64, 4>(a, blocks, s); break;
+    case 72: launch_part<64, 8>(a, blocks, s); break;
+    default: launch_part<64, 16>(a, blocks, s); break;
   }
-  const int cg = (E + MOE_WAVE - 1) / MOE_WAVE;
-  hipLaunchKernelGGL(balance_sum_kernel, dim3(cg, S), dim3(BAL_NT), 0, s, a);
   MOE_TRY(moe_check_launch(fn));
-  hipLaunchKernelGGL(balance_loss_kernel, dim3(1), dim3(BAL_NT), 0, s, a, cg);
+  if (one) return MOE_OK;
+  hipLaunchKernelGGL(balance_sum_kernel, dim3((E + MOE_WAVE - 1) / MOE_WAVE, S), dim3(BAL_NT), 0, s,
+                     a);
   return moe_check_launch(fn);
 }
 
@@ -432,12 +544,14 @@ extern "C" int moe_balance_loss_bwd(const float* logits, const int32_t* idx, con
   BalBwd a = {logits, idx, dgate, keep, seq, counts, tokens, dloss, T, E, k, S,
               w_balance, w_z, dlogits};
   hipStream_t s = (hipStream_t)stream;
-  switch (bal_width(E)) {
-    case 1: launch_bwd<1>(a, s); break;
-    case 2: launch_bwd<2>(a, s); break;
-    case 4: launch_bwd<4>(a, s); break;
-    case 8: launch_bwd<8>(a, s); break;
-    default: launch_bwd<16>(a, s); break;
+  switch (bal_lanes(E) + bal_width(E)) {
+    case 17: launch_bwd<16, 1>(a, s); break;
+    case 33: launch_bwd<32, 1>(a, s); break;
+    case 65: launch_bwd<64, 1>(a, s); break;
+    case 66: launch_bwd<64, 2>(a, s); break;
+    case 68: launch_bwd<64, 4>(a, s); break;
+    case 72: launch_bwd<64, 8>(a, s); break;
+    default: launch_bwd<64, 16>(a, s); break;
   }
   return moe_check_launch(fn);
 }

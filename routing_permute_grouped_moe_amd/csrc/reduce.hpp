@@ -19,8 +19,17 @@ __device__ __forceinline__ float add_swap16(float v) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// The sum over each N lanes in a row (8, 16, 32 or 64), in all of them.  For 64
-// the pairs are those of wave_sum, so the bits are the same.
+__device__ __forceinline__ float max_swap32(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float max_swap16(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// The sum over each N lanes in a row (8, 16, 32 or 64), in all of them.  From 16
+// on the pairs are those of wave_sum, so the bits are the same.
 template <int N>
 __device__ __forceinline__ float lanes_sum(float v) {
   static_assert(N == 8 || N == 16 || N == 32 || N == 64, "lanes");
@@ -37,4 +46,14 @@ __device__ __forceinline__ float lanes_sum(float v) {
     v += dpp<0x121>(v);
   }
   return v;
+}
+template <int N>
+__device__ __forceinline__ float lanes_max(float v) {
+  static_assert(N == 16 || N == 32 || N == 64, "lanes");
+  if constexpr (N == 64) v = max_swap32(v);
+  if constexpr (N >= 32) v = max_swap16(v);
+  v = fmaxf(v, dpp<0x128>(v));
+  v = fmaxf(v, dpp<0x124>(v));
+  v = fmaxf(v, dpp<0x122>(v));
+  return fmaxf(v, dpp<0x121>(v));
 }
