@@ -4,9 +4,8 @@
 // Gradients are cut into chunks of one length; a workgroup takes one.  Which
 // chunk belongs to which gradient stands in a table that travels with the
 // launch's arguments (no copy to the device, and a captured launch keeps its
-// own); where the gradients are more than a table holds there are several
-// launches.  A chunk's sum is kept in fp64 -- squares of every fp32 value are
-// in its range -- and a second launch adds the chunks in order.
+// own).  A chunk's sum is kept in fp64 -- squares of every fp32 value are in its
+// range -- and a last launch adds the chunks in order.
 #include <algorithm>
 #include <new>
 
@@ -19,13 +18,19 @@ constexpr int CLIP_WAVES = CLIP_NT / MOE_WAVE;
 constexpr int CLIP_SUM_NT = 1024;
 constexpr int NORM_TABLE = 176;      // gradients of one launch: tables below 4 KB
 constexpr int CLIP_TABLE = 128;
-constexpr long long CLIP_CHUNK = 16384;   // elements of a chunk, at least
-constexpr long long CLIP_CHUNKS = 8192;   // chunks, at most, but for one a gradient
+constexpr long long CLIP_CHUNK = 2048;    // elements of a chunk, at least
+// chunks, at most, but for one a gradient: of the norm, of what is scaled
+constexpr long long NORM_CHUNKS = 2048, CLIP_CHUNKS = 8192;
 
 struct NormTable {
   const void* g[NORM_TABLE];
   unsigned long long n[NORM_TABLE];   // elements; top bit: bf16
-  int first[NORM_TABLE + 1];          // first chunk, within this launch
+  int first[NORM_TABLE + 1];          // first chunk
+  int count;
+};
+// The same in memory, of any length.
+struct NormList {
+  const void** g; unsigned long long* n; int* first;
   int count;
 };
 struct ClipTable {
@@ -41,23 +46,51 @@ constexpr unsigned long long G_BF16 = 1ull << 63, OUT_BF16 = 1ull << 62,
 // 16 bytes, aligned to an element only
 typedef unsigned int u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef unsigned int u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
-__device__ __forceinline__ u32x4 load16(const float* p) { return *(const u32x4_a4*)p; }
-__device__ __forceinline__ u32x4 load16(const bf16_t* p) { return *(const u32x4_a2*)p; }
-__device__ __forceinline__ void store16(float* p, u32x4 v) { *(u32x4_a4*)p = v; }
-__device__ __forceinline__ void store16(bf16_t* p, u32x4 v) { *(u32x4_a2*)p = v; }
+typedef unsigned int u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
+// (streaming: read once here, written for whoever comes later)
+__device__ __forceinline__ u32x4 load16(const float* p) {
+  return __builtin_nontemporal_load((const u32x4_a4*)p);
+}
+__device__ __forceinline__ u32x4 load16(const bf16_t* p) {
+  return __builtin_nontemporal_load((const u32x4_a2*)p);
+}
+__device__ __forceinline__ void store16(float* p, u32x4 v) {
+  __builtin_nontemporal_store(v, (u32x4_a4*)p);
+}
+__device__ __forceinline__ void store16(bf16_t* p, u32x4 v) {
+  __builtin_nontemporal_store(v, (u32x4_a2*)p);
+}
+__device__ __forceinline__ void load_vec(const float* p, float (&v)[4]) {
+  unpack16(load16(p), v, float());
+}
+__device__ __forceinline__ void load_vec(const bf16_t* p, float (&v)[8]) {
+  unpack16(load16(p), v, bf16_t());
+}
+__device__ __forceinline__ void load_vec(const bf16_t* p, float (&v)[4]) {
+  const u32x2 x = __builtin_nontemporal_load((const u32x2_a2*)p);
+  v[0] = __uint_as_float(x.x << 16); v[1] = __uint_as_float(x.x & 0xffff0000u);
+  v[2] = __uint_as_float(x.y << 16); v[3] = __uint_as_float(x.y & 0xffff0000u);
+}
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ float load1(const bf16_t* p) { return bf16_to_f32(*p); }
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(bf16_t* p, float v) { *p = (bf16_t)f32_to_bf16(v); }
 
-// The gradient that chunk c belongs to.
-__device__ __forceinline__ int grad_of(const int* first, int count, int c) {
-  int lo = 0, hi = count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (first[mid] <= c) lo = mid; else hi = mid - 1;
+// The gradient that chunk c belongs to: the last whose first chunk is not behind
+// it, by a whole wave, 64 entries at a time.
+template <typename Table>
+__device__ __forceinline__ int grad_of(const Table& t, int c) {
+  const int lane = threadIdx.x % MOE_WAVE;
+  int lo = 0, len = t.count;                  // it is in [lo, lo + len)
+  while (len > 1) {
+    const int step = (len + MOE_WAVE - 1) / MOE_WAVE, at = lane * step;
+    const bool mine = at < len && t.first[lo + at] <= c;
+    int runs = __popcll(__ballot(mine));
+    runs = runs > 0 ? runs - 1 : 0;
+    lo += runs * step;
+    len = len - runs * step < step ? len - runs * step : step;
   }
-  return lo;
+  return uniform(lo);
 }
 
 // (a NaN is larger than any number)
@@ -76,28 +109,51 @@ __device__ __forceinline__ double take(double acc, float v) {
   return MAX ? max_nan(acc, fabs((double)v)) : fma((double)v, (double)v, acc);
 }
 
+// The squares (or the largest) of n values, this thread's part of them: four
+// loads in flight, four chains of additions.
 template <bool MAX, typename T>
 __device__ __forceinline__ double chunk_sum(const T* g, long long n) {
-  constexpr int VEC = Elem<T>::VEC;
-  double acc = 0;
+  constexpr int VEC = Elem<T>::VEC, STEP = CLIP_NT * VEC, U = 4;
+  double acc[U] = {0, 0, 0, 0};
   const long long whole = n / VEC * VEC;
-  for (long long i = (long long)threadIdx.x * VEC; i < whole; i += CLIP_NT * VEC) {
+  long long i = (long long)threadIdx.x * VEC;
+  auto add = [&](double& to, const u32x4& x) {
     float v[VEC];
-    unpack16(load16(g + i), v, T());
+    unpack16(x, v, T());
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) acc = take<MAX>(acc, v[j]);
+    for (int j = 0; j < VEC; ++j) to = take<MAX>(to, v[j]);
+  };
+  for (; i + (U - 1) * STEP < whole; i += U * STEP) {
+    u32x4 x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u] = load16(g + i + u * STEP);
+#pragma unroll
+    for (int u = 0; u < U; ++u) add(acc[u], x[u]);
   }
-  if (whole + threadIdx.x < n) acc = take<MAX>(acc, load1(g + whole + threadIdx.x));
-  return acc;
+  for (; i < whole; i += STEP) add(acc[0], load16(g + i));
+  if (whole + threadIdx.x < n) acc[1] = take<MAX>(acc[1], load1(g + whole + threadIdx.x));
+  return join<MAX>(join<MAX>(acc[0], acc[1]), join<MAX>(acc[2], acc[3]));
 }
 
-template <bool MAX>
-__global__ __launch_bounds__(CLIP_NT) void grad_part_kernel(NormTable t, long long chunk, int base,
-                                                            int grad0, double* part, int* starts) {
+// A table's entries, into memory.
+__global__ __launch_bounds__(CLIP_NT) void grad_table_kernel(NormTable t, int at, NormList to) {
+  const int i = threadIdx.x;
+  if (i < t.count) {
+    to.g[at + i] = t.g[i];
+    to.n[at + i] = t.n[i];
+  }
+  if (i <= t.count) to.first[at + i] = t.first[i];
+}
+static_assert(NORM_TABLE < CLIP_NT, "a thread an entry");
+
+// first: the table's first chunks go there, for the launch that adds the parts.
+template <bool MAX, typename Table>
+__global__ __launch_bounds__(CLIP_NT) void grad_part_kernel(Table t, long long chunk, double* part,
+                                                            int* first) {
   __shared__ double red[CLIP_WAVES];
-  const int c = blockIdx.x, i = grad_of(t.first, t.count, c);
-  if (c == 0)
-    for (int j = threadIdx.x; j <= t.count; j += CLIP_NT) starts[grad0 + j] = base + t.first[j];
+  const int c = blockIdx.x, i = grad_of(t, c);
+  if (first != nullptr && c == 0 && threadIdx.x <= (unsigned)t.count)
+    first[threadIdx.x] = t.first[threadIdx.x];
   const unsigned long long word = t.n[i];
   const long long n = (long long)(word & N_MASK), at = (long long)(c - t.first[i]) * chunk;
   const long long len = n - at < chunk ? n - at : chunk;
@@ -106,26 +162,58 @@ __global__ __launch_bounds__(CLIP_NT) void grad_part_kernel(NormTable t, long lo
   v = wave_join<MAX>(v);
   if (threadIdx.x % MOE_WAVE == 0) red[threadIdx.x / MOE_WAVE] = v;
   __syncthreads();
-  if (threadIdx.x == 0 && c < t.first[t.count]) {
+  if (threadIdx.x == 0 && len > 0) {          // (no chunk: one workgroup, for `first`)
     v = red[0];
 #pragma unroll
     for (int w = 1; w < CLIP_WAVES; ++w) v = join<MAX>(v, red[w]);
-    part[base + c] = v;
+    part[c] = v;
   }
 }
 
+// Chunks of a gradient, and gradients.  A thread adds a gradient of few chunks, a
+// wave one of many: at most NORM_CHUNKS / FEW, since there are at most
+// NORM_CHUNKS chunks and one a gradient.
+constexpr int FEW = 16, MANY = NORM_CHUNKS / (FEW - 1) + 8;
 template <bool MAX>
 __global__ __launch_bounds__(CLIP_SUM_NT) void grad_norm_kernel(const double* part,
-                                                                const int* starts, int count,
+                                                                const int* first, int count,
                                                                 float* norm, float* norms,
                                                                 double* total) {
   constexpr int WAVES = CLIP_SUM_NT / MOE_WAVE;
   __shared__ double red[WAVES];
+  __shared__ int found, list[MANY], sorted[MANY];
   const int lane = threadIdx.x % MOE_WAVE, wave = threadIdx.x / MOE_WAVE;
+  if (threadIdx.x == 0) found = 0;
+  __syncthreads();
   double all = 0;
-  for (int i = wave; i < count; i += WAVES) {
+  for (int i = threadIdx.x; i < count; i += CLIP_SUM_NT) {
+    const int c0 = first[i], c1 = first[i + 1];
+    if (c1 - c0 > FEW) {
+      const int at = atomicAdd(&found, 1);
+      if (at < MANY) list[at] = i;
+      continue;
+    }
     double v = 0;
-    for (int c = starts[i] + lane; c < starts[i + 1]; c += MOE_WAVE) v = join<MAX>(v, part[c]);
+#pragma unroll 4
+    for (int c = c0; c < c1; ++c) v = join<MAX>(v, part[c]);
+    all = join<MAX>(all, v);
+    if (norms) norms[i] = (float)(MAX ? v : sqrt(v));
+  }
+  __syncthreads();
+  const int many = found < MANY ? found : MANY;
+  if (threadIdx.x < many) {                   // in their order, whoever came first
+    const int mine = list[threadIdx.x];
+    int at = 0;
+    for (int j = 0; j < many; ++j) at += list[j] < mine;
+    sorted[at] = mine;
+  }
+  __syncthreads();
+  all = wave_join<MAX>(all);
+  for (int j = wave; j < many; j += WAVES) {
+    const int i = sorted[j], c1 = first[i + 1];
+    double v = 0;
+#pragma unroll 8
+    for (int c = first[i] + lane; c < c1; c += MOE_WAVE) v = join<MAX>(v, part[c]);
     v = wave_join<MAX>(v);
     all = join<MAX>(all, v);
     if (norms && lane == 0) norms[i] = (float)(MAX ? v : sqrt(v));
@@ -141,18 +229,30 @@ __global__ __launch_bounds__(CLIP_SUM_NT) void grad_norm_kernel(const double* pa
   }
 }
 
+// n values times c.  A thread's store is 16 bytes and a wave's 1 KB without
+// gaps, whatever a thread loads for it (425 M values, bf16 to fp32: 485 us, 5.3
+// TB/s; with 32 bytes a thread, whose streaming stores leave gaps, 700).
 template <typename G, typename O>
 __device__ __forceinline__ void scale_chunk(const G* g, O* out, long long n, float c) {
-  constexpr int VEC = 8;
+  constexpr int VEC = Elem<O>::VEC, STEP = CLIP_NT * VEC, U = 4;
   const long long whole = n / VEC * VEC;
-  for (long long i = (long long)threadIdx.x * VEC; i < whole; i += CLIP_NT * VEC) {
-    float v[VEC];
-#pragma unroll
-    for (int j = 0; j < VEC; j += Elem<G>::VEC) unpack16(load16(g + i + j), v + j, G());
+  long long i = (long long)threadIdx.x * VEC;
+  auto put = [&](O* to, float (&v)[VEC]) {
 #pragma unroll
     for (int j = 0; j < VEC; ++j) v[j] *= c;
+    store16(to, pack16(v, O()));
+  };
+  for (; i + (U - 1) * STEP < whole; i += U * STEP) {
+    float v[U][VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; j += Elem<O>::VEC) store16(out + i + j, pack16(v + j, O()));
+    for (int u = 0; u < U; ++u) load_vec(g + i + u * STEP, v[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) put(out + i + u * STEP, v[u]);
+  }
+  for (; i < whole; i += STEP) {
+    float v[VEC];
+    load_vec(g + i, v);
+    put(out + i, v);
   }
   if (whole + threadIdx.x < n)
     store1(out + whole + threadIdx.x, load1(g + whole + threadIdx.x) * c);
@@ -160,7 +260,7 @@ __device__ __forceinline__ void scale_chunk(const G* g, O* out, long long n, flo
 
 __global__ __launch_bounds__(CLIP_NT) void grad_clip_kernel(ClipTable t, long long chunk,
                                                             const float* norm, float max_norm) {
-  const int b = blockIdx.x, i = grad_of(t.first, t.count, b);
+  const int b = blockIdx.x, i = grad_of(t, b);
   float c = max_norm / (norm[0] + 1e-6f);
   c = c > 1.f ? 1.f : c;        // (a NaN stays one)
   if (c == 1.f && t.out[i] == t.g[i]) return;
@@ -176,12 +276,11 @@ __global__ __launch_bounds__(CLIP_NT) void grad_clip_kernel(ClipTable t, long lo
 }
 
 // Elements of a chunk: a whole number of all lanes' loads.
-long long chunk_of(const moe_grad* g, int count) {
+long long chunk_of(const moe_grad* g, int count, long long most) {
   long long n = 0;
   for (int i = 0; i < count; ++i) n += g[i].n;
-  long long c = (n + CLIP_CHUNKS - 1) / CLIP_CHUNKS;
-  c = (c + 2047) / 2048 * 2048;
-  return c < CLIP_CHUNK ? CLIP_CHUNK : c;
+  const long long c = (n + most - 1) / most;
+  return c < CLIP_CHUNK ? CLIP_CHUNK : (c + CLIP_CHUNK - 1) / CLIP_CHUNK * CLIP_CHUNK;
 }
 long long chunks_of(const moe_grad* g, int count, long long chunk) {
   long long c = 0;
@@ -247,10 +346,29 @@ int clip_overlaps(const char* fn, const moe_grad* g, int count) {
 
 }  // namespace
 
+namespace {
+// part [chunks] fp64, first [count + 1], and beyond a table's length g, n [count]
+struct NormWs {
+  long long chunk, chunks;
+  size_t first, g, n, total;
+};
+NormWs norm_ws(const moe_grad* grads, int count) {
+  auto up = [](size_t b) { return (b + 255) / 256 * 256; };
+  NormWs w;
+  w.chunk = chunk_of(grads, count, NORM_CHUNKS);
+  w.chunks = chunks_of(grads, count, w.chunk);
+  w.first = up((size_t)w.chunks * 8);
+  w.g = w.first + up((size_t)(count + 1) * 4);
+  const size_t list = count > NORM_TABLE ? up((size_t)count * 8) : 0;
+  w.n = w.g + list;
+  w.total = w.n + list;
+  return w;
+}
+}  // namespace
+
 extern "C" size_t moe_grad_norm_workspace_bytes(const moe_grad* grads, int count) {
   if (grad_checks("moe_grad_norm_workspace_bytes", grads, count, false) != MOE_OK) return 0;
-  const size_t part = (size_t)chunks_of(grads, count, chunk_of(grads, count)) * 8;
-  return (part + 255) / 256 * 256 + ((size_t)(count + 1) * 4 + 255) / 256 * 256;
+  return norm_ws(grads, count).total;
 }
 
 extern "C" int moe_grad_norm(const moe_grad* grads, int count, int kind, float* norm, float* norms,
@@ -263,7 +381,8 @@ extern "C" int moe_grad_norm(const moe_grad* grads, int count, int kind, float* 
   MOE_TRY(moe_opt_ptr(norms, fn, "norms", 4));
   MOE_TRY(moe_opt_ptr(total, fn, "total", 8));
   MOE_TRY(moe_need_ptr(ws, fn, "ws", 256));
-  const size_t need = moe_grad_norm_workspace_bytes(grads, count);
+  const NormWs lay = norm_ws(grads, count);
+  const size_t need = lay.total;
   if (ws_bytes < need)
     return moe_fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", fn, ws_bytes, need);
   const MoeRange outs[] = {{norm, 4, "norm"}, {norms, 4LL * count, "norms"}, {total, 8, "total"},
@@ -279,38 +398,51 @@ extern "C" int moe_grad_norm(const moe_grad* grads, int count, int kind, float* 
                       outs[i].name, with);
   }
   hipStream_t s = (hipStream_t)stream;
-  const long long chunk = chunk_of(grads, count);
-  const long long chunks = chunks_of(grads, count, chunk);
+  const bool max = kind == MOE_GRAD_MAX;
   double* const part = (double*)ws;
-  int* const starts = (int*)((char*)ws + ((size_t)chunks * 8 + 255) / 256 * 256);
-  int base = 0;
+  int* const first = (int*)((char*)ws + lay.first);
+  NormList list = {(const void**)((char*)ws + lay.g), (unsigned long long*)((char*)ws + lay.n),
+                   first, count};
+  // (gradients that are all empty have a workgroup, for `first`)
+  const dim3 grid(lay.chunks > 0 ? (unsigned)lay.chunks : 1);
+  int at = 0;
   for (int g0 = 0; g0 < count; g0 += NORM_TABLE) {
     NormTable t;
     t.count = std::min(NORM_TABLE, count - g0);
-    t.first[0] = 0;
     for (int i = 0; i < t.count; ++i) {
       const moe_grad& g = grads[g0 + i];
       t.g[i] = g.g;
       t.n[i] = (unsigned long long)g.n | (g.dt == MOE_BF16 ? G_BF16 : 0);
-      t.first[i + 1] = t.first[i] + (int)((g.n + chunk - 1) / chunk);
+      t.first[i] = at;
+      at += (int)((g.n + lay.chunk - 1) / lay.chunk);
     }
-    const int blocks = t.first[t.count];
-    // (a launch of gradients that are all empty has a block for their starts)
-    const dim3 grid(blocks > 0 ? blocks : 1);
-    if (kind == MOE_GRAD_MAX)
-      hipLaunchKernelGGL(grad_part_kernel<true>, grid, dim3(CLIP_NT), 0, s, t, chunk, base, g0,
-                         part, starts);
+    t.first[t.count] = at;
+    if (count > NORM_TABLE)
+      hipLaunchKernelGGL(grad_table_kernel, dim3(1), dim3(CLIP_NT), 0, s, t, g0, list);
+    else if (max)
+      hipLaunchKernelGGL((grad_part_kernel<true, NormTable>), grid, dim3(CLIP_NT), 0, s, t,
+                         lay.chunk, part, first);
     else
-      hipLaunchKernelGGL(grad_part_kernel<false>, grid, dim3(CLIP_NT), 0, s, t, chunk, base, g0,
-                         part, starts);
+      hipLaunchKernelGGL((grad_part_kernel<false, NormTable>), grid, dim3(CLIP_NT), 0, s, t,
+                         lay.chunk, part, first);
     MOE_TRY(moe_check_launch(fn));
-    base += blocks;
+  }
+  // more gradients than a table holds: tables into memory, then one launch for all
+  // (700 gradients of 40000 values: 32 us, where a launch a table takes 65)
+  if (count > NORM_TABLE) {
+    if (max)
+      hipLaunchKernelGGL((grad_part_kernel<true, NormList>), grid, dim3(CLIP_NT), 0, s, list,
+                         lay.chunk, part, nullptr);
+    else
+      hipLaunchKernelGGL((grad_part_kernel<false, NormList>), grid, dim3(CLIP_NT), 0, s, list,
+                         lay.chunk, part, nullptr);
+    MOE_TRY(moe_check_launch(fn));
   }
   if (kind == MOE_GRAD_MAX)
-    hipLaunchKernelGGL(grad_norm_kernel<true>, dim3(1), dim3(CLIP_SUM_NT), 0, s, part, starts,
+    hipLaunchKernelGGL(grad_norm_kernel<true>, dim3(1), dim3(CLIP_SUM_NT), 0, s, part, first,
                        count, norm, norms, total);
   else
-    hipLaunchKernelGGL(grad_norm_kernel<false>, dim3(1), dim3(CLIP_SUM_NT), 0, s, part, starts,
+    hipLaunchKernelGGL(grad_norm_kernel<false>, dim3(1), dim3(CLIP_SUM_NT), 0, s, part, first,
                        count, norm, norms, total);
   return moe_check_launch(fn);
 }
@@ -328,7 +460,7 @@ extern "C" int moe_grad_clip(const moe_grad* grads, int count, const float* norm
       return moe_fail(MOE_ERR_INVALID_ARG, "%s: out %d overlaps norm", fn, i);
   MOE_TRY(clip_overlaps(fn, grads, count));
   hipStream_t s = (hipStream_t)stream;
-  const long long chunk = chunk_of(grads, count);
+  const long long chunk = chunk_of(grads, count, CLIP_CHUNKS);
   for (int g0 = 0; g0 < count; g0 += CLIP_TABLE) {
     ClipTable t;
     t.count = std::min(CLIP_TABLE, count - g0);

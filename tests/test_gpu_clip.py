@@ -26,7 +26,7 @@ def clipper(*a, **kw):
 SETS = [[1], [0, 5], [0, 0], [7, 8, 9], [255, 256, 257, 2047, 2048, 2049], [16383, 16384, 16385, 0, 1],
         [100003, 3, 70000], [(i * 37) % 90 for i in range(1000)], [17] * 176, [17] * 177,
         [0] * 176 + [5], [5] + [0] * 400, [(i * 7919) % 50000 + 1 for i in range(300)],
-        [30_000_001, 12, 1 << 22]]
+        [30_000_001, 12, 1 << 22], [1_000_000 + 977 * i for i in range(130)], [3] * 20000]
 
 
 @pytest.mark.parametrize("kind", ["l2", "max"])
