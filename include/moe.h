@@ -459,8 +459,8 @@ int moe_linear_bwd(const void* dy, const void* z, const void* x, const void* w, 
  *   prob [S,E] fp32    P_se (nullable; a statistic, zeros where n_s = 0)
  * A logit of -inf masks an expert; NaN or +inf in a token that counts gives
  * NaN losses.  idx entries outside [0, E) are not counted.  T == 0 writes zeros.  ws:
- * scratch of moe_balance_loss_workspace_bytes bytes, 256-byte aligned, not
- * shared by calls that may overlap.  Outputs share memory with nothing else.
+ * scratch of moe_balance_loss_workspace_bytes bytes, 256-byte aligned (NULL
+ * where that is 0), not shared by calls that may overlap.  Outputs share memory with nothing else.
  */
 size_t moe_balance_loss_workspace_bytes(int T, int E, int k, int S);
 int moe_balance_loss(const float* logits, const int32_t* idx, const uint8_t* keep,

@@ -48,10 +48,7 @@ struct BalWs {
 };
 BalWs bal_ws(int T, int E, int S) {
   BalWs w = {};
-  if (bal_one(T, E, S)) {
-    w.total = 256;
-    return w;
-  }
+  if (bal_one(T, E, S)) return w;
   const size_t rows = (size_t)bal_blocks(T, E) + S, cg = (E + MOE_WAVE - 1) / MOE_WAVE;
   auto up = [](size_t b) { return (b + 255) / 256 * 256; };
   w.q = 256;                                  // (in front: the count of workgroups that are done)
@@ -75,17 +72,6 @@ __device__ __forceinline__ int bal_seq(const int32_t* seq, int s, int T) {
   const int v = seq[s];
   return v < 0 ? 0 : v > T ? T : v;
 }
-__device__ __forceinline__ double wave_sum64(double v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, MOE_WAVE);
-  return v;
-}
-__device__ __forceinline__ int wave_sum_int(int v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, MOE_WAVE);
-  return v;
-}
-
 // First sequence that ends behind token t (S if none does), by a whole wave: 64
 // ends at a time cut the range to a 64th, so that 64 sequences take one trip to
 // memory where halving takes six.
@@ -104,13 +90,16 @@ __device__ __forceinline__ int bal_first(const int32_t* seq, int S, int T, int t
   return lo;
 }
 
-// A token's softmax over its lanes: v <- exp(v - max), the reciprocal of their
-// sum (0 where all logits are -inf) and the sum's log; whether one is not -inf.
-// (A NaN or +inf among them makes the sum NaN.)
-template <int TPR, int V>
-__device__ __forceinline__ bool bal_softmax(float (&v)[V], int E, float& inv, float& lse) {
+// A token's softmax over its lanes: v <- exp(v - max), m the maximum and s their
+// sum (s = 0 where all logits are -inf; NaN where there is a NaN or +inf).
+// FAST: the exponential by the hardware's exp2, off by 2.4 |x| + 2 roundings (expf
+// and its range reduction are half of the forward's instructions, and the forward
+// of many tokens is bound by them: 65521 tokens of 256 experts 24 us so, 18 with
+// exp2); the backward keeps moe_route_bwd's expf and its bits.
+template <int TPR, int V, bool FAST>
+__device__ __forceinline__ void bal_softmax(float (&v)[V], int E, float& m, float& s) {
   const int lane = threadIdx.x % TPR;
-  float m = -INFINITY;
+  m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     v[i] = lane + i * TPR < E ? v[i] : -INFINITY;
@@ -118,23 +107,21 @@ __device__ __forceinline__ bool bal_softmax(float (&v)[V], int E, float& inv, fl
   }
   m = lanes_max<TPR>(m);
   m = m == -INFINITY ? 0.f : m;
-  float s = 0.f;
+  s = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    v[i] = lane + i * TPR < E ? expf(v[i] - m) : 0.f;
+    // (a lane without an expert holds -inf: 0, or NaN where the sum is one anyway)
+    if constexpr (FAST) v[i] = __builtin_amdgcn_exp2f((v[i] - m) * 1.44269504f);
+    else v[i] = lane + i * TPR < E ? expf(v[i] - m) : 0.f;
     s += v[i];
   }
   s = lanes_sum<TPR>(s);
-  const bool some = !(s == 0.f);
-  inv = some ? 1.0f / s : 0.f;
-  lse = m + logf(s);
-  return some;
 }
 
 template <int TPR, int V>
 __global__ __launch_bounds__(BAL_NT) void balance_part_kernel(BalArgs a) {
   constexpr int G = BAL_NT / TPR;             // tokens at a time
-  constexpr int U = V >= 16 ? 1 : V >= 8 ? 2 : 4;
+  constexpr int U = V >= 8 ? 1 : 2;           // rounds in flight
   __shared__ float q_s[BAL_WAVES][V * TPR];
   __shared__ int c_s[V * TPR];
   __shared__ double z_s[BAL_WAVES];
@@ -169,26 +156,42 @@ __global__ __launch_bounds__(BAL_NT) void balance_part_kernel(BalArgs a) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int t = base + u * G + grp;
-        use[u] = t < hi && (!a.keep || a.keep[t] != 0);
+        use[u] = t < hi;
+        if constexpr (TPR == MOE_WAVE) {      // (a row's address is the wave's)
+          const int tw = uniform(use[u] ? t : 0);
+          const uint32_t on = uniform(use[u] ? -1 : 0);
+          const auto rl = make_rsrc(a.logits + (long long)tw * E, (uint32_t)E * 4u & on);
+          const auto ri = make_rsrc(a.idx + (long long)tw * a.k, (uint32_t)a.k * 4u & on);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int e = lane + i * TPR;
-          v[u][i] = __uint_as_float(
-              buf_load4(rl, use[u] && e < E ? ((uint32_t)t * (uint32_t)E + e) * 4u : BAL_OOB));
+          for (int i = 0; i < V; ++i)
+            v[u][i] = __uint_as_float(buf_load4(rl, (uint32_t)lane * 4u + i * 256u));
+          e0[u] = (int)buf_load4(ri, (uint32_t)lane * 4u);
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const int e = lane + i * TPR;
+            v[u][i] = __uint_as_float(
+                buf_load4(rl, use[u] && e < E ? ((uint32_t)t * (uint32_t)E + e) * 4u : BAL_OOB));
+          }
+          e0[u] = (int)buf_load4(
+              ri, use[u] && lane < a.k ? ((uint32_t)t * (uint32_t)a.k + lane) * 4u : BAL_OOB);
         }
-        e0[u] = (int)buf_load4(
-            ri, use[u] && lane < a.k ? ((uint32_t)t * (uint32_t)a.k + lane) * 4u : BAL_OOB);
         e0[u] = lane < a.k ? e0[u] : -1;
+        if (a.keep && use[u]) use[u] = a.keep[t] != 0;
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        float inv, lse;
-        use[u] = bal_softmax<TPR, V>(v[u], E, inv, lse) && use[u];
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] += use[u] ? v[u][i] * inv : 0.f;
-        z += use[u] ? (double)lse * lse : 0.0;
-        n += use[u];
+        if (TPR == MOE_WAVE && base + u * G >= hi) break;
+        float m, sum;
+        bal_softmax<TPR, V, true>(v[u], E, m, sum);
+        use[u] = use[u] && !(sum == 0.f);
         if (use[u]) {
+          const float inv = __builtin_amdgcn_rcpf(sum);
+          const float lse = fmaf(__builtin_amdgcn_logf(sum), 0.693147181f, m);
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[i] = fmaf(v[u][i], inv, acc[i]);
+          z += (double)lse * lse;
+          ++n;
           if (e0[u] >= 0 && e0[u] < E) atomicAdd(&c_s[e0[u]], 1);
           const long long t = base + u * G + grp;
           for (int j = lane + TPR; j < a.k; j += TPR) {
@@ -204,8 +207,8 @@ __global__ __launch_bounds__(BAL_NT) void balance_part_kernel(BalArgs a) {
       for (int o = TPR; o < MOE_WAVE; o *= 2) acc[0] += __shfl_xor(acc[0], o, MOE_WAVE);
 #pragma unroll
     for (int i = 0; i < V; ++i) q_s[wave][lane + i * TPR] = acc[i];
-    z = wave_sum64(lane == 0 ? z : 0.0);
-    n = wave_sum_int(lane == 0 ? n : 0);
+    z = lanes_sum64(lane == 0 ? z : 0.0);
+    n = lanes_sum_int(lane == 0 ? n : 0);
     if (threadIdx.x % MOE_WAVE == 0) { z_s[wave] = z; n_s[wave] = n; }
     __syncthreads();
     z = 0, n = 0;
@@ -239,7 +242,7 @@ __global__ __launch_bounds__(BAL_NT) void balance_part_kernel(BalArgs a) {
     __syncthreads();
   }
   if (!a.one) return;
-  all_b = wave_sum64(all_b);
+  all_b = lanes_sum64(all_b);
   if (threadIdx.x % MOE_WAVE == 0) z_s[wave] = all_b;
   __syncthreads();
   if (threadIdx.x != 0) return;
@@ -253,6 +256,15 @@ __global__ __launch_bounds__(BAL_NT) void balance_part_kernel(BalArgs a) {
   a.loss[1] = (float)all_z;
   a.loss[2] = (float)(a.w_balance * all_b + a.w_z * all_z);
   a.tokens[a.S] = all_n;
+}
+
+template <typename T>
+__device__ __forceinline__ void put(T* p, T v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename T>
+__device__ __forceinline__ T get(const T* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // Rows of a sequence: counts, probabilities and its part of the losses, 64
@@ -281,8 +293,8 @@ __global__ __launch_bounds__(BAL_NT) void balance_sum_kernel(BalArgs a) {
     z += a.z[b + s];
     n += a.n[b + s];
   }
-  z = wave_sum64(z);
-  n = wave_sum_int((int)n);
+  z = lanes_sum64(z);
+  n = lanes_sum_int((int)n);
   q_s[wave][lane] = q;
   c_s[wave][lane] = c;
   if (lane == 0) { z_s[wave] = z; n_s[wave] = n; }
@@ -300,31 +312,31 @@ __global__ __launch_bounds__(BAL_NT) void balance_sum_kernel(BalArgs a) {
       a.counts[(long long)s * E + e] = c;
       if (a.prob) a.prob[(long long)s * E + e] = n > 0 ? (float)(q / n) : 0.f;
     }
-    const double part = wave_sum64(e < E && n > 0 ? c * q / n : 0.0);
+    const double part = lanes_sum64(e < E && n > 0 ? c * q / n : 0.0);
     if (lane == 0) {
-      a.term[(long long)s * cg + blockIdx.x] = part;
+      // written at device scope, past this XCD's L2, and complete before the count
+      put(a.term + (long long)s * cg + blockIdx.x, part);
       if (blockIdx.x == 0) {
-        a.term[(long long)a.S * cg + s] = z;
-        a.tokens[s] = (int)n;
+        put(a.term + (long long)a.S * cg + s, z);
+        put(a.tokens + s, (int)n);
       }
-      // what this workgroup wrote is seen by whoever sees the count
-      last = __hip_atomic_fetch_add(a.done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+      __builtin_amdgcn_s_waitcnt(0);
+      last = __hip_atomic_fetch_add(a.done, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
              cg * a.S - 1;
     }
   }
   __syncthreads();
   if (!last) return;
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
   double b = 0;
   z = 0, n = 0;
-  for (long long i = threadIdx.x; i < (long long)a.S * cg; i += BAL_NT) b += a.term[i];
+  for (long long i = threadIdx.x; i < (long long)a.S * cg; i += BAL_NT) b += get(a.term + i);
   for (int i = threadIdx.x; i < a.S; i += BAL_NT) {
-    z += a.term[(long long)a.S * cg + i];
-    n += a.tokens[i];
+    z += get(a.term + (long long)a.S * cg + i);
+    n += get(a.tokens + i);
   }
-  b = wave_sum64(b);
-  z = wave_sum64(z);
-  n = wave_sum_int((int)n);
+  b = lanes_sum64(b);
+  z = lanes_sum64(z);
+  n = lanes_sum_int((int)n);
   if (lane == 0) { b_s[wave] = b; z_s[wave] = z; n_s[wave] = n; }
   __syncthreads();
   if (threadIdx.x != 0) return;
@@ -348,78 +360,84 @@ struct BalBwd {
   float* dlogits;
 };
 
+// Bound by the row's trip to memory at few tokens, by memory at many.  A wave has
+// one token of many experts or several of few (four tokens a wave in
+// turn, all their rows in flight, end later: 8192 tokens of 256 experts 10.5 us,
+// so 7.6; 65521 tokens 38.2 and 39.3).  Streaming stores: 7.5 -> 6.7 us at 8192
+// tokens, 38.5 -> 34.7 at 65521 (3.9 TB/s).
 template <int TPR, int V>
 __global__ __launch_bounds__(BAL_BWD_NT) void balance_bwd_kernel(BalBwd a) {
-  constexpr int G = BAL_BWD_NT / TPR;
-  __shared__ float dp_s[G][V * TPR];
-  const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR, E = a.E;
-  const int t = blockIdx.x * G + grp;
-  const bool in = t < a.T;                    // (lanes past the end go along with their wave)
-  const auto rl = make_rsrc(a.logits, clamp_bytes(4LL * a.T * E));
+  constexpr int PER = MOE_WAVE / TPR, WAVES = BAL_BWD_NT / MOE_WAVE;
+  __shared__ float dp_s[WAVES][PER][V * TPR];
+  const int lane = threadIdx.x % TPR, sub = threadIdx.x % MOE_WAVE / TPR, E = a.E;
+  const int wave = uniform((int)(threadIdx.x / MOE_WAVE));
+  const int t0 = (blockIdx.x * WAVES + wave) * PER, t = t0 + sub;
+  if (t0 >= a.T) return;                      // whole waves; no block barrier below
+  // the wave's rows, as far as there are
+  const uint32_t bytes = (uint32_t)(a.T - t0 < PER ? a.T - t0 : PER) * (uint32_t)E * 4u;
+  const auto rl = make_rsrc(a.logits + (long long)t0 * E, bytes);
+  const auto rd = make_rsrc(a.dlogits + (long long)t0 * E, bytes);
+  uint32_t off[V];
   float v[V], g[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int e = lane + i * TPR;
-    v[i] = __uint_as_float(
-        buf_load4(rl, in && e < E ? ((uint32_t)t * (uint32_t)E + e) * 4u : BAL_OOB));
+    off[i] = e < E ? ((uint32_t)sub * (uint32_t)E + e) * 4u : BAL_OOB;
+    v[i] = __uint_as_float(buf_load4(rl, off[i]));
   }
-  bool counts = in && !(a.keep && a.keep[t] == 0);
+  const bool pair = a.dgate && t < a.T && lane < a.k;
+  const int e0 = pair ? a.idx[(long long)t * a.k + lane] : -1;
+  const float d0 = pair ? a.dgate[(long long)t * a.k + lane] : 0.f;
+  bool counts = t < a.T && !(a.keep && a.keep[t] == 0);
   int s = 0;
   if (a.seq) {
 #pragma unroll
-    for (int j = 0; j < MOE_WAVE / TPR; ++j) {   // the tokens of a wave
-      const int of = bal_first(a.seq, a.S, a.T, __builtin_amdgcn_readlane(t, j * TPR));
-      s = (int)(threadIdx.x % MOE_WAVE) / TPR == j ? of : s;
+    for (int j = 0; j < PER; ++j) {
+      const int of = bal_first(a.seq, a.S, a.T, t0 + j);
+      s = sub == j ? of : s;
     }
     counts = counts && s < a.S && bal_seq(a.seq, s, a.T) <= t;
     s = s < a.S ? s : 0;
   }
-  float fs = 0.f, zs = 0.f;
-  {
-    const float dl = a.dloss ? a.dloss[0] : 1.f;
-    const int N = a.tokens[a.S], n = a.tokens[s];
-    const float per = dl / (float)(N > 0 ? N : 1);
-    fs = a.w_balance * per * ((float)E / ((float)a.k * (float)(n > 0 ? n : 1)));
-    zs = 2.f * a.w_z * per;
-  }
+  const int N = a.tokens[a.S], n = a.tokens[s];
+  const float per = (a.dloss ? a.dloss[0] : 1.f) / (float)(N > 0 ? N : 1);
+  const float fs = a.w_balance * per * ((float)E / ((float)a.k * (float)(n > 0 ? n : 1)));
+  if constexpr (TPR == MOE_WAVE) {            // (the sequence's row is the wave's)
+    const auto rc = make_rsrc(a.counts + (long long)uniform(s) * E, (uint32_t)E * 4u);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane + i * TPR;
-    g[i] = counts && e < E ? fs * (float)a.counts[(long long)s * E + e] : 0.f;
+    for (int i = 0; i < V; ++i) g[i] = counts ? fs * (float)(int)buf_load4(rc, off[i]) : 0.f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      g[i] = counts && off[i] != BAL_OOB ? fs * (float)a.counts[(long long)s * E + lane + i * TPR]
+                                         : 0.f;
   }
   if (a.dgate) {
-    float* const dp = dp_s[grp];
+    float* const dp = dp_s[wave][sub];
 #pragma unroll
     for (int i = 0; i < V; ++i) dp[lane + i * TPR] = 0.f;
-    __builtin_amdgcn_s_waitcnt(0xc07f);       // (LDS alone)
-    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_wave_barrier();          // (a wave's LDS accesses happen in order)
     // chosen experts of a token are distinct, so these writes never collide
-    for (int j = lane; j < a.k; j += TPR) {
-      const long long at = (long long)t * a.k + j;
-      const int e = in ? a.idx[at] : -1;
-      if (e >= 0 && e < E) dp[e] = a.dgate[at];
+    if (e0 >= 0 && e0 < E) dp[e0] = d0;
+    for (int j = lane + TPR; j < a.k && t < a.T; j += TPR) {
+      const int e = a.idx[(long long)t * a.k + j];
+      if (e >= 0 && e < E) dp[e] = a.dgate[(long long)t * a.k + j];
     }
-    __builtin_amdgcn_s_waitcnt(0xc07f);
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int i = 0; i < V; ++i) g[i] += dp[lane + i * TPR];
   }
-  float inv, lse;
-  const bool some = bal_softmax<TPR, V>(v, E, inv, lse);
-  if (!(counts && some)) {
-    zs = 0.f;
-  } else {
-    zs *= lse;
-  }
-  float acc = 0.f;
+  float m, sum, acc = 0.f, zs = 0.f;
+  bal_softmax<TPR, V, false>(v, E, m, sum);
+  const bool some = !(sum == 0.f);
+  const float inv = some ? 1.0f / sum : 0.f;
+  if (a.w_z != 0.f && some && counts) zs = 2.f * a.w_z * per * (m + logf(sum));
 #pragma unroll
   for (int i = 0; i < V; ++i) acc += v[i] * inv * g[i];
   acc = lanes_sum<TPR>(acc);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane + i * TPR;
-    if (in && e < E) a.dlogits[(long long)t * E + e] = v[i] * inv * (g[i] - acc + zs);
-  }
+  for (int i = 0; i < V; ++i)
+    buf_store4_nt(rd, off[i], __float_as_uint(v[i] * inv * (g[i] - acc + zs)));
 }
 
 template <int TPR, int V>
@@ -469,8 +487,8 @@ extern "C" int moe_balance_loss(const float* logits, const int32_t* idx, const u
   MOE_TRY(moe_need_ptr(counts, fn, "counts", 4));
   MOE_TRY(moe_need_ptr(tokens, fn, "tokens", 4));
   MOE_TRY(moe_opt_ptr(prob, fn, "prob", 4));
-  MOE_TRY(moe_need_ptr(ws, fn, "ws", 256));
   const BalWs lay = bal_ws(T, E, S);
+  if (lay.total > 0) MOE_TRY(moe_need_ptr(ws, fn, "ws", 256));
   if (ws_bytes < lay.total)
     return moe_fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", fn, ws_bytes,
                     lay.total);
@@ -478,7 +496,7 @@ extern "C" int moe_balance_loss(const float* logits, const int32_t* idx, const u
                          {keep, T, "keep"}, {seq, 4LL * (S + 1), "seq"}},
                  outs[] = {{loss, 12, "loss"}, {counts, 4LL * S * E, "counts"},
                            {tokens, 4LL * (S + 1), "tokens"}, {prob, 4LL * S * E, "prob"},
-                           {ws, (long long)lay.total, "ws"}};
+                           {lay.total > 0 ? ws : nullptr, (long long)lay.total, "ws"}};
   for (int i = 0; i < 5; ++i) {
     const char* with = moe_shares(outs[i], {in[0], in[1], in[2], in[3]});
     for (int j = 0; j < i && with == nullptr; ++j) with = moe_shares(outs[i], {outs[j]});

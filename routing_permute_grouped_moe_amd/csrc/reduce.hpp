@@ -57,3 +57,41 @@ __device__ __forceinline__ float lanes_max(float v) {
   v = fmaxf(v, dpp<0x122>(v));
   return fmaxf(v, dpp<0x121>(v));
 }
+
+// The same of a double: its halves move side by side.
+template <int CTRL>
+__device__ __forceinline__ double dpp64(double v) {
+  const unsigned long long u = __builtin_bit_cast(unsigned long long, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xf, 0xf, true);
+  const uint32_t hi =
+      (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xf, 0xf, true);
+  return __builtin_bit_cast(double, ((unsigned long long)hi << 32) | lo);
+}
+__device__ __forceinline__ double lanes_sum64(double v) {
+  auto join = [](uint32_t hi, uint32_t lo) {
+    return __builtin_bit_cast(double, ((unsigned long long)hi << 32) | lo);
+  };
+  unsigned long long u = __builtin_bit_cast(unsigned long long, v);
+  auto lo = __builtin_amdgcn_permlane32_swap((uint32_t)u, (uint32_t)u, false, false);
+  auto hi = __builtin_amdgcn_permlane32_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
+  v = join(hi[0], lo[0]) + join(hi[1], lo[1]);
+  u = __builtin_bit_cast(unsigned long long, v);
+  lo = __builtin_amdgcn_permlane16_swap((uint32_t)u, (uint32_t)u, false, false);
+  hi = __builtin_amdgcn_permlane16_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
+  v = join(hi[0], lo[0]) + join(hi[1], lo[1]);
+  v += dpp64<0x128>(v);
+  v += dpp64<0x124>(v);
+  v += dpp64<0x122>(v);
+  return v + dpp64<0x121>(v);
+}
+// A whole number's, over the 64 lanes.
+__device__ __forceinline__ int lanes_sum_int(int v) {
+  const auto a = __builtin_amdgcn_permlane32_swap((uint32_t)v, (uint32_t)v, false, false);
+  v = (int)(a[0] + a[1]);
+  const auto b = __builtin_amdgcn_permlane16_swap((uint32_t)v, (uint32_t)v, false, false);
+  v = (int)(b[0] + b[1]);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x128, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x124, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x122, 0xf, 0xf, true);
+  return v + __builtin_amdgcn_update_dpp(0, v, 0x121, 0xf, 0xf, true);
+}

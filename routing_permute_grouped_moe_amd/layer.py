@@ -567,6 +567,7 @@ class BalanceLoss:
 
     def __init__(self, weight: float = 0.01, z_weight: float = 0.0):
         self.weight, self.z_weight = float(weight), float(z_weight)
+        self._ws_bytes = {}
 
     @staticmethod
     def _inputs(logits, idx, seq, keep):
@@ -596,12 +597,15 @@ class BalanceLoss:
         dev, T, E, k, S = self._inputs(logits, idx, seq, keep)
 
         def call(st):
-            n = abi.moe_balance_loss_workspace_bytes(T, E, k, S)
+            n = self._ws_bytes.get((T, E, k, S))
+            if n is None:
+                n = abi.moe_balance_loss_workspace_bytes(T, E, k, S)
+                self._ws_bytes[T, E, k, S] = n
             loss, prob = logits.new_empty(3), logits.new_empty((S, E))
             counts, tokens = idx.new_empty((S, E)), idx.new_empty(S + 1)
             # a workspace per call, from the stream's own pool: calls on several
             # streams, or captured into several graphs, never share one
-            ws = logits.new_empty(n, dtype=torch.uint8)
+            ws = logits.new_empty(n, dtype=torch.uint8) if n else None
             abi.moe_balance_loss(logits, idx, keep, seq, T, E, k, S, self.weight, self.z_weight,
                                  loss, counts, tokens, prob, ws, n, st)
             return Balance(loss, counts, tokens, prob)
@@ -662,6 +666,7 @@ class Norm:
         if not 0.0 < eps < float("inf"):
             raise ValueError(f"eps {eps} is not positive and finite")
         self.w, self.bias, self.kind, self.eps = w, bias, NORMS[kind], float(eps)
+        self._ws_bytes = {}
 
     def _rows(self, x):
         if x.dim() != 2:
@@ -716,7 +721,11 @@ class Norm:
             dx = None if not x_grad else torch.empty_like(h) if out is None else out
             dw = torch.empty_like(self.w) if w_grad else None
             db = torch.empty_like(self.w) if bias_grad else None
-            n = abi.moe_norm_bwd_workspace_bytes(M, H, dt) if w_grad or bias_grad else 0
+            n = 0
+            if w_grad or bias_grad:
+                n = self._ws_bytes.get((M, dt))
+                if n is None:
+                    n = self._ws_bytes[M, dt] = abi.moe_norm_bwd_workspace_bytes(M, H, dt)
             ws = h.new_empty(n, dtype=torch.uint8) if n else None
             abi.moe_norm_bwd(dy, h, dh, dt, M, H, self.kind, self.w, mean, rstd, dx, dw, db, ws, n,
                              st)

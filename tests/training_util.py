@@ -88,8 +88,13 @@ def ref_norm_bwd(dy, h, w, mean, rstd, dh, kind, dtype):
 
 # ---------------------------------------------------------------- losses of the router
 
-def ref_rows(z):
-    """(p, lse, rel. bound of p, bound of lse, whether a logit is not -inf) of fp32 logits."""
+def ref_rows(z, arg=1.0):
+    """(p, lse, rel. bound of p, bound of lse, whether a logit is not -inf) of fp32 logits.
+
+    ``arg``: roundings of the exp's argument: 1, the difference to the maximum; 2.4
+    where it is taken as exp2 of the difference times log2 e, for the product is
+    rounded too and the constant off by 0.4 u.  A log is off by 3 u: log2's own, and
+    the product's, and the constant's."""
     z = f64(z)
     live = (z != -float("inf")).any(1)
     zz = torch.where(live[:, None], z, torch.zeros_like(z))
@@ -97,10 +102,10 @@ def ref_rows(z):
     spread = torch.where(zz > -float("inf"), m - zz, torch.zeros_like(zz))
     p = torch.softmax(zz, 1)
     D = z.shape[1] / 64 + 12
-    drift = ((spread + 3) * p).sum(1, keepdim=True) + D
-    rel = (spread + 6 + drift) * U
+    drift = ((arg * spread + 3) * p).sum(1, keepdim=True) + D
+    rel = (arg * spread + 6 + drift) * U
     lse = torch.logsumexp(zz, 1)
-    dl = drift[:, 0] * U + 2 * U * (lse - m[:, 0]).abs() + U * lse.abs() + U
+    dl = drift[:, 0] * U + 3 * U * (lse - m[:, 0]).abs() + U * lse.abs() + U
     return p * live[:, None], lse * live, rel, dl, live
 
 
@@ -118,7 +123,7 @@ def ref_balance(z, idx, seq, keep, weight, z_weight):
     T, E = z.shape
     k = idx.shape[1]
     S = 1 if seq is None else seq.shape[0] - 1
-    p, lse, rel, dl, live = ref_rows(z)
+    p, lse, rel, dl, live = ref_rows(z, 2.4)
     of = ref_members(T, seq, keep, live, S).double()
     n = of.sum(1)
     N = max(1.0, n.sum().item())
