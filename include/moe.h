@@ -511,7 +511,8 @@ int moe_norm(const void* x, const void* residual, int dt, int M, int H, int kind
  * stream: dx is then the gradient of x and of the residual both.  dx [M,H], dw
  * and db [H] fp32 are each written if not NULL; dx may be dh's buffer, and
  * shares memory with nothing else.  M == 0 writes zeros to dw and db.  ws:
- * scratch of moe_norm_bwd_workspace_bytes bytes, 256-byte aligned.
+ * scratch of moe_norm_bwd_workspace_bytes bytes, 256-byte aligned, not shared by
+ * calls that may overlap (NULL where neither dw nor db is asked for).
  */
 size_t moe_norm_bwd_workspace_bytes(int M, int H, int dt);
 int moe_norm_bwd(const void* dy, const void* h, const void* dh, int dt, int M, int H, int kind,
@@ -530,7 +531,7 @@ int moe_norm_bwd(const void* dy, const void* h, const void* dh, int dt, int M, i
  * the sum of all squares, or the maximum: what ranks that hold parts of a model
  * reduce before they clip.  Without a gradient all are 0.  out and out_dt are
  * not used.  ws: scratch of moe_grad_norm_workspace_bytes bytes, 256-byte
- * aligned.
+ * aligned, not shared by calls that may overlap.
  */
 typedef struct moe_grad {
   const void* g;

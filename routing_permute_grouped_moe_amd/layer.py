@@ -268,6 +268,8 @@ class MoeLayer:
     def route_bwd(self, stream=None):
         s = self.s
         if self.balance is not None:      # the gates' and the losses' gradient in one pass
+            if self.losses is None:
+                raise RuntimeError("the backward of the router's losses before their forward")
             self.balance.backward(self.logits, self.idx, self.losses.counts, self.losses.tokens,
                                   seq=self.seq, keep=self.keep, dgate=self.dgate,
                                   out=self.dlogits, stream=stream)
@@ -742,8 +744,8 @@ class GradClip:
 
     ``grads`` are dense tensors of any shapes, fp32 or bf16, on one GPU; ``outs``:
     where the clipped ones go, of the same sizes and of the same type or fp32
-    (None: in place).  The tensors stay the caller's; each call takes their
-    present contents, and their addresses as they are then."""
+    (None: in place).  The tensors stay the caller's and keep their sizes; each
+    call takes their present contents, and their addresses as they are then."""
 
     def __init__(self, grads, outs=None, kind: str = "l2"):
         self.grads = list(grads)
@@ -767,12 +769,12 @@ class GradClip:
         self._lay_out()
 
     def _lay_out(self):
-        self._at = [t.data_ptr() for t in self._tensors]
+        self._at = list(map(torch.Tensor.data_ptr, self._tensors))
         self._arr = abi.grads(self.grads, self.outs)
         self._ws_bytes = abi.moe_grad_norm_workspace_bytes(self._arr, len(self.grads))
 
     def _array(self):
-        if [t.data_ptr() for t in self._tensors] != self._at:   # (storage that was replaced)
+        if list(map(torch.Tensor.data_ptr, self._tensors)) != self._at:   # (storage was replaced)
             self.__init__(self.grads, None if self.outs is self.grads else self.outs,
                           {v: k for k, v in GRAD_NORMS.items()}[self.kind])
         return self._arr

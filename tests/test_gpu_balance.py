@@ -266,3 +266,65 @@ def test_replays_from_a_graph(T, S):
             assert torch.equal(a, b)
         for a, b in zip(step(), want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,E", [(67_000_001, 16), (16_777_213, 64), (1_048_575, 1024)])
+def test_tensors_of_almost_four_gib(T, E):
+    """Byte offsets up to 2^32: all logits alike but those of the last tokens."""
+    k, last = 1, 777
+    z = torch.zeros(T, E, device="cuda")
+    zl, il, _, _, _ = inputs(last, E, k)
+    z[-last:] = zl
+    idx = torch.zeros(T, k, dtype=I32, device="cuda")
+    idx[-last:] = il
+    keep = torch.zeros(T, dtype=torch.uint8, device="cuda")
+    keep[-last:] = 1
+    keep[0] = 1
+    op = loss_op()
+    r = op.forward(z, idx, keep=keep)
+    some = torch.cat([z[:1], z[-last:]]), torch.cat([idx[:1], idx[-last:]])
+    want = ref_balance(*some, None, None, 0.02, 0.003)
+    assert torch.equal(f64(r.counts), want["counts"]) and r.tokens.tolist() == [last + 1] * 2
+    assert_within("prob", r.prob, want["prob"])
+    assert_within("loss", r.loss, want["loss"])
+    out = torch.full_like(z, 7.0)
+    op.backward(z, idx, r.counts, r.tokens, keep=keep, out=out)
+    ref, bound = ref_balance_bwd(*some, None, None, 0.02, 0.003, 1.0, None)
+    assert_within("dlogits", torch.cat([out[:1], out[-last:]]), (ref, bound))
+    assert out[1:100].abs().max() == 0 and out[T // 2].abs().max() == 0
+
+
+def test_two_at_once_and_again():
+    """Calls on two streams side by side, over and over: the same bits."""
+    z, idx, seq, kp, n = inputs(20000, 256, 8, 30, True)
+    z2, idx2, _, _, _ = inputs(300, 1024, 4)
+    op = loss_op()
+    want, want2 = op.forward(z, idx, seq=seq, keep=kp), op.forward(z2, idx2)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in (a, b):
+        s.wait_stream(torch.cuda.current_stream())
+    got = [(op.forward(z, idx, seq=seq, keep=kp, stream=a), op.forward(z2, idx2, stream=b))
+           for _ in range(8)]
+    torch.cuda.synchronize()
+    for x, y in got:
+        assert all(torch.equal(p, q) for p, q in zip(x, want))
+        assert all(torch.equal(p, q) for p, q in zip(y, want2))
+
+
+def test_many_sequences_of_few_experts():
+    """More sequences than tokens, tokens of several sequences in a wave, an end at
+    every token, padding behind."""
+    T, E, k = 1000, 12, 3
+    z, idx, _, kp, n = inputs(T, E, k, keep=True)
+    op, dg = loss_op(), n(T, k)
+    for ends in (torch.arange(0, T - 50), torch.arange(0, 3 * T, 2).clamp(max=T - 1),
+                 torch.tensor([0] * 3000 + [T]), torch.tensor([0, 5] + [5] * 700 + [T - 1])):
+        seq = ends.int().cuda()
+        r = op.forward(z, idx, seq=seq, keep=kp)
+        want = ref_balance(z, idx, seq, kp, 0.02, 0.003)
+        assert torch.equal(f64(r.counts), want["counts"])
+        assert torch.equal(f64(r.tokens), want["tokens"])
+        assert_within("loss", r.loss, want["loss"])
+        assert_within("prob", r.prob, want["prob"])
+        got = op.backward(z, idx, r.counts, r.tokens, seq=seq, keep=kp, dgate=dg)
+        assert_within("dlogits", got, ref_balance_bwd(z, idx, seq, kp, 0.02, 0.003, 1.0, dg))

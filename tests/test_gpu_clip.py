@@ -246,3 +246,35 @@ def test_replays_from_a_graph():
             assert torch.equal(a, b)
         for a, b in zip(step(), want):
             assert torch.equal(a, b)
+
+
+def test_two_at_once_and_again():
+    """Calls on two streams side by side, over and over: the same bits."""
+    one, two = grads_of([400000, 3, 77777]), grads_of([(i * 131) % 3000 for i in range(500)], 1)
+    a, b = clipper(one), clipper(two)
+    want, want2 = a.norm(each=True, total=True), b.norm(each=True, total=True)
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    for st in (s, t):
+        st.wait_stream(torch.cuda.current_stream())
+    got = [(a.norm(each=True, total=True, stream=s), b.norm(each=True, total=True, stream=t))
+           for _ in range(8)]
+    torch.cuda.synchronize()
+    for x, y in got:
+        assert all(torch.equal(p, q) for p, q in zip(x, want))
+        assert all(torch.equal(p, q) for p, q in zip(y, want2))
+
+
+def test_parts_of_a_model_reduce_to_the_whole():
+    """Squares of two halves added, as ranks do, give the norm of all; each half is
+    clipped by it."""
+    grads = grads_of([5000, 70001, 12, 333])
+    want, _ = ref_norms(grads, "l2")
+    halves = clipper(grads[:2]), clipper(grads[2:])
+    total = sum(h.norm(total=True)[1] for h in halves)
+    norm = total.sqrt().float()
+    assert_within("norm", norm, (want, 1.01 * U * want))
+    before = [g.clone() for g in grads]
+    for h in halves:
+        h.clip(1.5, norm=norm)
+    for g, b in zip(grads, before):
+        assert_within("out", g, ref_clip(b, norm, 1.5, g.dtype))

@@ -150,3 +150,12 @@ def test_the_layers_own_clipping():
     assert abs(norm.double() - want) <= 2.0 ** -23 * want
     for g, b in zip(L.grads(), before):
         assert torch.allclose(g.double(), b * (0.25 / (norm.double() + 1e-6)), rtol=2.0 ** -21, atol=1e-30)
+
+
+def test_backward_before_forward_is_refused():
+    from routing_permute_grouped_moe_amd.layer import BalanceLoss
+    cfg = synth.get_config("tiny")
+    L = make_layer(cfg, synth.make_inputs(cfg))
+    L.balance = BalanceLoss()
+    with pytest.raises(RuntimeError, match="before their forward"):
+        L.route_bwd()
