@@ -522,8 +522,8 @@ int moe_norm_bwd(const void* dy, const void* h, const void* dh, int dt, int M, i
 /* ---------------------------------------------------------------- norm of all gradients, clipping
  * Gradients g_0 .. g_{count-1} of any sizes, fp32 and bf16 mixed, given by a
  * host array that is read before the call returns.  A gradient is dense and
- * aligned to its elements (a view into a flat buffer will do); n may pass 2^31,
- * n == 0 is skipped and g may be NULL then.
+ * aligned to its elements (a view into a flat buffer will do); n may pass 2^31
+ * (below 2^40), n == 0 is skipped and g may be NULL then; count is at most 2^20.
  *   kind MOE_GRAD_L2:  norms[i] = sqrt(sum g_i^2),  norm = sqrt(sum of all squares)
  *   kind MOE_GRAD_MAX: norms[i] = max |g_i|,        norm = the largest
  * Squares and sums are fp64: no finite gradient overflows, and a NaN gives NaN.

@@ -6,6 +6,10 @@
 // launch's arguments (no copy to the device, and a captured launch keeps its
 // own).  A chunk's sum is kept in fp64 -- squares of every fp32 value are in its
 // range -- and a last launch adds the chunks in order.
+// Bound by HBM: 425 M gradients in bf16 (0.85 GB) have their norm in 147 us, 5.8
+// TB/s; clipped into fp32 485 us more, 5.3 TB/s, where a copy moves 5.1.  (Chunks
+// taken in reverse to find the end of the norm's pass in the cache, plain loads and
+// plain stores: 638 to 650 us together, 632 so.)
 #include <algorithm>
 #include <new>
 
@@ -16,10 +20,11 @@ namespace {
 constexpr int CLIP_NT = 256;
 constexpr int CLIP_WAVES = CLIP_NT / MOE_WAVE;
 constexpr int CLIP_SUM_NT = 1024;
-constexpr int NORM_TABLE = 176;      // gradients of one launch: tables below 4 KB
+constexpr int NORM_TABLE = 176;           // gradients of one launch: tables below 4 KB
 constexpr int CLIP_TABLE = 128;
 constexpr long long CLIP_CHUNK = 2048;    // elements of a chunk, at least
-// chunks, at most, but for one a gradient: of the norm, of what is scaled
+// chunks, at most, but for one a gradient: of the norm (all of them resident, and
+// few to add: 147 us above, 149 with 8192), of what is scaled
 constexpr long long NORM_CHUNKS = 2048, CLIP_CHUNKS = 8192;
 
 struct NormTable {
@@ -170,9 +175,9 @@ __global__ __launch_bounds__(CLIP_NT) void grad_part_kernel(Table t, long long c
   }
 }
 
-// Chunks of a gradient, and gradients.  A thread adds a gradient of few chunks, a
-// wave one of many: at most NORM_CHUNKS / FEW, since there are at most
-// NORM_CHUNKS chunks and one a gradient.
+// A thread adds a gradient of few chunks, a wave one of many (a wave for each of 700
+// gradients: 25 us, so 4.8).  Of more than FEW chunks are at most NORM_CHUNKS / FEW,
+// since there are at most NORM_CHUNKS chunks and one a gradient.
 constexpr int FEW = 16, MANY = NORM_CHUNKS / (FEW - 1) + 8;
 template <bool MAX>
 __global__ __launch_bounds__(CLIP_SUM_NT) void grad_norm_kernel(const double* part,

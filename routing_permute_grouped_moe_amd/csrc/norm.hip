@@ -2,6 +2,16 @@
 // gradients:
 //   h = x + residual,  q = (h - m) rstd,  y = q w + bias
 //   g = dy w,  dx = rstd (g - mean(g) - q mean(g q)) + dh,  dw = sum dy q,  db = sum dy
+//
+// Bound by HBM: every row is read once and stays in registers between its sums,
+// as 16-byte chunks of the storage type; the weight stays in registers from row
+// to row, and the next row is on its way while this one's sums are made.  The
+// backward keeps a column's part of dw and db in registers too; each workgroup
+// leaves one row of them, and a second launch adds those rows in fp64, in order.
+// Measured (one MI355X, where a 1 GiB copy moves 5.1 TB/s): 8192 x 7680 bf16 with
+// a residual 89 us (5.7 TB/s), its backward 95 us (5.3 TB/s; 5 us of it the
+// second launch); backwards of 4095 x 2048 fp32 and of 131071 x 128 bf16, 100 MB
+// each, 21.0 and 21.7 us; one row of 7680 3 us.
 #include "reduce.hpp"
 #include "validate.hpp"
 
@@ -11,7 +21,7 @@ constexpr int NORM_MAX_H = 16384;
 constexpr uint32_t NORM_OOB = 0x80000000u;   // past every row: reads zeros, stores are dropped
 
 // TPR threads hold a row, C chunks of 16 bytes each; rows of less than a
-// workgroup share one.
+// workgroup share one.  PRE: registers suffice for the next row and the weight.
 template <typename T, int TPR, int C, int THREADS>
 struct Rows {
   static constexpr int VEC = Elem<T>::VEC;
@@ -57,14 +67,19 @@ __device__ __forceinline__ float row_sum(float a, float2 (*red)[WAVES], int& tur
   return a;
 }
 
+template <bool STREAM>
+__device__ __forceinline__ u32x4 row_load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return STREAM ? buf_load16_nt(r, off) : buf_load16(r, off);
+}
+
 struct NormArgs {
   const void* x; const void* residual; const float* w; const float* bias;
   void* h; void* y; float* mean; float* rstd;
-  int M, H, rms, stream;
+  int M, H, rms;
   float eps, inv_h;
 };
 
-template <typename T, int TPR, int C, int NT_>
+template <typename T, int TPR, int C, int NT_, bool STREAM>
 __global__ __launch_bounds__(NT_) void norm_kernel(NormArgs a) {
   using R = Rows<T, TPR, C, NT_>;
   constexpr int VEC = R::VEC, ES = sizeof(T);
@@ -96,12 +111,10 @@ __global__ __launch_bounds__(NT_) void norm_kernel(NormArgs a) {
   u32x4 x[C], res[C];
   auto fetch = [&](int r0) {
     const auto rx = rows(a.x, r0), rr = rows(a.residual, r0);
-    if (a.stream) {
 #pragma unroll
-      for (int i = 0; i < C; ++i) x[i] = buf_load16_nt(rx, off[i]), res[i] = buf_load16_nt(rr, off[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < C; ++i) x[i] = buf_load16(rx, off[i]), res[i] = buf_load16(rr, off[i]);
+    for (int i = 0; i < C; ++i) {
+      x[i] = row_load<STREAM>(rx, off[i]);
+      res[i] = row_load<STREAM>(rr, off[i]);
     }
   };
   const int step = gridDim.x * R::G;
@@ -159,11 +172,11 @@ struct NormBwdArgs {
   const void* dy; const void* h; const void* dh; const float* w; const float* mean;
   const float* rstd;
   void* dx; float* dw; float* db; float* part;
-  int M, H, rms, stream, parts;
+  int M, H, rms, parts;
   float inv_h;
 };
 
-template <typename T, int TPR, int C, int NT_>
+template <typename T, int TPR, int C, int NT_, bool STREAM>
 __global__ __launch_bounds__(NT_) void norm_bwd_kernel(NormBwdArgs a) {
   using R = Rows<T, TPR, C, NT_>;
   constexpr int VEC = R::VEC, ES = sizeof(T);
@@ -206,12 +219,10 @@ __global__ __launch_bounds__(NT_) void norm_bwd_kernel(NormBwdArgs a) {
   float mean, rstd;
   auto fetch = [&](int r0) {
     const auto ry = rows(a.dy, r0), rx = rows(a.h, r0);
-    if (a.stream) {
 #pragma unroll
-      for (int i = 0; i < C; ++i) y[i] = buf_load16_nt(ry, off[i]), x[i] = buf_load16_nt(rx, off[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < C; ++i) y[i] = buf_load16(ry, off[i]), x[i] = buf_load16(rx, off[i]);
+    for (int i = 0; i < C; ++i) {
+      y[i] = row_load<STREAM>(ry, off[i]);
+      x[i] = row_load<STREAM>(rx, off[i]);
     }
     const int r = r0 + grp;
     mean = !a.rms && r < a.M ? a.mean[r] : 0.f;
@@ -225,14 +236,10 @@ __global__ __launch_bounds__(NT_) void norm_bwd_kernel(NormBwdArgs a) {
     float s1 = 0.f, s2 = 0.f;
     u32x4 yc[C], xc[C], ac[C];
     const float m = mean, rs = rstd;
+    // (asked for here and not with the next row: 95 us, 99 with it)
     const auto ra = rows(a.dx ? a.dh : nullptr, r0);
-    if (a.stream) {
 #pragma unroll
-      for (int i = 0; i < C; ++i) ac[i] = buf_load16_nt(ra, off[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < C; ++i) ac[i] = buf_load16(ra, off[i]);
-    }
+    for (int i = 0; i < C; ++i) ac[i] = row_load<STREAM>(ra, off[i]);
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       yc[i] = y[i], xc[i] = x[i];
@@ -349,9 +356,13 @@ struct Shape {
   int waves;        // resident in a CU
 };
 
-// Threads of a row by its 16-byte chunks.  Rows that a wave can hold need no
-// barrier; longer ones have at most two chunks a thread where registers allow
-// two rows in flight and the weight besides.
+// Threads of a row by its 16-byte chunks.  Where 64 lanes hold a row in two chunks
+// they do, without a barrier (1000 x 1024 bf16: 3.1 us, 3.8 with 256 threads a
+// row); from 256 chunks on 256 threads and more (8 x 2048 bf16: 2.5 us, 3.0 by a
+// wave; 8192 x 4096: 50 us at two chunks a thread, 53 by a wave), and two chunks a
+// thread rather than four (8192 x 7680: 91 us, 95 with four, 90 to 94 with one).  Workgroups
+// of a CU: enough rows in flight, which are 8 waves with a residual (91 us, 95 at
+// 16) and 16 without (52 us, 69 at 8).
 Shape norm_shape(int chunks, bool residual) {
   if (chunks <= 8) return {8, 1, 256, 16};
   if (chunks <= 16) return {16, 1, 256, 16};
@@ -365,6 +376,11 @@ Shape norm_shape(int chunks, bool residual) {
   if (chunks <= 2048) return {512, 4, 512, waves};
   return {1024, 4, 1024, 16};
 }
+// The backward: a workgroup's last row of sums is written and read again, so few
+// large workgroups, 8 waves a CU (8192 x 7680: 95 us, 101 at 16; 4095 x 2048 fp32:
+// 21 us, 23 in workgroups of 256 at 16 waves, 28 with one chunk a thread at 8),
+// but for rows of one chunk a thread, whose registers are few (131071 x 128: 21.6
+// us, 22.2 at 8 waves).  Above 1024 chunks 1024 threads without the next row.
 Shape norm_bwd_shape(int chunks) {
   if (chunks <= 8) return {8, 1, 512, 16};
   if (chunks <= 16) return {16, 1, 512, 16};
@@ -394,31 +410,34 @@ int norm_parts(int M, int H, int dt) {
   X(256, 2, 512) X(512, 2, 512) X(1024, 2, 1024) X(1024, 4, 1024)
 
 // (rows of bf16 end at 2048 chunks)
-template <typename T>
+template <typename T, bool STREAM>
 int norm_launch(const NormArgs& a, Shape s, hipStream_t st) {
   const dim3 grid(norm_blocks(a.M, s));
 #define X(P, N, TH)                                                                        \
   if constexpr (P * N * Elem<T>::VEC <= NORM_MAX_H)                                        \
     if (s.tpr == P && s.c == N)                                                            \
-      hipLaunchKernelGGL((norm_kernel<T, P, N, TH>), grid, dim3(TH), 0, st, a);
+      hipLaunchKernelGGL((norm_kernel<T, P, N, TH, STREAM>), grid, dim3(TH), 0, st, a);
   NORM_SHAPES(X)
 #undef X
   return moe_check_launch("moe_norm");
 }
-template <typename T>
+template <typename T, bool STREAM>
 int norm_bwd_launch(const NormBwdArgs& a, Shape s, hipStream_t st) {
   const dim3 grid(a.parts);
 #define X(P, N, TH)                                                                        \
   if constexpr (P * N * Elem<T>::VEC <= NORM_MAX_H)                                        \
     if (s.tpr == P && s.c == N)                                                            \
-      hipLaunchKernelGGL((norm_bwd_kernel<T, P, N, TH>), grid, dim3(TH), 0, st, a);
+      hipLaunchKernelGGL((norm_bwd_kernel<T, P, N, TH, STREAM>), grid, dim3(TH), 0, st, a);
   NORM_BWD_SHAPES(X)
 #undef X
   return moe_check_launch("moe_norm_bwd");
 }
 
-// Rows beyond what the 256 MB memory-side cache holds are read with the
-// streaming policy.
+// A call whose rows, read and written, are more than the 256 MB memory-side cache
+// holds reads them with the streaming policy (8192 x 7680, forward: 87 us, 91
+// without; 4095 x 2048 fp32, which the cache holds, 16 us with it and 12 without),
+// in a kernel of its own: with a branch between the two kinds of load the backward
+// of 8192 x 7680 took 105 us, so 95.  Stores are streaming always (87 and 94 us).
 bool norm_streams(long long bytes) { return bytes > (256LL << 20); }
 
 int norm_checks(const char* fn, int dt, int M, int H, int kind) {
@@ -475,10 +494,13 @@ extern "C" int moe_norm(const void* x, const void* residual, int dt, int M, int 
                     "%s: %s overlaps %s (h alone may be x's or the residual's buffer)", fn, out,
                     with);
   NormArgs a = {x, residual, w, bias, h, y, mean, rstd, M, H, kind == MOE_NORM_RMS,
-                norm_streams(mh * (residual ? 2 : 1)), eps, 1.0f / H};
+                eps, 1.0f / H};
   hipStream_t s = (hipStream_t)stream;
   const Shape shape = norm_shape(H * moe_dt_bytes(dt) / 16, residual != nullptr);
-  return dt == MOE_BF16 ? norm_launch<bf16_t>(a, shape, s) : norm_launch<float>(a, shape, s);
+  const bool far = norm_streams(mh * (2 + (residual != nullptr) + (h != nullptr)));
+  if (dt == MOE_BF16)
+    return far ? norm_launch<bf16_t, true>(a, shape, s) : norm_launch<bf16_t, false>(a, shape, s);
+  return far ? norm_launch<float, true>(a, shape, s) : norm_launch<float, false>(a, shape, s);
 }
 
 extern "C" size_t moe_norm_bwd_workspace_bytes(int M, int H, int dt) {
@@ -527,12 +549,16 @@ extern "C" int moe_norm_bwd(const void* dy, const void* h, const void* dh, int d
                       outs[i].name, with);
   }
   NormBwdArgs a = {dy, h, dh, w, mean, rstd, dx, dw, db, sums ? (float*)ws : nullptr, M, H,
-                   kind == MOE_NORM_RMS, norm_streams(2 * mh), norm_parts(M, H, dt), 1.0f / H};
+                   kind == MOE_NORM_RMS, norm_parts(M, H, dt), 1.0f / H};
   hipStream_t s = (hipStream_t)stream;
   if (M > 0 && (dx != nullptr || sums)) {
     const Shape shape = norm_bwd_shape(H * moe_dt_bytes(dt) / 16);
-    MOE_TRY(dt == MOE_BF16 ? norm_bwd_launch<bf16_t>(a, shape, s)
-                           : norm_bwd_launch<float>(a, shape, s));
+    const bool far = norm_streams(mh * (2 + (dx != nullptr) + (dx != nullptr && dh != nullptr)));
+    const int st = dt == MOE_BF16 ? far ? norm_bwd_launch<bf16_t, true>(a, shape, s)
+                                        : norm_bwd_launch<bf16_t, false>(a, shape, s)
+                   : far          ? norm_bwd_launch<float, true>(a, shape, s)
+                                  : norm_bwd_launch<float, false>(a, shape, s);
+    MOE_TRY(st);
   }
   if (!sums) return MOE_OK;
   hipLaunchKernelGGL(norm_sum_kernel, dim3((2 * H + SUM_COLS - 1) / SUM_COLS),
