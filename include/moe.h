@@ -553,6 +553,13 @@ int moe_grad_norm(const moe_grad* grads, int count, int kind, float* norm, float
 int moe_grad_clip(const moe_grad* grads, int count, const float* norm, float max_norm,
                   moe_stream_t stream);
 
+/* Both in one call, with a launch less where the gradients are few and small: norm
+ * (and norms, nullable) as moe_grad_norm writes them, then every gradient scaled by
+ * its own norm as moe_grad_clip does; the same bits.  ws as moe_grad_norm's; norm,
+ * norms and ws share no memory with an out. */
+int moe_grad_norm_clip(const moe_grad* grads, int count, int kind, float max_norm, float* norm,
+                       float* norms, void* ws, size_t ws_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -105,6 +105,7 @@ _SIGS = {
     "moe_grad_norm_workspace_bytes": (_SZ, [ctypes.POINTER(Grad), _I]),
     "moe_grad_norm": (_I, [ctypes.POINTER(Grad), _I, _I, _P, _P, _P, _P, _SZ, _P]),
     "moe_grad_clip": (_I, [ctypes.POINTER(Grad), _I, _P, _F, _P]),
+    "moe_grad_norm_clip": (_I, [ctypes.POINTER(Grad), _I, _I, _F, _P, _P, _P, _SZ, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -380,3 +381,8 @@ def moe_grad_norm(grads, count, kind, norm, norms, total, ws, ws_bytes, stream=N
 
 def moe_grad_clip(grads, count, norm, max_norm, stream=None):
     _call("moe_grad_clip", grads, count, addr(norm), max_norm, _stream(stream))
+
+
+def moe_grad_norm_clip(grads, count, kind, max_norm, norm, norms, ws, ws_bytes, stream=None):
+    _call("moe_grad_norm_clip", grads, count, kind, max_norm, addr(norm), addr(norms), addr(ws),
+          ws_bytes, _stream(stream))

@@ -26,6 +26,10 @@ constexpr long long CLIP_CHUNK = 2048;    // elements of a chunk, at least
 // chunks, at most, but for one a gradient: of the norm (all of them resident, and
 // few to add: 147 us above, 149 with 8192), of what is scaled
 constexpr long long NORM_CHUNKS = 2048, CLIP_CHUNKS = 8192;
+// chunks, at most, where each workgroup that scales adds the parts itself, instead of
+// a launch between (a call on 6 gradients of 32768 values: 12.1 us, 14.5 with the
+// launch; 1 M values 11.5 and 14.4, 4 M values 23 and 14.3)
+constexpr long long FUSED_CHUNKS = 512;
 
 struct NormTable {
   const void* g[NORM_TABLE];
@@ -180,10 +184,8 @@ __global__ __launch_bounds__(CLIP_NT) void grad_part_kernel(Table t, long long c
 // since there are at most NORM_CHUNKS chunks and one a gradient.
 constexpr int FEW = 16, MANY = NORM_CHUNKS / (FEW - 1) + 8;
 template <bool MAX>
-__global__ __launch_bounds__(CLIP_SUM_NT) void grad_norm_kernel(const double* part,
-                                                                const int* first, int count,
-                                                                float* norm, float* norms,
-                                                                double* total) {
+__device__ __forceinline__ double grad_total(const double* part, const int* first, int count,
+                                             float* norms) {
   constexpr int WAVES = CLIP_SUM_NT / MOE_WAVE;
   __shared__ double red[WAVES];
   __shared__ int found, list[MANY], sorted[MANY];
@@ -225,10 +227,19 @@ __global__ __launch_bounds__(CLIP_SUM_NT) void grad_norm_kernel(const double* pa
   }
   if (lane == 0) red[wave] = all;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    all = red[0];
+  all = red[0];
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) all = join<MAX>(all, red[w]);
+  for (int w = 1; w < WAVES; ++w) all = join<MAX>(all, red[w]);
+  return all;
+}
+
+template <bool MAX>
+__global__ __launch_bounds__(CLIP_SUM_NT) void grad_norm_kernel(const double* part,
+                                                                const int* first, int count,
+                                                                float* norm, float* norms,
+                                                                double* total) {
+  const double all = grad_total<MAX>(part, first, count, norms);
+  if (threadIdx.x == 0) {
     norm[0] = (float)(MAX ? all : sqrt(all));
     if (total) total[0] = all;
   }
@@ -237,9 +248,9 @@ __global__ __launch_bounds__(CLIP_SUM_NT) void grad_norm_kernel(const double* pa
 // n values times c.  A thread's store is 16 bytes and a wave's 1 KB without
 // gaps, whatever a thread loads for it (425 M values, bf16 to fp32: 485 us, 5.3
 // TB/s; with 32 bytes a thread, whose streaming stores leave gaps, 700).
-template <typename G, typename O>
+template <int NT, typename G, typename O>
 __device__ __forceinline__ void scale_chunk(const G* g, O* out, long long n, float c) {
-  constexpr int VEC = Elem<O>::VEC, STEP = CLIP_NT * VEC, U = 4;
+  constexpr int VEC = Elem<O>::VEC, STEP = NT * VEC, U = 4;
   const long long whole = n / VEC * VEC;
   long long i = (long long)threadIdx.x * VEC;
   auto put = [&](O* to, float (&v)[VEC]) {
@@ -263,21 +274,39 @@ __device__ __forceinline__ void scale_chunk(const G* g, O* out, long long n, flo
     store1(out + whole + threadIdx.x, load1(g + whole + threadIdx.x) * c);
 }
 
-__global__ __launch_bounds__(CLIP_NT) void grad_clip_kernel(ClipTable t, long long chunk,
-                                                            const float* norm, float max_norm) {
-  const int b = blockIdx.x, i = grad_of(t, b);
-  float c = max_norm / (norm[0] + 1e-6f);
+// Chunk b of the table, scaled for a norm.
+template <int NT>
+__device__ __forceinline__ void clip_chunk(const ClipTable& t, int b, long long chunk, float norm,
+                                           float max_norm) {
+  const int i = grad_of(t, b);
+  float c = max_norm / (norm + 1e-6f);
   c = c > 1.f ? 1.f : c;        // (a NaN stays one)
   if (c == 1.f && t.out[i] == t.g[i]) return;
   const unsigned long long word = t.n[i];
   const long long n = (long long)(word & N_MASK), at = (long long)(b - t.first[i]) * chunk;
   const long long len = n - at < chunk ? n - at : chunk;
   if (!(word & G_BF16))
-    scale_chunk((const float*)t.g[i] + at, (float*)t.out[i] + at, len, c);
+    scale_chunk<NT>((const float*)t.g[i] + at, (float*)t.out[i] + at, len, c);
   else if (word & OUT_BF16)
-    scale_chunk((const bf16_t*)t.g[i] + at, (bf16_t*)t.out[i] + at, len, c);
+    scale_chunk<NT>((const bf16_t*)t.g[i] + at, (bf16_t*)t.out[i] + at, len, c);
   else
-    scale_chunk((const bf16_t*)t.g[i] + at, (float*)t.out[i] + at, len, c);
+    scale_chunk<NT>((const bf16_t*)t.g[i] + at, (float*)t.out[i] + at, len, c);
+}
+__global__ __launch_bounds__(CLIP_NT) void grad_clip_kernel(ClipTable t, long long chunk,
+                                                            const float* norm, float max_norm) {
+  clip_chunk<CLIP_NT>(t, blockIdx.x, chunk, norm[0], max_norm);
+}
+// The same, and the norm from its parts, by every workgroup for itself.
+template <bool MAX>
+__global__ __launch_bounds__(CLIP_SUM_NT) void grad_norm_clip_kernel(
+    ClipTable t, long long chunk, const double* part, const int* first, float* norm, float* norms,
+    float max_norm) {
+  const bool one = blockIdx.x == 0;
+  const double all = grad_total<MAX>(part, first, t.count, one ? norms : nullptr);
+  const float by = (float)(MAX ? all : sqrt(all));
+  if (one && threadIdx.x == 0) norm[0] = by;
+  if ((int)blockIdx.x < t.first[t.count])     // (no chunk: one workgroup, for the norm)
+    clip_chunk<CLIP_SUM_NT>(t, blockIdx.x, chunk, by, max_norm);
 }
 
 // Elements of a chunk: a whole number of all lanes' loads.
@@ -349,9 +378,6 @@ int clip_overlaps(const char* fn, const moe_grad* g, int count) {
   return st;
 }
 
-}  // namespace
-
-namespace {
 // part [chunks] fp64, first [count + 1], and beyond a table's length g, n [count]
 struct NormWs {
   long long chunk, chunks;
@@ -369,29 +395,21 @@ NormWs norm_ws(const moe_grad* grads, int count) {
   w.total = w.n + list;
   return w;
 }
-}  // namespace
 
-extern "C" size_t moe_grad_norm_workspace_bytes(const moe_grad* grads, int count) {
-  if (grad_checks("moe_grad_norm_workspace_bytes", grads, count, false) != MOE_OK) return 0;
-  return norm_ws(grads, count).total;
-}
-
-extern "C" int moe_grad_norm(const moe_grad* grads, int count, int kind, float* norm, float* norms,
-                             double* total, void* ws, size_t ws_bytes, moe_stream_t stream) {
-  const char* fn = "moe_grad_norm";
-  MOE_TRY(grad_checks(fn, grads, count, false));
+int norm_checks(const char* fn, const moe_grad* grads, int count, int kind, const float* norm,
+                const float* norms, const double* total, const void* ws, size_t ws_bytes,
+                const NormWs& lay) {
   if (kind != MOE_GRAD_L2 && kind != MOE_GRAD_MAX)
     return moe_fail(MOE_ERR_INVALID_ARG, "%s: kind %d is none of the MOE_GRAD values", fn, kind);
   MOE_TRY(moe_need_ptr(norm, fn, "norm", 4));
   MOE_TRY(moe_opt_ptr(norms, fn, "norms", 4));
   MOE_TRY(moe_opt_ptr(total, fn, "total", 8));
   MOE_TRY(moe_need_ptr(ws, fn, "ws", 256));
-  const NormWs lay = norm_ws(grads, count);
-  const size_t need = lay.total;
-  if (ws_bytes < need)
-    return moe_fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", fn, ws_bytes, need);
+  if (ws_bytes < lay.total)
+    return moe_fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", fn, ws_bytes,
+                    lay.total);
   const MoeRange outs[] = {{norm, 4, "norm"}, {norms, 4LL * count, "norms"}, {total, 8, "total"},
-                           {ws, (long long)need, "ws"}};
+                           {ws, (long long)lay.total, "ws"}};
   for (int i = 0; i < 4; ++i) {
     const char* with = nullptr;
     for (int j = 0; j < i && with == nullptr; ++j) with = moe_shares(outs[i], {outs[j]});
@@ -402,8 +420,23 @@ extern "C" int moe_grad_norm(const moe_grad* grads, int count, int kind, float* 
       return moe_fail(MOE_ERR_INVALID_ARG, "%s: %s needs a buffer of its own, it overlaps %s", fn,
                       outs[i].name, with);
   }
-  hipStream_t s = (hipStream_t)stream;
-  const bool max = kind == MOE_GRAD_MAX;
+  return MOE_OK;
+}
+int clip_checks(const char* fn, const moe_grad* grads, int count, const float* norm,
+                float max_norm) {
+  if (!(max_norm >= 0.f))
+    return moe_fail(MOE_ERR_INVALID_ARG, "%s: max_norm = %g is negative or NaN", fn, max_norm);
+  MOE_TRY(moe_need_ptr(norm, fn, "norm", 4));
+  for (int i = 0; i < count; ++i)
+    if (moe_shares({grads[i].out, grads[i].n * moe_dt_bytes(grads[i].out_dt), "out"},
+                   {{norm, 4, "norm"}}))
+      return moe_fail(MOE_ERR_INVALID_ARG, "%s: out %d overlaps norm", fn, i);
+  return clip_overlaps(fn, grads, count);
+}
+
+// The parts of the norm, in ws.
+int launch_parts(const char* fn, const moe_grad* grads, int count, bool max, const NormWs& lay,
+                 void* ws, hipStream_t s) {
   double* const part = (double*)ws;
   int* const first = (int*)((char*)ws + lay.first);
   NormList list = {(const void**)((char*)ws + lay.g), (unsigned long long*)((char*)ws + lay.n),
@@ -432,18 +465,22 @@ extern "C" int moe_grad_norm(const moe_grad* grads, int count, int kind, float* 
                          lay.chunk, part, first);
     MOE_TRY(moe_check_launch(fn));
   }
+  if (count <= NORM_TABLE) return MOE_OK;
   // more gradients than a table holds: tables into memory, then one launch for all
   // (700 gradients of 40000 values: 32 us, where a launch a table takes 65)
-  if (count > NORM_TABLE) {
-    if (max)
-      hipLaunchKernelGGL((grad_part_kernel<true, NormList>), grid, dim3(CLIP_NT), 0, s, list,
-                         lay.chunk, part, nullptr);
-    else
-      hipLaunchKernelGGL((grad_part_kernel<false, NormList>), grid, dim3(CLIP_NT), 0, s, list,
-                         lay.chunk, part, nullptr);
-    MOE_TRY(moe_check_launch(fn));
-  }
-  if (kind == MOE_GRAD_MAX)
+  if (max)
+    hipLaunchKernelGGL((grad_part_kernel<true, NormList>), grid, dim3(CLIP_NT), 0, s, list,
+                       lay.chunk, part, nullptr);
+  else
+    hipLaunchKernelGGL((grad_part_kernel<false, NormList>), grid, dim3(CLIP_NT), 0, s, list,
+                       lay.chunk, part, nullptr);
+  return moe_check_launch(fn);
+}
+int launch_norm(const char* fn, int count, bool max, const NormWs& lay, void* ws, float* norm,
+                float* norms, double* total, hipStream_t s) {
+  const double* const part = (const double*)ws;
+  const int* const first = (const int*)((char*)ws + lay.first);
+  if (max)
     hipLaunchKernelGGL(grad_norm_kernel<true>, dim3(1), dim3(CLIP_SUM_NT), 0, s, part, first,
                        count, norm, norms, total);
   else
@@ -452,36 +489,90 @@ extern "C" int moe_grad_norm(const moe_grad* grads, int count, int kind, float* 
   return moe_check_launch(fn);
 }
 
-extern "C" int moe_grad_clip(const moe_grad* grads, int count, const float* norm, float max_norm,
-                             moe_stream_t stream) {
-  const char* fn = "moe_grad_clip";
-  MOE_TRY(grad_checks(fn, grads, count, true));
-  if (!(max_norm >= 0.f))
-    return moe_fail(MOE_ERR_INVALID_ARG, "%s: max_norm = %g is negative or NaN", fn, max_norm);
-  MOE_TRY(moe_need_ptr(norm, fn, "norm", 4));
-  for (int i = 0; i < count; ++i)
-    if (moe_shares({grads[i].out, grads[i].n * moe_dt_bytes(grads[i].out_dt), "out"},
-                   {{norm, 4, "norm"}}))
-      return moe_fail(MOE_ERR_INVALID_ARG, "%s: out %d overlaps norm", fn, i);
-  MOE_TRY(clip_overlaps(fn, grads, count));
-  hipStream_t s = (hipStream_t)stream;
+ClipTable clip_table(const moe_grad* grads, int count, long long chunk) {
+  ClipTable t;
+  t.count = count;
+  t.first[0] = 0;
+  for (int i = 0; i < count; ++i) {
+    t.g[i] = grads[i].g;
+    t.out[i] = grads[i].out;
+    t.n[i] = (unsigned long long)grads[i].n | (grads[i].dt == MOE_BF16 ? G_BF16 : 0) |
+             (grads[i].out_dt == MOE_BF16 ? OUT_BF16 : 0);
+    t.first[i + 1] = t.first[i] + (int)((grads[i].n + chunk - 1) / chunk);
+  }
+  return t;
+}
+int launch_clip(const char* fn, const moe_grad* grads, int count, const float* norm,
+                float max_norm, hipStream_t s) {
   const long long chunk = chunk_of(grads, count, CLIP_CHUNKS);
   for (int g0 = 0; g0 < count; g0 += CLIP_TABLE) {
-    ClipTable t;
-    t.count = std::min(CLIP_TABLE, count - g0);
-    t.first[0] = 0;
-    for (int i = 0; i < t.count; ++i) {
-      const moe_grad& g = grads[g0 + i];
-      t.g[i] = g.g;
-      t.out[i] = g.out;
-      t.n[i] = (unsigned long long)g.n | (g.dt == MOE_BF16 ? G_BF16 : 0) |
-               (g.out_dt == MOE_BF16 ? OUT_BF16 : 0);
-      t.first[i + 1] = t.first[i] + (int)((g.n + chunk - 1) / chunk);
-    }
+    const ClipTable t = clip_table(grads + g0, std::min(CLIP_TABLE, count - g0), chunk);
     if (t.first[t.count] == 0) continue;
     hipLaunchKernelGGL(grad_clip_kernel, dim3(t.first[t.count]), dim3(CLIP_NT), 0, s, t, chunk,
                        norm, max_norm);
     MOE_TRY(moe_check_launch(fn));
   }
   return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" size_t moe_grad_norm_workspace_bytes(const moe_grad* grads, int count) {
+  if (grad_checks("moe_grad_norm_workspace_bytes", grads, count, false) != MOE_OK) return 0;
+  return norm_ws(grads, count).total;
+}
+
+extern "C" int moe_grad_norm(const moe_grad* grads, int count, int kind, float* norm, float* norms,
+                             double* total, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  const char* fn = "moe_grad_norm";
+  MOE_TRY(grad_checks(fn, grads, count, false));
+  const NormWs lay = norm_ws(grads, count);
+  MOE_TRY(norm_checks(fn, grads, count, kind, norm, norms, total, ws, ws_bytes, lay));
+  hipStream_t s = (hipStream_t)stream;
+  const bool max = kind == MOE_GRAD_MAX;
+  MOE_TRY(launch_parts(fn, grads, count, max, lay, ws, s));
+  return launch_norm(fn, count, max, lay, ws, norm, norms, total, s);
+}
+
+extern "C" int moe_grad_clip(const moe_grad* grads, int count, const float* norm, float max_norm,
+                             moe_stream_t stream) {
+  const char* fn = "moe_grad_clip";
+  MOE_TRY(grad_checks(fn, grads, count, true));
+  MOE_TRY(clip_checks(fn, grads, count, norm, max_norm));
+  return launch_clip(fn, grads, count, norm, max_norm, (hipStream_t)stream);
+}
+
+extern "C" int moe_grad_norm_clip(const moe_grad* grads, int count, int kind, float max_norm,
+                                  float* norm, float* norms, void* ws, size_t ws_bytes,
+                                  moe_stream_t stream) {
+  const char* fn = "moe_grad_norm_clip";
+  MOE_TRY(grad_checks(fn, grads, count, true));
+  const NormWs lay = norm_ws(grads, count);
+  MOE_TRY(norm_checks(fn, grads, count, kind, norm, norms, nullptr, ws, ws_bytes, lay));
+  MOE_TRY(clip_checks(fn, grads, count, norm, max_norm));
+  for (int i = 0; i < count; ++i) {   // (the parts and the norms are read while outs are written)
+    const char* with = moe_shares(
+        {grads[i].out, grads[i].n * moe_dt_bytes(grads[i].out_dt), "out"},
+        {{norms, 4LL * count, "norms"}, {ws, (long long)lay.total, "ws"}});
+    if (with != nullptr)
+      return moe_fail(MOE_ERR_INVALID_ARG, "%s: out %d overlaps %s", fn, i, with);
+  }
+  hipStream_t s = (hipStream_t)stream;
+  const bool max = kind == MOE_GRAD_MAX;
+  MOE_TRY(launch_parts(fn, grads, count, max, lay, ws, s));
+  if (count > CLIP_TABLE || lay.chunks > FUSED_CHUNKS) {
+    MOE_TRY(launch_norm(fn, count, max, lay, ws, norm, norms, nullptr, s));
+    return launch_clip(fn, grads, count, norm, max_norm, s);
+  }
+  const ClipTable t = clip_table(grads, count, lay.chunk);
+  const double* const part = (const double*)ws;
+  const int* const first = (const int*)((char*)ws + lay.first);
+  const dim3 grid(lay.chunks > 0 ? (unsigned)lay.chunks : 1);
+  if (max)
+    hipLaunchKernelGGL(grad_norm_clip_kernel<true>, grid, dim3(CLIP_SUM_NT), 0, s, t, lay.chunk,
+                       part, first, norm, norms, max_norm);
+  else
+    hipLaunchKernelGGL(grad_norm_clip_kernel<false>, grid, dim3(CLIP_SUM_NT), 0, s, t, lay.chunk,
+                       part, first, norm, norms, max_norm);
+  return moe_check_launch(fn);
 }

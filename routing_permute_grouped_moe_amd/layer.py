@@ -779,39 +779,37 @@ class GradClip:
                           {v: k for k, v in GRAD_NORMS.items()}[self.kind])
         return self._arr
 
-    def _norm(self, arr, st, each=False, total=False):
-        dev, n = self.device, len(self.grads)
-        norm = torch.empty((), dtype=torch.float32, device=dev)
-        norms = torch.empty(n, dtype=torch.float32, device=dev) if each else None
-        whole = torch.empty((), dtype=torch.float64, device=dev) if total else None
-        ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=dev)
-        abi.moe_grad_norm(arr, n, self.kind, norm, norms, whole, ws, self._ws_bytes, st)
-        return norm, norms, whole
-
     def norm(self, each=False, total=False, stream=None):
         """The norm (fp32, no dimensions), with ``each`` also those of the
         gradients one by one [n], with ``total`` also the sum of all squares in
         64 bits (the maximum): what ranks that hold parts of a model reduce."""
-        arr = self._array()
+        arr, dev, n = self._array(), self.device, len(self.grads)
 
         def call(st):
-            norm, norms, whole = self._norm(arr, st, each, total)
+            norm = torch.empty((), dtype=torch.float32, device=dev)
+            norms = torch.empty(n, dtype=torch.float32, device=dev) if each else None
+            whole = torch.empty((), dtype=torch.float64, device=dev) if total else None
+            ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=dev)
+            abi.moe_grad_norm(arr, n, self.kind, norm, norms, whole, ws, self._ws_bytes, st)
             more = tuple(t for t in (norms, whole) if t is not None)
             return (norm, *more) if more else norm
-        return _on(self.device, stream, call, *self.grads)
+        return _on(dev, stream, call, *self.grads)
 
     def clip(self, max_norm: float, norm=None, stream=None):
         """Scales the gradients by min(1, max_norm / (norm + 1e-6)); returns the
         norm.  ``norm``: one fp32 value to take instead of the gradients' own."""
-        arr = self._array()
+        arr, dev, n = self._array(), self.device, len(self.grads)
         if norm is not None:
             if norm.numel() != 1:
                 raise ValueError(f"norm has {norm.numel()} values, not 1")
-            _check("norm", norm, torch.float32, self.device, *norm.shape,
-                   beside="the gradients are")
+            _check("norm", norm, torch.float32, dev, *norm.shape, beside="the gradients are")
 
         def call(st):
-            by = self._norm(arr, st)[0] if norm is None else norm
-            abi.moe_grad_clip(arr, len(self.grads), by, max_norm, st)
-            return by
-        return _on(self.device, stream, call, norm, *self._tensors)
+            if norm is not None:
+                abi.moe_grad_clip(arr, n, norm, max_norm, st)
+                return norm
+            own = torch.empty((), dtype=torch.float32, device=dev)
+            ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=dev)
+            abi.moe_grad_norm_clip(arr, n, self.kind, max_norm, own, None, ws, self._ws_bytes, st)
+            return own
+        return _on(dev, stream, call, norm, *self._tensors)

@@ -278,3 +278,26 @@ def test_parts_of_a_model_reduce_to_the_whole():
         h.clip(1.5, norm=norm)
     for g, b in zip(grads, before):
         assert_within("out", g, ref_clip(b, norm, 1.5, g.dtype))
+
+
+@pytest.mark.parametrize("sizes", [[1], [0, 0, 3], [0], [2048] * 128, [2049] * 129, [8000] * 128,
+                                   [1048576], [1048577], [300000, 7, 0, 600000, 100000], [70000] * 20])
+@pytest.mark.parametrize("kind", ["l2", "max"])
+def test_in_one_call_or_two(sizes, kind):
+    """On either side of where the norm's last launch goes into the scaling: the bits of
+    the norm by itself and of scaling by it."""
+    grads = grads_of(sizes)
+    one, two = [torch.empty_like(g) for g in grads], [torch.empty_like(g) for g in grads]
+    norm = clipper(grads, kind=kind).norm()
+    got = clipper(grads, outs=one, kind=kind).clip(0.05)
+    clipper(grads, outs=two, kind=kind).clip(0.05, norm=norm)
+    assert torch.equal(got, norm)
+    assert all(torch.equal(a, b) for a, b in zip(one, two))
+    from routing_permute_grouped_moe_amd import abi
+    a = abi.grads(grads, one)
+    nb = abi.moe_grad_norm_workspace_bytes(a, len(grads))
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    n1, each = torch.empty(1, device="cuda"), torch.empty(len(grads), device="cuda")
+    abi.moe_grad_norm_clip(a, len(grads), abi.MOE_GRAD_MAX if kind == "max" else abi.MOE_GRAD_L2, 0.05, n1,
+                           each, ws, nb)
+    assert torch.equal(each, clipper(grads, kind=kind).norm(each=True)[1]) and n1.item() == norm.item()

@@ -249,6 +249,25 @@ def test_grad_clip_refuses(abi, rows, max_norm, norm, text):
     refused(abi, "moe_grad_clip", args, "INVALID_ARG", text)
 
 
+@pytest.mark.parametrize("rows,change,status,text", [
+    ([(A, A, 5, 0, 0)], {"kind": 3}, "INVALID_ARG", "kind 3"),
+    ([(A, A, 5, 0, 0)], {"max_norm": -0.5}, "INVALID_ARG", "max_norm"),
+    ([(A, A, 5, 0, 0)], {"norm": None}, "INVALID_ARG", "norm is NULL"),
+    ([(A, A, 5, 0, 0)], {"ws_bytes": 64}, "WORKSPACE", "workspace 64"),
+    ([(A, None, 5, 0, 0)], {}, "INVALID_ARG", "an out is NULL"),
+    ([(A, C, 5, 0, 1)], {}, "INVALID_ARG", "neither its gradient's nor MOE_F32"),
+    ([(A, A, 5, 0, 0), (A + 8, A + 8, 5, 0, 0)], {}, "INVALID_ARG", "also another's"),
+    ([(A, B + 4, 5, 0, 0)], {"norms": B + 16}, "INVALID_ARG", "overlaps norms"),
+    ([(A, B, 5, 0, 0)], {}, "INVALID_ARG", "out 0 overlaps norm"),
+    ([(A, W + 16, 5, 0, 0)], {}, "INVALID_ARG", "out 0 overlaps ws"),
+    ([(A, A, 5, 0, 0)], {"norm": A}, "INVALID_ARG", "norm needs a buffer of its own"),
+])
+def test_grad_norm_clip_refuses(abi, rows, change, status, text):
+    args = {**dict(grads=arr(abi, *rows), count=len(rows), kind=0, max_norm=1.0, norm=B, norms=None,
+                   ws=W, ws_bytes=1 << 26, stream=None), **change}
+    refused(abi, "moe_grad_norm_clip", args, status, text)
+
+
 def test_clip_of_nothing_is_a_noop(abi):
     args = dict(grads=None, count=0, norm=B, max_norm=1.0, stream=None)
     assert abi._lib.moe_grad_clip(*args.values()) == abi.MOE_OK
