@@ -2,7 +2,9 @@
  * moe.h -- C ABI of a single-GPU MoE expert layer for AMD Instinct MI355X
  * (gfx950): softmax top-k routing, permute into per-expert groups, grouped
  * SwiGLU GEMM (forward, backward dX, backward dW), unpermute + gate-weighted
- * combine, and the backward of each step.
+ * combine, and the backward of each step; for a training step around it row
+ * norms, the router's losses and gradient clipping; for serving the layer of
+ * few tokens; and linear products.
  *
  * Sources, cited by page title and section:
  *  [CANN-MoE]  "MoE算子优化：动态路由硬件加速与零拷贝通信实践" (gtnt.cn):

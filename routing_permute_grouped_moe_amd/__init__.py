@@ -1,5 +1,6 @@
 """MI355X-native MoE expert layer: routing, permute, grouped SwiGLU GEMM,
-unpermute/combine and their backward, as hand-written HIP kernels behind a
+unpermute/combine and their backward, with row norms, the router's losses and
+gradient clipping around it, as hand-written HIP kernels behind a
 C ABI (``include/moe.h``).  ``abi`` is the ctypes binding; ``layer`` strings
 the calls together for one layer."""
 

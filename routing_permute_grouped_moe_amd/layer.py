@@ -24,6 +24,10 @@ expert owns C rows, pairs past an expert's first C (in token order) are
 dropped, unfilled rows are zero, and the grouped GEMM runs on the padded
 groups.
 
+With ``balance`` (a :class:`BalanceLoss`) the forward computes the router's losses
+after the routing and the backward takes their gradient into dlogits, in one pass
+with the gates'.  Without it the layer makes the calls it always made.
+
 Experts outside ``[g0, g0+G)`` are remote: their rows are moved by the
 permute and the combine, their expert outputs and input gradients are zero
 (the buffers are cleared once at allocation and never written), and they get
