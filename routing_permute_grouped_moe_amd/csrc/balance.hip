@@ -24,25 +24,29 @@ namespace {
 constexpr int BAL_NT = 1024;                  // forward
 constexpr int BAL_WAVES = BAL_NT / MOE_WAVE;
 constexpr int BAL_BWD_NT = 256;
-constexpr int BAL_MAX_S = 65535;              // sequences: a grid's second dimension
+// sequences from which on each is added by a wave, not a workgroup (8192 tokens of 256
+// experts in 24 sequences: 17.2 and 14.3 us, in 64 17.8 and 17.5, in 1000 32 and 75)
+constexpr int BAL_MANY = 64;
+constexpr int BAL_MAX_S = 65535;              // sequences
 constexpr uint32_t BAL_OOB = 0xffffffffu;     // past every tensor: reads zeros
 
 // Lanes of a token in the forward: a wave has one of many experts, or several of
 // few, whose sums over lanes then cost as much as one's (65536 tokens of 64
 // experts: 19.5 -> 13.1 us, 65521 of 256 22.3 -> 21.0; four of 256 a wave 21.6).
 int bal_lanes(int E) { return E <= 64 ? 16 : E <= 256 ? 32 : 64; }
-// Tokens of a block: at most 256 blocks, one for each CU, of whole rounds of its waves.
-int bal_block_tokens(int T, int E) {
+// Tokens of a block: at most 256 blocks, one for each CU, of whole rounds of its
+// waves; few tokens in few sequences are one block.
+bool bal_one(int T, int E, int S) { return T <= 4 * (BAL_NT / bal_lanes(E)) && S <= 16; }
+int bal_block_tokens(int T, int E, int S) {
+  if (bal_one(T, E, S)) return T > 0 ? T : 1;
   const int round = BAL_NT / bal_lanes(E);
-  if (T <= 4 * round) return T > 0 ? T : 1;
   const long long per = ((long long)T + 255) / 256;
-  return (int)((per + round - 1) / round * round);
+  return per > 0 ? (int)((per + round - 1) / round * round) : round;
 }
-int bal_blocks(int T, int E) {
-  const int tb = bal_block_tokens(T, E);
+int bal_blocks(int T, int E, int S) {
+  const int tb = bal_block_tokens(T, E, S);
   return T > 0 ? (int)(((long long)T + tb - 1) / tb) : 1;
 }
-bool bal_one(int T, int E, int S) { return bal_blocks(T, E) == 1 && S <= 16; }
 
 struct BalWs {
   size_t q, c, z, n, term, total;
@@ -50,7 +54,7 @@ struct BalWs {
 BalWs bal_ws(int T, int E, int S) {
   BalWs w = {};
   if (bal_one(T, E, S)) return w;
-  const size_t rows = (size_t)bal_blocks(T, E) + S, cg = (E + MOE_WAVE - 1) / MOE_WAVE;
+  const size_t rows = (size_t)bal_blocks(T, E, S) + S, cg = (E + MOE_WAVE - 1) / MOE_WAVE;
   auto up = [](size_t b) { return (b + 255) / 256 * 256; };
   w.q = 256;                                  // (in front: the count of workgroups that are done)
   w.c = w.q + up(rows * E * 4);
@@ -262,47 +266,54 @@ __device__ __forceinline__ T get(const T* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Rows of a sequence: counts, probabilities and its part of the losses, 64
-// experts a workgroup, a 16th of the rows a wave.  The workgroup that is done
-// last adds the parts, in their order.
+// Rows of a sequence: counts, probabilities and its part of the losses, for 64
+// experts by PER waves, each its share of the rows; 16 / PER sequences a workgroup.
+// The workgroup that is done last adds the parts, in their order.
+template <int PER>
 __global__ __launch_bounds__(BAL_NT) void balance_sum_kernel(BalArgs a) {
+  constexpr int SEQ = BAL_WAVES / PER;
   __shared__ double q_s[BAL_WAVES][MOE_WAVE], z_s[BAL_WAVES], b_s[BAL_WAVES];
   __shared__ int c_s[BAL_WAVES][MOE_WAVE];
   __shared__ long long n_s[BAL_WAVES];
   __shared__ int last;
-  const int lane = threadIdx.x % MOE_WAVE, wave = threadIdx.x / MOE_WAVE;
-  const int s = blockIdx.y, E = a.E, e = blockIdx.x * MOE_WAVE + lane, cg = gridDim.x;
-  const int lo = a.seq ? bal_seq(a.seq, s, a.T) : 0, hi = a.seq ? bal_seq(a.seq, s + 1, a.T) : a.T;
+  const int lane = threadIdx.x % MOE_WAVE, wave = uniform((int)(threadIdx.x / MOE_WAVE));
+  const int s = blockIdx.y * SEQ + wave / PER, mine = wave % PER;
+  const int E = a.E, e = blockIdx.x * MOE_WAVE + lane, cg = gridDim.x;
+  int lo = 0, hi = s < a.S ? a.T : 0;
+  if (a.seq && s < a.S) lo = bal_seq(a.seq, s, a.T), hi = bal_seq(a.seq, s + 1, a.T);
   const int b0 = lo / a.tb, b1 = lo < hi ? (hi - 1) / a.tb + 1 : b0;
   double q = 0, z = 0;
   int c = 0;
   long long n = 0;
   if (e < E)
 #pragma unroll 4
-    for (int b = b0 + wave; b < b1; b += BAL_WAVES) {
+    for (int b = b0 + mine; b < b1; b += PER) {
       const long long at = (long long)(b + s) * E + e;
       q += a.q[at];
       c += a.c[at];
     }
-  for (int b = b0 + threadIdx.x; b < b1; b += BAL_NT) {
+  for (int b = b0 + mine * MOE_WAVE + lane; b < b1; b += PER * MOE_WAVE) {
     z += a.z[b + s];
     n += a.n[b + s];
   }
   z = lanes_sum64(z);
   n = lanes_sum_int((int)n);
-  q_s[wave][lane] = q;
-  c_s[wave][lane] = c;
-  if (lane == 0) { z_s[wave] = z; n_s[wave] = n; }
-  __syncthreads();
-  if (wave == 0) {
+  if constexpr (PER > 1) {
+    q_s[wave][lane] = q;
+    c_s[wave][lane] = c;
+    if (lane == 0) { z_s[wave] = z; n_s[wave] = n; }
+    __syncthreads();
     q = 0, z = 0, c = 0, n = 0;
+    if (mine == 0)
 #pragma unroll
-    for (int w = 0; w < BAL_WAVES; ++w) {
-      q += q_s[w][lane];
-      c += c_s[w][lane];
-      z += z_s[w];
-      n += n_s[w];
-    }
+      for (int w = 0; w < PER; ++w) {
+        q += q_s[wave + w][lane];
+        c += c_s[wave + w][lane];
+        z += z_s[wave + w];
+        n += n_s[wave + w];
+      }
+  }
+  if (mine == 0 && s < a.S) {
     if (e < E) {
       a.counts[(long long)s * E + e] = c;
       if (a.prob) a.prob[(long long)s * E + e] = n > 0 ? (float)(q / n) : 0.f;
@@ -315,11 +326,13 @@ __global__ __launch_bounds__(BAL_NT) void balance_sum_kernel(BalArgs a) {
         put(a.term + (long long)a.S * cg + s, z);
         put(a.tokens + s, (int)n);
       }
-      __builtin_amdgcn_s_waitcnt(0);
-      last = __hip_atomic_fetch_add(a.done, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-             cg * a.S - 1;
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   }
+  __syncthreads();
+  if (threadIdx.x == 0)
+    last = __hip_atomic_fetch_add(a.done, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+           (int)(gridDim.x * gridDim.y) - 1;
   __syncthreads();
   if (!last) return;
   double b = 0;
@@ -501,12 +514,12 @@ extern "C" int moe_balance_loss(const float* logits, const int32_t* idx, const u
   }
   char* const w = (char*)ws;
   const bool one = bal_one(T, E, S);
-  BalArgs a = {logits, idx, keep, seq, T, E, k, S, bal_block_tokens(T, E), one, (int*)w,
+  BalArgs a = {logits, idx, keep, seq, T, E, k, S, bal_block_tokens(T, E, S), one, (int*)w,
                (float*)(w + lay.q), (int32_t*)(w + lay.c), (double*)(w + lay.z),
                (int32_t*)(w + lay.n), (double*)(w + lay.term), w_balance, w_z,
                loss, counts, tokens, prob};
   hipStream_t s = (hipStream_t)stream;
-  const int blocks = bal_blocks(T, E);
+  const int blocks = bal_blocks(T, E, S);
   if (E <= 16) launch_part<16, 1>(a, blocks, s);
   else if (E <= 32) launch_part<16, 2>(a, blocks, s);
   else if (E <= 64) launch_part<16, 4>(a, blocks, s);
@@ -516,8 +529,13 @@ extern "C" int moe_balance_loss(const float* logits, const int32_t* idx, const u
   else launch_part<64, 16>(a, blocks, s);
   MOE_TRY(moe_check_launch(fn));
   if (one) return MOE_OK;
-  hipLaunchKernelGGL(balance_sum_kernel, dim3((E + MOE_WAVE - 1) / MOE_WAVE, S), dim3(BAL_NT), 0, s,
-                     a);
+  // (of many sequences each has few rows)
+  const int cg = (E + MOE_WAVE - 1) / MOE_WAVE;
+  if (S < BAL_MANY)
+    hipLaunchKernelGGL(balance_sum_kernel<BAL_WAVES>, dim3(cg, S), dim3(BAL_NT), 0, s, a);
+  else
+    hipLaunchKernelGGL(balance_sum_kernel<1>, dim3(cg, (S + BAL_WAVES - 1) / BAL_WAVES),
+                       dim3(BAL_NT), 0, s, a);
   return moe_check_launch(fn);
 }
 
