@@ -6,10 +6,10 @@
 // launch's arguments (no copy to the device, and a captured launch keeps its
 // own).  A chunk's sum is kept in fp64 -- squares of every fp32 value are in its
 // range -- and a last launch adds the chunks in order.
-// Bound by HBM: 425 M gradients in bf16 (0.85 GB) have their norm in 147 us, 5.8
-// TB/s; clipped into fp32 485 us more, 5.3 TB/s, where a copy moves 5.1.  (Chunks
-// taken in reverse to find the end of the norm's pass in the cache, plain loads and
-// plain stores: 638 to 650 us together, 632 so.)
+// Bound by HBM: 425 M gradients in bf16 (0.85 GB) have their norm in 134 us, 6.3
+// TB/s; clipped into fp32 417 us more, 6.1 TB/s, in bf16 272, 6.2 TB/s, where a copy
+// moves 5.1.  (Chunks taken in reverse to find the end of the norm's pass in the
+// cache, plain loads and plain stores gave nothing.)
 #include <algorithm>
 #include <new>
 
@@ -22,10 +22,13 @@ constexpr int CLIP_WAVES = CLIP_NT / MOE_WAVE;
 constexpr int CLIP_SUM_NT = 1024;
 constexpr int NORM_TABLE = 176;           // gradients of one launch: tables below 4 KB
 constexpr int CLIP_TABLE = 128;
-constexpr long long CLIP_CHUNK = 2048;    // elements of a chunk, at least
-// chunks, at most, but for one a gradient: of the norm (all of them resident, and
-// few to add: 147 us above, 149 with 8192), of what is scaled
-constexpr long long NORM_CHUNKS = 2048, CLIP_CHUNKS = 8192;
+// Elements of a chunk, at least, and chunks, at most (but for one a gradient).  The
+// norm's are few, for a launch adds them (425 M bf16: 134 us at 4096, 138 at 2048 and
+// at 32768).  What is scaled is cut as fine as a workgroup's two rounds of loads: then
+// what runs at one time lies together in memory (into fp32 417 us; 434 at 8192
+// elements a chunk, 454 at 16384, 483 at 52000; into bf16 272, 276, 281 and 316).
+constexpr long long NORM_CHUNK = 2048, CLIP_CHUNK = 4096;
+constexpr long long NORM_CHUNKS = 4096, CLIP_CHUNKS = 1 << 24;
 // chunks, at most, where each workgroup that scales adds the parts itself, instead of
 // a launch between (a call on 6 gradients of 32768 values: 12.1 us, 14.5 with the
 // launch; 1 M values 11.5 and 14.4, 4 M values 23 and 14.3)
@@ -246,11 +249,12 @@ __global__ __launch_bounds__(CLIP_SUM_NT) void grad_norm_kernel(const double* pa
 }
 
 // n values times c.  A thread's store is 16 bytes and a wave's 1 KB without
-// gaps, whatever a thread loads for it (425 M values, bf16 to fp32: 485 us, 5.3
-// TB/s; with 32 bytes a thread, whose streaming stores leave gaps, 700).
+// gaps, whatever a thread loads for it (bf16 to fp32 with 32 bytes a thread, whose
+// streaming stores leave gaps: 700 us in place of 485, both in long chunks).  Two
+// loads in flight: 417 us, 448 with four, 442 with one.
 template <int NT, typename G, typename O>
 __device__ __forceinline__ void scale_chunk(const G* g, O* out, long long n, float c) {
-  constexpr int VEC = Elem<O>::VEC, STEP = NT * VEC, U = 4;
+  constexpr int VEC = Elem<O>::VEC, STEP = NT * VEC, U = 2;
   const long long whole = n / VEC * VEC;
   long long i = (long long)threadIdx.x * VEC;
   auto put = [&](O* to, float (&v)[VEC]) {
@@ -309,12 +313,12 @@ __global__ __launch_bounds__(CLIP_SUM_NT) void grad_norm_clip_kernel(
     clip_chunk<CLIP_SUM_NT>(t, blockIdx.x, chunk, by, max_norm);
 }
 
-// Elements of a chunk: a whole number of all lanes' loads.
-long long chunk_of(const moe_grad* g, int count, long long most) {
+// Elements of a chunk: a multiple of the least.
+long long chunk_of(const moe_grad* g, int count, long long least, long long most) {
   long long n = 0;
   for (int i = 0; i < count; ++i) n += g[i].n;
   const long long c = (n + most - 1) / most;
-  return c < CLIP_CHUNK ? CLIP_CHUNK : (c + CLIP_CHUNK - 1) / CLIP_CHUNK * CLIP_CHUNK;
+  return c < least ? least : (c + least - 1) / least * least;
 }
 long long chunks_of(const moe_grad* g, int count, long long chunk) {
   long long c = 0;
@@ -386,7 +390,7 @@ struct NormWs {
 NormWs norm_ws(const moe_grad* grads, int count) {
   auto up = [](size_t b) { return (b + 255) / 256 * 256; };
   NormWs w;
-  w.chunk = chunk_of(grads, count, NORM_CHUNKS);
+  w.chunk = chunk_of(grads, count, NORM_CHUNK, NORM_CHUNKS);
   w.chunks = chunks_of(grads, count, w.chunk);
   w.first = up((size_t)w.chunks * 8);
   w.g = w.first + up((size_t)(count + 1) * 4);
@@ -504,7 +508,7 @@ ClipTable clip_table(const moe_grad* grads, int count, long long chunk) {
 }
 int launch_clip(const char* fn, const moe_grad* grads, int count, const float* norm,
                 float max_norm, hipStream_t s) {
-  const long long chunk = chunk_of(grads, count, CLIP_CHUNKS);
+  const long long chunk = chunk_of(grads, count, CLIP_CHUNK, CLIP_CHUNKS);
   for (int g0 = 0; g0 < count; g0 += CLIP_TABLE) {
     const ClipTable t = clip_table(grads + g0, std::min(CLIP_TABLE, count - g0), chunk);
     if (t.first[t.count] == 0) continue;
