@@ -247,3 +247,43 @@ def test_replays_from_a_graph(M, H, dt):
             assert torch.equal(a, b)
         for a, b in zip(step(), want):
             assert torch.equal(a, b)
+
+
+def test_two_at_once_and_again():
+    """Calls on two streams side by side, over and over: the same bits."""
+    n = normal(12)
+    one, two = make(7680, "layer", True, n), make(128, "rms", False, n)
+    x, dy = n(600, 7680), n(600, 7680)
+    x2, dy2 = n(30011, 128, d=F32), n(30011, 128, d=F32)
+
+    def step(op, x, dy, stream=None):
+        r = op.forward(x, residual=dy, save=True, stream=stream)
+        grads = op.backward(dy, r.h, r.rstd, mean=r.mean, bias_grad=True, stream=stream)
+        return [t for t in (*r, *grads) if t is not None]
+
+    want, want2 = step(one, x, dy), step(two, x2, dy2)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in (a, b):
+        s.wait_stream(torch.cuda.current_stream())
+    got = [(step(one, x, dy, a), step(two, x2, dy2, b)) for _ in range(6)]
+    torch.cuda.synchronize()
+    for p, q in got:
+        assert all(torch.equal(u, v) for u, v in zip(p, want))
+        assert all(torch.equal(u, v) for u, v in zip(q, want2))
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_either_side_of_the_streaming_policy(dt):
+    """Rows of just under and just over 256 MB, read and written: the same bits for
+    the rows that both have."""
+    n = normal(13)
+    H = 2048
+    M = (64 << 20) // (H * (2 if dt == BF else 4))          # four tensors of 64 MB
+    op = make(H, "layer", True, n)
+    x, res, dy = (n(M + 1, H, d=dt) for _ in range(3))
+    out = []
+    for m in (M, M + 1):
+        r = op.forward(x[:m], residual=res[:m], save=True)
+        dx, _, _ = op.backward(dy[:m], r.h, r.rstd, mean=r.mean, dh=res[:m])
+        out.append([t[:M] for t in (r.y, r.h, r.mean, r.rstd, dx)])
+    assert all(torch.equal(a, b) for a, b in zip(*out))

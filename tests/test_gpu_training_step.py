@@ -6,6 +6,7 @@ import torch
 
 import synth
 from gpu_util import have_gpu, make_layer, rel_err, host
+from training_util import assert_within, ref_balance_bwd
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not have_gpu(), reason="needs a GPU")]
@@ -19,7 +20,7 @@ class Step:
     gradient dh of the residual stream, every gradient, clipped."""
 
     def __init__(self, name="tiny", overlap=False, limit=0.5):
-        from routing_permute_grouped_moe_amd.layer import BalanceLoss, GradClip, Norm
+        from routing_permute_grouped_moe_amd.layer import BalanceLoss, Norm
         cfg = self.cfg = synth.get_config(name)
         self.L = make_layer(cfg, synth.make_inputs(cfg), overlap=overlap)
         self.L.balance = BalanceLoss(A, B)
@@ -159,3 +160,22 @@ def test_backward_before_forward_is_refused():
     L.balance = BalanceLoss()
     with pytest.raises(RuntimeError, match="before their forward"):
         L.route_bwd()
+
+
+@pytest.mark.parametrize("how", ["recompute", "capacity", "overlap", "given logits"])
+def test_layer_variants_with_losses(how):
+    """The layer's dlogits are its gates' gradient and the losses' in one, whatever the
+    experts do."""
+    from routing_permute_grouped_moe_amd.layer import BalanceLoss
+    cfg = synth.get_config("stress" if how == "given logits" else "small")
+    kw = {"recompute": dict(recompute=True), "overlap": dict(overlap=True),
+          "capacity": dict(capacity=300)}.get(how, {})
+    L = make_layer(cfg, synth.make_inputs(cfg), **kw)
+    L.balance = BalanceLoss(0.5, 0.01)
+    L.step()
+    torch.cuda.synchronize()
+    one = L.balance.backward(L.logits, L.idx, L.losses.counts, L.losses.tokens, dgate=L.dgate)
+    assert torch.equal(one, L.dlogits)
+    assert_within("dlogits", L.dlogits, ref_balance_bwd(L.logits, L.idx, None, None, 0.5, 0.01, 1.0,
+                                                        L.dgate))
+    assert torch.equal(L.losses.counts[0], L.counts)
