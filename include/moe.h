@@ -495,7 +495,8 @@ int moe_balance_loss_bwd(const float* logits, const int32_t* idx, const float* d
  * nullable).  h [M,H] is written if not NULL and only with a residual; it may
  * be the residual's buffer or x's.  mean and rstd [M] fp32 are nullable, what
  * the backward needs (mean is not written for RMS).  Statistics and products
- * are fp32, y is rounded once.  H is a multiple of 8, at most 16384; eps > 0;
+ * are fp32 (a mean far from zero is corrected by the mean of the deviations from
+ * it), y is rounded once.  H is a multiple of 8, at most 16384; eps > 0;
  * rows whose sum of squares passes fp32's range give wrong numbers, a NaN or
  * an infinity in a row NaN in that row alone.
  */

@@ -122,6 +122,9 @@ __global__ __launch_bounds__(NT_) void norm_kernel(NormArgs a) {
   int r0 = blockIdx.x * R::G;
   fetch(r0);
   for (; r0 < a.M; r0 += step) {
+    // (no fma but where it says so: the mean is a product, and as part of one it would be
+    // another mean)
+#pragma clang fp contract(off)
     u32x4 h[C];
     float s = 0.f;
 #pragma unroll
@@ -137,20 +140,36 @@ __global__ __launch_bounds__(NT_) void norm_kernel(NormArgs a) {
       for (int j = 0; j < VEC; ++j) s += v[j];
     }
     fetch(r0 + step);                        // in flight during the sums
-    const float mean = a.rms ? 0.f : row_sum<TPR>(s, red, turn) * a.inv_h;
-    float d2 = 0.f;
+    const float m0 = a.rms ? 0.f : row_sum<TPR>(s, red, turn) * a.inv_h;
+    float mean = m0, d2 = 0.f;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       float v[VEC], e = 0.f;
       unpack16(h[i], v, T());
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float d = v[j] - mean;
-        e = fmaf(d, d, e);
-      }
+      for (int j = 0; j < VEC; ++j) e = fmaf(v[j] - m0, v[j] - m0, e);
       d2 += off[i] != NORM_OOB ? e : 0.f;
     }
-    const float rstd = 1.0f / sqrtf(row_sum<TPR>(d2, red, turn) * a.inv_h + a.eps);
+    float var = row_sum<TPR>(d2, red, turn) * a.inv_h;
+    // Where the mean is beyond twice the deviations its rounding counts, and the mean of
+    // what is left corrects it: m + E[d], E[d^2] - E[d]^2.  (In every row that would take
+    // 2 us of the 88 of 8192 x 7680, 5 of the 52 without a residual.)
+    if (!a.rms && m0 * m0 > 4.f * var) {
+      float d1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        float v[VEC], f = 0.f;
+        unpack16(h[i], v, T());
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) f += v[j] - m0;
+        d1 += off[i] != NORM_OOB ? f : 0.f;
+      }
+      d1 = row_sum<TPR>(d1, red, turn) * a.inv_h;
+      mean = m0 + d1;
+      var -= d1 * d1;
+      var = var < 0.f ? 0.f : var;
+    }
+    const float rstd = 1.0f / sqrtf(var + a.eps);
     const auto rh = rows(a.h, r0), ry = rows(a.y, r0);
 #pragma unroll
     for (int i = 0; i < C; ++i) {

@@ -287,3 +287,21 @@ def test_either_side_of_the_streaming_policy(dt):
         dx, _, _ = op.backward(dy[:m], r.h, r.rstd, mean=r.mean, dh=res[:m])
         out.append([t[:M] for t in (r.y, r.h, r.mean, r.rstd, dx)])
     assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
+@pytest.mark.parametrize("M,H", [(50, 64), (40, 1000), (33, 2056), (9, 7680), (5, 16384)])
+@pytest.mark.parametrize("offset", [1.5, 1000.0, -3e4])
+def test_rows_far_from_zero(M, H, offset):
+    """Deviations far smaller than the mean, or none at all: the mean is corrected by
+    the deviations from it."""
+    n = normal(14)
+    for dt in (F32, BF):
+        op = make(H, "layer", True, n)
+        x = n(M, H, std=abs(offset) * (1e-4 if dt == F32 else 0.02), mean=offset, d=dt)
+        x[1] = offset
+        x[2, 1:] = offset
+        r = op.forward(x, save=True)
+        want = ref_norm(x, op.w, op.bias, "layer", dt)
+        for name in ("mean", "rstd", "y"):
+            assert_within(name, getattr(r, name), want[name])
+        assert torch.equal(r.y[1], op.bias.to(dt)) and r.mean[1] == x[1, 0].float()

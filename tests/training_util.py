@@ -44,10 +44,19 @@ def ref_norm(h, w, b, kind, dtype):
     H = h.shape[1]
     D = H / 64 + 24
     mean = h.mean(1, keepdim=True) if kind == "layer" else torch.zeros_like(h[:, :1])
-    dm = (D + 2) * U * h.abs().mean(1, keepdim=True) if kind == "layer" else 0.0 * mean
     d = h - mean
     var = (d * d).mean(1, keepdim=True)
-    dv = (D + 5) * U * var + 2 * d.abs().mean(1, keepdim=True) * dm + dm * dm
+    if kind == "layer":
+        # a first mean off by e; where it is beyond twice the deviations (5: or near), their
+        # mean from it is added to it
+        e = (D + 2) * U * h.abs().mean(1, keepdim=True)
+        ad = d.abs().mean(1, keepdim=True)
+        far = mean * mean > 5 * var
+        dm = torch.where(far, 1.01 * U * mean.abs() + (D + 4) * U * (ad + e), e)
+        dv = (D + 8) * U * (var + e * e) + torch.where(
+            far, 2 * e * (D + 4) * U * (ad + e) + 1.01 * dm * dm, 2 * ad * e + e * e)
+    else:
+        dm, dv = 0.0 * mean, (D + 5) * U * var
     rstd = 1 / torch.sqrt(var + EPS[kind])
     rel = 0.5 * dv / (var + EPS[kind]) + 5 * U
     rel = rel + rel * rel * 2                       # (the root's second order)
