@@ -374,14 +374,18 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 def _on(device, stream, call, *inputs):
     """call(raw stream) with the device of a call's tensors current, and the
-    given stream too (None: the device's current one), so that outputs and
-    workspaces allocated inside belong to it; the inputs and weights, which may
-    not, are kept from reuse until the stream has passed."""
+    given stream too (None: the device's current one; a raw handle as well as a
+    torch stream, as the layer's own calls take both), so that outputs and workspaces
+    allocated inside belong to it; the inputs and weights, which may not, are kept
+    from reuse until the stream has passed."""
     if stream is None:
         if torch.cuda.current_device() == device.index:
             return call(_raw_stream(device.index))
         with torch.cuda.device(device):
             return call(_raw_stream(device.index))
+    if isinstance(stream, int):
+        stream = (torch.cuda.ExternalStream(stream, device=device) if stream else
+                  torch.cuda.default_stream(device))
     if stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
     with torch.cuda.stream(stream):   # (makes the stream's device current too)

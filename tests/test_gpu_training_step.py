@@ -179,3 +179,25 @@ def test_layer_variants_with_losses(how):
     assert_within("dlogits", L.dlogits, ref_balance_bwd(L.logits, L.idx, None, None, 0.5, 0.01, 1.0,
                                                         L.dgate))
     assert torch.equal(L.losses.counts[0], L.counts)
+
+
+@pytest.mark.parametrize("null", [False, True])
+def test_layer_on_a_raw_stream(null):
+    """The layer's calls take a stream's handle; with losses and clipping they do too."""
+    from routing_permute_grouped_moe_amd.layer import BalanceLoss
+    cfg = synth.get_config("tiny")
+    inp = synth.make_inputs(cfg)
+    one, two = make_layer(cfg, inp), make_layer(cfg, inp)
+    one.balance = two.balance = BalanceLoss(0.5, 0.01)
+    side = torch.cuda.Stream()
+    handle = 0 if null else side.cuda_stream
+    torch.cuda.synchronize()
+    one.step()
+    a = one.clip_grads(0.25)
+    two.step(handle)
+    b = two.clip_grads(0.25, stream=handle)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
+    for u, v in zip([one.y, one.dlogits, one.losses.loss] + one.grads(),
+                    [two.y, two.dlogits, two.losses.loss] + two.grads()):
+        assert torch.equal(u, v)
