@@ -478,7 +478,7 @@ int moe_balance_loss(const float* logits, const int32_t* idx, const uint8_t* kee
  * constant (counts have no gradient).  counts and tokens are the forward's.
  * dgate is nullable; with it idx names a token's experts once each (as
  * moe_route does), without it idx is not read and may be NULL.  dlogits [T,E]
- * is written whole.  With w_balance = w_z = 0 and finite logits it holds
+ * is written whole; T is below 2^27.  With w_balance = w_z = 0 and finite logits it holds
  * moe_route_bwd's values.
  */
 int moe_balance_loss_bwd(const float* logits, const int32_t* idx, const float* dgate,

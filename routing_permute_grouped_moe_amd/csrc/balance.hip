@@ -546,6 +546,8 @@ extern "C" int moe_balance_loss_bwd(const float* logits, const int32_t* idx, con
                                     float* dlogits, moe_stream_t stream) {
   const char* fn = "moe_balance_loss_bwd";
   MOE_TRY(bal_checks(fn, T, E, k, S));
+  if (T >= 1 << 27)                           // (16 lanes each; a launch ends at 2^32)
+    return moe_fail(MOE_ERR_UNSUPPORTED, "%s: T = %d, above the limit", fn, T);
   if (T == 0) return MOE_OK;
   MOE_TRY(moe_need_ptr(logits, fn, "logits", 4));
   if (dgate != nullptr) MOE_TRY(moe_need_ptr(idx, fn, "idx", 4));

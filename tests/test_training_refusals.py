@@ -156,6 +156,7 @@ BALANCE_BWD = dict(logits=A, idx=B, dgate=C, keep=None, seq=None, counts=D, toke
     ({"T": -1}, "INVALID_ARG", "T = -1"),
     ({"k": 9}, "UNSUPPORTED", "k = 9"),
     ({"S": 3}, "INVALID_ARG", "without seq"),
+    ({"T": 1 << 27, "E": 7}, "UNSUPPORTED", "T = 134217728"),
     ({"logits": None}, "INVALID_ARG", "logits is NULL"),
     ({"idx": None}, "INVALID_ARG", "idx is NULL"),
     ({"dgate": C + 1}, "INVALID_ARG", "dgate is not"),
