@@ -529,7 +529,8 @@ int moe_norm_bwd(const void* dy, const void* h, const void* dh, int dt, int M, i
  * (below 2^40), n == 0 is skipped and g may be NULL then; count is at most 2^20.
  *   kind MOE_GRAD_L2:  norms[i] = sqrt(sum g_i^2),  norm = sqrt(sum of all squares)
  *   kind MOE_GRAD_MAX: norms[i] = max |g_i|,        norm = the largest
- * Squares and sums are fp64: no finite gradient overflows, and a NaN gives NaN.
+ * Squares and sums are fp64: no finite gradient overflows there (a norm past fp32's
+ * range is inf in norm and norms, total has it), and a NaN gives NaN.
  * norm [1] and norms [count] (nullable) are fp32; total [1] fp64 (nullable) is
  * the sum of all squares, or the maximum: what ranks that hold parts of a model
  * reduce before they clip.  Without a gradient all are 0.  out and out_dt are

@@ -28,11 +28,13 @@ constexpr int CLIP_TABLE = 128;
 // what runs at one time lies together in memory (into fp32 417 us; 434 at 8192
 // elements a chunk, 454 at 16384, 483 at 52000; into bf16 272, 276, 281 and 316).
 constexpr long long NORM_CHUNK = 2048, CLIP_CHUNK = 4096;
-constexpr long long NORM_CHUNKS = 4096, CLIP_CHUNKS = 1 << 24;
+constexpr long long NORM_CHUNKS = 4096, CLIP_CHUNKS = 1 << 23;
 // chunks, at most, where each workgroup that scales adds the parts itself, instead of
 // a launch between (a call on 6 gradients of 32768 values: 12.1 us, 14.5 with the
 // launch; 1 M values 11.5 and 14.4, 4 M values 23 and 14.3)
 constexpr long long FUSED_CHUNKS = 512;
+
+static_assert((CLIP_CHUNKS + CLIP_TABLE) * CLIP_NT < (1LL << 32), "a launch ends at 2^32 threads");
 
 struct NormTable {
   const void* g[NORM_TABLE];
