@@ -719,6 +719,8 @@ class Norm:
         for name, t in (("dy", dy), ("dh", dh), ("out", out)):
             if t is not None:
                 _check(name, t, h.dtype, dev, M, H)
+        if rstd is None:
+            raise ValueError("no rstd: it comes from a forward with save")
         _check("rstd", rstd, f32, dev, M)
         if (mean is None) != (self.kind == abi.MOE_NORM_RMS):
             raise ValueError("mean comes with a layer norm, and only with it")

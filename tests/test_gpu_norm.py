@@ -305,3 +305,13 @@ def test_rows_far_from_zero(M, H, offset):
         for name in ("mean", "rstd", "y"):
             assert_within(name, getattr(r, name), want[name])
         assert torch.equal(r.y[1], op.bias.to(dt)) and r.mean[1] == x[1, 0].float()
+
+
+def test_backward_without_statistics_is_refused():
+    n = normal(15)
+    op = make(64, "layer", False, n)
+    x = n(3, 64)
+    r = op.forward(x)
+    assert r.mean is None and r.rstd is None
+    with pytest.raises(ValueError, match="a forward with save"):
+        op.backward(x, r.h, r.rstd, mean=r.mean)
