@@ -8,10 +8,11 @@
 // to row, and the next row is on its way while this one's sums are made.  The
 // backward keeps a column's part of dw and db in registers too; each workgroup
 // leaves one row of them, and a second launch adds those rows in fp64, in order.
-// Measured (one MI355X, where a 1 GiB copy moves 5.1 TB/s): 8192 x 7680 bf16 with
-// a residual 89 us (5.7 TB/s), its backward 95 us (5.3 TB/s; 5 us of it the
-// second launch); backwards of 4095 x 2048 fp32 and of 131071 x 128 bf16, 100 MB
-// each, 21.0 and 21.7 us; one row of 7680 3 us.
+// Measured among calls back to back (one MI355X, where a 1 GiB copy moves 5.1 TB/s):
+// 8192 x 7680 bf16 with a residual 85 us (5.9 TB/s), its backward 91 us (5.5 TB/s; 5 us
+// of it the second launch); backwards of 4095 x 2048 fp32 and of 131071 x 128 bf16,
+// 100 MB each, 20.0 and 20.7 us; one row of 7680 3 us.  (Times beside the choices below
+// are of the step that made them.)
 #include "reduce.hpp"
 #include "validate.hpp"
 
