@@ -475,7 +475,9 @@ int moe_balance_loss(const float* logits, const int32_t* idx, const uint8_t* kee
  *   dlogits[t,e] = p_te (g_te - sum_e' p_te' g_te' + 2 w_z dloss/N lse_t)
  *   g_te = w_balance dloss/N f_se + (dgate[t,j] where idx[t,j] = e)
  * The first and the last term are zero for a token that does not count, f is a
- * constant (counts have no gradient).  counts and tokens are the forward's.
+ * constant (counts have no gradient); without dgate, or with zeros there, such a
+ * token's row is zeros, whatever its logits hold.  In any other a NaN or +inf among
+ * the logits gives a row of NaN.  counts and tokens are the forward's.
  * dgate is nullable; with it idx names a token's experts once each (as
  * moe_route does), without it idx is not read and may be NULL.  dlogits [T,E]
  * is written whole; T is below 2^27.  With w_balance = w_z = 0 and finite logits it holds

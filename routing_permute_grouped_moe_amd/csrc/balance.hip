@@ -435,6 +435,13 @@ __global__ __launch_bounds__(BAL_BWD_NT) void balance_bwd_kernel(BalBwd a) {
 #pragma unroll
     for (int i = 0; i < V; ++i) g[i] += dp[lane + i * TPR];
   }
+  // a token that does not count and has no gates' gradient has zeros: its logits may be
+  // NaN or infinite, and 0 times its probabilities is NaN then
+  bool mine = false;
+#pragma unroll
+  for (int i = 0; i < V; ++i) mine = mine || !(g[i] == 0.f);
+  const unsigned long long lanes = ~0ull >> (MOE_WAVE - TPR) << sub * TPR;
+  const bool none = !counts && (__ballot(mine) & lanes) == 0;
   float m, sum, acc = 0.f, zs = 0.f;
   bal_softmax<TPR, V, false>(v, E, m, sum);
   const bool some = !(sum == 0.f);
@@ -445,7 +452,7 @@ __global__ __launch_bounds__(BAL_BWD_NT) void balance_bwd_kernel(BalBwd a) {
   acc = lanes_sum<TPR>(acc);
 #pragma unroll
   for (int i = 0; i < V; ++i)
-    buf_store4_nt(rd, off[i], __float_as_uint(v[i] * inv * (g[i] - acc + zs)));
+    buf_store4_nt(rd, off[i], none ? 0u : __float_as_uint(v[i] * inv * (g[i] - acc + zs)));
 }
 
 template <int TPR, int V>

@@ -328,3 +328,71 @@ def test_many_sequences_of_few_experts():
         assert_within("prob", r.prob, want["prob"])
         got = op.backward(z, idx, r.counts, r.tokens, seq=seq, keep=kp, dgate=dg)
         assert_within("dlogits", got, ref_balance_bwd(z, idx, seq, kp, 0.02, 0.003, 1.0, dg))
+
+
+@pytest.mark.parametrize("E", [9, 30, 64, 100, 256, 500, 1000])
+def test_tokens_that_do_not_count_have_no_gradient_whatever_they_hold(E):
+    """NaN or infinities in a token that is not kept, or lies in no sequence: zeros in its
+    row, and in its neighbours' their own bits; with a gates' gradient there the row is
+    the gates' (NaN), without it zeros."""
+    T, k = 90, 4
+    z, idx, _, _, n = inputs(T, E, k)
+    keep = torch.ones(T, dtype=torch.uint8, device="cuda")
+    out = [0, 7, 8, 21, 42, 43]
+    keep[out] = 0
+    seq = torch.tensor([5, 40, 40, T - 6], dtype=I32, device="cuda")
+    away = sorted(set(out + [0, 1, 2, 3, 4] + list(range(T - 6, T))))
+    stay = [t for t in range(T) if t not in away]
+    dgate = n(T, k, std=0.1)
+    dgate[away] = 0.0
+    dgate[7, 1] = -0.0
+    op = loss_op()
+    r = op.forward(z, idx, seq=seq, keep=keep)
+    want = [op.backward(z, idx, r.counts, r.tokens, seq=seq, keep=keep, dgate=dg)
+            for dg in (None, dgate)]
+    for bad in (float("nan"), INF, -INF):
+        zz = z.clone()
+        zz[away, 2] = bad
+        zz[8] = bad
+        q = op.forward(zz, idx, seq=seq, keep=keep)
+        assert all(torch.equal(a, b) for a, b in zip(q, r))
+        for dg, w in zip((None, dgate), want):
+            d = op.backward(zz, idx, r.counts, r.tokens, seq=seq, keep=keep, dgate=dg)
+            assert (d[away] == 0).all() and torch.equal(d[stay], w[stay])
+    assert all((w[away] == 0).all() for w in want)
+    # a gradient of the gates reaches such a token all the same
+    dg = dgate.clone()
+    dg[21, 3] = 0.25
+    d = op.backward(z, idx, r.counts, r.tokens, seq=seq, keep=keep, dgate=dg)
+    assert (d[21] != 0).any() and torch.equal(d[stay], want[1][stay])
+    zz = z.clone()
+    zz[21, 2] = float("nan")
+    d = op.backward(zz, idx, r.counts, r.tokens, seq=seq, keep=keep, dgate=dg)
+    assert torch.isnan(d[21]).all()
+    rest = [t for t in range(T) if t != 21]
+    assert torch.isfinite(d[rest]).all()
+
+
+def test_a_padded_batch_does_not_poison_the_routers_weights():
+    """NaN logits in the padding: dWg and dbias of the router are those without it."""
+    from routing_permute_grouped_moe_amd import abi
+    T, H, E, k = 512, 128, 64, 4
+    z, idx, _, _, n = inputs(T, E, k)
+    x, wg = n(T, H), n(H, E, std=0.1)
+    keep = torch.ones(T, dtype=torch.bool, device="cuda")
+    keep[400:] = False
+    op = loss_op()
+    got = []
+    for bad in (False, True):
+        zz = z.clone()
+        if bad:
+            zz[400:] = float("nan")
+        r = op.forward(zz, idx, keep=keep)
+        d = op.backward(zz, idx, r.counts, r.tokens, keep=keep)
+        nb = abi.moe_router_workspace_bytes(T, H, E, abi.MOE_F32)
+        ws = torch.empty(max(nb, 256), dtype=torch.uint8, device="cuda")
+        dx, dwg, db = torch.empty_like(x), torch.empty_like(wg), torch.empty(E, device="cuda")
+        abi.moe_router_logits_bwd(d, x, abi.MOE_F32, wg, T, H, E, dx, dwg, db, ws, nb)
+        got.append((dx, dwg, db))
+    for a, b in zip(*got):
+        assert torch.isfinite(b).all() and torch.equal(a, b)
