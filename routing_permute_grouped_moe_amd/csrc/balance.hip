@@ -424,14 +424,14 @@ __global__ __launch_bounds__(BAL_BWD_NT) void balance_bwd_kernel(BalBwd a) {
     float* const dp = dp_s[wave][sub];
 #pragma unroll
     for (int i = 0; i < V; ++i) dp[lane + i * TPR] = 0.f;
-    __builtin_amdgcn_wave_barrier();          // (a wave's LDS accesses happen in order)
+    wave_lds_sync();
     // chosen experts of a token are distinct, so these writes never collide
     if (e0 >= 0 && e0 < E) dp[e0] = d0;
     for (int j = lane + TPR; j < a.k && t < a.T; j += TPR) {
       const int e = a.idx[(long long)t * a.k + j];
       if (e >= 0 && e < E) dp[e] = a.dgate[(long long)t * a.k + j];
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_sync();
 #pragma unroll
     for (int i = 0; i < V; ++i) g[i] += dp[lane + i * TPR];
   }

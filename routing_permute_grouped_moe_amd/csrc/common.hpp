@@ -156,6 +156,16 @@ __device__ __forceinline__ float wave_max(float v) {
   return v;
 }
 
+// Between a wave's writes to LDS and its other lanes' reads of them.  The hardware
+// keeps a wave's LDS accesses in order; the fences (no instruction) keep the compiler
+// from moving them, or answering a lane's read with that lane's own last write, also
+// where it takes the barrier for one that touches no memory.
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ long long uniform(long long v) {
   const unsigned long long u = (unsigned long long)v;

@@ -241,8 +241,7 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int m0, int n0, i
         *(f32x4*)(ep + (lane & 31) * PITCH + 32 * j + 8 * q + 4 * (lane >> 5)) =
             f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
                   acc[i][j][4 * q + 3]};
-    // (one wave's own words: its LDS accesses stay in order)
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_sync();   // (one wave's own words)
     constexpr int CPR = WB / 4, RPP = 64 / CPR;   // chunks of 4 columns per row, rows per pass
 #pragma unroll
     for (int p = 0; p < 32 / RPP; ++p) {
@@ -254,7 +253,7 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int m0, int n0, i
         else dense_finish<T>(a, m, n, v);
       }
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_sync();
   }
 }
 

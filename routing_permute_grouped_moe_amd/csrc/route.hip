@@ -55,15 +55,13 @@ __global__ __launch_bounds__(ROUTE_WAVES * MOE_WAVE) void route_bwd_kernel(
   const float* row = logits + (long long)t * E;
   float* dp = dp_s[w];
   for (int e = lane; e < E; e += MOE_WAVE) dp[e] = 0.f;
-  __builtin_amdgcn_s_waitcnt(0);
-  __builtin_amdgcn_wave_barrier();
+  wave_lds_sync();
   // chosen experts of a token are distinct, so these writes never collide
   for (int j = lane; j < k; j += MOE_WAVE) {
     int e = idx[(long long)t * k + j];
     if (e >= 0 && e < E) dp[e] = dgate[(long long)t * k + j];
   }
-  __builtin_amdgcn_s_waitcnt(0);
-  __builtin_amdgcn_wave_barrier();
+  wave_lds_sync();
   float v[V];
   float m = -INFINITY;
 #pragma unroll
