@@ -435,13 +435,6 @@ __global__ __launch_bounds__(BAL_BWD_NT) void balance_bwd_kernel(BalBwd a) {
 #pragma unroll
     for (int i = 0; i < V; ++i) g[i] += dp[lane + i * TPR];
   }
-  // a token that does not count and has no gates' gradient has zeros: its logits may be
-  // NaN or infinite, and 0 times its probabilities is NaN then
-  bool mine = false;
-#pragma unroll
-  for (int i = 0; i < V; ++i) mine = mine || !(g[i] == 0.f);
-  const unsigned long long lanes = ~0ull >> (MOE_WAVE - TPR) << sub * TPR;
-  const bool none = !counts && (__ballot(mine) & lanes) == 0;
   float m, sum, acc = 0.f, zs = 0.f;
   bal_softmax<TPR, V, false>(v, E, m, sum);
   const bool some = !(sum == 0.f);
@@ -450,6 +443,13 @@ __global__ __launch_bounds__(BAL_BWD_NT) void balance_bwd_kernel(BalBwd a) {
 #pragma unroll
   for (int i = 0; i < V; ++i) acc += v[i] * inv * g[i];
   acc = lanes_sum<TPR>(acc);
+  // a token that does not count and has no gates' gradient has zeros: its logits may be
+  // NaN or infinite, and 0 times its probabilities is NaN then
+  uint32_t some_g = counts;
+#pragma unroll
+  for (int i = 0; i < V; ++i) some_g |= __float_as_uint(g[i]) << 1;
+  const unsigned long long lanes = ~0ull >> (MOE_WAVE - TPR) << sub * TPR;
+  const bool none = (__ballot(some_g != 0) & lanes) == 0;
 #pragma unroll
   for (int i = 0; i < V; ++i)
     buf_store4_nt(rd, off[i], none ? 0u : __float_as_uint(v[i] * inv * (g[i] - acc + zs)));
