@@ -28,20 +28,25 @@ constexpr int BAL_BWD_NT = 256;
 // experts in 24 sequences: 17.2 and 14.3 us, in 64 17.8 and 17.5, in 1000 32 and 75)
 constexpr int BAL_MANY = 64;
 constexpr int BAL_MAX_S = 65535;              // sequences
+// rounds of a block, at most: a lane adds that many probabilities in fp32, 18 more additions
+// join lanes and waves, the rest is fp64 (2^26 tokens of 3 experts have 4608 blocks so; in 256
+// their probabilities, added 4096 times, were off by 430 roundings)
+constexpr int BAL_CHAIN = 240;
 constexpr uint32_t BAL_OOB = 0xffffffffu;     // past every tensor: reads zeros
 
 // Lanes of a token in the forward: a wave has one of many experts, or several of
 // few, whose sums over lanes then cost as much as one's (65536 tokens of 64
 // experts: 19.5 -> 13.1 us, 65521 of 256 22.3 -> 21.0; four of 256 a wave 21.6).
 int bal_lanes(int E) { return E <= 64 ? 16 : E <= 256 ? 32 : 64; }
-// Tokens of a block: at most 256 blocks, one for each CU, of whole rounds of its
-// waves; few tokens in few sequences are one block.
+// Tokens of a block: 256 blocks, one for each CU, or as many times 256 as keep a block's
+// rounds of its waves at BAL_CHAIN; few tokens in few sequences are one block.
 bool bal_one(int T, int E, int S) { return T <= 4 * (BAL_NT / bal_lanes(E)) && S <= 16; }
 int bal_block_tokens(int T, int E, int S) {
   if (bal_one(T, E, S)) return T > 0 ? T : 1;
   const int round = BAL_NT / bal_lanes(E);
   const long long per = ((long long)T + 255) / 256;
-  return per > 0 ? (int)((per + round - 1) / round * round) : round;
+  const long long rounds = (per + round - 1) / round, times = (rounds + BAL_CHAIN - 1) / BAL_CHAIN;
+  return times > 0 ? (int)((rounds + times - 1) / times) * round : round;
 }
 int bal_blocks(int T, int E, int S) {
   const int tb = bal_block_tokens(T, E, S);
@@ -473,7 +478,7 @@ int bal_checks(const char* fn, int T, int E, int k, int S) {
   if (S > BAL_MAX_S)
     return moe_fail(MOE_ERR_UNSUPPORTED, "%s: S = %d above %d", fn, S, BAL_MAX_S);
   MOE_TRY(moe_need_elems(T, E, 4, fn, "logits"));
-  // (rows of partial sums: at most 256 and one a sequence)
+  // (and rows of partial sums where blocks are 256; where they are more T is in the millions)
   MOE_TRY(moe_need_elems((long long)S + 256, E, 4, fn, "counts"));
   return MOE_OK;
 }
@@ -536,9 +541,9 @@ extern "C" int moe_balance_loss(const float* logits, const int32_t* idx, const u
   else launch_part<64, 16>(a, blocks, s);
   MOE_TRY(moe_check_launch(fn));
   if (one) return MOE_OK;
-  // (of many sequences each has few rows)
+  // (of many sequences each has few rows; one of them may have all, up to 256, whatever S)
   const int cg = (E + MOE_WAVE - 1) / MOE_WAVE;
-  if (S < BAL_MANY)
+  if (S < BAL_MANY || (blocks > 256 && S < blocks))
     hipLaunchKernelGGL(balance_sum_kernel<BAL_WAVES>, dim3(cg, S), dim3(BAL_NT), 0, s, a);
   else
     hipLaunchKernelGGL(balance_sum_kernel<1>, dim3(cg, (S + BAL_WAVES - 1) / BAL_WAVES),

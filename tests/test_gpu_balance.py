@@ -396,3 +396,26 @@ def test_a_padded_batch_does_not_poison_the_routers_weights():
         got.append((dx, dwg, db))
     for a, b in zip(*got):
         assert torch.isfinite(b).all() and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,E,rows", [(1 << 26, 3, [[0.3, -0.4, 0.05]]), ((1 << 26) - 65, 2, [[0.1, 0.4]]),
+                                      (1 << 21, 500, None), (9_000_001, 48, None)])
+def test_long_sums_of_like_probabilities(T, E, rows):
+    """Every token counts and all are alike, so that every addition of a sum rounds the
+    same way: the bound is that of short chains, whatever T."""
+    k = 2
+    row = torch.linspace(-0.3, 0.4, E)[None] if rows is None else torch.tensor(rows)
+    row = row.cuda()
+    z = row.expand(T, E).contiguous()
+    idx = torch.tensor([[0, 1]], dtype=I32, device="cuda").expand(T, k).contiguous()
+    r = loss_op().forward(z, idx)
+    want = ref_balance(row, idx[:1], None, None, 0.02, 0.003)   # (means: of one token as of T)
+    assert torch.equal(f64(r.counts), want["counts"] * T) and r.tokens.tolist() == [T, T]
+    assert_within("prob", r.prob, want["prob"])
+    assert_within("loss", r.loss, want["loss"])
+    # and in two sequences, the shorter ended inside a block
+    ends = [0, 1_000_003, T]
+    r = loss_op().forward(z, idx, seq=torch.tensor(ends, dtype=I32, device="cuda"))
+    p, bound = want["prob"]
+    assert_within("prob", r.prob, (p.expand(2, E), bound.expand(2, E)))
+    assert r.counts[:, 0].tolist() == [ends[1], T - ends[1]] and (r.counts[:, 2:] == 0).all()
