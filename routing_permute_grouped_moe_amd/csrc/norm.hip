@@ -413,13 +413,21 @@ Shape norm_bwd_shape(int chunks) {
   if (chunks <= 2048) return {1024, 2, 1024, 16};
   return {1024, 4, 1024, 16};
 }
-int norm_blocks(int M, Shape s) {
+// Workgroups, as many as are resident, or as many times that as keep a thread's rows at
+// `chain`.
+int norm_blocks(int M, Shape s, long long chain) {
   const long long G = s.nt / s.tpr, most = (long long)moe_cu_count() * s.waves * MOE_WAVE / s.nt;
   const long long need = (M + G - 1) / G, per = (need + most - 1) / most;
-  return per ? (int)((need + per - 1) / per) : 0;
+  if (per == 0) return 0;
+  const long long times = (per + chain - 1) / chain, each = (per + times - 1) / times;
+  return (int)((need + each - 1) / each);
 }
+// Rows whose part of dw and db a thread adds in fp32, at most; 10 more additions join the
+// rows of a workgroup, and the workgroups' sums are fp64.  (Alike in 2^27 rows of 8 values,
+// 4096 a thread, they were off by 890 roundings.)
+constexpr int NORM_CHAIN = 240;
 int norm_parts(int M, int H, int dt) {
-  return norm_blocks(M, norm_bwd_shape(H * moe_dt_bytes(dt) / 16));
+  return norm_blocks(M, norm_bwd_shape(H * moe_dt_bytes(dt) / 16), NORM_CHAIN);
 }
 
 #define NORM_SHAPES(X)                                                                    \
@@ -432,7 +440,7 @@ int norm_parts(int M, int H, int dt) {
 // (rows of bf16 end at 2048 chunks)
 template <typename T, bool STREAM>
 int norm_launch(const NormArgs& a, Shape s, hipStream_t st) {
-  const dim3 grid(norm_blocks(a.M, s));
+  const dim3 grid(norm_blocks(a.M, s, a.M));
 #define X(P, N, TH)                                                                        \
   if constexpr (P * N * Elem<T>::VEC <= NORM_MAX_H)                                        \
     if (s.tpr == P && s.c == N)                                                            \

@@ -315,3 +315,19 @@ def test_backward_without_statistics_is_refused():
     assert r.mean is None and r.rstd is None
     with pytest.raises(ValueError, match="a forward with save"):
         op.backward(x, r.h, r.rstd, mean=r.mean)
+
+
+@pytest.mark.parametrize("M,H", [((1 << 27) - 70, 8), ((1 << 23) - 3, 128), (100_003, 8192)])
+def test_long_sums_of_like_rows(M, H):
+    """All rows alike, so that every addition of dw and db rounds the same way.  At most 240
+    rows are added in fp32 by a thread, then 3 lanes' worth and 7 waves' (8 rows side by side
+    in a wave, 8 waves), the rest in 64 bits, rounded once: 251 u; dy / 2 is exact."""
+    n = normal(16)
+    op = make(H, "rms", True, n)
+    row = torch.tensor([0.1, 0.3, -0.7, 1.1, 1 / 3, 0.9, -0.123, 0.6], device="cuda").repeat(H // 8)
+    dy = row.expand(M, H).contiguous()
+    h = torch.full((M, H), 0.5, device="cuda")
+    rstd = torch.ones(M, device="cuda")
+    _, dw, db = op.backward(dy, h, rstd, x_grad=False)
+    for name, got, each in (("db", db, f64(row)), ("dw", dw, 0.5 * f64(row))):
+        assert_within(name, got, (M * each, 251 * U * M * each.abs()))
