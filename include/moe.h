@@ -554,7 +554,8 @@ int moe_grad_norm(const moe_grad* grads, int count, int kind, float* norm, float
  * is read on the device.  out is g's own buffer with g's type (then nothing is
  * moved where c is 1), or a buffer that overlaps no gradient and no other out,
  * of type g's or MOE_F32.  In place a gradient is given once.  max_norm >= 0.  A
- * NaN norm gives c = NaN, an infinite one c = 0, as the formula does.
+ * NaN norm gives c = NaN; an infinite one c = 0, as the formula does, but 1 where
+ * max_norm is infinite too: without a limit nothing is scaled.
  */
 int moe_grad_clip(const moe_grad* grads, int count, const float* norm, float max_norm,
                   moe_stream_t stream);

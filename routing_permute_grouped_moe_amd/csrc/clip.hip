@@ -1,5 +1,6 @@
 // The norm of many gradients together and of each, and clipping by it.
-//   norm = sqrt(sum g^2) or max |g|;  out = min(1, max_norm / (norm + 1e-6)) g
+//   norm = sqrt(sum g^2) or max |g|;  out = min(1, max_norm / (norm + 1e-6)) g, or g
+//   where max_norm is infinite
 //
 // Gradients are cut into chunks of one length; a workgroup takes one.  Which
 // chunk belongs to which gradient stands in a table that travels with the
@@ -286,7 +287,8 @@ __device__ __forceinline__ void clip_chunk(const ClipTable& t, int b, long long 
                                            float max_norm) {
   const int i = grad_of(t, b);
   float c = max_norm / (norm + 1e-6f);
-  c = c > 1.f ? 1.f : c;        // (a NaN stays one)
+  // (a NaN norm stays one; no limit scales nothing, an infinite norm either)
+  c = c > 1.f || (max_norm == INFINITY && norm == norm) ? 1.f : c;
   if (c == 1.f && t.out[i] == t.g[i]) return;
   const unsigned long long word = t.n[i];
   const long long n = (long long)(word & N_MASK), at = (long long)(b - t.first[i]) * chunk;

@@ -806,8 +806,9 @@ class GradClip:
         return _on(dev, stream, call, *self.grads)
 
     def clip(self, max_norm: float, norm=None, stream=None):
-        """Scales the gradients by min(1, max_norm / (norm + 1e-6)); returns the
-        norm.  ``norm``: one fp32 value to take instead of the gradients' own."""
+        """Scales the gradients by min(1, max_norm / (norm + 1e-6)), not at all with an
+        infinite ``max_norm``; returns the norm.  ``norm``: one fp32 value to take
+        instead of the gradients' own."""
         arr, dev, n = self._array(), self.device, len(self.grads)
         if norm is not None:
             if norm.numel() != 1:

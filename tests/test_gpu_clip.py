@@ -301,3 +301,31 @@ def test_in_one_call_or_two(sizes, kind):
     abi.moe_grad_norm_clip(a, len(grads), abi.MOE_GRAD_MAX if kind == "max" else abi.MOE_GRAD_L2, 0.05, n1,
                            each, ws, nb)
     assert torch.equal(each, clipper(grads, kind=kind).norm(each=True)[1]) and n1.item() == norm.item()
+
+
+@pytest.mark.parametrize("kind", ["l2", "max"])
+@pytest.mark.parametrize("sizes", [[5000, 700], [300000, 900001], [100] * 150])
+def test_no_limit_scales_nothing_even_an_infinite_norm(sizes, kind):
+    """In one call, in two, by a norm that is given, in place and not; a NaN norm is NaN."""
+    grads = grads_of(sizes)
+    grads[1][13] = -INF
+    before = [g.clone() for g in grads]
+    outs = [torch.empty_like(g, dtype=F32) for g in grads]
+    given = torch.tensor(INF, device="cuda")
+    for norm in (None, given):
+        assert torch.isinf(clipper(grads, outs=outs, kind=kind).clip(INF, norm=norm))
+        assert all(torch.equal(o, b.float()) for o, b in zip(outs, before))
+        assert torch.isinf(clipper(grads, kind=kind).clip(INF, norm=norm))
+        assert all(torch.equal(g, b) for g, b in zip(grads, before))
+    # finite gradients whose norm is beyond fp32
+    big = [torch.full((9,), 3e38, device="cuda")]
+    if kind == "l2":
+        assert torch.isinf(clipper(big).clip(INF)) and (big[0] == 3e38).all()
+    # a finite limit still gives c = 0, a NaN norm NaN
+    clipper(grads, outs=outs, kind=kind).clip(1e30, norm=given)
+    assert (outs[0] == 0).all()
+    clipper(grads, outs=outs, kind=kind).clip(INF, norm=torch.tensor(NAN, device="cuda"))
+    assert all(torch.isnan(o).all() for o in outs)
+    grads[0][7] = NAN
+    assert torch.isnan(clipper(grads, outs=outs, kind=kind).clip(INF))
+    assert all(torch.isnan(o).all() for o in outs)
