@@ -460,7 +460,8 @@ int moe_linear_bwd(const void* dy, const void* z, const void* x, const void* w, 
  *   counts [S,E] int32 c_se;  tokens [S+1] int32: n_s, then N
  *   prob [S,E] fp32    P_se (nullable; a statistic, zeros where n_s = 0)
  * A logit of -inf masks an expert; NaN or +inf in a token that counts gives
- * NaN losses.  idx entries outside [0, E) are not counted.  T == 0 writes zeros.  ws:
+ * NaN losses.  idx entries outside [0, E) are not counted.  T is below 2^27, as the
+ * backward's; T == 0 writes zeros.  ws:
  * scratch of moe_balance_loss_workspace_bytes bytes, 256-byte aligned (NULL
  * where that is 0), not shared by calls that may overlap.  Outputs share memory with nothing else.
  */

@@ -483,6 +483,13 @@ int bal_checks(const char* fn, int T, int E, int k, int S) {
   return MOE_OK;
 }
 
+// Forward and backward take the same tokens.  The backward's launch has 16 lanes or more for
+// each and ends at 2^32 of them, so below 2^28; 2^27 is half of that.
+int bal_need_tokens(const char* fn, int T) {
+  if (T < 1 << 27) return MOE_OK;
+  return moe_fail(MOE_ERR_UNSUPPORTED, "%s: T = %d, above the limit", fn, T);
+}
+
 }  // namespace
 
 extern "C" size_t moe_balance_loss_workspace_bytes(int T, int E, int k, int S) {
@@ -496,6 +503,7 @@ extern "C" int moe_balance_loss(const float* logits, const int32_t* idx, const u
                                 float* prob, void* ws, size_t ws_bytes, moe_stream_t stream) {
   const char* fn = "moe_balance_loss";
   MOE_TRY(bal_checks(fn, T, E, k, S));
+  MOE_TRY(bal_need_tokens(fn, T));
   if (T > 0) {
     MOE_TRY(moe_need_ptr(logits, fn, "logits", 4));
     MOE_TRY(moe_need_ptr(idx, fn, "idx", 4));
@@ -558,8 +566,7 @@ extern "C" int moe_balance_loss_bwd(const float* logits, const int32_t* idx, con
                                     float* dlogits, moe_stream_t stream) {
   const char* fn = "moe_balance_loss_bwd";
   MOE_TRY(bal_checks(fn, T, E, k, S));
-  if (T >= 1 << 27)                           // (16 lanes each; a launch ends at 2^32)
-    return moe_fail(MOE_ERR_UNSUPPORTED, "%s: T = %d, above the limit", fn, T);
+  MOE_TRY(bal_need_tokens(fn, T));
   if (T == 0) return MOE_OK;
   MOE_TRY(moe_need_ptr(logits, fn, "logits", 4));
   if (dgate != nullptr) MOE_TRY(moe_need_ptr(idx, fn, "idx", 4));

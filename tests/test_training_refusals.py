@@ -295,3 +295,17 @@ def test_classes_want_tensors_on_a_gpu(abi):
         BalanceLoss().forward(torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32))
     with pytest.raises(ValueError, match="gradients are on cpu, not on a GPU"):
         GradClip([w])
+
+
+@pytest.mark.parametrize("T", [1 << 27, (1 << 27) + 5, 1 << 28, (1 << 30) - 1])
+def test_balance_forward_and_backward_refuse_the_same_tokens(abi, T):
+    """What a forward takes its backward takes: neither takes 2^27 tokens."""
+    text = f"T = {T}, above the limit"
+    change = {"T": T, "E": 1, "k": 1, "ws_bytes": 1 << 40}
+    far = dict(logits=A, idx=A + (1 << 34), loss=A + (2 << 34), counts=A + (3 << 34),
+               tokens=A + (4 << 34), prob=A + (5 << 34), ws=A + (6 << 34))
+    refused(abi, "moe_balance_loss", {**BALANCE, **change, **far}, "UNSUPPORTED", text)
+    far = dict(logits=A, idx=A + (1 << 34), dgate=A + (2 << 34), counts=A + (3 << 34),
+               tokens=A + (4 << 34), dlogits=A + (5 << 34))
+    change = {n: change[n] for n in ("T", "E", "k")}
+    refused(abi, "moe_balance_loss_bwd", {**BALANCE_BWD, **change, **far}, "UNSUPPORTED", text)
