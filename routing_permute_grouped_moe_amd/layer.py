@@ -78,6 +78,7 @@ class MoeLayer:
         # tokens to ``keep`` (set by the caller; None: one sequence, all tokens)
         self.balance = balance
         self.seq = self.keep = self.losses = None
+        self._counted = (None, None, None)   # losses, and the seq and keep they were taken over
         # recompute: no permuted copy of x (the grouped GEMMs gather token
         # rows through src_token) and act is recomputed from h13 for dW
         self.recompute = recompute
@@ -178,9 +179,13 @@ class MoeLayer:
 
     def balance_loss(self, stream=None):
         """``losses`` (a :class:`Balance`): read its ``loss`` after the forward; the
-        backward takes the gradient of ``loss[2]`` into dlogits."""
-        self.losses = self.balance.forward(self.logits, self.idx, seq=self.seq, keep=self.keep,
+        backward takes the gradient of ``loss[2]`` into dlogits, over the ``seq`` and
+        ``keep`` of this call: a caller may have set other tensors by then, for the next
+        batch, but leaves the contents of these."""
+        seq, keep = self.seq, self.keep
+        self.losses = self.balance.forward(self.logits, self.idx, seq=seq, keep=keep,
                                            stream=stream)
+        self._counted = (self.losses, seq, keep)
 
     def permute(self, stream=None):
         s = self.s
@@ -274,9 +279,12 @@ class MoeLayer:
         if self.balance is not None:      # the gates' and the losses' gradient in one pass
             if self.losses is None:
                 raise RuntimeError("the backward of the router's losses before their forward")
+            of, seq, keep = self._counted
+            if of is not self.losses:     # (the caller's own)
+                seq, keep = self.seq, self.keep
             self.balance.backward(self.logits, self.idx, self.losses.counts, self.losses.tokens,
-                                  seq=self.seq, keep=self.keep, dgate=self.dgate,
-                                  out=self.dlogits, stream=stream)
+                                  seq=seq, keep=keep, dgate=self.dgate, out=self.dlogits,
+                                  stream=stream)
             return
         abi.moe_route_bwd(self.logits, self.idx, self.dgate, s.T, s.E, s.k, self.dlogits, stream)
 

@@ -201,3 +201,46 @@ def test_layer_on_a_raw_stream(null):
     for u, v in zip([one.y, one.dlogits, one.losses.loss] + one.grads(),
                     [two.y, two.dlogits, two.losses.loss] + two.grads()):
         assert torch.equal(u, v)
+
+
+@pytest.mark.parametrize("later", ["seq of as many", "seq of more", "keep", "both gone"])
+@pytest.mark.parametrize("overlap", [False, True])
+def test_the_backward_is_of_the_batch_that_the_forward_took(later, overlap):
+    """seq and keep set for the next batch before this one's backward."""
+    one, two = Step("small", overlap), Step("small", overlap)
+    for s in (one, two):
+        s.L.x.copy_(s.x)
+        s.L.forward()
+    one.L.backward()
+    T, L = two.cfg.T, two.L
+    if later == "seq of as many":
+        L.seq = torch.tensor([0, 3, 9, 20, T], dtype=torch.int32, device="cuda")
+    elif later == "seq of more":
+        L.seq = torch.tensor([0, 1, 2, 3, 4, 5, T], dtype=torch.int32, device="cuda")
+    elif later == "keep":
+        L.keep = torch.zeros(T, dtype=torch.bool, device="cuda")
+    else:
+        L.seq = L.keep = None
+    L.backward()
+    torch.cuda.synchronize()
+    assert torch.equal(one.L.losses.loss, L.losses.loss)
+    for a, b in zip([one.L.dlogits, one.L.dx] + one.L.grads(), [L.dlogits, L.dx] + L.grads()):
+        assert torch.equal(a, b)
+    # the next forward takes what is set
+    L.forward()
+    want = L.balance.forward(L.logits, L.idx, seq=L.seq, keep=L.keep)
+    assert torch.equal(want.counts, L.losses.counts) and torch.equal(want.loss, L.losses.loss)
+
+
+def test_losses_that_the_caller_sets():
+    """Losses of the caller's own, in place of the forward's: over what is set with them."""
+    s = Step()
+    L = s.L
+    L.x.copy_(s.x)
+    L.forward()
+    L.seq = torch.tensor([0, 11, s.cfg.T], dtype=torch.int32, device="cuda")
+    L.keep = None
+    L.losses = L.balance.forward(L.logits, L.idx, seq=L.seq)
+    L.backward()
+    want = L.balance.backward(L.logits, L.idx, L.losses.counts, L.losses.tokens, seq=L.seq, dgate=L.dgate)
+    assert torch.equal(want, L.dlogits)
