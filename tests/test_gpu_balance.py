@@ -419,3 +419,47 @@ def test_long_sums_of_like_probabilities(T, E, rows):
     p, bound = want["prob"]
     assert_within("prob", r.prob, (p.expand(2, E), bound.expand(2, E)))
     assert r.counts[:, 0].tolist() == [ends[1], T - ends[1]] and (r.counts[:, 2:] == 0).all()
+
+
+def guarded(n, dtype, fill):
+    """n values between guards of 4 KB, and a check that the guards are as they were."""
+    g = 4096 // torch.empty((), dtype=dtype).element_size()
+    whole = torch.full((n + 2 * g,), fill, dtype=dtype, device="cuda")
+
+    def untouched():
+        return bool((whole[:g] == fill).all()) and bool((whole[g + n:] == fill).all())
+    return whole[g:g + n], untouched
+
+
+@pytest.mark.parametrize("T,E,k", [(500, 40, 4), (90, 12, 3), (3000, 300, 5), (700, 1024, 2)])
+@pytest.mark.parametrize("S", [4, 90])
+def test_writes_are_the_outputs_and_the_planned_workspace(T, E, k, S):
+    """Through the C calls, with guards around every output and a workspace of exactly the
+    planned bytes: sequence ends in order, out of order and out of range, experts out of
+    range."""
+    from routing_permute_grouped_moe_amd import abi
+    z, idx, _, kp, n = inputs(T, E, k, keep=True)
+    idx = idx.clone()
+    idx[::3, 1] = 1 << 30
+    idx[1::3, 0] = -5
+    dgate = n(T, k)
+    gen = torch.Generator().manual_seed(S)
+    fine = torch.randint(0, T + 1, (S + 1,), generator=gen).sort().values
+    some = torch.randint(-T, 2 * T, (S + 1,), generator=gen)
+    far = some.clone()
+    far[::2] = torch.tensor([-(1 << 31), (1 << 31) - 1])[torch.arange(far[::2].numel()) % 2]
+    for ends in (fine, fine.flip(0), some, far):
+        seq = ends.to(I32).cuda()
+        nb = abi.moe_balance_loss_workspace_bytes(T, E, k, S)
+        outs = {"loss": guarded(3, F32, 7.0), "counts": guarded(S * E, I32, -9),
+                "tokens": guarded(S + 1, I32, -9), "prob": guarded(S * E, F32, 7.0),
+                "ws": guarded(nb, torch.uint8, 201), "dlogits": guarded(T * E, F32, 7.0)}
+        at = {name: t for name, (t, _) in outs.items()}
+        abi.moe_balance_loss(z, idx, kp, seq, T, E, k, S, 0.02, 0.003, at["loss"], at["counts"],
+                             at["tokens"], at["prob"], at["ws"] if nb else None, nb)
+        abi.moe_balance_loss_bwd(z, idx, dgate, kp, seq, at["counts"], at["tokens"], T, E, k, S, 0.02,
+                                 0.003, None, at["dlogits"])
+        torch.cuda.synchronize()
+        for name, (_, untouched) in outs.items():
+            assert untouched(), name
+        assert at["dlogits"].shape[0] == T * E and not (at["dlogits"] == 7.0).all()
