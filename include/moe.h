@@ -459,6 +459,9 @@ int moe_linear_bwd(const void* dy, const void* z, const void* x, const void* w, 
  *   loss [3] fp32      balance, z, and w_balance balance + w_z z (zeros if N = 0)
  *   counts [S,E] int32 c_se;  tokens [S+1] int32: n_s, then N
  *   prob [S,E] fp32    P_se (nullable; a statistic, zeros where n_s = 0)
+ * Their exponentials, logarithms and reciprocals are the hardware's, so that a token's
+ * probability is off by some 10 fp32 roundings and 2.4 for each unit that its logit lies
+ * below the largest; the backward takes moe_route_bwd's exponentials.
  * A logit of -inf masks an expert; NaN or +inf in a token that counts gives
  * NaN losses.  idx entries outside [0, E) are not counted.  T is below 2^27, as the
  * backward's; T == 0 writes zeros.  ws:
@@ -499,7 +502,8 @@ int moe_balance_loss_bwd(const float* logits, const int32_t* idx, const float* d
  * be the residual's buffer or x's.  mean and rstd [M] fp32 are nullable, what
  * the backward needs (mean is not written for RMS).  Statistics and products
  * are fp32 (a mean far from zero is corrected by the mean of the deviations from
- * it), y is rounded once.  H is a multiple of 8, at most 16384; eps > 0;
+ * it), y is rounded once.  H is a multiple of 8, at most 16384, and a tensor below 4 GiB
+ * and 2^31 elements (the backward's too); eps > 0;
  * rows whose sum of squares passes fp32's range give wrong numbers, a NaN or
  * an infinity in a row NaN in that row alone.
  */

@@ -25,7 +25,10 @@ constexpr int BAL_NT = 1024;                  // forward
 constexpr int BAL_WAVES = BAL_NT / MOE_WAVE;
 constexpr int BAL_BWD_NT = 256;
 // sequences from which on each is added by a wave, not a workgroup (8192 tokens of 256
-// experts in 24 sequences: 17.2 and 14.3 us, in 64 17.8 and 17.5, in 1000 32 and 75)
+// experts in 24 sequences: 17.2 and 14.3 us, in 64 17.8 and 17.5, in 1000 32 and 75; their
+// lengths are not known to the host, and where one has nearly all tokens the workgroup wins:
+// 8192 tokens behind 63 sequences of one 85 and 66 us, 65536 tokens 155 and 134, most of it
+// the first block's 64 sequences one after the other)
 constexpr int BAL_MANY = 64;
 constexpr int BAL_MAX_S = 65535;              // sequences
 // rounds of a block, at most: a lane adds that many probabilities in fp32, 18 more additions
@@ -189,6 +192,8 @@ __global__ __launch_bounds__(BAL_NT) void balance_part_kernel(BalArgs a) {
         bal_softmax<TPR, V, true>(v[u], E, m, sum);
         use[u] = use[u] && !(sum == 0.f);
         if (use[u]) {
+          // (the hardware's reciprocal and log2, each off by a rounding at most: sum is in
+          // [1, E], where neither needs the range steps of a division and of logf)
           const float inv = __builtin_amdgcn_rcpf(sum);
           const float lse = fmaf(__builtin_amdgcn_logf(sum), 0.693147181f, m);
 #pragma unroll
@@ -549,7 +554,7 @@ extern "C" int moe_balance_loss(const float* logits, const int32_t* idx, const u
   else launch_part<64, 16>(a, blocks, s);
   MOE_TRY(moe_check_launch(fn));
   if (one) return MOE_OK;
-  // (of many sequences each has few rows; one of them may have all, up to 256, whatever S)
+  // (of many sequences each has few rows, where all of them are 256 and one a sequence)
   const int cg = (E + MOE_WAVE - 1) / MOE_WAVE;
   if (S < BAL_MANY || (blocks > 256 && S < blocks))
     hipLaunchKernelGGL(balance_sum_kernel<BAL_WAVES>, dim3(cg, S), dim3(BAL_NT), 0, s, a);

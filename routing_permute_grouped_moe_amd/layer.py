@@ -357,7 +357,8 @@ class MoeLayer:
 
     def clip_grads(self, max_norm: float, stream=None):
         """Clips the layer's gradients by their norm together, in place; returns the
-        norm (:class:`GradClip` takes the gradients of several layers)."""
+        norm (:class:`GradClip` takes the gradients of several layers, and one that is
+        kept saves the 8 us of making it here)."""
         return GradClip(self.grads()).clip(max_norm, stream=stream)
 
 
@@ -762,8 +763,10 @@ class GradClip:
 
     ``grads`` are dense tensors of any shapes, fp32 or bf16, on one GPU; ``outs``:
     where the clipped ones go, of the same sizes and of the same type or fp32
-    (None: in place).  The tensors stay the caller's and keep their sizes; each
-    call takes their present contents, and their addresses as they are then."""
+    (None: in place).  The tensors stay the caller's and keep their sizes and
+    types; each call takes their present contents, and their addresses as they are
+    then.  Making one looks at every tensor (about 8 us for four, 1.1 ms for 700):
+    where gradients keep their buffers, keep it from step to step."""
 
     def __init__(self, grads, outs=None, kind: str = "l2"):
         self.grads = list(grads)
